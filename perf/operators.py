@@ -227,14 +227,14 @@ def _run_own(st, case):
                         st["v_cache"], q_out=st["q_out"], rotary=st["rotary"])
         return st["q_out"], st["k_cache"], st["v_cache"]
     if case["kind"] == "append":
-        h.ddt_append_kv4(st["q"], st["k"], st["v"], st["q_start"], st["ctx_lens"], st["table"], R, st["kv4"],
+        h.ddt_append_kvq(st["q"], st["k"], st["v"], st["q_start"], st["ctx_lens"], st["table"], R, st["kv4"],
                          q_out=st["q_out"], rotary=st["rotary"], k_held=st["k_held"], v_held=st["v_held"])
         return st["q_out"], st["k_held"], st["v_held"], st["k_codes"], st["v_codes"], st["k_scales"], st["v_scales"]
     if case["bits"] == 16:
         h.ddt_prompt_attention(st["q"], st["q_start"], st["ctx_lens"], st["table"], R, st["k_cache"], st["v_cache"],
                                st["out"])
     else:
-        h.ddt_prompt_attention_kv4(st["q"], st["q_start"], st["ctx_lens"], st["table"], R, st["kv4"], st["out"])
+        h.ddt_prompt_attention_kvq(st["q"], st["q_start"], st["ctx_lens"], st["table"], R, st["kv4"], st["out"])
     return st["out"]
 
 
