@@ -25,6 +25,12 @@
  *   ddt_schedule_prefix
  *       the hardware-aware prefix scheduler (guesses to verify per request;
  *       its output is ddt_accept_stochastic's prefix lengths)
+ *   ddt_append_kv / ddt_append_kvq
+ *       new tokens' keys and values into the paged cache (bf16, or held in 4
+ *       bits), queries and keys rotated by their positions on the way
+ *   ddt_prompt_attention / ddt_prompt_attention_kvq
+ *       causal attention of packed sequences over that cache: prompts, chunks
+ *       of prompts, drafted chains, single tokens
  *   ddt_topk_logprobs_noalloc
  *       a1 without a context
  *
@@ -51,7 +57,8 @@
  *   - Logit tensors (draft, target) are bf16 or fp32 as the context's
  *     config says; their pointers are const void*.
  *   - All tensors are dense row-major with the shapes given below; no
- *     strides are accepted. Vectorised paths need 16-byte-aligned base
+ *     strides are accepted (but for the token strides of packed q, k and v,
+ *     where a call names them). Vectorised paths need 16-byte-aligned base
  *     pointers; every other pointer needs its element's alignment (4 bytes
  *     for i32 and f32, 8 for f64). Unaligned ones are rejected with
  *     DDT_EINVAL.
@@ -96,6 +103,7 @@ typedef enum ddt_dtype { DDT_BF16 = 0, DDT_F32 = 1 } ddt_dtype;
 #define DDT_DEV_BAD_PAGE 0x2   /* a block-table entry was outside [0, num_pages) */
 #define DDT_DEV_BAD_TREE 0x4   /* parents/n_nodes/acc arrays out of range */
 #define DDT_DEV_TIMEOUT 0x8    /* a bounded on-device wait gave up (the kernel wound down) */
+#define DDT_DEV_BAD_LENGTH 0x10 /* q_start or ctx_lens out of range (that request was skipped) */
 
 typedef struct ddt_config {
     int32_t R_max;             /* most requests a call may carry (1..2048) */
@@ -402,6 +410,102 @@ ddt_status ddt_accept_stochastic(ddt_ctx *ctx, const void *draft_logits,
 #define DDT_SCHED_MAX_SLOTS 8192
 ddt_status ddt_schedule_prefix(ddt_ctx *ctx, const float *conf, int32_t R, const float *cost_ms,
                                int32_t *n_keep, int32_t *n_total, double *stats, void *stream);
+
+/* Packed sequences (the four calls below). T new tokens of R requests lie one
+ * behind the other: request r's are rows q_start[r] .. q_start[r+1] - 1 of q,
+ * k and v (q_start [R+1] i32 on the device, ascending, within [0, T]; a request
+ * may have none). The i-th of them has position ctx_lens[r] + i, which is also
+ * its slot: page block_table[r][slot / page_size], row slot % page_size.
+ * ctx_lens[r] is the length before these tokens, in every one of the calls: a
+ * model of several layers appends and attends in each and moves its lengths on
+ * afterwards (see new_lens). A request is skipped, and DDT_DEV_BAD_LENGTH set,
+ * when q_start[r] > q_start[r+1], either lies outside [0, T], ctx_lens[r] < 0,
+ * or its last slot passes max_pages_per_req * page_size (for the append with a
+ * rotation: or its last position passes max_pos). Rows of no request (before
+ * q_start[0], behind q_start[R]) are neither read for a result nor written. */
+typedef struct ddt_append_args {
+    int32_t R;                  /* requests, at most R_max */
+    int32_t T;                  /* rows of q, k, v and q_out */
+    const uint16_t *q;          /* [T, Hq, d] bf16, or NULL (then q_out is NULL too) */
+    const uint16_t *k;          /* [T, Hkv, d] bf16 */
+    const uint16_t *v;          /* [T, Hkv, d] bf16 */
+    int64_t q_stride, k_stride, v_stride; /* elements from token to token: multiples of 8, at
+                                   least heads * d; 0 = dense. So q, k and v may be parts of
+                                   the rows of one fused projection. */
+    const int32_t *q_start;     /* [R+1] */
+    const int32_t *ctx_lens;    /* [R] */
+    const int32_t *block_table; /* [R, max_pages_per_req] */
+    const float *cos_sin;       /* [max_pos, rotary_dim] f32: row p holds rotary_dim / 2 cosines,
+                                   then as many sines, of position p's angles; NULL: no rotation */
+    int32_t rotary_dim;         /* leading channels that are turned: a multiple of 32, at most d */
+    int32_t max_pos;            /* rows of cos_sin */
+    int32_t interleaved;        /* 0: channels (j, j + rotary_dim / 2) form a pair; 1: (2j, 2j + 1) */
+    uint16_t *q_out;            /* [T, Hq, d] bf16, dense: the turned queries; may be q itself when
+                                   q is dense (any other overlap is DDT_EINVAL) */
+    int32_t *new_lens;          /* [R] or NULL: ctx_lens[r] + the request's tokens (ctx_lens[r] for
+                                   a skipped request); must not overlap ctx_lens */
+} ddt_append_args;
+
+/* Append: q and k of every new token turned by its position,
+ *     x1' = x1 cos - x2 sin,  x2' = x2 cos + x1 sin
+ * (fp32, each product and sum rounded to nearest, one rounding to bf16), the
+ * queries to q_out, keys and values to the token's cache slot. Nothing else of
+ * the cache is written. Page ids out of range set DDT_DEV_BAD_PAGE and that
+ * row's keys and values are dropped. Two requests that append to one and the
+ * same slot leave either's row there. T = 0 or R = 0 writes only new_lens. */
+ddt_status ddt_append_kv(ddt_ctx *ctx, const ddt_append_args *args, uint16_t *k_cache,
+                         uint16_t *v_cache, void *stream);
+
+/* A cache held in 4 bits: each token's head row of d channels is d / 16 blocks
+ * of 16 neighbouring channels, a block is 16 e2m1 codes (sign, magnitudes 0,
+ * 0.5, 1, 1.5, 2, 3, 4, 6) and one e4m3 scale, and its values are
+ * magnitude * scale * k_scale (or v_scale). Eight channels lie in four bytes:
+ * byte b holds channel 4b (low nibble) and 4b + 2 (high) for b = 0, 1, channel
+ * 4(b - 2) + 1 and 4(b - 2) + 3 for b = 2, 3. One head's rows of a page are
+ * contiguous. The product of a code and a scale has at most six significant
+ * bits, so a bf16 holds it exactly. */
+typedef struct ddt_kv4 {
+    uint8_t *k_codes;  /* [num_pages, Hkv, page_size, d / 2], 16-byte aligned */
+    uint8_t *v_codes;
+    uint8_t *k_scales; /* [num_pages, Hkv, page_size, d / 16] e4m3 bits, 16-byte aligned */
+    uint8_t *v_scales;
+    float k_scale;     /* finite and within [2^-40, 2^40]: what every scale of k_scales is in units of */
+    float v_scale;
+} ddt_kv4;
+
+/* The same append into a cache held in 4 bits: for each block, with g the
+ * cache's k_scale or v_scale, scale = e4m3(min(amax * (1 / (6 g)), 448)) and
+ * each channel's code the nearest magnitude of |x| / (scale g), ties to the
+ * even code, 6 where it is larger. A block with a NaN gets a NaN scale and so
+ * reads as NaN. k_held, v_held ([T, Hkv, d] bf16, dense, both or neither NULL):
+ * the values that the cache now holds for the new tokens. */
+ddt_status ddt_append_kvq(ddt_ctx *ctx, const ddt_append_args *args, const ddt_kv4 *cache,
+                          uint16_t *k_held, uint16_t *v_held, void *stream);
+
+/* Causal attention of the packed queries over the paged cache, to which the
+ * same tokens' keys and values have been appended: the query at position p
+ * attends, with scale 1/sqrt(d), to positions 0..p of its request and KV head
+ * h / (Hq / Hkv); softmax and sums in fp32, probabilities rounded to bf16 for
+ * the product with the values, one rounding of the result.
+ *   q        [T, Hq, d] bf16 with q_stride elements from token to token (a
+ *            multiple of 8, at least Hq * d; 0 = dense)
+ *   out      [T, Hq, d] bf16, dense; must not overlap q
+ *   k_cache, v_cache, block_table, ctx_lens, q_start: as above
+ * Page ids out of range set DDT_DEV_BAD_PAGE and are read as zeros. Slots past
+ * a request's last token are never attended to, whatever they hold; a NaN or
+ * an infinity among a request's own values can reach every query of the same
+ * request from 255 positions before it on. One token per request is a decoding
+ * step; a chain's tokens are its verification pass. */
+ddt_status ddt_prompt_attention(ddt_ctx *ctx, const uint16_t *q, int64_t q_stride,
+                                const int32_t *q_start, const int32_t *ctx_lens, int32_t R,
+                                int32_t T, const uint16_t *k_cache, const uint16_t *v_cache,
+                                const int32_t *block_table, uint16_t *out, void *stream);
+
+/* The same over a cache held in 4 bits. */
+ddt_status ddt_prompt_attention_kvq(ddt_ctx *ctx, const uint16_t *q, int64_t q_stride,
+                                    const int32_t *q_start, const int32_t *ctx_lens, int32_t R,
+                                    int32_t T, const ddt_kv4 *cache, const int32_t *block_table,
+                                    uint16_t *out, void *stream);
 
 /* Wait for the context's device to finish all enqueued work, copy the
  * device status word to *host_out (DDT_DEV_* bits) and clear it. */

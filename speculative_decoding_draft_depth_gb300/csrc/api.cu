@@ -221,6 +221,101 @@ ddt_status chk_compact(const uint16_t *kc, const uint16_t *vc, const int32_t *bt
     return DDT_OK;
 }
 
+// byte ranges [a, a + na) and [b, b + nb) share a byte
+bool overlap(const void *a, int64_t na, const void *b, int64_t nb)
+{
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return na > 0 && nb > 0 && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
+// packed rows a call may carry (row indices plus a tile stay within 31 bits)
+const int32_t MAX_PACKED = 0x7fff0000;
+
+// a token stride of packed rows: 0 stands for dense
+bool good_stride(int64_t *stride, int64_t dense)
+{
+    if (*stride == 0)
+        *stride = dense;
+    // (the upper limit keeps T * stride * 2 bytes within 63 bits and a TMA stride within 40)
+    return *stride >= dense && *stride % 8 == 0 && *stride <= (int64_t)1 << 30;
+}
+
+// bytes from the first to behind the last element of T rows
+int64_t span_bytes(int64_t T, int64_t stride, int64_t dense)
+{
+    return T > 0 ? ((T - 1) * stride + dense) * 2 : 0;
+}
+
+ddt_status chk_kv4(const ddt_kv4 *c)
+{
+    DDT_CHECK(c && c->k_codes && c->v_codes && c->k_scales && c->v_scales);
+    DDT_CHECK(aligned16(c->k_codes) && aligned16(c->v_codes) && aligned16(c->k_scales) &&
+              aligned16(c->v_scales));
+    const float lo = 9.094947017729282e-13f, hi = 1.099511627776e12f;  // 2^-40, 2^40
+    DDT_CHECK(c->k_scale >= lo && c->k_scale <= hi && c->v_scale >= lo && c->v_scale <= hi);
+    return DDT_OK;
+}
+
+// the checks that both caches' appends share; *out: the arguments with strides resolved
+ddt_status chk_append(const ddt_ctx *ctx, const ddt_append_args *in, ddt_append_args *out)
+{
+    DDT_CHECK(in);
+    const ddt_status st = check_R(ctx, in->R);
+    if (st != DDT_OK)
+        return st;
+    ddt_append_args a = *in;
+    const int64_t nq = (int64_t)ctx->cfg.Hq * ctx->cfg.d, nk = (int64_t)ctx->cfg.Hkv * ctx->cfg.d;
+    DDT_CHECK(a.T >= 0 && a.T <= MAX_PACKED);
+    if (a.R == 0) {
+        *out = a;
+        return DDT_OK;
+    }
+    DDT_CHECK(a.q_start && a.ctx_lens && a.block_table && aligned4(a.q_start) &&
+              aligned4(a.ctx_lens) && aligned4(a.block_table));
+    DDT_CHECK(!a.new_lens || (aligned4(a.new_lens) &&
+                              !overlap(a.new_lens, 4 * (int64_t)a.R, a.ctx_lens, 4 * (int64_t)a.R)));
+    DDT_CHECK((a.q == nullptr) == (a.q_out == nullptr));
+    DDT_CHECK(good_stride(&a.q_stride, nq) && good_stride(&a.k_stride, nk) &&
+              good_stride(&a.v_stride, nk));
+    DDT_CHECK(a.T == 0 || (a.k && a.v));
+    DDT_CHECK(aligned16(a.q) && aligned16(a.k) && aligned16(a.v) && aligned16(a.q_out));
+    if (a.q) {
+        const bool in_place = a.q == a.q_out && a.q_stride == nq;
+        const int64_t out_bytes = span_bytes(a.T, nq, nq);
+        DDT_CHECK(in_place || !overlap(a.q, span_bytes(a.T, a.q_stride, nq), a.q_out, out_bytes));
+        DDT_CHECK(!overlap(a.k, span_bytes(a.T, a.k_stride, nk), a.q_out, out_bytes) &&
+                  !overlap(a.v, span_bytes(a.T, a.v_stride, nk), a.q_out, out_bytes));
+    }
+    if (a.cos_sin) {
+        DDT_CHECK(aligned16(a.cos_sin) && a.max_pos >= 1 && a.rotary_dim >= 32 &&
+                  a.rotary_dim % 32 == 0 && a.rotary_dim <= ctx->cfg.d);
+        DDT_CHECK(a.interleaved == 0 || a.interleaved == 1);
+    } else {
+        a.rotary_dim = 0;
+        a.max_pos = 0x7fffffff;
+    }
+    *out = a;
+    return DDT_OK;
+}
+
+ddt_status chk_prompt(const ddt_ctx *ctx, const uint16_t *q, int64_t *q_stride,
+                      const int32_t *q_start, const int32_t *ctx_lens, int32_t R, int32_t T,
+                      const int32_t *block_table, const uint16_t *out)
+{
+    const ddt_status st = check_R(ctx, R);
+    if (st != DDT_OK)
+        return st;
+    DDT_CHECK(T >= 0 && T <= MAX_PACKED);
+    if (R == 0 || T == 0)
+        return DDT_OK;
+    const int64_t nq = (int64_t)ctx->cfg.Hq * ctx->cfg.d;
+    DDT_CHECK(q && q_start && ctx_lens && block_table && out && good_stride(q_stride, nq));
+    DDT_CHECK(aligned16(q) && aligned16(out) && aligned4(q_start) && aligned4(ctx_lens) &&
+              aligned4(block_table));
+    DDT_CHECK(!overlap(q, span_bytes(T, *q_stride, nq), out, span_bytes(T, nq, nq)));
+    return DDT_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -787,6 +882,70 @@ ddt_status ddt_round_markov(ddt_ctx *ctx, const ddt_round_args *a, const uint16_
                                a->depths, a->n_nodes, a->mask, ctx->hi));
     DDT_TRY(cudaEventRecord(ctx->ev_tree, ctx->hi));
     return round_verify(ctx, a, s);
+}
+
+ddt_status ddt_append_kv(ddt_ctx *ctx, const ddt_append_args *args, uint16_t *k_cache,
+                         uint16_t *v_cache, void *stream)
+{
+    ddt_append_args a;
+    ddt_status st = chk_append(ctx, args, &a);
+    if (st != DDT_OK)
+        return st;
+    if (a.R == 0)
+        return DDT_OK;
+    DDT_CHECK(k_cache && v_cache && aligned16(k_cache) && aligned16(v_cache));
+    if ((st = set_device(ctx)) != DDT_OK)
+        return st;
+    DDT_TRY(launch_append(ctx, a, k_cache, v_cache, nullptr, nullptr, nullptr,
+                          (cudaStream_t)stream));
+    return DDT_OK;
+}
+
+ddt_status ddt_append_kvq(ddt_ctx *ctx, const ddt_append_args *args, const ddt_kv4 *cache,
+                          uint16_t *k_held, uint16_t *v_held, void *stream)
+{
+    ddt_append_args a;
+    ddt_status st = chk_append(ctx, args, &a);
+    if (st != DDT_OK || (st = chk_kv4(cache)) != DDT_OK)
+        return st;
+    if (a.R == 0)
+        return DDT_OK;
+    DDT_CHECK((k_held == nullptr) == (v_held == nullptr) && aligned16(k_held) && aligned16(v_held));
+    if ((st = set_device(ctx)) != DDT_OK)
+        return st;
+    DDT_TRY(launch_append(ctx, a, nullptr, nullptr, cache, k_held, v_held, (cudaStream_t)stream));
+    return DDT_OK;
+}
+
+ddt_status ddt_prompt_attention(ddt_ctx *ctx, const uint16_t *q, int64_t q_stride,
+                                const int32_t *q_start, const int32_t *ctx_lens, int32_t R,
+                                int32_t T, const uint16_t *k_cache, const uint16_t *v_cache,
+                                const int32_t *block_table, uint16_t *out, void *stream)
+{
+    ddt_status st = chk_prompt(ctx, q, &q_stride, q_start, ctx_lens, R, T, block_table, out);
+    if (st != DDT_OK || R == 0 || T == 0)
+        return st;
+    DDT_CHECK(k_cache && v_cache && aligned16(k_cache) && aligned16(v_cache));
+    if ((st = set_device(ctx)) != DDT_OK)
+        return st;
+    DDT_TRY(launch_prompt_attention(ctx, q, q_stride, q_start, ctx_lens, R, T, k_cache, v_cache,
+                                    nullptr, block_table, out, (cudaStream_t)stream));
+    return DDT_OK;
+}
+
+ddt_status ddt_prompt_attention_kvq(ddt_ctx *ctx, const uint16_t *q, int64_t q_stride,
+                                    const int32_t *q_start, const int32_t *ctx_lens, int32_t R,
+                                    int32_t T, const ddt_kv4 *cache, const int32_t *block_table,
+                                    uint16_t *out, void *stream)
+{
+    ddt_status st = chk_prompt(ctx, q, &q_stride, q_start, ctx_lens, R, T, block_table, out);
+    if (st != DDT_OK || (st = chk_kv4(cache)) != DDT_OK || R == 0 || T == 0)
+        return st;
+    if ((st = set_device(ctx)) != DDT_OK)
+        return st;
+    DDT_TRY(launch_prompt_attention(ctx, q, q_stride, q_start, ctx_lens, R, T, nullptr, nullptr,
+                                    cache, block_table, out, (cudaStream_t)stream));
+    return DDT_OK;
 }
 
 ddt_status ddt_device_status(ddt_ctx *ctx, int32_t *host_out)

@@ -147,6 +147,18 @@ cudaError_t launch_schedule_prefix(const ddt_ctx *c, const float *conf, int R, c
                                    int32_t *n_keep, int32_t *n_total, double *stats,
                                    cudaStream_t s);
 
+// packed tokens into the paged cache, bf16 or (kv4 != NULL) held in 4 bits (append.cu)
+cudaError_t launch_append(const ddt_ctx *c, const ddt_append_args &a, uint16_t *k_cache,
+                          uint16_t *v_cache, const ddt_kv4 *kv4, uint16_t *k_held,
+                          uint16_t *v_held, cudaStream_t s);
+
+// causal attention of packed sequences over it (prompt.cu)
+cudaError_t launch_prompt_attention(ddt_ctx *c, const uint16_t *q, int64_t q_stride,
+                                    const int32_t *q_start, const int32_t *ctx_lens, int R, int T,
+                                    const uint16_t *k_cache, const uint16_t *v_cache,
+                                    const ddt_kv4 *kv4, const int32_t *block_table, uint16_t *out,
+                                    cudaStream_t s);
+
 // a1 with caller-supplied scratch (used by the allocation-free entry point)
 cudaError_t launch_topk_scratch(const void *z, int dtype, int rows, int V, int K, int nch,
                                 int num_sms, uint16_t *gkey, uint16_t *wtop, float2 *part_ms,

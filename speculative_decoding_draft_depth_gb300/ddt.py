@@ -16,13 +16,14 @@ LIB_PATH = os.path.join(_HERE, "_build", "libddt.so")
 
 OK, EINVAL, EUNSUPPORTED, ECUDA, ENOMEM = 0, 1, 2, 3, 4
 BF16, F32 = 0, 1
-DEV_NAN_LOGITS, DEV_BAD_PAGE, DEV_BAD_TREE, DEV_TIMEOUT = 0x1, 0x2, 0x4, 0x8
+DEV_NAN_LOGITS, DEV_BAD_PAGE, DEV_BAD_TREE, DEV_TIMEOUT, DEV_BAD_LENGTH = 0x1, 0x2, 0x4, 0x8, 0x10
 
 EXPORTS = ("ddt_create", "ddt_destroy", "ddt_workspace_bytes", "ddt_topk_logprobs",
            "ddt_build_tree", "ddt_build_tree_conditioned", "ddt_build_mask", "ddt_tree_attention", "ddt_target_argmax",
            "ddt_walk", "ddt_compact", "ddt_accept", "ddt_round", "ddt_round_conditioned",
            "ddt_markov_table", "ddt_build_tree_markov", "ddt_round_markov",
-           "ddt_accept_stochastic", "ddt_schedule_prefix", "ddt_device_status", "ddt_strerror",
+           "ddt_accept_stochastic", "ddt_schedule_prefix", "ddt_append_kv", "ddt_append_kvq",
+           "ddt_prompt_attention", "ddt_prompt_attention_kvq", "ddt_device_status", "ddt_strerror",
            "ddt_last_cuda_error", "ddt_debug_arm_attention_timeout")
 
 
@@ -55,6 +56,123 @@ class RoundArgs(ctypes.Structure):
         "block_table", "ctx_lens", "top_lp", "top_ids", "tree_tokens", "parents", "depths",
         "n_nodes", "mask", "attn_out", "target_argmax", "acc_len", "acc_nodes", "acc_tokens",
         "bonus", "att_event_begin", "att_event_end")]
+
+
+class AppendArgs(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_int32), ("T", ctypes.c_int32), ("q", _P), ("k", _P), ("v", _P),
+                ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("q_start", _P), ("ctx_lens", _P),
+                ("block_table", _P), ("cos_sin", _P), ("rotary_dim", ctypes.c_int32),
+                ("max_pos", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("q_out", _P),
+                ("new_lens", _P)]
+
+
+class Kv4(ctypes.Structure):
+    _fields_ = [("k_codes", _P), ("v_codes", _P), ("k_scales", _P), ("v_scales", _P),
+                ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
+
+
+class Rotary:
+    """The position rotation of an append: a [max_pos, dim] f32 CUDA table of
+    dim / 2 cosines and dim / 2 sines per position (rotary_table makes one);
+    dim leading channels are turned, in pairs (j, j + dim / 2) or, interleaved,
+    (2j, 2j + 1)."""
+
+    def __init__(self, table, dim, interleaved=False):
+        if table.dtype != torch.float32 or table.dim() != 2 or table.shape[1] != dim:
+            raise ValueError("expected a [max_pos, %d] float32 table" % dim)
+        self.table, self.dim, self.interleaved = table, dim, bool(interleaved)
+
+
+def rotary_table(max_pos, dim, base=10000.0, inv_freq=None, device="cuda"):
+    """[max_pos, dim] f32: cos and sin of position * inv_freq[j], j < dim / 2
+    (default base ** (-2j / dim)); angles in fp64, since a far position's
+    angle has no fraction left in fp32."""
+    if inv_freq is None:
+        inv_freq = float(base) ** (-torch.arange(0, dim, 2, dtype=torch.float64) / dim)
+    inv_freq = torch.as_tensor(inv_freq, dtype=torch.float64).to(device)
+    if inv_freq.shape != (dim // 2,):
+        raise ValueError("expected %d inverse frequencies" % (dim // 2))
+    ang = torch.arange(max_pos, dtype=torch.float64, device=device)[:, None] * inv_freq
+    return torch.cat((ang.cos(), ang.sin()), dim=1).float().contiguous()
+
+
+class Kv4Cache:
+    """A KV cache held in 4 bits (ddt_kv4): uint8 CUDA tensors k_codes, v_codes
+    [num_pages, Hkv, page_size, d / 2], k_scales, v_scales [num_pages, Hkv,
+    page_size, d / 16] and the two global scales. Context.alloc_kv4 makes one."""
+
+    def __init__(self, k_codes, v_codes, k_scales, v_scales, k_scale=1.0, v_scale=1.0):
+        self.k_codes, self.v_codes, self.k_scales, self.v_scales = k_codes, v_codes, k_scales, v_scales
+        self.k_scale, self.v_scale = float(k_scale), float(v_scale)
+
+    def check(self, cfg):
+        for n in ("k", "v"):
+            _shaped(getattr(self, n + "_codes"), n + "_codes", (torch.uint8,),
+                    (cfg.num_pages, cfg.Hkv, cfg.page_size, cfg.d // 2))
+            _shaped(getattr(self, n + "_scales"), n + "_scales", (torch.uint8,),
+                    (cfg.num_pages, cfg.Hkv, cfg.page_size, cfg.d // 16))
+
+
+_BF16 = (torch.bfloat16, torch.int16, torch.uint16)
+_I32 = (torch.int32,)
+
+
+def _shaped(t, name, dtypes, shape):
+    """Raise unless t has one of the types and the shape (None: any extent)."""
+    if t.dtype not in dtypes:
+        raise ValueError("%s: expected %s, got %s" % (name, dtypes[0], t.dtype))
+    if t.dim() != len(shape) or any(w is not None and g != w for g, w in zip(t.shape, shape)):
+        raise ValueError("%s: expected shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+
+
+def _rows(t, name, T, heads, d):
+    """The token stride of packed rows [T, heads, d], each row dense."""
+    _shaped(t, name, _BF16, (T, heads, d))
+    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+        raise ValueError("%s: expected each token's heads and channels dense" % name)
+    # (a single row has no next one)
+    return t.stride(0) if T > 1 else heads * d
+
+
+def check_append(cfg, q, k, v, q_start, ctx_lens, block_table, R, q_out, rotary, new_lens):
+    """Types and shapes of an append's tensors; the token strides of q, k, v."""
+    T = k.shape[0]
+    ks, vs = _rows(k, "k", T, cfg.Hkv, cfg.d), _rows(v, "v", T, cfg.Hkv, cfg.d)
+    qs = 0
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is not None:
+        qs = _rows(q, "q", T, cfg.Hq, cfg.d)
+        _shaped(q_out, "q_out", _BF16, (T, cfg.Hq, cfg.d))
+    check_packed(cfg, q_start, ctx_lens, block_table, R)
+    if rotary is not None and (rotary.dim % 32 or not 32 <= rotary.dim <= cfg.d):
+        raise ValueError("rotary: expected a multiple of 32 channels up to %d" % cfg.d)
+    if new_lens is not None:
+        _shaped(new_lens, "new_lens", _I32, (R,))
+    return qs, ks, vs
+
+
+def check_packed(cfg, q_start, ctx_lens, block_table, R):
+    if not 0 <= R <= cfg.R_max:
+        raise ValueError("R: expected 0..%d" % cfg.R_max)
+    _shaped(q_start, "q_start", _I32, (R + 1,))
+    _shaped(ctx_lens, "ctx_lens", _I32, (R,))
+    _shaped(block_table, "block_table", _I32, (R, cfg.max_pages_per_req))
+
+
+def check_prompt(cfg, q, q_start, ctx_lens, block_table, R, out):
+    """Types and shapes of a prompt attention's tensors; q's token stride."""
+    T = q.shape[0]
+    qs = _rows(q, "q", T, cfg.Hq, cfg.d)
+    _shaped(out, "out", _BF16, (T, cfg.Hq, cfg.d))
+    check_packed(cfg, q_start, ctx_lens, block_table, R)
+    return qs
+
+
+def _cache_shapes(cfg, k_cache, v_cache):
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _shaped(t, n, _BF16, (cfg.num_pages, cfg.page_size, cfg.Hkv, cfg.d))
 
 
 _lib = None
@@ -91,6 +209,11 @@ def load(path=LIB_PATH):
         "ddt_round_markov": ([_P, ctypes.POINTER(RoundArgs), _P, _P, _P, _P], i32),
         "ddt_accept_stochastic": ([_P, _P, _P, _P, _P, _P, i32, _P, _P, _P, _P], i32),
         "ddt_schedule_prefix": ([_P, _P, i32, _P, _P, _P, _P, _P], i32),
+        "ddt_append_kv": ([_P, ctypes.POINTER(AppendArgs), _P, _P, _P], i32),
+        "ddt_append_kvq": ([_P, ctypes.POINTER(AppendArgs), ctypes.POINTER(Kv4), _P, _P, _P], i32),
+        "ddt_prompt_attention": ([_P, _P, i64, _P, _P, i32, i32, _P, _P, _P, _P, _P], i32),
+        "ddt_prompt_attention_kvq": ([_P, _P, i64, _P, _P, i32, i32, ctypes.POINTER(Kv4), _P, _P,
+                                      _P], i32),
         "ddt_device_status": ([_P, ctypes.POINTER(i32)], i32),
         "ddt_debug_arm_attention_timeout": ([_P, i64], i32),
         "ddt_strerror": ([i32], ctypes.c_char_p),
@@ -144,6 +267,7 @@ class Context:
         h = _P()
         _check(lib.ddt_create(ctypes.byref(cfg), ctypes.byref(h)), "ddt_create")
         self._h = h
+        self.device = torch.cuda.current_device()
         self.K = cfg.K if cfg.K else min(cfg.B, cfg.V)
         self.P = cfg.B + 1
         self.W = (self.P + 31) // 32
@@ -231,6 +355,97 @@ class Context:
         _check(_lib.ddt_schedule_prefix(self._h, _ptr(conf), R, _ptr(cost_ms), _ptr(n_keep),
                                         _ptr(n_total), _ptr(stats), _stream(stream)),
                "ddt_schedule_prefix")
+
+    # -- packed sequences over the paged cache --------------------------------
+    def _on_device(self, *tensors, dense=True):
+        """Device pointers of tensors on this context's device (None: NULL)."""
+        out = []
+        for t in tensors:
+            if t is not None and (not t.is_cuda or t.device.index != self.device):
+                raise ValueError("expected a tensor on CUDA device %d" % self.device)
+            if t is not None and dense and not t.is_contiguous():
+                raise ValueError("expected a contiguous tensor")
+            out.append(None if t is None else ctypes.c_void_p(t.data_ptr()))
+        return out
+
+    def _own_stream(self, stream):
+        """The given stream, or the current one of this context's device."""
+        return _stream(torch.cuda.current_stream(self.device) if stream is None else stream)
+
+    def _kv4(self, cache):
+        cache.check(self.cfg)
+        ptrs = self._on_device(cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales)
+        return Kv4(*ptrs, cache.k_scale, cache.v_scale)
+
+    def _append_args(self, q, k, v, q_start, ctx_lens, block_table, R, q_out, rotary, new_lens):
+        qs, ks, vs = check_append(self.cfg, q, k, v, q_start, ctx_lens, block_table, R, q_out,
+                                  rotary, new_lens)
+        a = AppendArgs()
+        a.R, a.T = R, k.shape[0]
+        a.q, a.k, a.v = self._on_device(q, k, v, dense=False)
+        a.q_stride, a.k_stride, a.v_stride = qs, ks, vs
+        a.q_start, a.ctx_lens, a.block_table, a.q_out, a.new_lens = self._on_device(
+            q_start, ctx_lens, block_table, q_out, new_lens)
+        if rotary is not None:
+            a.cos_sin, = self._on_device(rotary.table)
+            a.rotary_dim, a.max_pos = rotary.dim, rotary.table.shape[0]
+            a.interleaved = int(rotary.interleaved)
+        return a
+
+    def ddt_append_kv(self, q, k, v, q_start, ctx_lens, block_table, R, k_cache, v_cache,
+                      q_out=None, rotary=None, new_lens=None, stream=None):
+        """Append R requests' packed new tokens to the paged cache: k, v
+        [T, Hkv, d] (and q [T, Hq, d] to q_out) bf16, turned by `rotary` (a
+        Rotary, or None). q, k and v may be views of one projection's rows;
+        q_out may be q itself when q is dense. new_lens [R] i32 (optional):
+        the lengths after the append; ctx_lens stays as it is."""
+        a = self._append_args(q, k, v, q_start, ctx_lens, block_table, R, q_out, rotary, new_lens)
+        _cache_shapes(self.cfg, k_cache, v_cache)
+        _check(_lib.ddt_append_kv(self._h, ctypes.byref(a), *self._on_device(k_cache, v_cache),
+                                  self._own_stream(stream)), "ddt_append_kv")
+
+    def ddt_append_kvq(self, q, k, v, q_start, ctx_lens, block_table, R, cache, q_out=None,
+                       rotary=None, new_lens=None, k_held=None, v_held=None, stream=None):
+        """The same into a Kv4Cache; k_held, v_held [T, Hkv, d] bf16 (optional):
+        the values that the cache now holds for the new tokens."""
+        a = self._append_args(q, k, v, q_start, ctx_lens, block_table, R, q_out, rotary, new_lens)
+        for t, n in ((k_held, "k_held"), (v_held, "v_held")):
+            if t is not None:
+                _shaped(t, n, _BF16, (k.shape[0], self.cfg.Hkv, self.cfg.d))
+        c = self._kv4(cache)
+        _check(_lib.ddt_append_kvq(self._h, ctypes.byref(a), ctypes.byref(c),
+                                   *self._on_device(k_held, v_held), self._own_stream(stream)),
+               "ddt_append_kvq")
+
+    def ddt_prompt_attention(self, q, q_start, ctx_lens, block_table, R, k_cache, v_cache, out,
+                             stream=None):
+        """Causal attention of R requests' packed queries q [T, Hq, d] bf16 over
+        the paged cache that holds their keys and values (ctx_lens [R]: the
+        lengths before these tokens) into out [T, Hq, d] bf16."""
+        qs = check_prompt(self.cfg, q, q_start, ctx_lens, block_table, R, out)
+        _cache_shapes(self.cfg, k_cache, v_cache)
+        pq, = self._on_device(q, dense=False)
+        ps, pc, pb, po, pk, pv = self._on_device(q_start, ctx_lens, block_table, out, k_cache, v_cache)
+        _check(_lib.ddt_prompt_attention(self._h, pq, qs, ps, pc, R, q.shape[0], pk, pv, pb, po,
+                                         self._own_stream(stream)), "ddt_prompt_attention")
+
+    def ddt_prompt_attention_kvq(self, q, q_start, ctx_lens, block_table, R, cache, out,
+                                 stream=None):
+        """The same over a Kv4Cache."""
+        qs = check_prompt(self.cfg, q, q_start, ctx_lens, block_table, R, out)
+        c = self._kv4(cache)
+        pq, = self._on_device(q, dense=False)
+        ps, pc, pb, po = self._on_device(q_start, ctx_lens, block_table, out)
+        _check(_lib.ddt_prompt_attention_kvq(self._h, pq, qs, ps, pc, R, q.shape[0],
+                                             ctypes.byref(c), pb, po, self._own_stream(stream)),
+               "ddt_prompt_attention_kvq")
+
+    def alloc_kv4(self, k_scale=1.0, v_scale=1.0, device="cuda"):
+        """An empty (all zero) Kv4Cache of this context's page pool."""
+        c = self.cfg
+        t = [torch.zeros((c.num_pages, c.Hkv, c.page_size, n), dtype=torch.uint8, device=device)
+             for n in (c.d // 2, c.d // 2, c.d // 16, c.d // 16)]
+        return Kv4Cache(*t, k_scale=k_scale, v_scale=v_scale)
 
     def ddt_round(self, R, bufs, stream=None, att_events=None):
         """bufs: dict of tensors named like the fields of ddt_round_args.
