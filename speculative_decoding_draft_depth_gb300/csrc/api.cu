@@ -97,8 +97,11 @@ Layout layout_for(const ddt_config &c)
     L.tk_ms = take(rows_d * L.tk_nch * (TOPK_THREADS / 32) * sizeof(float2));
     L.am_val = take(rows_t * L.am_nch * sizeof(float));
     L.am_idx = take(rows_t * L.am_nch * sizeof(int32_t));
-    L.att_part_o = take((size_t)L.max_items * ATT_ROWS * c.d * sizeof(float));
-    L.att_part_ml = take((size_t)L.max_items * ATT_ROWS * sizeof(float2));
+    // (a4 and prompt attention use the same partials, one call after the other)
+    const size_t pr_rows = (size_t)2 * PR_MAX_CTAS * PR_ROWS, att_rows = (size_t)L.max_items * ATT_ROWS;
+    const size_t part_rows = pr_rows > att_rows ? pr_rows : att_rows;
+    L.att_part_o = take(part_rows * c.d * sizeof(float));
+    L.att_part_ml = take(part_rows * sizeof(float2));
     // parent-conditioned tree (sized for up to CG_GRID_MAX CTAs of its GEMM)
     const size_t np = c.markov_dim > 0 ? (size_t)c.R_max * c.frontier : 0;
     const size_t cmax = c.markov_dim > 0 ? (size_t)cond_tree_cmax(c) : 0;

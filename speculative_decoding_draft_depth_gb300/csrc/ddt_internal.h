@@ -31,6 +31,11 @@ constexpr int ATT_ROWS = 144;
 constexpr int ATT_MAX_CTAS = 256;
 constexpr int ATT_MAX_CTX = 262144;  // tokens of context per request
 
+// prompt attention: rows of one partial output, and the most CTAs of its grid
+// (two partial slots each; the partials share a4's memory)
+constexpr int PR_ROWS = 256;
+constexpr int PR_MAX_CTAS = 160;
+
 // parent-conditioned tree: most CTAs of its per-depth GEMM (partials per CTA)
 constexpr int CG_GRID_MAX = 256;
 constexpr int CG_NP_MAX = 128;  // parents of one depth of the conditioned tree (R * F)

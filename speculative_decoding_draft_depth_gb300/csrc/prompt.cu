@@ -118,12 +118,18 @@ __global__ void __launch_bounds__(256) prompt_rows_kernel(const PrArgs p)
 
 }  // namespace
 
+cudaError_t launch_prompt_tc(ddt_ctx *c, const uint16_t *q, int64_t q_stride, const int32_t *q_start,
+                             const int32_t *ctx_lens, int R, int T, const uint16_t *k_cache,
+                             const uint16_t *v_cache, const int32_t *block_table, uint16_t *out, cudaStream_t s);
+
 cudaError_t launch_prompt_attention(ddt_ctx *c, const uint16_t *q, int64_t q_stride,
                                     const int32_t *q_start, const int32_t *ctx_lens, int R, int T,
                                     const uint16_t *k_cache, const uint16_t *v_cache,
                                     const ddt_kv4 *kv4, const int32_t *block_table, uint16_t *out,
                                     cudaStream_t s)
 {
+    if (!kv4)
+        return launch_prompt_tc(c, q, q_stride, q_start, ctx_lens, R, T, k_cache, v_cache, block_table, out, s);
     const ddt_config &cfg = c->cfg;
     PrArgs p = {};
     p.q = q;
