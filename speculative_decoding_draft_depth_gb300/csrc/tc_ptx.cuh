@@ -124,6 +124,14 @@ TC_DEVINL void cp_async_arrive_noinc(uint32_t bar)
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
+// ---------------------------------------------------------------- registers
+// move this warpgroup's registers per thread up or down (the block's sum stays
+// within what it was launched with)
+template <int N>
+TC_DEVINL void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+TC_DEVINL void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
 // ---------------------------------------------------------------- fences
 TC_DEVINL void fence_proxy_async_smem()
 {
@@ -232,6 +240,12 @@ TC_DEVINL constexpr uint32_t idesc_bf16(int M, int N, bool a_mn_major, bool b_mn
            | ((b_mn_major ? 1u : 0u) << 16)      // B major-ness
            | ((uint32_t)(N >> 3) << 17)          // N / 8
            | ((uint32_t)(M >> 4) << 24);         // M / 16
+}
+
+// the same with fp16 A and B (both; the two types never meet in one product)
+TC_DEVINL constexpr uint32_t idesc_f16(int M, int N, bool a_mn_major, bool b_mn_major)
+{
+    return idesc_bf16(M, N, a_mn_major, b_mn_major) & ~((1u << 7) | (1u << 10));
 }
 
 // shared-memory matrix descriptor, 128-byte swizzle: start address, leading
