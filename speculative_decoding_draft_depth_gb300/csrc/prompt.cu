@@ -274,6 +274,28 @@ DDT_DEVINL void find_share(const PtArgs &a, int tq, int grid, int cta, long long
     __syncthreads();
 }
 
+// whole warp: one thread issues a tile's boxes, 16 tokens by 64 channels each, but
+// for group `skip`; z: lane u holds group u's pool row
+template <int D>
+DDT_DEVINL void load_boxes(const void *map, uint32_t dst, int h, int z, int skip, uint32_t fb, uint32_t bytes)
+{
+    int zu[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+        zu[u] = __shfl_sync(0xFFFFFFFFu, z, u);
+    if (elect_one()) {
+        mbar_arrive_expect_tx(fb, bytes);
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (u != skip) {
+                tma_load_3d(dst + u * 2048, map, 0, h, zu[u], fb);
+                if (D == 128)
+                    tma_load_3d(dst + 16384 + u * 2048, map, 64, h, zu[u], fb);
+            }
+    }
+    __syncwarp();
+}
+
 // what a raw slot holds (B_META): its kind, and for K and V the rows that count
 // and, by 16-row groups, the ones whose page is out of range
 constexpr int CMD_K = 0, CMD_V = 1, CMD_Q = 2, CMD_END = 3;
@@ -485,22 +507,29 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             const bool in = lane < 8 && 16 * lane < valid;
             const unsigned copies = __ballot_sync(0xFFFFFFFFu, in && z >= 0);
             const unsigned bad = __ballot_sync(0xFFFFFFFFu, in && z < 0);
+            // pool row -> the head's rows of its page
+            const int64_t mine = (((int64_t)(z >> a.page_shift) * a.Hkv + s.h) << a.page_shift) +
+                                 (z & ((1 << a.page_shift) - 1));
+            int64_t row[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                row[u] = __shfl_sync(0xFFFFFFFFu, mine, u);
             const int sl = raw_slot();
             if (!ok)
                 return;
             const uint32_t fb = bar + B_RAWFULL + 8 * sl, dst = sb + SM_RAW<KV4> + sl * RAW;
-            if (lane == 0) {
+            if (elect_one()) {
                 metas[sl] = kind | (valid << 8) | ((int)bad << 16);
                 mbar_arrive_expect_tx(fb, __popc(copies) * 16 * (D / 2 + D / 16));
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    if ((copies >> u) & 1) {
+                        bulk_load(dst + u * 16 * (D / 2), a.codes[kind] + row[u] * (D / 2), 16 * (D / 2), fb);
+                        bulk_load(dst + 128 * (D / 2) + u * 16 * (D / 16), a.scales[kind] + row[u] * (D / 16),
+                                  16 * (D / 16), fb);
+                    }
             }
             __syncwarp();
-            if (in && z >= 0) {
-                // pool row -> the head's rows of its page
-                const int64_t pg = z >> a.page_shift;
-                const int64_t row = ((pg * a.Hkv + s.h) << a.page_shift) + (z & ((1 << a.page_shift) - 1));
-                bulk_load(dst + lane * 16 * (D / 2), a.codes[kind] + row * (D / 2), 16 * (D / 2), fb);
-                bulk_load(dst + 128 * (D / 2) + lane * 16 * (D / 16), a.scales[kind] + row * (D / 16), 16 * (D / 16), fb);
-            }
             ++nraw;
         };
         while (ok) {
@@ -561,7 +590,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 break;
             if (k >= 1 && !wait_warp(bar + B_QEMPTY, (k - 1) & 1, abort_flag, a.status))
                 break;
-            if (lane == 0) {
+            if (elect_one()) {
                 const int y = s.h << a.g_shift;
                 mbar_arrive_expect_tx(bar + B_QFULL, 16384u * (D / 64) * (s.split ? 1 : 2));
                 for (int g = 0; g < (s.split ? 1 : 2); ++g)
@@ -589,14 +618,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     break;
                 }
                 const uint32_t fb = bar + B_KFULL + 8 * sl, dst = sb + SM_K<KV4> + sl * 32768u;
-                if (lane == 0)
-                    mbar_arrive_expect_tx(fb, 16384u * (D / 64));
-                __syncwarp();
-                if (lane < 8) {
-                    tma_load_3d(dst + lane * 2048, &tm_k, 0, s.h, z, fb);
-                    if (D == 128)
-                        tma_load_3d(dst + 16384 + lane * 2048, &tm_k, 64, s.h, z, fb);
-                }
+                load_boxes<D>(&tm_k, dst, s.h, z, -1, fb, 16384u * (D / 64));
             }
         }
         if constexpr (KV4) {
@@ -630,11 +652,6 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 const uint32_t fb = bar + B_VFULL + 8 * sl, dst = sb + SM_V<KV4> + sl * 32768u;
                 // the 16-token group that holds the item's last key and rows behind it
                 const int cut = (end & 15) != 0 && (end >> 7) == j ? (end & 127) >> 4 : -1;
-                if (lane < 8 && lane != cut) {
-                    tma_load_3d(dst + lane * 2048, &tm_v, 0, s.h, z, fb);
-                    if (D == 128)
-                        tma_load_3d(dst + 16384 + lane * 2048, &tm_v, 64, s.h, z, fb);
-                }
                 if (cut >= 0) {
                     const int zc = __shfl_sync(0xFFFFFFFFu, z, cut), nrow = end & 15;
                     unsigned char *d = sgen + SM_V<KV4> + sl * 32768u + cut * 2048;
@@ -651,24 +668,20 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     fence_proxy_async_smem();
                 }
                 __syncwarp();
-                // (the transaction count may run ahead of this arrival: the phase
-                // cannot complete without it)
-                if (lane == 0)
-                    mbar_arrive_expect_tx(fb, (cut >= 0 ? 14336u : 16384u) * (D / 64));
+                load_boxes<D>(&tm_v, dst, s.h, z, cut, fb, (cut >= 0 ? 14336u : 16384u) * (D / 64));
             }
         }
         for (int m = max(0, vn - NV<KV4>); m < vn; ++m)
             drain_bar(bar + B_VFULL + 8 * (m % NV<KV4>), (m / NV<KV4>) & 1);
     } else if (warp == W_MMA) {
         // ============================================================ MMA issuer
-        if (lane == 0) {
+        if (elect_one()) {
             const uint64_t dQ = sdesc_sw128(sb + SM_Q, 16, 1024);
             const uint64_t dK = sdesc_sw128(sb + SM_K<KV4>, 16, 1024);
             const uint64_t dV = sdesc_sw128(sb + SM_V<KV4>, 16384, 1024);
-            int kq = 0;            // item of the next S
-            int kbase = 0, vbase = 0;  // K tiles before that item, V tiles before the current one
+            int kbase = 0, vbase = 0;  // K tiles before the item of the next S, V tiles before the current one
             int kseen = 0, vseen = 0;  // tiles waited for
-            uint32_t pbits = 0;  // phase of each group's next P
+            uint32_t pbits = 0;        // phase of each group's next P
             bool ok = true;
             auto need = [&](uint32_t b, uint32_t parity) { ok = ok && wait_bar(b, parity, abort_flag, a.status); };
             auto fetch = [&](int k, Seg &s) {
@@ -683,82 +696,82 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 mbar_arrive(bar + B_REMPTY + 8 * slot);
                 seg_decode(w, s);
             };
-            // S of group g for step j of item s (number kq)
-            auto issue_s = [&](const Seg &s, int j, int g) {
-                if (j == 0 && g == 0)
-                    need(bar + (KV4 ? B_QREADY : B_QFULL), kq & 1);
-                const int t = kbase + s.tile(g, j) - s.t0, sl = t % NK;
-                if (t >= kseen) {
-                    need(bar + B_KFULL + 8 * sl, (t / NK) & 1);
-                    kseen = t + 1;
-                }
-                if (!ok)
-                    return;
-                tc_fence_after();
-                const uint64_t q = dQ + (uint64_t)((!KV4 && !s.split && g) ? (32768u >> 4) : 0u);
-                const uint64_t kk = dK + (uint64_t)sl * (32768u >> 4);
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    const uint32_t off = ((i >> 2) * 16384u + (i & 3) * 32u) >> 4;
-                    mma_bf16(tmem + TM_S + 128u * g, q + off, kk + off, IDESC_QK<KV4>, i > 0 ? 1u : 0u);
-                }
-                mma_commit(bar + B_SFULL + 8 * g);
-                if (s.split || g == 1)
-                    mma_commit(bar + B_KEMPTY + 8 * sl);
-                // the item's last S: its Q is free
-                if (s.split ? s.tile(g, j) == s.t1 - 1 : (g == 1 && j == s.steps(1) - 1))
-                    mma_commit(bar + B_QEMPTY);
-            };
-            auto issue_pv = [&](const Seg &s, int j, int g) {
-                const int t = vbase + s.tile(g, j) - s.t0, sl = t % NV<KV4>;
-                need(bar + B_PFULL + 8 * g, (pbits >> g) & 1);
-                pbits ^= 1u << g;
-                if (t >= vseen) {
-                    need(bar + B_VFULL + 8 * sl, (t / NV<KV4>) & 1);
-                    vseen = t + 1;
-                }
-                if (!ok)
-                    return;
-                tc_fence_after();
-                const uint64_t v = dV + (uint64_t)sl * (32768u >> 4);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    mma_bf16_ts(tmem + TM_O + 128u * g, tmem + TM_S + 128u * g + 8u * i, v + i * (2048u >> 4),
-                                IDESC_PV<D, KV4>, (j > 0 || i > 0) ? 1u : 0u);
-                if (s.split || g == 1)
-                    mma_commit(bar + B_VEMPTY + 8 * sl);
-                if (j == s.steps(g) - 1)
-                    mma_commit(bar + B_OFULL + 8 * g);
-            };
             Seg cur, nxt;
             fetch(0, cur);
-            if (ok && cur.r >= 0)
-                for (int g = 0; g < 2; ++g)
-                    if (cur.steps(g) > 0)
-                        issue_s(cur, 0, g);
-            for (int k = 0; ok && cur.r >= 0; ++k) {
-                const int steps = cur.steps(0), n = cur.t1 - cur.t0;
-                nxt.r = -1;
-                for (int j = 0; ok && j < steps; ++j) {
-                    const bool last = j == steps - 1;
-                    if (last) {
-                        kbase += n;
-                        kq = k + 1;
-                        fetch(k + 1, nxt);
+            // one body for every product (the thread's code stays in the instruction
+            // cache): step j of item k, P V of group g, then that group's next S, which
+            // may be the next item's first (j = -1: only the first item's)
+            int k = 0, j = -1, g = 0, steps = cur.r >= 0 ? cur.steps(0) : 0;
+            nxt.r = -1;
+#pragma unroll 1
+            while (ok && cur.r >= 0) {
+                const bool last = j == steps - 1;
+                if (last && g == 0)
+                    fetch(k + 1, nxt);
+                if (j >= 0 && j < cur.steps(g)) {
+                    const int t = vbase + cur.tile(g, j) - cur.t0, sl = t % NV<KV4>;
+                    need(bar + B_PFULL + 8 * g, (pbits >> g) & 1);
+                    pbits ^= 1u << g;
+                    if (t >= vseen) {
+                        need(bar + B_VFULL + 8 * sl, (t / NV<KV4>) & 1);
+                        vseen = t + 1;
                     }
-                    for (int g = 0; ok && g < 2; ++g) {
-                        if (j < cur.steps(g))
-                            issue_pv(cur, j, g);
-                        if (!last) {
-                            if (j + 1 < cur.steps(g))
-                                issue_s(cur, j + 1, g);
-                        } else if (ok && nxt.r >= 0 && nxt.steps(g) > 0) {
-                            issue_s(nxt, 0, g);
-                        }
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    const uint64_t v = dV + (uint64_t)sl * (32768u >> 4);
+                    const uint32_t o = tmem + TM_O + 128u * g, pp = tmem + TM_S + 128u * g;
+                    const uint32_t more = j > 0 ? 1u : 0u;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        mma_bf16_ts(o, pp + 8u * i, v + i * (2048u >> 4), IDESC_PV<D, KV4>, i > 0 ? 1u : more);
+                    if (cur.split || g == 1)
+                        mma_commit(bar + B_VEMPTY + 8 * sl);
+                    if (j == cur.steps(g) - 1)
+                        mma_commit(bar + B_OFULL + 8 * g);
+                }
+                // the group's next S: (item, step)
+                const bool over = last;
+                const Seg &s = over ? nxt : cur;
+                const int js = over ? 0 : j + 1;
+                if (s.r >= 0 && js < s.steps(g)) {
+                    const int t = (over ? kbase + cur.t1 - cur.t0 : kbase) + s.tile(g, js) - s.t0, sl = t % NK;
+                    if (js == 0 && g == 0)
+                        need(bar + (KV4 ? B_QREADY : B_QFULL), (over ? k + 1 : k) & 1);
+                    if (t >= kseen) {
+                        need(bar + B_KFULL + 8 * sl, (t / NK) & 1);
+                        kseen = t + 1;
+                    }
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    const uint64_t q = dQ + (uint64_t)((!KV4 && !s.split && g) ? (32768u >> 4) : 0u);
+                    const uint64_t kk = dK + (uint64_t)sl * (32768u >> 4);
+                    const uint32_t d = tmem + TM_S + 128u * g;
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        const uint32_t off = ((i >> 2) * 16384u + (i & 3) * 32u) >> 4;
+                        mma_bf16(d, q + off, kk + off, IDESC_QK<KV4>, i > 0 ? 1u : 0u);
+                    }
+                    mma_commit(bar + B_SFULL + 8 * g);
+                    if (s.split || g == 1)
+                        mma_commit(bar + B_KEMPTY + 8 * sl);
+                    // the item's last S: its Q is free
+                    if (s.split ? s.tile(g, js) == s.t1 - 1 : (g == 1 && js == s.steps(1) - 1))
+                        mma_commit(bar + B_QEMPTY);
+                }
+                g ^= 1;
+                if (g == 0) {
+                    ++j;
+                    if (last) {
+                        kbase += cur.t1 - cur.t0;
+                        vbase = kbase;
+                        cur = nxt;
+                        ++k;
+                        j = 0;
+                        steps = cur.r >= 0 ? cur.steps(0) : 0;
                     }
                 }
-                vbase += n;
-                cur = nxt;
             }
             // wind down: every MMA issued here has completed
             mma_commit(bar + B_FINAL);

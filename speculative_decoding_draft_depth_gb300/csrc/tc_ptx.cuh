@@ -132,6 +132,15 @@ TC_DEVINL void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :
 template <int N>
 TC_DEVINL void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
+// one thread of a converged warp (the compiler knows that it is one: operands of
+// single-thread instructions go to uniform registers without a loop over lanes)
+TC_DEVINL bool elect_one()
+{
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xFFFFFFFF;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok));
+    return ok != 0;
+}
+
 // ---------------------------------------------------------------- fences
 TC_DEVINL void fence_proxy_async_smem()
 {
