@@ -39,22 +39,24 @@
 namespace {
 
 template <bool KV4>
-constexpr int NT = KV4 ? 512 : 384;
-constexpr int W_MMA = 8, W_WALK = 9, W_VLOAD = 10, W_DQ = 12;
-constexpr int NDQ = 4;  // 4-bit cache: warps that turn codes into fp16 tiles (one warpgroup)
-// registers per thread of the two softmax warpgroups and of the others, and what
-// the kernel has to be launched with: they add up to no more than that
+constexpr int NT = KV4 ? 640 : 384;
+constexpr int W_MMA = 8, W_WALK = 9, W_VLOAD = 10, W_MMB = 11, W_DQ = 12;  // (4 bits: 10 loads Q)
+constexpr int NDQ = 4;  // 4-bit cache: warps that fetch codes and turn them into fp16 tiles, of K and of V each
+// registers per thread of the two softmax warpgroups, of the one with the issuers
+// and loaders and of the two that make fp16 tiles, and what the kernel has to be
+// launched with: they add up to no more than that
 template <bool KV4>
-constexpr int REGS_SM = KV4 ? 176 : 208;
+constexpr int REGS_SM = KV4 ? 120 : 208;
 template <bool KV4>
-constexpr int REGS_OTHER = KV4 ? 80 : 88;
+constexpr int REGS_OTHER = KV4 ? 72 : 88;
+constexpr int REGS_DQ = 80;
 template <bool KV4>
-constexpr int REGS_LAUNCH = KV4 ? 128 : 168;
-static_assert(256 * REGS_SM<true> + 256 * REGS_OTHER<true> <= REGS_LAUNCH<true> * NT<true>, "register split");
-static_assert(256 * REGS_SM<false> + 128 * REGS_OTHER<false> <= REGS_LAUNCH<false> * NT<false>, "register split");
-constexpr int NRING = 4;
+constexpr int REGS_LAUNCH = KV4 ? 96 : 168;
+static_assert(256 * REGS_SM<true> + 128 * REGS_OTHER<true> + 256 * REGS_DQ <= REGS_LAUNCH<true> * NT<true>, "registers");
+static_assert(256 * REGS_SM<false> + 128 * REGS_OTHER<false> <= REGS_LAUNCH<false> * NT<false>, "registers");
+constexpr int NRING = 8;
 template <bool KV4>
-constexpr int RING_CONSUMERS = 8 + 1 + (KV4 ? 0 : 1);  // softmax warps, MMA issuer, V loader
+constexpr int RING_CONSUMERS = 8 + 2 + 1 + (KV4 ? 2 * NDQ : 0);  // softmax warps, MMA issuers, V or Q loader, ...
 constexpr int MIN_UNITS = 4;               // of a share
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t TM_S = 0;    // S (and P) of A, B: 128 columns each
@@ -67,7 +69,7 @@ constexpr long long DRAIN_LIMIT = 200000000LL;
 constexpr int NK = 2;
 template <bool KV4>
 constexpr int NV = KV4 ? 2 : 3;
-constexpr int NRAW = 6;          // 4-bit cache: tiles of codes and scales in flight
+constexpr int NRAW = 3;          // 4-bit cache: tiles of codes and scales of K, and of V, in flight
 constexpr uint32_t RAW = 9216;   // 128 rows of 64 bytes of codes, then of 8 scales
 constexpr uint32_t SM_Q = 0;     // A, B: 32 KB each (two 16 KB halves); 4 bits: one for both
 template <bool KV4>
@@ -77,26 +79,25 @@ constexpr uint32_t SM_V = SM_K<KV4> + NK * 32768;
 template <bool KV4>
 constexpr uint32_t SM_RAW = SM_V<KV4> + NV<KV4> * 32768;
 template <bool KV4>
-constexpr uint32_t SM_BAR = SM_RAW<KV4> + (KV4 ? NRAW * RAW : 0);
+constexpr uint32_t SM_BAR = SM_RAW<KV4> + (KV4 ? 2 * NRAW * RAW : 0);
 constexpr uint32_t B_QFULL = 0, B_QEMPTY = 8, B_KFULL = 16, B_KEMPTY = 32, B_VFULL = 48, B_VEMPTY = 72,
                    B_SFULL = 96,   // [2 groups]
-                   B_PFULL = 112,  // [2] 4 arrivals: the group's warps
+                   B_PFULL = 112,  // [2] 4 arrivals (the group's warps): P of keys 0..63 is there
                    B_OFULL = 128,  // [2]
                    B_XB = 144,     // B's (m, l) published and its O complete (4 arrivals)
                    B_XA = 152,     // A has read them (4 arrivals)
-                   B_RFULL = 160,  // [NRING]
-                   B_REMPTY = 192,
-                   B_FINAL = 224, B_TMEM = 232, B_ABORT = 236, B_FOUND = 240,  // 32 bytes
-                   B_RING = 272,   // [NRING][8] ints
-                   B_ML = 400,     // [128] float2: B's (m, l); before the roles start, the scan's sums
-                   // 4-bit cache only:
-                   B_RAWFULL = 1424,           // [NRAW]
-                   B_RAWEMPTY = 1424 + 48,     // [NRAW] NDQ arrivals
-                   B_QREADY = 1424 + 96,       // NDQ arrivals
-                   B_META = 1424 + 104,        // [NRAW] int: what the slot holds
-                   B_ROWSC = 1424 + 128;       // [2][128] floats: the row's factor, by item parity
+                   B_FINAL = 160,  // [2]
+                   B_PHALF = 176,  // [2] 4 arrivals: P of keys 64..127
+                   B_TMEM = 192, B_ABORT = 196,
+                   B_QREADY = 200,    // 4 bits: Q is fp16 (NDQ arrivals)
+                   B_RFULL = 208,     // [NRING]
+                   B_REMPTY = 272,    // [NRING]
+                   B_RING = 336,      // [NRING][8] ints
+                   B_FOUND = B_RING,  // three 64-bit words, before the walk begins
+                   B_ML = 592,        // [128] float2: B's (m, l); before the roles start, the scan's sums
+                   B_ROWSC = 1616;    // 4 bits: [2][128] floats: the row's factor, by item parity
 template <bool KV4>
-constexpr uint32_t B_END = KV4 ? B_ROWSC + 1024 : B_RAWFULL;
+constexpr uint32_t B_END = KV4 ? B_ROWSC + 1024 : B_ROWSC;
 template <bool KV4>
 constexpr uint32_t SM_ALLOC = SM_BAR<KV4> + B_END<KV4> + 1024;
 static_assert(SM_ALLOC<false> <= 232448 && SM_ALLOC<true> <= 232448, "shared memory of one CTA");
@@ -296,10 +297,6 @@ DDT_DEVINL void load_boxes(const void *map, uint32_t dst, int h, int z, int skip
     __syncwarp();
 }
 
-// what a raw slot holds (B_META): its kind, and for K and V the rows that count
-// and, by 16-row groups, the ones whose page is out of range
-constexpr int CMD_K = 0, CMD_V = 1, CMD_Q = 2, CMD_END = 3;
-
 // eight 4-bit codes to four fp16 pairs times sc; byte b holds channels in the
 // order 0 2 4 6 1 3 5 7, which the fp16 tiles keep (Q's channels are laid out the
 // same way, and the output's are put back by naming)
@@ -326,33 +323,93 @@ DDT_DEVINL uint32_t pack_f16x2(float lo, float hi)
     return r;
 }
 
-// a warp's part of a tile of codes and scales -> its fp16 tile (128-byte swizzle)
+// A warp's part of a tile of codes and scales: 16-byte vectors of codes, CH to a
+// row, numbered so that eight neighbouring lanes' stores of the fp16 rows fall into
+// eight bank groups; each row's first lane also fetches the row's scales. The
+// warp that fetches a part is the one that turns it into values.
 template <int D>
-DDT_DEVINL void dequant_tile(const unsigned char *rawp, unsigned char *dst, int meta, int wq, int lane)
+struct Part {
+    static constexpr int CH = D / 32, N = 128 * CH / (NDQ * 32);
+    DDT_DEVINL static int index(int i, int wq, int lane) { return (i * NDQ + wq) * 32 + lane; }
+};
+
+// base: lane u holds the byte offset of the tile's 16-token group u in the codes
+// (-1: zeros; the scales' is an eighth of it); rows from `valid` on become zeros
+template <int D>
+DDT_DEVINL void fetch_part(const uint8_t *codes, const uint8_t *scales, long long base, int valid, uint32_t dst, int wq,
+                           int lane)
 {
-    constexpr int CH = D / 32;  // 16-byte vectors of codes in a row
-    const int nvalid = (meta >> 8) & 0xFF, bad = (meta >> 16) & 0xFF;
+    using P = Part<D>;
 #pragma unroll
-    for (int i = 0; i < 128 * CH / (NDQ * 32); ++i) {
-        const int idx = (i * NDQ + wq) * 32 + lane, row = idx / CH, q = idx % CH;
-        uint4 w = *reinterpret_cast<const uint4 *>(rawp + idx * 16);
-        uint32_t two = *reinterpret_cast<const uint16_t *>(rawp + 128 * (D / 2) + row * (D / 16) + 2 * q), sc;
-        if (row >= nvalid || ((bad >> (row >> 4)) & 1)) {
-            w = make_uint4(0u, 0u, 0u, 0u);
-            two = 0u;
+    for (int i = 0; i < P::N; ++i) {
+        const int idx = P::index(i, wq, lane), row = idx / P::CH, q = idx % P::CH;
+        const long long b = __shfl_sync(0xFFFFFFFFu, base, row >> 4);
+        const bool in = b >= 0 && row < valid;
+        const long long at = in ? b + (row & 15) * (D / 2) : 0;
+        cp_async_16(dst + idx * 16, codes + at + q * 16, in ? 16u : 0u);
+        if (q == 0) {
+            const uint32_t so = dst + 128 * (D / 2) + row * (D / 16);
+            if (D == 128)
+                cp_async_8(so, scales + (at >> 3), in ? 8u : 0u);
+            else
+                cp_async_4(so, scales + (at >> 3), in ? 4u : 0u);
         }
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(sc) : "h"((uint16_t)two));
+    }
+}
+
+template <int D>
+DDT_DEVINL void dequant_part(const unsigned char *rawp, unsigned char *dst, int wq, int lane)
+{
+    using P = Part<D>;
+    uint4 w[P::N];
+    uint32_t two[P::N];
+#pragma unroll
+    for (int i = 0; i < P::N; ++i) {
+        const int idx = P::index(i, wq, lane), row = idx / P::CH, q = idx % P::CH;
+        w[i] = *reinterpret_cast<const uint4 *>(rawp + idx * 16);
+        two[i] = *reinterpret_cast<const uint16_t *>(rawp + 128 * (D / 2) + row * (D / 16) + 2 * q);
+    }
+#pragma unroll
+    for (int i = 0; i < P::N; ++i) {
+        const int idx = P::index(i, wq, lane), row = idx / P::CH, q = idx % P::CH;
+        uint32_t sc;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(sc) : "h"((uint16_t)two[i]));
         const uint32_t s0 = __byte_perm(sc, sc, 0x1010), s1 = __byte_perm(sc, sc, 0x3232);
-        // vectors 4 q + x of the row; lanes of its upper half go in another order,
-        // so that eight lanes' stores fall into eight bank groups
+        // vectors 4 q + x of the row; lanes of its upper half go in another order
         const bool up = D == 128 && (q & 2);
-        const uint32_t wx[4] = {up ? w.z : w.x, up ? w.w : w.y, up ? w.x : w.z, up ? w.y : w.w};
+        const uint32_t wx[4] = {up ? w[i].z : w[i].x, up ? w[i].w : w[i].y, up ? w[i].x : w[i].z,
+                                up ? w[i].y : w[i].w};
         const uint32_t sa = up ? s1 : s0, sb = up ? s0 : s1;
         unsigned char *d = dst + (D == 128 ? (q >> 1) * 16384 : 0) + row * 128;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
             const int ch = ((q & 1) * 4 + x) ^ (up ? 2 : 0);
             *reinterpret_cast<uint4 *>(d + ((ch ^ (row & 7)) << 4)) = values8(wx[x], x < 2 ? sa : sb);
+        }
+    }
+}
+
+// lane i of four holds w = quarters 0..3 (four words each) of its own row; after it
+// has quarter i of the four lanes' rows
+DDT_DEVINL void quads_transpose(uint32_t *w, int lane)
+{
+    // exchange with lane ^ 2, then lane ^ 1: swap the off-diagonal blocks of 2x2 quarters
+#pragma unroll
+    for (int x = 2; x >= 1; x >>= 1) {
+        const bool up = lane & x;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (q & x)
+                continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                uint32_t &lo = w[4 * q + e], &hi = w[4 * (q | x) + e];
+                const uint32_t got = __shfl_xor_sync(0xFFFFFFFFu, up ? lo : hi, x);
+                if (up)
+                    lo = got;
+                else
+                    hi = got;
+            }
         }
     }
 }
@@ -406,18 +463,19 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 
     if (tid == 0) {
         mbar_init(bar + B_QFULL, 1);
-        mbar_init(bar + B_QEMPTY, 1);
+        mbar_init(bar + B_QEMPTY, 2);
         for (int i = 0; i < NK; ++i) {
             mbar_init(bar + B_KFULL + 8 * i, KV4 ? NDQ : 1);
-            mbar_init(bar + B_KEMPTY + 8 * i, 1);
+            mbar_init(bar + B_KEMPTY + 8 * i, 2);
         }
         for (int i = 0; i < NV<KV4>; ++i) {
             mbar_init(bar + B_VFULL + 8 * i, KV4 ? NDQ : 1);
-            mbar_init(bar + B_VEMPTY + 8 * i, 1);
+            mbar_init(bar + B_VEMPTY + 8 * i, 2);
         }
         for (int g = 0; g < 2; ++g) {
             mbar_init(bar + B_SFULL + 8 * g, 1);
             mbar_init(bar + B_PFULL + 8 * g, 4);
+            mbar_init(bar + B_PHALF + 8 * g, 4);
             mbar_init(bar + B_OFULL + 8 * g, 1);
         }
         mbar_init(bar + B_XB, 4);
@@ -427,13 +485,8 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             mbar_init(bar + B_REMPTY + 8 * i, RING_CONSUMERS<KV4>);
         }
         mbar_init(bar + B_FINAL, 1);
-        if (KV4) {
-            for (int i = 0; i < NRAW; ++i) {
-                mbar_init(bar + B_RAWFULL + 8 * i, 1);
-                mbar_init(bar + B_RAWEMPTY + 8 * i, NDQ);
-            }
-            mbar_init(bar + B_QREADY, NDQ);
-        }
+        mbar_init(bar + B_FINAL + 8, 1);
+        mbar_init(bar + B_QREADY, NDQ);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -455,7 +508,24 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     tc_fence_after();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(sgen + SM_BAR<KV4> + B_TMEM);
 
-    if (warp >= 8)
+    // a whole warp: Q of item k, once the item before is done with its own
+    auto load_q = [&](const Seg &s, int k) {
+        if (k >= 1 && !wait_warp(bar + B_QEMPTY, (k - 1) & 1, abort_flag, a.status))
+            return false;
+        if (elect_one()) {
+            mbar_arrive_expect_tx(bar + B_QFULL, 16384u * (D / 64) * (s.split ? 1 : 2));
+            for (int g = 0; g < (s.split ? 1 : 2); ++g)
+                for (int x = 0; x < D / 64; ++x)
+                    tma_load_3d(sb + SM_Q + g * 32768 + x * 16384, &tm_q, x * 64, s.h << a.g_shift,
+                                s.row0 + g * (tq / 2), bar + B_QFULL);
+        }
+        __syncwarp();
+        return true;
+    };
+
+    if (warp >= W_DQ)
+        regs_dec<REGS_DQ>();
+    else if (warp >= 8)
         regs_dec<REGS_OTHER<KV4>>();
 
     if (warp == W_WALK) {
@@ -480,58 +550,6 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
         int k = 0, kn = 0;
         bool ok = true;
-        // 4-bit cache: the next raw slot gets a tile's codes and scales, or a word
-        // (Q has been asked for; the end) for the dequantising warps
-        int nraw = 0;
-        Seg pend;      // the tile whose K has been asked for, but not its V
-        int pend_j = -1;
-        auto raw_slot = [&]() {
-            ok = ok && (nraw < NRAW ||
-                        wait_warp(bar + B_RAWEMPTY + 8 * (nraw % NRAW), ((nraw / NRAW) - 1) & 1, abort_flag, a.status));
-            return nraw % NRAW;
-        };
-        volatile int *metas = reinterpret_cast<volatile int *>(sgen + SM_BAR<KV4> + B_META);
-        auto say = [&](int cmd) {
-            const int sl = raw_slot();
-            if (ok) {
-                if (lane == 0) {
-                    metas[sl] = cmd;
-                    mbar_arrive(bar + B_RAWFULL + 8 * sl);
-                }
-                ++nraw;
-            }
-        };
-        auto load_raw = [&](const Seg &s, int j, int kind) {
-            const int z = lane < 8 ? group_row(a, s, j, lane) : -16;
-            const int valid = min(PP_TILE, s.pos0 + s.ntok - j * PP_TILE);
-            const bool in = lane < 8 && 16 * lane < valid;
-            const unsigned copies = __ballot_sync(0xFFFFFFFFu, in && z >= 0);
-            const unsigned bad = __ballot_sync(0xFFFFFFFFu, in && z < 0);
-            // pool row -> the head's rows of its page
-            const int64_t mine = (((int64_t)(z >> a.page_shift) * a.Hkv + s.h) << a.page_shift) +
-                                 (z & ((1 << a.page_shift) - 1));
-            int64_t row[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-                row[u] = __shfl_sync(0xFFFFFFFFu, mine, u);
-            const int sl = raw_slot();
-            if (!ok)
-                return;
-            const uint32_t fb = bar + B_RAWFULL + 8 * sl, dst = sb + SM_RAW<KV4> + sl * RAW;
-            if (elect_one()) {
-                metas[sl] = kind | (valid << 8) | ((int)bad << 16);
-                mbar_arrive_expect_tx(fb, __popc(copies) * 16 * (D / 2 + D / 16));
-#pragma unroll
-                for (int u = 0; u < 8; ++u)
-                    if ((copies >> u) & 1) {
-                        bulk_load(dst + u * 16 * (D / 2), a.codes[kind] + row[u] * (D / 2), 16 * (D / 2), fb);
-                        bulk_load(dst + 128 * (D / 2) + u * 16 * (D / 16), a.scales[kind] + row[u] * (D / 16),
-                                  16 * (D / 16), fb);
-                    }
-            }
-            __syncwarp();
-            ++nraw;
-        };
         while (ok) {
             // the next segment that holds tiles
             Seg s;
@@ -588,29 +606,12 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
             if (s.r < 0)
                 break;
-            if (k >= 1 && !wait_warp(bar + B_QEMPTY, (k - 1) & 1, abort_flag, a.status))
-                break;
-            if (elect_one()) {
-                const int y = s.h << a.g_shift;
-                mbar_arrive_expect_tx(bar + B_QFULL, 16384u * (D / 64) * (s.split ? 1 : 2));
-                for (int g = 0; g < (s.split ? 1 : 2); ++g)
-                    for (int x = 0; x < D / 64; ++x)
-                        tma_load_3d(sb + SM_Q + g * 32768 + x * 16384, &tm_q, x * 64, y, s.row0 + g * (tq / 2),
-                                    bar + B_QFULL);
-            }
             ++k;
-            if constexpr (KV4) {
-                // K one tile ahead of V, across items too
-                say(CMD_Q);
-                for (int j = s.t0; ok && j < s.t1; ++j) {
-                    load_raw(s, j, CMD_K);
-                    if (pend_j >= 0)
-                        load_raw(pend, pend_j, CMD_V);
-                    pend = s;
-                    pend_j = j;
-                }
-            }
-            for (int j = s.t0; !KV4 && j < s.t1; ++j, ++kn) {
+            if constexpr (KV4)
+                continue;
+            if (!load_q(s, k - 1))
+                break;
+            for (int j = s.t0; j < s.t1; ++j, ++kn) {
                 const int sl = kn % NK;
                 const int z = lane < 8 ? group_row(a, s, j, lane) : 0;
                 if (kn >= NK && !wait_warp(bar + B_KEMPTY + 8 * sl, ((kn / NK) - 1) & 1, abort_flag, a.status)) {
@@ -621,34 +622,39 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 load_boxes<D>(&tm_k, dst, s.h, z, -1, fb, 16384u * (D / 64));
             }
         }
-        if constexpr (KV4) {
-            if (ok && pend_j >= 0)
-                load_raw(pend, pend_j, CMD_V);
-            say(CMD_END);
-            for (int m = max(0, nraw - NRAW); m < nraw; ++m)
-                drain_bar(bar + B_RAWFULL + 8 * (m % NRAW), (m / NRAW) & 1);
-        }
         // wind down: the copies that this warp issued have landed
-        if (k > 0)
+        if (!KV4 && k > 0)
             drain_bar(bar + B_QFULL, (k - 1) & 1);
         for (int m = max(0, kn - NK); m < kn; ++m)
             drain_bar(bar + B_KFULL + 8 * (m % NK), (m / NK) & 1);
-    } else if (!KV4 && warp == W_VLOAD) {
+    } else if (KV4 && warp == W_VLOAD) {
+        // ============================================================ Q loads
+        int k = 0;
+        for (;; ++k) {
+            Seg s;
+            if (!ring_get(a, bar, ring, k, lane, abort_flag, s) || !load_q(s, k))
+                break;
+        }
+        if (k > 0)
+            drain_bar(bar + B_QFULL, (k - 1) & 1);
+    } else if (warp == W_VLOAD) {
         // ============================================================ V loads
-        int vn = 0;
+        uint32_t vfill = 0;  // phase of each slot's next fill
         bool ok = true;
         for (int k = 0; ok; ++k) {
             Seg s;
             if (!ring_get(a, bar, ring, k, lane, abort_flag, s))
                 break;
             const int end = s.pos0 + s.ntok;
-            for (int j = s.t0; j < s.t1; ++j, ++vn) {
-                const int sl = vn % NV<KV4>;
+            int sl = 0;  // the ring of three from the start, or a slot for each group
+            for (int j = s.t0; j < s.t1; ++j) {
                 const int z = lane < 8 ? group_row(a, s, j, lane) : 0;
-                if (vn >= NV<KV4> && !wait_warp(bar + B_VEMPTY + 8 * sl, ((vn / NV<KV4>) - 1) & 1, abort_flag, a.status)) {
+                // (a slot never filled passes: its phase "before" is complete)
+                if (!wait_warp(bar + B_VEMPTY + 8 * sl, ((vfill >> sl) & 1) ^ 1, abort_flag, a.status)) {
                     ok = false;
                     break;
                 }
+                vfill ^= 1u << sl;
                 const uint32_t fb = bar + B_VFULL + 8 * sl, dst = sb + SM_V<KV4> + sl * 32768u;
                 // the 16-token group that holds the item's last key and rows behind it
                 const int cut = (end & 15) != 0 && (end >> 7) == j ? (end & 127) >> 4 : -1;
@@ -669,155 +675,182 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 }
                 __syncwarp();
                 load_boxes<D>(&tm_v, dst, s.h, z, cut, fb, (cut >= 0 ? 14336u : 16384u) * (D / 64));
+                if (++sl == (s.split ? 2 : NV<KV4>))
+                    sl = 0;
             }
         }
-        for (int m = max(0, vn - NV<KV4>); m < vn; ++m)
-            drain_bar(bar + B_VFULL + 8 * (m % NV<KV4>), (m / NV<KV4>) & 1);
-    } else if (warp == W_MMA) {
-        // ============================================================ MMA issuer
+        for (int m = 0; m < NV<KV4>; ++m)
+            drain_bar(bar + B_VFULL + 8 * m, ((vfill >> m) & 1) ^ 1);
+    } else if (warp == W_MMA || warp == W_MMB) {
+        // ============================================================ MMA issuers, one per group
         if (elect_one()) {
+            const uint32_t g = warp == W_MMB;
             const uint64_t dQ = sdesc_sw128(sb + SM_Q, 16, 1024);
             const uint64_t dK = sdesc_sw128(sb + SM_K<KV4>, 16, 1024);
             const uint64_t dV = sdesc_sw128(sb + SM_V<KV4>, 16384, 1024);
-            int kbase = 0, vbase = 0;  // K tiles before the item of the next S, V tiles before the current one
-            int kseen = 0, vseen = 0;  // tiles waited for
-            uint32_t pbits = 0;        // phase of each group's next P
+            const uint32_t o = tmem + TM_O + 128u * g, sp = tmem + TM_S + 128u * g;
+            // A parity wait is sound only if the phase before is known to be complete. So
+            // in a split item every K and V slot belongs to one group; K's fills of
+            // earlier items are complete once this item's Q is there (it waited for both
+            // groups' last S), V's once the group's P is (its softmax has finished the
+            // item before, with the other group's last product): P is waited for first.
+            uint32_t base = 0, pph = 0;  // tiles before the item; phase of the group's next P
+            uint32_t vfill = 0;          // phase of each V slot's next fill, at the item's start
             bool ok = true;
-            auto need = [&](uint32_t b, uint32_t parity) { ok = ok && wait_bar(b, parity, abort_flag, a.status); };
-            auto fetch = [&](int k, Seg &s) {
+            // (after a wait that gave up, what the body still issues reads and writes
+            // this CTA's own memory; the loop then ends)
+            auto need = [&](uint32_t b, uint32_t parity) { ok &= wait_bar(b, parity, abort_flag, a.status); };
+            for (int k = 0; ok; ++k) {
                 const int slot = k & (NRING - 1);
                 need(bar + B_RFULL + 8 * slot, (k / NRING) & 1);
-                s.r = -1;
                 if (!ok)
-                    return;
+                    break;
                 int w[7];
                 for (int i = 0; i < 7; ++i)
                     w[i] = ring[8 * slot + i];
                 mbar_arrive(bar + B_REMPTY + 8 * slot);
+                Seg s;
                 seg_decode(w, s);
-            };
-            Seg cur, nxt;
-            fetch(0, cur);
-            // one body for every product (the thread's code stays in the instruction
-            // cache): step j of item k, P V of group g, then that group's next S, which
-            // may be the next item's first (j = -1: only the first item's)
-            int k = 0, j = -1, g = 0, steps = cur.r >= 0 ? cur.steps(0) : 0;
-            nxt.r = -1;
+                if (s.r < 0)
+                    break;
+                const int steps = s.steps(g);
+                // the group's first tile and its slots; then every tile, or every second
+                const uint32_t first = base + (s.split ? g : 0u), by = s.split ? 2u : 1u;
+                uint32_t ks = first % NK, kph = (first / NK) & 1;
+                uint32_t vs = KV4 ? first & 1u : s.split ? g : 0u, vbits = KV4 ? ((first >> 1) & 1u) << vs : vfill;
+                const uint64_t q = dQ + (uint64_t)((!KV4 && !s.split && g) ? (32768u >> 4) : 0u);
+                need(bar + (KV4 ? B_QREADY : B_QFULL), k & 1);
+                // S of tile j behind P V of tile j - 1, whose P lies in the same columns
 #pragma unroll 1
-            while (ok && cur.r >= 0) {
-                const bool last = j == steps - 1;
-                if (last && g == 0)
-                    fetch(k + 1, nxt);
-                if (j >= 0 && j < cur.steps(g)) {
-                    const int t = vbase + cur.tile(g, j) - cur.t0, sl = t % NV<KV4>;
-                    need(bar + B_PFULL + 8 * g, (pbits >> g) & 1);
-                    pbits ^= 1u << g;
-                    if (t >= vseen) {
-                        need(bar + B_VFULL + 8 * sl, (t / NV<KV4>) & 1);
-                        vseen = t + 1;
-                    }
-                    if (!ok)
-                        break;
-                    tc_fence_after();
-                    const uint64_t v = dV + (uint64_t)sl * (32768u >> 4);
-                    const uint32_t o = tmem + TM_O + 128u * g, pp = tmem + TM_S + 128u * g;
-                    const uint32_t more = j > 0 ? 1u : 0u;
+                for (int j = 0; j <= steps && ok; ++j) {
+                    if (j > 0) {
+                        const uint64_t v = dV + (uint64_t)(vs * (32768u >> 4));
+                        const uint32_t more = j > 1 ? 1u : 0u;
+                        need(bar + B_PFULL + 8 * g, pph);
+                        need(bar + B_VFULL + 8 * vs, (vbits >> vs) & 1);
+                        tc_fence_after();
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        mma_bf16_ts(o, pp + 8u * i, v + i * (2048u >> 4), IDESC_PV<D, KV4>, i > 0 ? 1u : more);
-                    if (cur.split || g == 1)
-                        mma_commit(bar + B_VEMPTY + 8 * sl);
-                    if (j == cur.steps(g) - 1)
-                        mma_commit(bar + B_OFULL + 8 * g);
-                }
-                // the group's next S: (item, step)
-                const bool over = last;
-                const Seg &s = over ? nxt : cur;
-                const int js = over ? 0 : j + 1;
-                if (s.r >= 0 && js < s.steps(g)) {
-                    const int t = (over ? kbase + cur.t1 - cur.t0 : kbase) + s.tile(g, js) - s.t0, sl = t % NK;
-                    if (js == 0 && g == 0)
-                        need(bar + (KV4 ? B_QREADY : B_QFULL), (over ? k + 1 : k) & 1);
-                    if (t >= kseen) {
-                        need(bar + B_KFULL + 8 * sl, (t / NK) & 1);
-                        kseen = t + 1;
-                    }
-                    if (!ok)
-                        break;
-                    tc_fence_after();
-                    const uint64_t q = dQ + (uint64_t)((!KV4 && !s.split && g) ? (32768u >> 4) : 0u);
-                    const uint64_t kk = dK + (uint64_t)sl * (32768u >> 4);
-                    const uint32_t d = tmem + TM_S + 128u * g;
+                        for (int i = 0; i < 4; ++i)
+                            mma_bf16_ts(o, sp + 8u * i, v + i * (2048u >> 4), IDESC_PV<D, KV4>, i > 0 ? 1u : more);
+                        need(bar + B_PHALF + 8 * g, pph);
+                        tc_fence_after();
 #pragma unroll
-                    for (int i = 0; i < D / 16; ++i) {
-                        const uint32_t off = ((i >> 2) * 16384u + (i & 3) * 32u) >> 4;
-                        mma_bf16(d, q + off, kk + off, IDESC_QK<KV4>, i > 0 ? 1u : 0u);
+                        for (int i = 4; i < 8; ++i)
+                            mma_bf16_ts(o, sp + 8u * i, v + i * (2048u >> 4), IDESC_PV<D, KV4>, 1u);
+                        pph ^= 1;
+                        mma_commit(bar + B_VEMPTY + 8 * vs);
+                        if (s.split)  // (a slot counts two releases: of both groups, or two of its one)
+                            mbar_arrive(bar + B_VEMPTY + 8 * vs);
+                        vbits ^= 1u << vs;
+                        if (!KV4 && !s.split && ++vs == NV<KV4>)
+                            vs = 0;
+                        if (j == steps)
+                            mma_commit(bar + B_OFULL + 8 * g);
                     }
-                    mma_commit(bar + B_SFULL + 8 * g);
-                    if (s.split || g == 1)
-                        mma_commit(bar + B_KEMPTY + 8 * sl);
-                    // the item's last S: its Q is free
-                    if (s.split ? s.tile(g, js) == s.t1 - 1 : (g == 1 && js == s.steps(1) - 1))
-                        mma_commit(bar + B_QEMPTY);
-                }
-                g ^= 1;
-                if (g == 0) {
-                    ++j;
-                    if (last) {
-                        kbase += cur.t1 - cur.t0;
-                        vbase = kbase;
-                        cur = nxt;
-                        ++k;
-                        j = 0;
-                        steps = cur.r >= 0 ? cur.steps(0) : 0;
+                    if (j < steps) {
+                        const uint64_t kk = dK + (uint64_t)(ks * (32768u >> 4));
+                        need(bar + B_KFULL + 8 * ks, kph);
+                        tc_fence_after();
+#pragma unroll
+                        for (int i = 0; i < D / 16; ++i) {
+                            const uint32_t off = ((i >> 2) * 16384u + (i & 3) * 32u) >> 4;
+                            mma_bf16(sp, q + off, kk + off, IDESC_QK<KV4>, i > 0 ? 1u : 0u);
+                        }
+                        mma_commit(bar + B_SFULL + 8 * g);
+                        mma_commit(bar + B_KEMPTY + 8 * ks);
+                        if (s.split)
+                            mbar_arrive(bar + B_KEMPTY + 8 * ks);
+                        ks += by;
+                        if (ks >= NK) {
+                            ks -= NK;
+                            kph ^= 1;
+                        }
+                        if (j == steps - 1)  // the group is done with the item's Q
+                            mma_commit(bar + B_QEMPTY);
                     }
                 }
+                if (steps == 0)  // (the wait for this item's Q keeps this arrival in its phase)
+                    mbar_arrive(bar + B_QEMPTY);
+                const uint32_t n = s.t1 - s.t0;
+                base += n;
+                vfill = s.split ? vfill ^ (((n + 1) >> 1) & 1u) ^ (((n >> 1) & 1u) << 1) : vbits;
             }
             // wind down: every MMA issued here has completed
-            mma_commit(bar + B_FINAL);
-            drain_bar(bar + B_FINAL, 0);
+            mma_commit(bar + B_FINAL + 8 * g);
+            drain_bar(bar + B_FINAL + 8 * g, 0);
         }
         __syncwarp();
     } else if (KV4 && warp >= W_DQ) {
         // ============================================================ codes to fp16 tiles
-        const int wq = warp - W_DQ;
-        const volatile int *metas = reinterpret_cast<const volatile int *>(sgen + SM_BAR<KV4> + B_META);
-        int kn = 0, vn = 0, qn = 0;
-        for (int c = 0;; ++c) {
-            const int sl = c % NRAW;
-            if (!wait_warp(bar + B_RAWFULL + 8 * sl, (c / NRAW) & 1, abort_flag, a.status))
-                break;
-            const int meta = metas[sl], kind = meta & 0xFF;
-            if (kind == CMD_END)
-                break;
-            uint32_t full;
-            if (kind == CMD_Q) {
+        // (one warpgroup K's, the other V's). Fetches run three tiles ahead: cp.async
+        // into this warp's part of the raw slots, one group a tile.
+        const bool v = warp >= W_DQ + NDQ;
+        const int wq = warp & 3;
+        const uint32_t raws = SM_RAW<KV4> + (v ? NRAW * RAW : 0);
+        const uint32_t tiles = v ? SM_V<KV4> : SM_K<KV4>;
+        const uint32_t full = bar + (v ? B_VFULL : B_KFULL), empty = bar + (v ? B_VEMPTY : B_KEMPTY);
+        Seg f;  // the fetched item, and its next tile
+        int fk = 0, fj = 0, fend = 0, total = 0x7fffffff;
+        long long fbase = -1;
+        uint32_t firsts = 0;  // bit t & 3: tile t is its item's first
+        auto look_up = [&]() {
+            const int z = fj < fend && lane < 8 ? group_row(a, f, fj, lane) : -16;
+            fbase = z < 0 ? -1
+                          : ((((long long)(z >> a.page_shift) * a.Hkv + f.h) << a.page_shift) +
+                             (z & ((1 << a.page_shift) - 1))) * (D / 2);
+        };
+        auto fetch = [&](int t) {
+            if (total > t) {
+                const bool first = fj == fend;
+                if (first) {
+                    if (ring_get(a, bar, ring, fk, lane, abort_flag, f)) {
+                        ++fk;
+                        fj = f.t0;
+                        fend = f.t1;
+                        look_up();
+                    } else {
+                        total = t;
+                    }
+                }
+                if (total > t) {
+                    firsts = (firsts & ~(1u << (t & 3))) | ((first ? 1u : 0u) << (t & 3));
+                    fetch_part<D>(a.codes[v], a.scales[v], fbase, f.pos0 + f.ntok - fj * PP_TILE,
+                                  sb + raws + (t % NRAW) * RAW, wq, lane);
+                    ++fj;
+                    look_up();  // (for the next one)
+                }
+            }
+            cp_async_commit();
+        };
+        for (int t = 0; t < NRAW; ++t)
+            fetch(t);
+        int qn = 0;
+        for (int t = 0; t < total; ++t) {
+            cp_async_wait_group<NRAW - 1>();
+            __syncwarp();
+            if (!v && ((firsts >> (t & 3)) & 1)) {
                 if (!wait_warp(bar + B_QFULL, qn & 1, abort_flag, a.status))
                     break;
                 const int row = wq * 32 + lane;
-                float *rowsc = reinterpret_cast<float *>(sgen + SM_BAR<KV4> + B_ROWSC) + (qn & 1) * 128;
-                rowsc[row] = halve_row<D>(sgen + SM_Q, row);
+                reinterpret_cast<float *>(sgen + SM_BAR<KV4> + B_ROWSC)[(qn & 1) * 128 + row] =
+                    halve_row<D>(sgen + SM_Q, row);
                 ++qn;
-                full = bar + B_QREADY;
-            } else {
-                const bool v = kind == CMD_V;
-                int &n = v ? vn : kn;
-                const int at = n & 1;
-                const uint32_t empty = bar + (v ? B_VEMPTY : B_KEMPTY) + 8 * at;
-                if (n >= 2 && !wait_warp(empty, ((n >> 1) - 1) & 1, abort_flag, a.status))
-                    break;
-                dequant_tile<D>(sgen + SM_RAW<KV4> + sl * RAW, sgen + (v ? SM_V<KV4> : SM_K<KV4>) + at * 32768u, meta,
-                                wq, lane);
-                full = bar + (v ? B_VFULL : B_KFULL) + 8 * at;
-                ++n;
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar + B_QREADY);
             }
+            const int sl = t & 1;
+            if (t >= 2 && !wait_warp(empty + 8 * sl, ((t >> 1) - 1) & 1, abort_flag, a.status))
+                break;
+            dequant_part<D>(sgen + raws + (t % NRAW) * RAW, sgen + tiles + sl * 32768u, wq, lane);
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(full);
-                mbar_arrive(bar + B_RAWEMPTY + 8 * sl);
-            }
+            if (lane == 0)
+                mbar_arrive(full + 8 * sl);
+            fetch(t + NRAW);
         }
+        cp_async_wait_all();
     } else if (warp < 8) {
         // ============================================================ softmax and epilogue
         regs_inc<REGS_SM<KV4>>();
@@ -847,25 +880,49 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 tc_fence_after();
                 if (KV4 && j == 0)
                     scale = a.scale_log2 * reinterpret_cast<const volatile float *>(sgen + SM_BAR<KV4> + B_ROWSC)[(k & 1) * 128 + row];
-                uint32_t sv[128];
+                const int lim = pos - s.tile(g, j) * PP_TILE;  // the row's last key, in this tile's columns
+                // The scores stay in registers; the 4-bit form has fewer (two warpgroups make
+                // tiles) and loads keys 64..127 again for their exponentials.
+                constexpr bool KEEP = !KV4;
+                const bool cut = s.tile(g, j) * PP_TILE + PP_TILE - 1 > pos_warp;
+                uint32_t sv[KEEP ? 128 : 64];
+                auto load = [&](int c0, uint32_t *x) {  // 64 columns, masked once waited for
+                    tmem_ld32(s_addr + c0, x);
+                    tmem_ld32(s_addr + c0 + 32u, x + 32);
+                };
+                auto mask = [&](int c0, uint32_t *x) {
+                    if (cut) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    tmem_ld32(s_addr + 32u * c, sv + 32 * c);
-                tmem_wait_ld();
-                const int key0 = s.tile(g, j) * PP_TILE;
-                if (key0 + PP_TILE - 1 > pos_warp) {
-                    const int lim = pos - key0;
-#pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (c > lim)
-                            sv[c] = __float_as_uint(DDT_NEG_INF);
-                }
+                        for (int c = 0; c < 64; ++c)
+                            if (c0 + c > lim)
+                                x[c] = __float_as_uint(DDT_NEG_INF);
+                    }
+                };
                 float m4[4] = {DDT_NEG_INF, DDT_NEG_INF, DDT_NEG_INF, DDT_NEG_INF};
+                auto largest = [&](const uint32_t *x) {
 #pragma unroll
-                for (int c = 0; c < 128; c += 8)
+                    for (int c = 0; c < 64; c += 8)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        m4[e] = fmaxf(m4[e], fmaxf(__uint_as_float(sv[c + 2 * e]), __uint_as_float(sv[c + 2 * e + 1])));
+                        for (int e = 0; e < 4; ++e)
+                            m4[e] = fmaxf(m4[e], fmaxf(__uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1])));
+                };
+                if constexpr (KEEP) {
+                    load(0, sv);
+                    load(64, sv + 64);
+                    tmem_wait_ld();
+                    mask(0, sv);
+                    mask(64, sv + 64);
+                    largest(sv);
+                    largest(sv + 64);
+                } else {
+#pragma unroll
+                    for (int h = 1; h >= 0; --h) {
+                        load(64 * h, sv);
+                        tmem_wait_ld();
+                        mask(64 * h, sv);
+                        largest(sv);
+                    }
+                }
                 const float mcand = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * scale;
                 float alpha = 1.f;
                 const bool grow = mcand > m_used + TAU;
@@ -893,12 +950,17 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 uint64_t sum0 = f2pack(0.f, 0.f), sum1 = sum0;
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
+                    const uint32_t *x = sv + (KEEP ? 64 * c : 0);
+                    if (!KEEP && c == 1) {
+                        load(64, sv);
+                        tmem_wait_ld();
+                        mask(64, sv);
+                    }
                     uint32_t pw[32];
 #pragma unroll
                     for (int e = 0; e < 32; ++e) {
                         float x0, x1;
-                        f2unpack(f2fma(f2pack(__uint_as_float(sv[64 * c + 2 * e]), __uint_as_float(sv[64 * c + 2 * e + 1])),
-                                       sc2, nm2), x0, x1);
+                        f2unpack(f2fma(f2pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sc2, nm2), x0, x1);
                         x0 = ex2(x0);
                         x1 = ex2(x1);
                         pw[e] = KV4 ? pack_f16x2(x0, x1) : pack_bf16x2(x0, x1);
@@ -908,15 +970,16 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                             sum0 = f2add(sum0, f2pack(x0, x1));
                     }
                     tmem_st32(s_addr + 32u * c, pw);
+                    // the first half's products may begin while the second is computed
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(bar + (c == 0 ? B_PFULL : B_PHALF) + 8 * g);
                 }
                 float r0, r1;
                 f2unpack(f2add(sum0, sum1), r0, r1);
                 l = l * alpha + (r0 + r1);
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(bar + B_PFULL + 8 * g);
             }
             if (!alive)
                 break;
@@ -958,9 +1021,9 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             }
             const bool row_ok = tok < s.ntok;
             const float inv = s.whole ? (l > 0.f || l != l ? a.out_scale / l : 0.f) : 1.f;
-            uint16_t *dst = a.out + ((int64_t)(s.row0 + tok) * a.Hq + (s.h << a.g_shift) + hl) * D;
+            const int64_t row_off = row_ok ? ((int64_t)(s.row0 + tok) * a.Hq + (s.h << a.g_shift) + hl) * D : -1;
             const int64_t prow = (int64_t)s.slot * PR_ROWS + (s.split ? 0 : 128 * g) + row;
-            float *pdst = a.part_o + prow * D;
+            float4 *pdst = reinterpret_cast<float4 *>(a.part_o + (int64_t)s.slot * PR_ROWS * D) + prow % PR_ROWS;
             auto at = [](int c) { return KV4 ? position_of(c) : c; };  // column of channel c
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
@@ -979,20 +1042,29 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     for (int e = 0; e < 32; ++e)
                         ov[e] = __float_as_uint(__uint_as_float(ov[e]) * inv);
                 }
-                if (row_ok && s.whole) {
+                if (s.whole) {
+                    // 64 bytes of this lane's row; four lanes exchange 16-byte quarters so
+                    // that each store covers eight rows' whole 64 bytes
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        w[e] = pack_bf16x2(__uint_as_float(ov[at(2 * e)]), __uint_as_float(ov[at(2 * e + 1)]));
+                    quads_transpose(w, lane);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int x = 0; x < 4; ++x)
-                            w[x] = pack_bf16x2(__uint_as_float(ov[at(8 * e + 2 * x)]), __uint_as_float(ov[at(8 * e + 2 * x + 1)]));
-                        reinterpret_cast<uint4 *>(dst + 32 * c)[e] = make_uint4(w[0], w[1], w[2], w[3]);
+                        const int src = (lane & ~3) + e;  // the lane whose row this is
+                        const int64_t off = __shfl_sync(0xFFFFFFFFu, row_off, src);
+                        if (off >= 0)
+                            *reinterpret_cast<uint4 *>(a.out + off + 32 * c + 8 * (lane & 3)) =
+                                make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
                     }
                 } else if (row_ok) {
+                    // partials: float4 columns, rows side by side (coalesced here and in the merge)
 #pragma unroll
                     for (int e = 0; e < 8; ++e)
-                        reinterpret_cast<uint4 *>(pdst + 32 * c)[e] =
-                            make_uint4(ov[at(4 * e)], ov[at(4 * e + 1)], ov[at(4 * e + 2)], ov[at(4 * e + 3)]);
+                        pdst[(8 * c + e) * PR_ROWS] =
+                            make_float4(__uint_as_float(ov[at(4 * e)]), __uint_as_float(ov[at(4 * e + 1)]),
+                                        __uint_as_float(ov[at(4 * e + 2)]), __uint_as_float(ov[at(4 * e + 3)]));
                 }
             }
             if (row_ok && !s.whole)
@@ -1017,7 +1089,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 // Merge of a cut item: boundary b (between CTAs b - 1 and b) takes the j-th of
 // the nb row blocks of the item that it cuts, if it lies among the item's tiles
 // (nb: the boundaries that do).
-constexpr int MG_THREADS = 256;
+constexpr int MG_THREADS = 256, MG_SPLIT = 8;
 
 template <int D>
 __global__ void __launch_bounds__(MG_THREADS) prompt_merge_kernel(const PtArgs a, int grid, int rows)
@@ -1038,25 +1110,32 @@ __global__ void __launch_bounds__(MG_THREADS) prompt_merge_kernel(const PtArgs a
     const int c0 = pp_cta_of(i0 + PP_ITEM, total, nc), c1 = pp_cta_of(i0 + PP_ITEM + it.n - 1, total, nc);
     const int ntok = min(tq, rq.len - it.qt * tq), nrows = ntok << a.g_shift, ns = c1 - c0 + 1;
     const int nb = ns - 1, j = b - c0 - 1;
-    const int lo = (int)((long long)j * nrows / nb), hi = (int)((long long)(j + 1) * nrows / nb);
+    // of the boundary's rows, this CTA's eighth
+    const int y = j * MG_SPLIT + blockIdx.y, ny = nb * MG_SPLIT;
+    const int lo = (int)((long long)y * nrows / ny), hi = (int)((long long)(y + 1) * nrows / ny);
     pdl_wait();  // the partials, once the main kernel has completed
-    constexpr int C4 = D / 4, RPB = MG_THREADS / C4;  // float4 of a row; rows at a time
-    for (int row = lo + tid / C4; row < hi; row += RPB) {
-        const int c4 = tid % C4;
+    // a warp: eight rows by four float4 columns (the partials' rows lie side by
+    // side, the output's columns do)
+    constexpr int C4 = D / 4;
+    const int lane = tid & 31, r8 = lane & 7;
+    for (int e = tid >> 5; e < ((hi - lo + 7) >> 3) * (C4 / 4); e += MG_THREADS / 32) {
+        const int row = lo + (e / (C4 / 4)) * 8 + r8, c4 = (e % (C4 / 4)) * 4 + (lane >> 3);
+        if (row >= hi)
+            continue;
         float M = DDT_NEG_INF, L = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
         for (int s = 0; s < ns; ++s) {
-            const int64_t pr = (int64_t)(s == 0 ? 2 * c0 + 1 : 2 * (c0 + s)) * PR_ROWS + row;
-            const float2 ml = __ldcg(&a.part_ml[pr]);
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.part_o + pr * D) + c4);
+            const int64_t slot = s == 0 ? 2 * c0 + 1 : 2 * (c0 + s);
+            const float2 ml = __ldcg(&a.part_ml[slot * PR_ROWS + row]);
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.part_o + slot * PR_ROWS * D) + c4 * PR_ROWS + row);
             const float Mn = fmaxf(M, ml.x);
-            const float f = M == DDT_NEG_INF ? 0.f : ex2(M - Mn), e = ml.x == DDT_NEG_INF ? 0.f : ex2(ml.x - Mn);
-            L = L * f + ml.y * e;
-            o.x = o.x * f + v.x * e;
-            o.y = o.y * f + v.y * e;
-            o.z = o.z * f + v.z * e;
-            o.w = o.w * f + v.w * e;
+            const float f = M == DDT_NEG_INF ? 0.f : ex2(M - Mn), w = ml.x == DDT_NEG_INF ? 0.f : ex2(ml.x - Mn);
+            L = L * f + ml.y * w;
+            o.x = o.x * f + v.x * w;
+            o.y = o.y * f + v.y * w;
+            o.z = o.z * f + v.z * w;
+            o.w = o.w * f + v.w * w;
             M = Mn;
         }
         const float inv = L > 0.f || L != L ? a.out_scale / L : 0.f;
@@ -1124,7 +1203,7 @@ cudaError_t launch_d(int grid, const CUtensorMap &tq, const CUtensorMap &tk, con
     if (e != cudaSuccess || grid == 1)
         return e;
     cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3(grid - 1);
+    lc.gridDim = dim3(grid - 1, MG_SPLIT);
     lc.blockDim = dim3(MG_THREADS);
     lc.stream = s;
     cudaLaunchAttribute at[1];
