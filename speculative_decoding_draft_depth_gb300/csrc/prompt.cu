@@ -46,10 +46,10 @@ constexpr int NDQ = 4;  // 4-bit cache: warps that fetch codes and turn them int
 // and loaders and of the two that make fp16 tiles, and what the kernel has to be
 // launched with: they add up to no more than that
 template <bool KV4>
-constexpr int REGS_SM = KV4 ? 120 : 208;
+constexpr int REGS_SM = KV4 ? 112 : 208;
 template <bool KV4>
-constexpr int REGS_OTHER = KV4 ? 72 : 88;
-constexpr int REGS_DQ = 80;
+constexpr int REGS_OTHER = KV4 ? 64 : 88;
+constexpr int REGS_DQ = 96;
 template <bool KV4>
 constexpr int REGS_LAUNCH = KV4 ? 96 : 168;
 static_assert(256 * REGS_SM<true> + 128 * REGS_OTHER<true> + 256 * REGS_DQ <= REGS_LAUNCH<true> * NT<true>, "registers");
@@ -69,17 +69,15 @@ constexpr long long DRAIN_LIMIT = 200000000LL;
 constexpr int NK = 2;
 template <bool KV4>
 constexpr int NV = KV4 ? 2 : 3;
-constexpr int NRAW = 3;          // 4-bit cache: tiles of codes and scales of K, and of V, in flight
+constexpr int NRK = 2, NRV = 1;  // 4-bit cache: tiles of K's and of V's codes and scales in flight
 constexpr uint32_t RAW = 9216;   // 128 rows of 64 bytes of codes, then of 8 scales
-constexpr uint32_t SM_Q = 0;     // A, B: 32 KB each (two 16 KB halves); 4 bits: one for both
+constexpr uint32_t SM_Q = 0;     // A, B: 32 KB each (two 16 KB halves)
+constexpr uint32_t SM_K = 65536;
+constexpr uint32_t SM_V = SM_K + NK * 32768;
 template <bool KV4>
-constexpr uint32_t SM_K = KV4 ? 32768 : 65536;
+constexpr uint32_t SM_RAW = SM_V + NV<KV4> * 32768;
 template <bool KV4>
-constexpr uint32_t SM_V = SM_K<KV4> + NK * 32768;
-template <bool KV4>
-constexpr uint32_t SM_RAW = SM_V<KV4> + NV<KV4> * 32768;
-template <bool KV4>
-constexpr uint32_t SM_BAR = SM_RAW<KV4> + (KV4 ? 2 * NRAW * RAW : 0);
+constexpr uint32_t SM_BAR = SM_RAW<KV4> + (KV4 ? (NRK + NRV) * RAW : 0);
 constexpr uint32_t B_QFULL = 0, B_QEMPTY = 8, B_KFULL = 16, B_KEMPTY = 32, B_VFULL = 48, B_VEMPTY = 72,
                    B_SFULL = 96,   // [2 groups]
                    B_PFULL = 112,  // [2] 4 arrivals (the group's warps): P of keys 0..63 is there
@@ -95,9 +93,9 @@ constexpr uint32_t B_QFULL = 0, B_QEMPTY = 8, B_KFULL = 16, B_KEMPTY = 32, B_VFU
                    B_RING = 336,      // [NRING][8] ints
                    B_FOUND = B_RING,  // three 64-bit words, before the walk begins
                    B_ML = 592,        // [128] float2: B's (m, l); before the roles start, the scan's sums
-                   B_ROWSC = 1616;    // 4 bits: [2][128] floats: the row's factor, by item parity
+                   B_ROWSC = 1616;    // 4 bits: [2][256] floats: the row's factor, by item parity
 template <bool KV4>
-constexpr uint32_t B_END = KV4 ? B_ROWSC + 1024 : B_ROWSC;
+constexpr uint32_t B_END = KV4 ? B_ROWSC + 2048 : B_ROWSC;
 template <bool KV4>
 constexpr uint32_t SM_ALLOC = SM_BAR<KV4> + B_END<KV4> + 1024;
 static_assert(SM_ALLOC<false> <= 232448 && SM_ALLOC<true> <= 232448, "shared memory of one CTA");
@@ -208,19 +206,28 @@ DDT_DEVINL bool ring_get(const PtArgs &a, uint32_t bar, const volatile int *ring
     return s.r >= 0;
 }
 
-// the pool row of 16-token group u of key tile j; -16: past the item's last key,
-// or a page out of range (the TMA fills zeros)
-DDT_DEVINL int group_row(const PtArgs &a, const Seg &s, int j, int u)
+// the page of 16-token group u of key tile j (NO_PAGE: past the item's last key)
+constexpr int NO_PAGE = -0x7fffffff - 1;
+DDT_DEVINL int group_page(const PtArgs &a, const Seg &s, int j, int u)
 {
     const int t16 = j * PP_TILE + 16 * u;  // never straddles a page (page % 16 == 0)
-    if (t16 >= s.pos0 + s.ntok)
-        return -16;
-    const int pg = __ldg(&a.block_table[(int64_t)s.r * a.max_pages + (t16 >> a.page_shift)]);
-    if (pg < 0 || pg >= a.num_pages) {
+    return t16 >= s.pos0 + s.ntok ? NO_PAGE
+                                  : __ldg(&a.block_table[(int64_t)s.r * a.max_pages + (t16 >> a.page_shift)]);
+}
+// whether the group has rows to read; a page out of range is reported
+DDT_DEVINL bool page_ok(const PtArgs &a, int pg)
+{
+    if (pg >= 0 && pg < a.num_pages)
+        return true;
+    if (pg != NO_PAGE)
         atomicOr(a.status, DDT_DEV_BAD_PAGE);
-        return -16;
-    }
-    return (pg << a.page_shift) + (t16 & ((1 << a.page_shift) - 1));
+    return false;
+}
+// the pool row of that group; -16: none (the TMA fills zeros)
+DDT_DEVINL int group_row(const PtArgs &a, const Seg &s, int j, int u)
+{
+    const int pg = group_page(a, s, j, u);
+    return page_ok(a, pg) ? (pg << a.page_shift) + ((j * PP_TILE + 16 * u) & ((1 << a.page_shift) - 1)) : -16;
 }
 
 // this CTA's share: the totals by a scan over the requests (whole block), then
@@ -340,20 +347,24 @@ DDT_DEVINL void fetch_part(const uint8_t *codes, const uint8_t *scales, long lon
                            int lane)
 {
     using P = Part<D>;
+    long long b[P::N];
+#pragma unroll
+    for (int i = 0; i < P::N; ++i)
+        b[i] = __shfl_sync(0xFFFFFFFFu, base, P::index(i, wq, lane) / P::CH >> 4);
+    // this warp's rows' scales: 16 bytes (SR rows) a lane, four lanes to a part
+    constexpr int SR = 256 / D;
+    const int srow = P::index((lane >> 2) % P::N, wq, 0) / P::CH + (lane & 3) * SR;
+    const long long sbase = __shfl_sync(0xFFFFFFFFu, base, srow >> 4);
 #pragma unroll
     for (int i = 0; i < P::N; ++i) {
         const int idx = P::index(i, wq, lane), row = idx / P::CH, q = idx % P::CH;
-        const long long b = __shfl_sync(0xFFFFFFFFu, base, row >> 4);
-        const bool in = b >= 0 && row < valid;
-        const long long at = in ? b + (row & 15) * (D / 2) : 0;
-        cp_async_16(dst + idx * 16, codes + at + q * 16, in ? 16u : 0u);
-        if (q == 0) {
-            const uint32_t so = dst + 128 * (D / 2) + row * (D / 16);
-            if (D == 128)
-                cp_async_8(so, scales + (at >> 3), in ? 8u : 0u);
-            else
-                cp_async_4(so, scales + (at >> 3), in ? 4u : 0u);
-        }
+        const bool in = b[i] >= 0 && row < valid;
+        cp_async_16(dst + idx * 16, codes + (in ? b[i] + (row & 15) * (D / 2) + q * 16 : 0), in ? 16u : 0u);
+    }
+    if (lane < 4 * P::N) {
+        const int n = sbase >= 0 ? max(0, min(SR, valid - srow)) : 0;
+        cp_async_16(dst + 128 * (D / 2) + srow * (D / 16),
+                    scales + (n > 0 ? (sbase >> 3) + (srow & 15) * (D / 16) : 0), n * (D / 16));
     }
 }
 
@@ -458,8 +469,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     volatile int *abort_flag = reinterpret_cast<volatile int *>(sgen + SM_BAR<KV4> + B_ABORT);
     volatile int *ring = reinterpret_cast<volatile int *>(sgen + SM_BAR<KV4> + B_RING);
     const uint32_t bar = sb + SM_BAR<KV4>;
-    constexpr int ROWS = KV4 ? 128 : PP_ROWS;  // of an item
-    const int tq = ROWS >> a.g_shift;
+    const int tq = PP_ROWS >> a.g_shift;
 
     if (tid == 0) {
         mbar_init(bar + B_QFULL, 1);
@@ -564,7 +574,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 s.t0 = t0;
                 s.t1 = t1;
                 s.whole = t0 == 0 && t1 == it.n;
-                s.split = KV4 || (s.ntok << a.g_shift) <= 128;
+                s.split = (s.ntok << a.g_shift) <= 128;
                 s.slot = 2 * blockIdx.x + (t0 > 0 ? 0 : 1);
                 const int sr = r;
                 cur = min(hi, i1);
@@ -618,7 +628,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     ok = false;
                     break;
                 }
-                const uint32_t fb = bar + B_KFULL + 8 * sl, dst = sb + SM_K<KV4> + sl * 32768u;
+                const uint32_t fb = bar + B_KFULL + 8 * sl, dst = sb + SM_K + sl * 32768u;
                 load_boxes<D>(&tm_k, dst, s.h, z, -1, fb, 16384u * (D / 64));
             }
         }
@@ -655,12 +665,12 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     break;
                 }
                 vfill ^= 1u << sl;
-                const uint32_t fb = bar + B_VFULL + 8 * sl, dst = sb + SM_V<KV4> + sl * 32768u;
+                const uint32_t fb = bar + B_VFULL + 8 * sl, dst = sb + SM_V + sl * 32768u;
                 // the 16-token group that holds the item's last key and rows behind it
                 const int cut = (end & 15) != 0 && (end >> 7) == j ? (end & 127) >> 4 : -1;
                 if (cut >= 0) {
                     const int zc = __shfl_sync(0xFFFFFFFFu, z, cut), nrow = end & 15;
-                    unsigned char *d = sgen + SM_V<KV4> + sl * 32768u + cut * 2048;
+                    unsigned char *d = sgen + SM_V + sl * 32768u + cut * 2048;
 #pragma unroll
                     for (int i = 0; i < 16 * (D / 8) / 32; ++i) {
                         const int c = lane + 32 * i, row = c / (D / 8), ch = c % (D / 8);
@@ -686,8 +696,8 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         if (elect_one()) {
             const uint32_t g = warp == W_MMB;
             const uint64_t dQ = sdesc_sw128(sb + SM_Q, 16, 1024);
-            const uint64_t dK = sdesc_sw128(sb + SM_K<KV4>, 16, 1024);
-            const uint64_t dV = sdesc_sw128(sb + SM_V<KV4>, 16384, 1024);
+            const uint64_t dK = sdesc_sw128(sb + SM_K, 16, 1024);
+            const uint64_t dV = sdesc_sw128(sb + SM_V, 16384, 1024);
             const uint32_t o = tmem + TM_O + 128u * g, sp = tmem + TM_S + 128u * g;
             // A parity wait is sound only if the phase before is known to be complete. So
             // in a split item every K and V slot belongs to one group; K's fills of
@@ -717,8 +727,8 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 // the group's first tile and its slots; then every tile, or every second
                 const uint32_t first = base + (s.split ? g : 0u), by = s.split ? 2u : 1u;
                 uint32_t ks = first % NK, kph = (first / NK) & 1;
-                uint32_t vs = KV4 ? first & 1u : s.split ? g : 0u, vbits = KV4 ? ((first >> 1) & 1u) << vs : vfill;
-                const uint64_t q = dQ + (uint64_t)((!KV4 && !s.split && g) ? (32768u >> 4) : 0u);
+                uint32_t vs = s.split ? g : 0u, vbits = vfill;
+                const uint64_t q = dQ + (uint64_t)((!s.split && g) ? (32768u >> 4) : 0u);
                 need(bar + (KV4 ? B_QREADY : B_QFULL), k & 1);
                 // S of tile j behind P V of tile j - 1, whose P lies in the same columns
 #pragma unroll 1
@@ -742,7 +752,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         if (s.split)  // (a slot counts two releases: of both groups, or two of its one)
                             mbar_arrive(bar + B_VEMPTY + 8 * vs);
                         vbits ^= 1u << vs;
-                        if (!KV4 && !s.split && ++vs == NV<KV4>)
+                        if (!s.split && ++vs == NV<KV4>)
                             vs = 0;
                         if (j == steps)
                             mma_commit(bar + B_OFULL + 8 * g);
@@ -782,24 +792,20 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         __syncwarp();
     } else if (KV4 && warp >= W_DQ) {
         // ============================================================ codes to fp16 tiles
-        // (one warpgroup K's, the other V's). Fetches run three tiles ahead: cp.async
-        // into this warp's part of the raw slots, one group a tile.
+        // (one warpgroup K's, the other V's). Fetches run ahead: cp.async into this
+        // warp's part of the raw slots, one group a tile.
         const bool v = warp >= W_DQ + NDQ;
-        const int wq = warp & 3;
-        const uint32_t raws = SM_RAW<KV4> + (v ? NRAW * RAW : 0);
-        const uint32_t tiles = v ? SM_V<KV4> : SM_K<KV4>;
+        const int wq = warp & 3, ahead = v ? NRV : NRK;
+        const uint32_t raws = SM_RAW<KV4> + (v ? NRK * RAW : 0);
+        const uint32_t tiles = v ? SM_V : SM_K;
         const uint32_t full = bar + (v ? B_VFULL : B_KFULL), empty = bar + (v ? B_VEMPTY : B_KEMPTY);
+        const uint8_t *codes = v ? a.codes[1] : a.codes[0], *scales = v ? a.scales[1] : a.scales[0];
         Seg f;  // the fetched item, and its next tile
         int fk = 0, fj = 0, fend = 0, total = 0x7fffffff;
-        long long fbase = -1;
-        uint32_t firsts = 0;  // bit t & 3: tile t is its item's first
-        auto look_up = [&]() {
-            const int z = fj < fend && lane < 8 ? group_row(a, f, fj, lane) : -16;
-            fbase = z < 0 ? -1
-                          : ((((long long)(z >> a.page_shift) * a.Hkv + f.h) << a.page_shift) +
-                             (z & ((1 << a.page_shift) - 1))) * (D / 2);
-        };
-        auto fetch = [&](int t) {
+        int fpage = NO_PAGE;  // lane u: page of group u of that tile (looked at when it is fetched)
+        uint32_t info = 0;    // by raw slot: bit 0, tile is its item's first; bit 1, item has both groups' rows
+        auto look_up = [&]() { fpage = fj < fend && lane < 8 ? group_page(a, f, fj, lane) : NO_PAGE; };
+        auto fetch = [&](int t, int raw) {
             if (total > t) {
                 const bool first = fj == fend;
                 if (first) {
@@ -813,42 +819,56 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     }
                 }
                 if (total > t) {
-                    firsts = (firsts & ~(1u << (t & 3))) | ((first ? 1u : 0u) << (t & 3));
-                    fetch_part<D>(a.codes[v], a.scales[v], fbase, f.pos0 + f.ntok - fj * PP_TILE,
-                                  sb + raws + (t % NRAW) * RAW, wq, lane);
+                    info = (info & ~(3u << (2 * raw))) | ((first ? 1u : 0u) | (f.split ? 0u : 2u)) << (2 * raw);
+                    const long long page0 = ((long long)fpage * a.Hkv + f.h) << a.page_shift;
+                    const int in_page = (fj * PP_TILE + 16 * lane) & ((1 << a.page_shift) - 1);
+                    const long long fbase = page_ok(a, fpage) ? (page0 + in_page) * (D / 2) : -1;
+                    fetch_part<D>(codes, scales, fbase, f.pos0 + f.ntok - fj * PP_TILE, sb + raws + raw * RAW, wq, lane);
                     ++fj;
                     look_up();  // (for the next one)
                 }
             }
             cp_async_commit();
         };
-        for (int t = 0; t < NRAW; ++t)
-            fetch(t);
-        int qn = 0;
+        for (int t = 0; t < ahead; ++t)
+            fetch(t, t);
+        uint32_t fill = 0;  // phase of each fp16 slot's next fill
+        int qn = 0, raw = 0, sl = 0;
         for (int t = 0; t < total; ++t) {
-            cp_async_wait_group<NRAW - 1>();
+            if (v)
+                cp_async_wait_group<NRV - 1>();
+            else
+                cp_async_wait_group<NRK - 1>();
             __syncwarp();
-            if (!v && ((firsts >> (t & 3)) & 1)) {
-                if (!wait_warp(bar + B_QFULL, qn & 1, abort_flag, a.status))
-                    break;
-                const int row = wq * 32 + lane;
-                reinterpret_cast<float *>(sgen + SM_BAR<KV4> + B_ROWSC)[(qn & 1) * 128 + row] =
-                    halve_row<D>(sgen + SM_Q, row);
-                ++qn;
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(bar + B_QREADY);
+            const uint32_t now = info >> (2 * raw);
+            if (now & 1) {
+                if (v) {
+                    sl = 0;  // (V's slots begin anew with each item)
+                } else {
+                    if (!wait_warp(bar + B_QFULL, qn & 1, abort_flag, a.status))
+                        break;
+                    float *rowsc = reinterpret_cast<float *>(sgen + SM_BAR<KV4> + B_ROWSC) + (qn & 1) * 256;
+                    for (int g = 0; g < ((now & 2) ? 2 : 1); ++g)
+                        rowsc[128 * g + wq * 32 + lane] = halve_row<D>(sgen + SM_Q + g * 32768, wq * 32 + lane);
+                    ++qn;
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(bar + B_QREADY);
+                }
             }
-            const int sl = t & 1;
-            if (t >= 2 && !wait_warp(empty + 8 * sl, ((t >> 1) - 1) & 1, abort_flag, a.status))
+            // (a slot never filled passes: its phase "before" is complete)
+            if (!wait_warp(empty + 8 * sl, ((fill >> sl) & 1) ^ 1, abort_flag, a.status))
                 break;
-            dequant_part<D>(sgen + raws + (t % NRAW) * RAW, sgen + tiles + sl * 32768u, wq, lane);
+            fill ^= 1u << sl;
+            dequant_part<D>(sgen + raws + raw * RAW, sgen + tiles + sl * 32768u, wq, lane);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(full + 8 * sl);
-            fetch(t + NRAW);
+            sl ^= 1;
+            fetch(t + ahead, raw);
+            raw = raw + 1 == ahead ? 0 : raw + 1;
         }
         cp_async_wait_all();
     } else if (warp < 8) {
@@ -879,7 +899,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 }
                 tc_fence_after();
                 if (KV4 && j == 0)
-                    scale = a.scale_log2 * reinterpret_cast<const volatile float *>(sgen + SM_BAR<KV4> + B_ROWSC)[(k & 1) * 128 + row];
+                    scale = a.scale_log2 * reinterpret_cast<const volatile float *>(sgen + SM_BAR<KV4> + B_ROWSC)[(k & 1) * 256 + (s.split ? 0 : 128 * g) + row];
                 const int lim = pos - s.tile(g, j) * PP_TILE;  // the row's last key, in this tile's columns
                 // The scores stay in registers; the 4-bit form has fewer (two warpgroups make
                 // tiles) and loads keys 64..127 again for their exponentials.
@@ -948,17 +968,17 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 const float off = (KV4 ? PBIAS : 0.f) - (m_used == DDT_NEG_INF ? 0.f : m_used);
                 const uint64_t sc2 = f2pack(scale, scale), nm2 = f2pack(off, off);
                 uint64_t sum0 = f2pack(0.f, 0.f), sum1 = sum0;
+                // the first half's products may begin while the second is computed
+                auto publish = [&](uint32_t b) {
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(bar + b + 8 * g);
+                };
+                auto exps = [&](const uint32_t *x, uint32_t *pw) {  // 32 scores to 16 pairs
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const uint32_t *x = sv + (KEEP ? 64 * c : 0);
-                    if (!KEEP && c == 1) {
-                        load(64, sv);
-                        tmem_wait_ld();
-                        mask(64, sv);
-                    }
-                    uint32_t pw[32];
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
+                    for (int e = 0; e < 16; ++e) {
                         float x0, x1;
                         f2unpack(f2fma(f2pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sc2, nm2), x0, x1);
                         x0 = ex2(x0);
@@ -969,13 +989,36 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         else
                             sum0 = f2add(sum0, f2pack(x0, x1));
                     }
-                    tmem_st32(s_addr + 32u * c, pw);
-                    // the first half's products may begin while the second is computed
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(bar + (c == 0 ? B_PFULL : B_PHALF) + 8 * g);
+                };
+                if constexpr (KEEP) {
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t pw[32];
+                        exps(sv + 64 * c, pw);
+                        exps(sv + 64 * c + 32, pw + 16);
+                        tmem_st32(s_addr + 32u * c, pw);
+                        publish(c == 0 ? B_PFULL : B_PHALF);
+                    }
+                } else {
+                    // (P's 16 columns never reach scores that are still to be loaded)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t *x = sv + 32 * (c & 1), pw[16];
+                        if (c >= 2) {
+                            tmem_ld32(s_addr + 32u * c, x);
+                            tmem_wait_ld();
+                            if (cut) {
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    if (32 * c + e > lim)
+                                        x[e] = __float_as_uint(DDT_NEG_INF);
+                            }
+                        }
+                        exps(x, pw);
+                        tmem_st16(s_addr + 16u * c, pw);
+                        if (c & 1)
+                            publish(c == 1 ? B_PFULL : B_PHALF);
+                    }
                 }
                 float r0, r1;
                 f2unpack(f2add(sum0, sum1), r0, r1);
@@ -1092,10 +1135,10 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 constexpr int MG_THREADS = 256, MG_SPLIT = 8;
 
 template <int D>
-__global__ void __launch_bounds__(MG_THREADS) prompt_merge_kernel(const PtArgs a, int grid, int rows)
+__global__ void __launch_bounds__(MG_THREADS) prompt_merge_kernel(const PtArgs a, int grid)
 {
     __shared__ long long s_sums[MG_THREADS / 32], s_found[3];
-    const int tq = rows >> a.g_shift, tid = threadIdx.x, b = blockIdx.x + 1;
+    const int tq = PP_ROWS >> a.g_shift, tid = threadIdx.x, b = blockIdx.x + 1;
     find_share(a, tq, grid, b, s_sums, s_found, tid, MG_THREADS);
     if (s_found[0] < 0)
         return;  // no such share
@@ -1211,7 +1254,7 @@ cudaError_t launch_d(int grid, const CUtensorMap &tq, const CUtensorMap &tk, con
     at[0].val.programmaticStreamSerializationAllowed = 1;
     lc.attrs = at;
     lc.numAttrs = 1;
-    return cudaLaunchKernelEx(&lc, prompt_merge_kernel<D>, a, grid, KV4 ? 128 : PP_ROWS);
+    return cudaLaunchKernelEx(&lc, prompt_merge_kernel<D>, a, grid);
 }
 
 }  // namespace
