@@ -33,7 +33,7 @@
 
 #include "ddt_device.cuh"
 #include "ddt_internal.h"
-#include "prompt_plan.h"
+#include "prompt_common.cuh"
 #include "tc_ptx.cuh"
 
 namespace {
@@ -57,11 +57,9 @@ static_assert(256 * REGS_SM<false> + 128 * REGS_OTHER<false> <= REGS_LAUNCH<fals
 constexpr int NRING = 8;
 template <bool KV4>
 constexpr int RING_CONSUMERS = 8 + 2 + 1 + (KV4 ? 2 * NDQ : 0);  // softmax warps, MMA issuers, V or Q loader, ...
-constexpr int MIN_UNITS = 4;               // of a share
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t TM_S = 0;    // S (and P) of A, B: 128 columns each
 constexpr uint32_t TM_O = 256;  // O of A, B: 128 columns each
-constexpr float TAU = 8.0f;     // lazy-rescale threshold (log2 units)
 constexpr long long WAIT_LIMIT = 4000000000LL;  // cycles (about 2 s)
 constexpr long long DRAIN_LIMIT = 200000000LL;
 
@@ -104,60 +102,6 @@ template <bool KV4>
 constexpr uint32_t IDESC_QK = KV4 ? idesc_f16(128, 128, false, false) : idesc_bf16(128, 128, false, false);
 template <int D, bool KV4>
 constexpr uint32_t IDESC_PV = KV4 ? idesc_f16(128, D, false, true) : idesc_bf16(128, D, false, true);
-// 4-bit cache: probabilities are held times 2^7, at most 2^(7 + TAU) (fp16 ends at
-// 65504), so that what fp16 cannot hold lies 2^-32 below the row's largest
-constexpr float PBIAS = 7.0f;
-
-struct PtArgs {
-    const int32_t *q_start, *ctx_lens, *block_table;
-    const uint16_t *v_cache;
-    const uint8_t *codes[2], *scales[2];  // of K, V
-    uint16_t *out;
-    float *part_o;
-    float2 *part_ml;
-    int32_t *status;
-    int R, T, Hq, Hkv, g_shift, page_shift, max_pages, cap;
-    int64_t num_pages;
-    float scale_log2, out_scale;
-};
-
-// a segment of an item: ring words
-//   0: request (-1: end of the share)   1: head | split << 8 | whole << 9 | slot << 10
-//   2: first packed row  3: tokens  4: position of the first  5, 6: key tiles [t0, t1)
-struct Seg {
-    int r, h, row0, ntok, pos0, t0, t1, slot;
-    bool split, whole;
-    DDT_DEVINL int steps(int g) const  // key tiles of group g
-    {
-        const int n = t1 - t0;
-        return split ? (n + 1 - g) >> 1 : n;
-    }
-    DDT_DEVINL int tile(int g, int j) const { return t0 + (split ? 2 * j + g : j); }
-};
-
-DDT_DEVINL void seg_decode(const int *w, Seg &s)
-{
-    s.r = w[0];
-    s.h = w[1] & 0xFF;
-    s.split = (w[1] >> 8) & 1;
-    s.whole = (w[1] >> 9) & 1;
-    s.slot = w[1] >> 10;
-    s.row0 = w[2];
-    s.ntok = w[3];
-    s.pos0 = w[4];
-    s.t0 = w[5];
-    s.t1 = w[6];
-}
-
-DDT_DEVINL PpReq load_req(const PtArgs &a, int r)
-{
-    const int s0 = __ldg(&a.q_start[r]), s1 = __ldg(&a.q_start[r + 1]), c = __ldg(&a.ctx_lens[r]);
-    PpReq q;
-    q.q0 = s0;
-    q.ctx = c;
-    q.len = packed_ok(s0, s1, a.T, c, a.cap) ? s1 - s0 : 0;
-    return q;
-}
 
 // bounded mbarrier wait; false (and the abort flag raised) on timeout
 DDT_DEVINL bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag, int32_t *status)
@@ -206,80 +150,11 @@ DDT_DEVINL bool ring_get(const PtArgs &a, uint32_t bar, const volatile int *ring
     return s.r >= 0;
 }
 
-// the page of 16-token group u of key tile j (NO_PAGE: past the item's last key)
-constexpr int NO_PAGE = -0x7fffffff - 1;
-DDT_DEVINL int group_page(const PtArgs &a, const Seg &s, int j, int u)
-{
-    const int t16 = j * PP_TILE + 16 * u;  // never straddles a page (page % 16 == 0)
-    return t16 >= s.pos0 + s.ntok ? NO_PAGE
-                                  : __ldg(&a.block_table[(int64_t)s.r * a.max_pages + (t16 >> a.page_shift)]);
-}
-// whether the group has rows to read; a page out of range is reported
-DDT_DEVINL bool page_ok(const PtArgs &a, int pg)
-{
-    if (pg >= 0 && pg < a.num_pages)
-        return true;
-    if (pg != NO_PAGE)
-        atomicOr(a.status, DDT_DEV_BAD_PAGE);
-    return false;
-}
 // the pool row of that group; -16: none (the TMA fills zeros)
 DDT_DEVINL int group_row(const PtArgs &a, const Seg &s, int j, int u)
 {
     const int pg = group_page(a, s, j, u);
     return page_ok(a, pg) ? (pg << a.page_shift) + ((j * PP_TILE + 16 * u) & ((1 << a.page_shift) - 1)) : -16;
-}
-
-// this CTA's share: the totals by a scan over the requests (whole block), then
-// the request that holds the share's first unit. found: [0] request, [1..2] its
-// first unit, [3..4] total
-DDT_DEVINL void find_share(const PtArgs &a, int tq, int grid, int cta, long long *sums,
-                           volatile long long *found, int tid, int nthreads)
-{
-    const int per = (a.R + nthreads - 1) / nthreads;
-    const int r0 = min(tid * per, a.R), r1 = min(r0 + per, a.R);
-    long long mine = 0;
-    for (int r = r0; r < r1; ++r)
-        mine += pp_units(load_req(a, r), tq, a.Hkv);
-    long long incl = mine;
-    const int lane = tid & 31, warp = tid >> 5;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-        if (lane >= o)
-            incl += y;
-    }
-    if (lane == 31)
-        sums[warp] = incl;
-    __syncthreads();
-    long long before = 0, total = 0;
-    for (int w = 0; w < nthreads / 32; ++w) {
-        before += w < warp ? sums[w] : 0;
-        total += sums[w];
-    }
-    const long long excl = before + incl - mine;
-    if (tid == 0) {
-        found[0] = -1;
-        found[2] = total;
-    }
-    __syncthreads();
-    if (total > 0) {
-        const int nc = pp_ctas(total, grid, MIN_UNITS);
-        const long long lo = pp_share(total, cta, nc);
-        if (cta < nc && excl <= lo && lo < excl + mine) {
-            long long acc = excl;
-            for (int r = r0; r < r1; ++r) {
-                const long long u = pp_units(load_req(a, r), tq, a.Hkv);
-                if (lo < acc + u) {
-                    found[0] = r;
-                    found[1] = acc;
-                    break;
-                }
-                acc += u;
-            }
-        }
-    }
-    __syncthreads();
 }
 
 // whole warp: one thread issues a tile's boxes, 16 tokens by 64 channels each, but
@@ -302,32 +177,6 @@ DDT_DEVINL void load_boxes(const void *map, uint32_t dst, int h, int z, int skip
             }
     }
     __syncwarp();
-}
-
-// eight 4-bit codes to four fp16 pairs times sc; byte b holds channels in the
-// order 0 2 4 6 1 3 5 7, which the fp16 tiles keep (Q's channels are laid out the
-// same way, and the output's are put back by naming)
-DDT_DEVINL uint4 values8(uint32_t w, uint32_t sc)
-{
-    uint4 r;
-    asm("{\n .reg .b8 a, b, c, d;\n .reg .b32 w0, w1, w2, w3;\n mov.b32 {a, b, c, d}, %4;\n"
-        " cvt.rn.f16x2.e2m1x2 w0, a;\n cvt.rn.f16x2.e2m1x2 w1, b;\n"
-        " cvt.rn.f16x2.e2m1x2 w2, c;\n cvt.rn.f16x2.e2m1x2 w3, d;\n"
-        " mul.rn.f16x2 %0, w0, %5;\n mul.rn.f16x2 %1, w1, %5;\n"
-        " mul.rn.f16x2 %2, w2, %5;\n mul.rn.f16x2 %3, w3, %5;\n}\n"
-        : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-        : "r"(w), "r"(sc));
-    return r;
-}
-// channel of position e of the fp16 tiles, within its 8
-DDT_DEVINL constexpr int channel_of(int e) { return (e & ~7) | ((e & 3) * 2 + ((e >> 2) & 1)); }
-DDT_DEVINL constexpr int position_of(int c) { return (c & ~7) | ((c & 6) >> 1) | ((c & 1) << 2); }
-
-DDT_DEVINL uint32_t pack_f16x2(float lo, float hi)
-{
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
 }
 
 // A warp's part of a tile of codes and scales: 16-byte vectors of codes, CH to a
@@ -546,58 +395,13 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 if (!packed_ok(s0, s1, a.T, __ldg(&a.ctx_lens[r]), a.cap))
                     atomicOr(a.status, DDT_DEV_BAD_LENGTH);
             }
-        const long long total = found[2];
-        int r = (int)found[0];
-        long long base = found[1], cur = 0, hi = 0;
-        PpReq rq = {0, 0, 0};
-        PpItem it = {0, 0, 0, 0};
-        if (r >= 0) {
-            const int nc = pp_ctas(total, gridDim.x, MIN_UNITS);
-            cur = pp_share(total, blockIdx.x, nc);
-            hi = pp_share(total, blockIdx.x + 1, nc);
-            rq = load_req(a, r);
-            it = pp_find(rq, cur - base, tq, a.Hkv);
-        }
+        ShareWalk walk;
+        walk.begin(a, found, tq, gridDim.x, blockIdx.x);
         int k = 0, kn = 0;
         bool ok = true;
         while (ok) {
-            // the next segment that holds tiles
             Seg s;
-            s.r = -1;
-            while (cur < hi) {
-                const long long i0 = base + it.start, i1 = i0 + it.n + PP_ITEM;
-                const int t0 = pp_tile_at(cur - i0), t1 = pp_tile_at(min(hi, i1) - i0);
-                s.h = it.h;
-                s.row0 = rq.q0 + it.qt * tq;
-                s.ntok = min(tq, rq.len - it.qt * tq);
-                s.pos0 = rq.ctx + it.qt * tq;
-                s.t0 = t0;
-                s.t1 = t1;
-                s.whole = t0 == 0 && t1 == it.n;
-                s.split = (s.ntok << a.g_shift) <= 128;
-                s.slot = 2 * blockIdx.x + (t0 > 0 ? 0 : 1);
-                const int sr = r;
-                cur = min(hi, i1);
-                if (cur < hi) {  // the item behind it
-                    it.start += it.n + PP_ITEM;
-                    if (++it.h == a.Hkv) {
-                        it.h = 0;
-                        if (++it.qt == pp_qtiles(rq, tq)) {
-                            base += it.start;
-                            it.start = 0;
-                            it.qt = 0;
-                            do
-                                rq = load_req(a, ++r);  // (units remain, so a request with tokens follows)
-                            while (rq.len == 0);
-                        }
-                        it.n = pp_tiles(rq, it.qt, tq);
-                    }
-                }
-                if (t1 > t0) {
-                    s.r = sr;
-                    break;
-                }
-            }
+            walk.next(a, tq, 128, s);
             const int slot = k & (NRING - 1);
             if (k >= NRING && !wait_warp(bar + B_REMPTY + 8 * slot, ((k / NRING) - 1) & 1, abort_flag, a.status))
                 break;
@@ -1129,67 +933,6 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         tmem_dealloc(tmem, TMEM_COLS);
 }
 
-// Merge of a cut item: boundary b (between CTAs b - 1 and b) takes the j-th of
-// the nb row blocks of the item that it cuts, if it lies among the item's tiles
-// (nb: the boundaries that do).
-constexpr int MG_THREADS = 256, MG_SPLIT = 8;
-
-template <int D>
-__global__ void __launch_bounds__(MG_THREADS) prompt_merge_kernel(const PtArgs a, int grid)
-{
-    __shared__ long long s_sums[MG_THREADS / 32], s_found[3];
-    const int tq = PP_ROWS >> a.g_shift, tid = threadIdx.x, b = blockIdx.x + 1;
-    find_share(a, tq, grid, b, s_sums, s_found, tid, MG_THREADS);
-    if (s_found[0] < 0)
-        return;  // no such share
-    const long long total = s_found[2], base = s_found[1];
-    const int nc = pp_ctas(total, grid, MIN_UNITS);
-    const PpReq rq = load_req(a, (int)s_found[0]);
-    const long long at = pp_share(total, b, nc);
-    const PpItem it = pp_find(rq, at - base, tq, a.Hkv);
-    const long long i0 = base + it.start;
-    if (pp_tile_at(at - i0) == 0)
-        return;  // the item's tiles all lie behind this boundary
-    const int c0 = pp_cta_of(i0 + PP_ITEM, total, nc), c1 = pp_cta_of(i0 + PP_ITEM + it.n - 1, total, nc);
-    const int ntok = min(tq, rq.len - it.qt * tq), nrows = ntok << a.g_shift, ns = c1 - c0 + 1;
-    const int nb = ns - 1, j = b - c0 - 1;
-    // of the boundary's rows, this CTA's eighth
-    const int y = j * MG_SPLIT + blockIdx.y, ny = nb * MG_SPLIT;
-    const int lo = (int)((long long)y * nrows / ny), hi = (int)((long long)(y + 1) * nrows / ny);
-    pdl_wait();  // the partials, once the main kernel has completed
-    // a warp: eight rows by four float4 columns (the partials' rows lie side by
-    // side, the output's columns do)
-    constexpr int C4 = D / 4;
-    const int lane = tid & 31, r8 = lane & 7;
-    for (int e = tid >> 5; e < ((hi - lo + 7) >> 3) * (C4 / 4); e += MG_THREADS / 32) {
-        const int row = lo + (e / (C4 / 4)) * 8 + r8, c4 = (e % (C4 / 4)) * 4 + (lane >> 3);
-        if (row >= hi)
-            continue;
-        float M = DDT_NEG_INF, L = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int s = 0; s < ns; ++s) {
-            const int64_t slot = s == 0 ? 2 * c0 + 1 : 2 * (c0 + s);
-            const float2 ml = __ldcg(&a.part_ml[slot * PR_ROWS + row]);
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(a.part_o + slot * PR_ROWS * D) + c4 * PR_ROWS + row);
-            const float Mn = fmaxf(M, ml.x);
-            const float f = M == DDT_NEG_INF ? 0.f : ex2(M - Mn), w = ml.x == DDT_NEG_INF ? 0.f : ex2(ml.x - Mn);
-            L = L * f + ml.y * w;
-            o.x = o.x * f + v.x * w;
-            o.y = o.y * f + v.y * w;
-            o.z = o.z * f + v.z * w;
-            o.w = o.w * f + v.w * w;
-            M = Mn;
-        }
-        const float inv = L > 0.f || L != L ? a.out_scale / L : 0.f;
-        const int tok = row >> a.g_shift, h = (it.h << a.g_shift) + (row & ((1 << a.g_shift) - 1));
-        uint32_t *dst = reinterpret_cast<uint32_t *>(
-            a.out + ((int64_t)(rq.q0 + it.qt * tq + tok) * a.Hq + h) * D) + c4 * 2;
-        *reinterpret_cast<uint2 *>(dst) =
-            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-    }
-}
-
 // ------------------------------------------------------------------ host side
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
@@ -1245,16 +988,7 @@ cudaError_t launch_d(int grid, const CUtensorMap &tq, const CUtensorMap &tk, con
     e = cudaGetLastError();
     if (e != cudaSuccess || grid == 1)
         return e;
-    cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3(grid - 1, MG_SPLIT);
-    lc.blockDim = dim3(MG_THREADS);
-    lc.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    lc.attrs = at;
-    lc.numAttrs = 1;
-    return cudaLaunchKernelEx(&lc, prompt_merge_kernel<D>, a, grid);
+    return launch_merge<D>(a, grid, PP_ROWS, s);
 }
 
 }  // namespace
@@ -1269,12 +1003,6 @@ cudaError_t launch_prompt_attention(ddt_ctx *c, const uint16_t *q, int64_t q_str
     const int G = cfg.Hq / cfg.Hkv, d = cfg.d;
     const int64_t rows = cfg.num_pages * cfg.page_size;
     const int64_t dense = (int64_t)cfg.Hkv * d;
-    CUtensorMap tq, tk = {}, tv = {};
-    if (!make_map(&tq, q, d, cfg.Hq, T, q_stride, G, 128 / G))
-        return cudaErrorInvalidValue;
-    if (!kv4 && (!make_map(&tk, k_cache, d, cfg.Hkv, rows, dense, 1, 16) ||
-                 !make_map(&tv, v_cache, d, cfg.Hkv, rows, dense, 1, 16)))
-        return cudaErrorInvalidValue;
     PtArgs a = {};
     a.q_start = q_start;
     a.ctx_lens = ctx_lens;
@@ -1305,6 +1033,16 @@ cudaError_t launch_prompt_attention(ddt_ctx *c, const uint16_t *q, int64_t q_str
         a.scale_log2 *= kv4->k_scale;
         a.out_scale = kv4->v_scale;
     }
+    // Few rows of a request (on average: lengths are the device's) over the 4-bit
+    // cache have a kernel of their own.
+    if (kv4 && (int64_t)T * G <= (int64_t)R * 16)
+        return launch_prompt_few(c, a, q, q_stride, G <= 8 && (int64_t)T * G <= (int64_t)R * 8 ? 8 : 16, s);
+    CUtensorMap tq, tk = {}, tv = {};
+    if (!make_map(&tq, q, d, cfg.Hq, T, q_stride, G, 128 / G))
+        return cudaErrorInvalidValue;
+    if (!kv4 && (!make_map(&tk, k_cache, d, cfg.Hkv, rows, dense, 1, 16) ||
+                 !make_map(&tv, v_cache, d, cfg.Hkv, rows, dense, 1, 16)))
+        return cudaErrorInvalidValue;
     const int grid = c->num_sms < PR_MAX_CTAS ? c->num_sms : PR_MAX_CTAS;
     if (kv4)
         return d == 128 ? launch_d<128, true>(grid, tq, tk, tv, a, s) : launch_d<64, true>(grid, tq, tk, tv, a, s);

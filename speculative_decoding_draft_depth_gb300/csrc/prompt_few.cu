@@ -1,0 +1,387 @@
+// prompt_few.cu -- attention of few rows over the cache held in 4 bits (a decoding
+// step, short chains): at most 8 NR rows of an item, keys as the long side of
+// warp-level products, values made in registers.
+//
+// Why not the kernel of prompt.cu: with few rows the cache's bytes are the bound,
+// and there each 128-key tile costs 64 KB of fp16 written to shared memory and as
+// much read back by the products, about 1600 cycles at 128 bytes a cycle, against
+// 900 for the tile's codes from HBM. Here a warp takes 16 keys at a time straight
+// from global memory to registers, where the codes become the products' A operand:
+//   S^T (16 keys x 8 rows) = K Q^T:  lane (i, c) = (lane / 4, lane % 4) holds keys i
+//     and i + 8, channels [c D/4, (c + 1) D/4) -- 16 bytes of codes of a key, whose
+//     pairs go to the products as they come; Q's are laid out alike, once an item;
+//   O^T (channels x 8 rows) += V^T P^T: lane (i, c) holds keys 2c, 2c + 1, 2c + 8,
+//     2c + 9, channels [i D/8, (i + 1) D/8); two keys' values of one channel are
+//     paired by a byte permutation, and P^T is transposed in the warp.
+// Eight warps of a CTA take the 16-key blocks of a segment in turn, each with its
+// own running maximum and sum, and meet at the segment's end. The next block's
+// codes are in flight while one is worked on. Shares of the work and the merge of
+// cut items as in prompt.cu.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "prompt_common.cuh"
+
+namespace {
+
+constexpr int FW = 8;  // warps of a CTA
+constexpr int FT = FW * 32;
+
+struct FewArgs {
+    PtArgs a;
+    const uint16_t *q;
+    int64_t q_stride;
+};
+
+DDT_DEVINL void mma_f16(float *d, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// an 8 x 8 matrix of 16-bit values (lane: row lane / 4, columns 2 (lane % 4), + 1), transposed
+DDT_DEVINL uint32_t transpose8(uint32_t x)
+{
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+DDT_DEVINL uint32_t scales2(uint32_t two)  // e4m3 pair -> fp16 pair
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
+    return r;
+}
+
+// one lane's codes of a 16-key block
+template <int D>
+struct Block {
+    static constexpr int KW = D / 32;  // words of a key's codes (K); V: half as many
+    uint32_t k[2][KW], ks[2];
+    uint32_t v[4][KW / 2], vs[4];
+};
+
+// page: the block's page (NO_PAGE: no rows); codes of keys from `end` on are zero
+template <int D>
+DDT_DEVINL void load_block(const PtArgs &a, Block<D> &b, int page, int key0, int end, int h, int lane)
+{
+    constexpr int KW = Block<D>::KW;
+    const bool ok = page_ok(a, page);
+    const int64_t row = (((int64_t)(ok ? page : 0) * a.Hkv + h) << a.page_shift) + (key0 & ((1 << a.page_shift) - 1));
+    const int i = lane >> 2, c = lane & 3, n = ok ? end - key0 : 0;  // keys that count
+    const uint8_t *kc = a.codes[0] + row * (D / 2) + i * (D / 2) + c * (D / 8);
+    const uint8_t *ks = a.scales[0] + row * (D / 16) + i * (D / 16) + c * (D / 64);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        const bool in = i + 8 * x < n;
+        if constexpr (D == 128) {
+            uint4 w = make_uint4(0u, 0u, 0u, 0u);
+            b.ks[x] = 0;
+            if (in) {
+                w = ldg_stream(kc + x * 8 * (D / 2));
+                b.ks[x] = __ldg(reinterpret_cast<const unsigned short *>(ks + x * 8 * (D / 16)));
+            }
+            b.k[x][0] = w.x, b.k[x][1] = w.y, b.k[x][KW - 2] = w.z, b.k[x][KW - 1] = w.w;
+        } else {
+            uint2 w = make_uint2(0u, 0u);
+            b.ks[x] = 0;
+            if (in) {
+                w = __ldg(reinterpret_cast<const uint2 *>(kc + x * 8 * (D / 2)));
+                b.ks[x] = __ldg(ks + x * 8 * (D / 16));
+            }
+            b.k[x][0] = w.x, b.k[x][1] = w.y;
+        }
+    }
+    const uint8_t *vc = a.codes[1] + row * (D / 2) + i * (D / 16);
+    const uint8_t *vs = a.scales[1] + row * (D / 16) + i * (D / 16) / 8;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        const int key = 2 * c + (x & 1) + 8 * (x >> 1);
+        const bool in = key < n;
+        b.vs[x] = 0;
+        if constexpr (D == 128) {
+            uint2 w = make_uint2(0u, 0u);
+            if (in)
+                w = __ldg(reinterpret_cast<const uint2 *>(vc + key * (D / 2)));
+            b.v[x][0] = w.x, b.v[x][KW / 2 - 1] = w.y;
+        } else {
+            b.v[x][0] = in ? __ldg(reinterpret_cast<const unsigned int *>(vc + key * (D / 2))) : 0u;
+        }
+        if (in)
+            b.vs[x] = __ldg(vs + key * (D / 16));
+    }
+}
+
+template <int D, int NR>
+__global__ void __launch_bounds__(FT, NR == 1 ? 2 : 1) prompt_few_kernel(const FewArgs f)
+{
+    constexpr int ROWS = 8 * NR, KW = Block<D>::KW, KS = D / 16, CH = D / 8;  // CH: channels of a lane's V
+    extern __shared__ float4 few_smem[];
+    float *so = reinterpret_cast<float *>(few_smem);  // [FW][ROWS][D]
+    float2 *sml = reinterpret_cast<float2 *>(so + FW * ROWS * D);  // [FW][ROWS]
+    __shared__ long long s_sums[FW], s_found[3];
+    const PtArgs &a = f.a;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, i = lane >> 2, c = lane & 3;
+    const int tq = ROWS >> a.g_shift, G = 1 << a.g_shift;
+    if (blockIdx.x == 0)
+        for (int r = tid; r < a.R; r += FT) {
+            const int s0 = __ldg(&a.q_start[r]), s1 = __ldg(&a.q_start[r + 1]);
+            if (!packed_ok(s0, s1, a.T, __ldg(&a.ctx_lens[r]), a.cap))
+                set_status(a.status, DDT_DEV_BAD_LENGTH);
+        }
+    find_share(a, tq, gridDim.x, blockIdx.x, s_sums, s_found, tid, FT);
+    ShareWalk walk;
+    walk.begin(a, s_found, tq, gridDim.x, blockIdx.x);
+    for (;;) {
+        Seg s;
+        walk.next(a, tq, 0, s);
+        if (s.r < 0)
+            break;
+        const int end = s.pos0 + s.ntok, nrows = s.ntok << a.g_shift;
+        // ---- this warp's blocks: the first one's codes, the second one's page
+        const int bend = (min(end, s.t1 * PP_TILE) + 15) >> 4;
+        int blk = s.t0 * (PP_TILE / 16) + warp;
+        const int32_t *pages = a.block_table + (int64_t)s.r * a.max_pages;
+        auto page_of = [&](int b) { return b < bend ? __ldg(pages + ((b * 16) >> a.page_shift)) : NO_PAGE; };
+        Block<D> next;
+        load_block<D>(a, next, page_of(blk), blk * 16, end, s.h, lane);
+        int page = page_of(blk + FW);
+        // ---- Q: row 8 y + i, channels [c D/4, + D/4), divided by a power of two of the
+        //      row's largest magnitude, to fp16 in the order of the codes' pairs
+        uint32_t qf[NR][2 * KS];
+        float sc[NR][2], m[NR][2], l[NR][2], o[NR][KS][4];
+        int pos[NR][2];
+#pragma unroll
+        for (int y = 0; y < NR; ++y) {
+            const int row = 8 * y + i;
+            uint4 w[D / 32];
+#pragma unroll
+            for (int x = 0; x < D / 32; ++x)
+                w[x] = make_uint4(0u, 0u, 0u, 0u);
+            if (row < nrows) {
+                const uint16_t *src = f.q + (int64_t)(s.row0 + (row >> a.g_shift)) * f.q_stride +
+                                      ((s.h << a.g_shift) + (row & (G - 1))) * D + c * (D / 4);
+#pragma unroll
+                for (int x = 0; x < D / 32; ++x)
+                    w[x] = __ldg(reinterpret_cast<const uint4 *>(src) + x);
+            }
+            uint32_t amax = 0;
+#pragma unroll
+            for (int x = 0; x < D / 32; ++x) {
+                const uint32_t u[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    amax = max(amax, max(u[e] & 0x7FFFu, (u[e] >> 16) & 0x7FFFu));
+            }
+            amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+            amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
+            int e2 = (int)(amax >> 7) - 127;
+            e2 = amax >= 0x7F80u ? 0 : max(-100, min(100, e2));  // (rows with NaN or inf as they are)
+            const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
+            const float up = __uint_as_float((uint32_t)(127 + e2) << 23) * a.scale_log2;
+#pragma unroll
+            for (int x = 0; x < D / 32; ++x) {
+                const float v[8] = {bf16lo(w[x].x), bf16hi(w[x].x), bf16lo(w[x].y), bf16hi(w[x].y),
+                                    bf16lo(w[x].z), bf16hi(w[x].z), bf16lo(w[x].w), bf16hi(w[x].w)};
+                qf[y][4 * x] = pack_f16x2(v[0] * down, v[2] * down);
+                qf[y][4 * x + 1] = pack_f16x2(v[4] * down, v[6] * down);
+                qf[y][4 * x + 2] = pack_f16x2(v[1] * down, v[3] * down);
+                qf[y][4 * x + 3] = pack_f16x2(v[5] * down, v[7] * down);
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {  // this lane's columns of S^T: rows 8 y + 2 c, + 1
+                sc[y][e] = __shfl_sync(0xFFFFFFFFu, up, (2 * c + e) * 4);
+                m[y][e] = DDT_NEG_INF;
+                l[y][e] = 0.f;
+                pos[y][e] = s.pos0 + min((8 * y + 2 * c + e) >> a.g_shift, s.ntok - 1);
+            }
+#pragma unroll
+            for (int j = 0; j < KS; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    o[y][j][e] = 0.f;
+        }
+        for (; blk < bend; blk += FW) {
+            const Block<D> b = next;
+            load_block<D>(a, next, page, (blk + FW) * 16, blk + FW < bend ? end : 0, s.h, lane);
+            page = page_of(blk + 2 * FW);
+            // ---- S^T
+            float st[NR][4];
+#pragma unroll
+            for (int y = 0; y < NR; ++y)
+                st[y][0] = st[y][1] = st[y][2] = st[y][3] = 0.f;
+            uint32_t s2[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                s2[x] = scales2(D == 128 ? b.ks[x] : b.ks[x] * 0x0101u);
+#pragma unroll
+            for (int w = 0; w < KW; ++w) {
+                // (D = 128: words 0, 1 lie in the first of the lane's two blocks)
+                const uint32_t sel = (D == 128 && w >= 2) ? 0x3232u : 0x1010u;
+                const uint4 x0 = values8(b.k[0][w], __byte_perm(s2[0], s2[0], sel));
+                const uint4 x1 = values8(b.k[1][w], __byte_perm(s2[1], s2[1], sel));
+#pragma unroll
+                for (int y = 0; y < NR; ++y) {
+                    mma_f16(st[y], x0.x, x1.x, x0.y, x1.y, qf[y][4 * w], qf[y][4 * w + 1]);
+                    mma_f16(st[y], x0.z, x1.z, x0.w, x1.w, qf[y][4 * w + 2], qf[y][4 * w + 3]);
+                }
+            }
+            // ---- softmax: keys key0 + i and + 8, rows 2 c and 2 c + 1
+            const int key0 = blk * 16;
+            if (key0 + 15 > s.pos0) {
+#pragma unroll
+                for (int y = 0; y < NR; ++y)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (key0 + i + 8 * (e >> 1) > pos[y][e & 1])
+                            st[y][e] = DDT_NEG_INF;
+            }
+            bool grow = false;
+#pragma unroll
+            for (int y = 0; y < NR; ++y)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    st[y][e] *= sc[y][e & 1];
+                    grow |= st[y][e] > m[y][e & 1] + TAU;
+                }
+            if (__any_sync(0xFFFFFFFFu, grow)) {
+#pragma unroll
+                for (int y = 0; y < NR; ++y)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float mx = fmaxf(st[y][e], st[y][e + 2]);
+#pragma unroll
+                        for (int x = 4; x <= 16; x <<= 1)
+                            mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, x));
+                        if (mx > m[y][e]) {
+                            const float alpha = ex2(m[y][e] - mx);
+                            m[y][e] = mx;
+                            l[y][e] *= alpha;
+#pragma unroll
+                            for (int j = 0; j < KS; ++j) {
+                                o[y][j][e] *= alpha;
+                                o[y][j][e + 2] *= alpha;
+                            }
+                        }
+                    }
+            }
+            uint32_t pb[NR][2];
+#pragma unroll
+            for (int y = 0; y < NR; ++y) {
+                float p[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    p[e] = ex2(st[y][e] + (PBIAS - (m[y][e & 1] == DDT_NEG_INF ? 0.f : m[y][e & 1])));
+                    l[y][e & 1] += p[e];
+                }
+                pb[y][0] = transpose8(pack_f16x2(p[0], p[1]));
+                pb[y][1] = transpose8(pack_f16x2(p[2], p[3]));
+            }
+            // ---- O^T
+            uint32_t vsc[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+                vsc[x] = scales2(b.vs[x] * 0x0101u);
+#pragma unroll
+            for (int w = 0; w < KW / 2; ++w) {
+                uint4 x[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x[e] = values8(b.v[e][w], vsc[e]);
+                const uint32_t u[4][4] = {{x[0].x, x[0].y, x[0].z, x[0].w}, {x[1].x, x[1].y, x[1].z, x[1].w},
+                                          {x[2].x, x[2].y, x[2].z, x[2].w}, {x[3].x, x[3].y, x[3].z, x[3].w}};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t a0 = __byte_perm(u[0][q], u[1][q], 0x5410), a1 = __byte_perm(u[0][q], u[1][q], 0x7632);
+                    const uint32_t a2 = __byte_perm(u[2][q], u[3][q], 0x5410), a3 = __byte_perm(u[2][q], u[3][q], 0x7632);
+#pragma unroll
+                    for (int y = 0; y < NR; ++y)
+                        mma_f16(o[y][4 * w + q], a0, a1, a2, a3, pb[y][0], pb[y][1]);
+                }
+            }
+        }
+        // ---- the warps' parts to shared memory: O row by row, (m, l)
+#pragma unroll
+        for (int y = 0; y < NR; ++y)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = 8 * y + 2 * c + e;
+#pragma unroll
+                for (int x = 4; x <= 16; x <<= 1)
+                    l[y][e] += __shfl_xor_sync(0xFFFFFFFFu, l[y][e], x);
+                if (i == 0)
+                    sml[warp * ROWS + row] = make_float2(m[y][e], l[y][e]);
+                float *dst = so + (warp * ROWS + row) * D + i * CH;
+                // product 4 w + q holds channels {0, 4, 1, 5}[q] and those + 2 of word w
+#pragma unroll
+                for (int w = 0; w < KW / 2; ++w) {
+                    reinterpret_cast<float4 *>(dst)[2 * w] =
+                        make_float4(o[y][4 * w][e], o[y][4 * w + 2][e], o[y][4 * w][e + 2], o[y][4 * w + 2][e + 2]);
+                    reinterpret_cast<float4 *>(dst)[2 * w + 1] =
+                        make_float4(o[y][4 * w + 1][e], o[y][4 * w + 3][e], o[y][4 * w + 1][e + 2], o[y][4 * w + 3][e + 2]);
+                }
+            }
+        __syncthreads();
+        for (int e = tid; e < nrows * (D / 4); e += FT) {
+            const int row = e / (D / 4), c4 = e % (D / 4);
+            float M = DDT_NEG_INF, L = 0.f;
+#pragma unroll
+            for (int w = 0; w < FW; ++w)
+                M = fmaxf(M, sml[w * ROWS + row].x);
+            float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < FW; ++w) {
+                const float2 ml = sml[w * ROWS + row];
+                const float k = ml.x == DDT_NEG_INF ? 0.f : ex2(ml.x - M);
+                const float4 v = reinterpret_cast<const float4 *>(so + (w * ROWS + row) * D)[c4];
+                L += ml.y * k;
+                r.x += v.x * k;
+                r.y += v.y * k;
+                r.z += v.z * k;
+                r.w += v.w * k;
+            }
+            if (s.whole) {
+                const float inv = L > 0.f || L != L ? a.out_scale / L : 0.f;
+                uint32_t *dst = reinterpret_cast<uint32_t *>(
+                    a.out + ((int64_t)(s.row0 + (row >> a.g_shift)) * a.Hq + (s.h << a.g_shift) + (row & (G - 1))) * D) + 2 * c4;
+                *reinterpret_cast<uint2 *>(dst) =
+                    make_uint2(pack_bf16x2(r.x * inv, r.y * inv), pack_bf16x2(r.z * inv, r.w * inv));
+            } else {
+                reinterpret_cast<float4 *>(a.part_o + (int64_t)s.slot * ROWS * D)[c4 * ROWS + row] = r;
+                if (c4 == 0)
+                    a.part_ml[(int64_t)s.slot * ROWS + row] = make_float2(M, L);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+template <int D, int NR>
+cudaError_t launch_few(const FewArgs &f, int num_sms, cudaStream_t s)
+{
+    constexpr int ROWS = 8 * NR, BYTES = FW * ROWS * (D * 4 + 8);
+    static_assert(ROWS * 2 * 2 * PR_MAX_CTAS <= 2 * PR_MAX_CTAS * PR_ROWS, "partial slots");
+    cudaError_t e = cudaFuncSetAttribute(prompt_few_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
+    if (e != cudaSuccess)
+        return e;
+    const int grid = (num_sms < PR_MAX_CTAS ? num_sms : PR_MAX_CTAS) * (NR == 1 ? 2 : 1);
+    prompt_few_kernel<D, NR><<<grid, FT, BYTES, s>>>(f);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || grid == 1)
+        return e;
+    return launch_merge<D>(f.a, grid, ROWS, s);
+}
+
+}  // namespace
+
+cudaError_t launch_prompt_few(ddt_ctx *c, const PtArgs &a, const uint16_t *q, int64_t q_stride, int rows, cudaStream_t s)
+{
+    FewArgs f;
+    f.a = a;
+    f.q = q;
+    f.q_stride = q_stride;
+    if (c->cfg.d == 128)
+        return rows <= 8 ? launch_few<128, 1>(f, c->num_sms, s) : launch_few<128, 2>(f, c->num_sms, s);
+    return rows <= 8 ? launch_few<64, 1>(f, c->num_sms, s) : launch_few<64, 2>(f, c->num_sms, s);
+}

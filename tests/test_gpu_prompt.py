@@ -68,6 +68,16 @@ def test_more_requests_than_threads(bits):
     run(Packed(rng.integers(0, 3, 900).tolist(), rng.integers(0, 80, 900).tolist(), 4, 1, 64, 16, bits, seed=23))
 
 
+@pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_few_tokens_unevenly_spread(bits, shape):
+    """Few tokens on average, all of them with two requests (for the 4-bit cache:
+    the few-rows kernel with items of several query tiles), and two each."""
+    Hq, Hkv, d, page = shape
+    run(Packed([37, 0, 0, 0, 0, 0, 0, 0, 0, 0, 43] + [0] * 69, [300, 5] * 40, Hq, Hkv, d, page, bits, seed=45, tail=1))
+    run(Packed([2, 1, 2, 2, 0, 2], [90, 0, 1000, 127, 3, 14], Hq, Hkv, d, page, bits, seed=46))
+
+
 def test_long_prompt():
     run(Packed([2500], [0], 8, 2, 128, 16, 16, seed=24))
 
