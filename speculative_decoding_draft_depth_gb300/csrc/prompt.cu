@@ -361,6 +361,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         }
     }
     volatile long long *found = reinterpret_cast<volatile long long *>(sgen + SM_BAR<KV4> + B_FOUND);
+    pdl_trigger();  // (the merge stages itself; it waits for this grid before it reads)
     find_share(a, tq, gridDim.x, blockIdx.x, reinterpret_cast<long long *>(sgen + SM_BAR<KV4> + B_ML), found, tid, NT<KV4>);
     tc_fence_before();
     __syncthreads();
@@ -970,20 +971,24 @@ bool make_map(CUtensorMap *m, const void *base, int d, int heads, int64_t rows, 
 }
 
 template <int D, bool KV4>
-cudaError_t launch_d(int grid, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const PtArgs &a,
+cudaError_t launch_d(int dev, int grid, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const PtArgs &a,
                      cudaStream_t s)
 {
-    cudaError_t e = cudaFuncSetAttribute(prompt_tc_kernel<D, KV4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)SM_ALLOC<KV4>);
-    if (e != cudaSuccess)
-        return e;
-    // a block launched with fewer registers would wait forever for its split
-    cudaFuncAttributes fa;
-    e = cudaFuncGetAttributes(&fa, prompt_tc_kernel<D, KV4>);
-    if (e != cudaSuccess)
-        return e;
-    if (fa.numRegs < REGS_LAUNCH<KV4>)
-        return cudaErrorLaunchOutOfResources;
+    static DeviceFlags ready;
+    cudaError_t e = cudaSuccess;
+    if (!ready.test(dev)) {
+        e = cudaFuncSetAttribute(prompt_tc_kernel<D, KV4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)SM_ALLOC<KV4>);
+        // a block launched with fewer registers would wait forever for its split
+        cudaFuncAttributes fa;
+        if (e == cudaSuccess)
+            e = cudaFuncGetAttributes(&fa, prompt_tc_kernel<D, KV4>);
+        if (e != cudaSuccess)
+            return e;
+        if (fa.numRegs < REGS_LAUNCH<KV4>)
+            return cudaErrorLaunchOutOfResources;
+        ready.set(dev);
+    }
     prompt_tc_kernel<D, KV4><<<grid, NT<KV4>, SM_ALLOC<KV4>, s>>>(tq, tk, tv, a);
     e = cudaGetLastError();
     if (e != cudaSuccess || grid == 1)
@@ -1045,6 +1050,6 @@ cudaError_t launch_prompt_attention(ddt_ctx *c, const uint16_t *q, int64_t q_str
         return cudaErrorInvalidValue;
     const int grid = c->num_sms < PR_MAX_CTAS ? c->num_sms : PR_MAX_CTAS;
     if (kv4)
-        return d == 128 ? launch_d<128, true>(grid, tq, tk, tv, a, s) : launch_d<64, true>(grid, tq, tk, tv, a, s);
-    return d == 128 ? launch_d<128, false>(grid, tq, tk, tv, a, s) : launch_d<64, false>(grid, tq, tk, tv, a, s);
+        return d == 128 ? launch_d<128, true>(c->device, grid, tq, tk, tv, a, s) : launch_d<64, true>(c->device, grid, tq, tk, tv, a, s);
+    return d == 128 ? launch_d<128, false>(c->device, grid, tq, tk, tv, a, s) : launch_d<64, false>(c->device, grid, tq, tk, tv, a, s);
 }

@@ -5,6 +5,8 @@
 
 #include <stdint.h>
 
+#include <atomic>
+
 #include "ddt_device.cuh"
 #include "ddt_internal.h"
 #include "prompt_plan.h"
@@ -296,8 +298,20 @@ __global__ void __launch_bounds__(MG_THREADS) prompt_merge_kernel(const PtArgs a
     }
 }
 
-// the merge as a programmatic dependent of the main kernel (its launch is staged
-// while the main kernel's last CTAs finish); grid: the main kernel's
+// devices for which a kernel's attributes have been set (setting them twice does no
+// harm, so two threads may come at once)
+struct DeviceFlags {
+    std::atomic<uint64_t> bits{0};
+    bool test(int dev) const { return dev < 64 && ((bits.load(std::memory_order_relaxed) >> dev) & 1); }
+    void set(int dev)
+    {
+        if (dev < 64)
+            bits.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
+    }
+};
+
+// the merge as a programmatic dependent of the main kernel (which lets it stage
+// itself at once); grid: the main kernel's
 template <int D>
 cudaError_t launch_merge(const PtArgs &a, int grid, int rows, cudaStream_t s)
 {

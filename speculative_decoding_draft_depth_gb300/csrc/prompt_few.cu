@@ -14,19 +14,21 @@
 //     2c + 9, channels [i D/8, (i + 1) D/8); two keys' values of one channel are
 //     paired by a byte permutation, and P^T is transposed in the warp.
 // Eight warps of a CTA take the 16-key blocks of a segment in turn, each with its
-// own running maximum and sum, and meet at the segment's end. The next block's
-// codes are in flight while one is worked on. Shares of the work and the merge of
+// own running maximum and sum, and meet at the segment's end; four blocks a warp
+// are in flight (cp.async into a ring of the warp's own). Shares of the work and the merge of
 // cut items as in prompt.cu.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
 #include "prompt_common.cuh"
+#include "tc_ptx.cuh"
 
 namespace {
 
 constexpr int FW = 8;  // warps of a CTA
 constexpr int FT = FW * 32;
+constexpr int FS = 4;  // blocks that a warp has in flight
 
 struct FewArgs {
     PtArgs a;
@@ -62,54 +64,75 @@ struct Block {
     uint32_t v[4][KW / 2], vs[4];
 };
 
-// page: the block's page (NO_PAGE: no rows); codes of keys from `end` on are zero
+// A raw block in shared memory: 16 keys' codes of K, of V, then their scales. A key's
+// row of V lies in the line of its pair of keys, at a half and a quarter that spread
+// the eight-byte reads of four even (or odd) keys over all banks (D = 128).
 template <int D>
-DDT_DEVINL void load_block(const PtArgs &a, Block<D> &b, int page, int key0, int end, int h, int lane)
+constexpr uint32_t RAW_CODES = 16 * (D / 2);
+template <int D>
+constexpr uint32_t RAW_SCALES = 16 * (D / 16);
+template <int D>
+constexpr uint32_t RAW_BYTES = 2 * (RAW_CODES<D> + RAW_SCALES<D>);
+template <int D>
+DDT_DEVINL uint32_t v_place(int key, int q)  // of 16-byte vector q of the key's codes
 {
-    constexpr int KW = Block<D>::KW;
+    if (D == 128)
+        return (key >> 1) * 128 + (((key & 1) ^ ((key >> 2) & 1)) << 6) + ((q ^ (key & 2)) << 4);
+    return key * 32 + q * 16;
+}
+
+// start the copies of a block into dst; page: the block's (NO_PAGE: no rows); rows of
+// keys from `end` on become zeros
+template <int D>
+DDT_DEVINL void fetch_block(const PtArgs &a, uint32_t dst, int page, int key0, int end, int h, int lane)
+{
+    constexpr int CH = D / 32, RS = 256 / D;  // vectors of a key's codes; keys of a vector of scales
     const bool ok = page_ok(a, page);
     const int64_t row = (((int64_t)(ok ? page : 0) * a.Hkv + h) << a.page_shift) + (key0 & ((1 << a.page_shift) - 1));
-    const int i = lane >> 2, c = lane & 3, n = ok ? end - key0 : 0;  // keys that count
-    const uint8_t *kc = a.codes[0] + row * (D / 2) + i * (D / 2) + c * (D / 8);
-    const uint8_t *ks = a.scales[0] + row * (D / 16) + i * (D / 16) + c * (D / 64);
+    const int n = ok ? end - key0 : 0;  // keys that count
+#pragma unroll
+    for (int x = 0; x < 16 * CH / 32; ++x) {
+        const int idx = x * 32 + lane, key = idx / CH, q = idx % CH;
+        const int64_t at = (key < n ? row * (D / 2) + idx * 16 : 0);
+        cp_async_16(dst + idx * 16, a.codes[0] + at, key < n ? 16u : 0u);
+        cp_async_16(dst + RAW_CODES<D> + v_place<D>(key, q), a.codes[1] + at, key < n ? 16u : 0u);
+    }
+    if (lane < 2 * (16 / RS)) {
+        const int v = lane / (16 / RS), first = lane % (16 / RS) * RS, k = max(0, min(RS, n - first));
+        cp_async_16(dst + 2 * RAW_CODES<D> + v * RAW_SCALES<D> + first * (D / 16),
+                    (v ? a.scales[1] : a.scales[0]) + (k > 0 ? (row + first) * (D / 16) : 0), k * (D / 16));
+    }
+}
+
+template <int D>
+DDT_DEVINL void read_block(const unsigned char *raw, Block<D> &b, int lane)
+{
+    const int i = lane >> 2, c = lane & 3;
+    const unsigned char *vr = raw + RAW_CODES<D>, *ks = vr + RAW_CODES<D>, *vs = ks + RAW_SCALES<D>;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-        const bool in = i + 8 * x < n;
+        const int key = i + 8 * x;
         if constexpr (D == 128) {
-            uint4 w = make_uint4(0u, 0u, 0u, 0u);
-            b.ks[x] = 0;
-            if (in) {
-                w = ldg_stream(kc + x * 8 * (D / 2));
-                b.ks[x] = __ldg(reinterpret_cast<const unsigned short *>(ks + x * 8 * (D / 16)));
-            }
-            b.k[x][0] = w.x, b.k[x][1] = w.y, b.k[x][KW - 2] = w.z, b.k[x][KW - 1] = w.w;
+            const uint4 w = *reinterpret_cast<const uint4 *>(raw + key * 64 + c * 16);
+            b.k[x][0] = w.x, b.k[x][1] = w.y, b.k[x][2] = w.z, b.k[x][3] = w.w;
+            b.ks[x] = *reinterpret_cast<const uint16_t *>(ks + key * 8 + c * 2);
         } else {
-            uint2 w = make_uint2(0u, 0u);
-            b.ks[x] = 0;
-            if (in) {
-                w = __ldg(reinterpret_cast<const uint2 *>(kc + x * 8 * (D / 2)));
-                b.ks[x] = __ldg(ks + x * 8 * (D / 16));
-            }
+            const uint2 w = *reinterpret_cast<const uint2 *>(raw + key * 32 + c * 8);
             b.k[x][0] = w.x, b.k[x][1] = w.y;
+            b.ks[x] = ks[key * 4 + c];
         }
     }
-    const uint8_t *vc = a.codes[1] + row * (D / 2) + i * (D / 16);
-    const uint8_t *vs = a.scales[1] + row * (D / 16) + i * (D / 16) / 8;
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
         const int key = 2 * c + (x & 1) + 8 * (x >> 1);
-        const bool in = key < n;
-        b.vs[x] = 0;
         if constexpr (D == 128) {
-            uint2 w = make_uint2(0u, 0u);
-            if (in)
-                w = __ldg(reinterpret_cast<const uint2 *>(vc + key * (D / 2)));
-            b.v[x][0] = w.x, b.v[x][KW / 2 - 1] = w.y;
+            const uint2 w = *reinterpret_cast<const uint2 *>(vr + v_place<D>(key, i >> 1) + (i & 1) * 8);
+            b.v[x][0] = w.x, b.v[x][1] = w.y;
+            b.vs[x] = vs[key * 8 + i];
         } else {
-            b.v[x][0] = in ? __ldg(reinterpret_cast<const unsigned int *>(vc + key * (D / 2))) : 0u;
+            b.v[x][0] = *reinterpret_cast<const uint32_t *>(vr + key * 32 + i * 4);
+            b.vs[x] = vs[key * 4 + (i >> 1)];
         }
-        if (in)
-            b.vs[x] = __ldg(vs + key * (D / 16));
     }
 }
 
@@ -120,6 +143,8 @@ __global__ void __launch_bounds__(FT, NR == 1 ? 2 : 1) prompt_few_kernel(const F
     extern __shared__ float4 few_smem[];
     float *so = reinterpret_cast<float *>(few_smem);  // [FW][ROWS][D]
     float2 *sml = reinterpret_cast<float2 *>(so + FW * ROWS * D);  // [FW][ROWS]
+    unsigned char *rawp = reinterpret_cast<unsigned char *>(sml + FW * ROWS) + (threadIdx.x >> 5) * FS * RAW_BYTES<D>;
+    const uint32_t raws = (uint32_t)__cvta_generic_to_shared(rawp);
     __shared__ long long s_sums[FW], s_found[3];
     const PtArgs &a = f.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, i = lane >> 2, c = lane & 3;
@@ -130,6 +155,7 @@ __global__ void __launch_bounds__(FT, NR == 1 ? 2 : 1) prompt_few_kernel(const F
             if (!packed_ok(s0, s1, a.T, __ldg(&a.ctx_lens[r]), a.cap))
                 set_status(a.status, DDT_DEV_BAD_LENGTH);
         }
+    pdl_trigger();  // (the merge stages itself; it waits for this grid before it reads)
     find_share(a, tq, gridDim.x, blockIdx.x, s_sums, s_found, tid, FT);
     ShareWalk walk;
     walk.begin(a, s_found, tq, gridDim.x, blockIdx.x);
@@ -144,9 +170,13 @@ __global__ void __launch_bounds__(FT, NR == 1 ? 2 : 1) prompt_few_kernel(const F
         int blk = s.t0 * (PP_TILE / 16) + warp;
         const int32_t *pages = a.block_table + (int64_t)s.r * a.max_pages;
         auto page_of = [&](int b) { return b < bend ? __ldg(pages + ((b * 16) >> a.page_shift)) : NO_PAGE; };
-        Block<D> next;
-        load_block<D>(a, next, page_of(blk), blk * 16, end, s.h, lane);
-        int page = page_of(blk + FW);
+#pragma unroll
+        for (int x = 0; x < FS; ++x) {
+            fetch_block<D>(a, raws + x * RAW_BYTES<D>, page_of(blk + x * FW), (blk + x * FW) * 16,
+                           blk + x * FW < bend ? end : 0, s.h, lane);
+            cp_async_commit();
+        }
+        int page = page_of(blk + FS * FW), slot = 0;
         // ---- Q: row 8 y + i, channels [c D/4, + D/4), divided by a power of two of the
         //      row's largest magnitude, to fp16 in the order of the codes' pairs
         uint32_t qf[NR][2 * KS];
@@ -203,9 +233,16 @@ __global__ void __launch_bounds__(FT, NR == 1 ? 2 : 1) prompt_few_kernel(const F
                     o[y][j][e] = 0.f;
         }
         for (; blk < bend; blk += FW) {
-            const Block<D> b = next;
-            load_block<D>(a, next, page, (blk + FW) * 16, blk + FW < bend ? end : 0, s.h, lane);
-            page = page_of(blk + 2 * FW);
+            cp_async_wait_group<FS - 1>();
+            __syncwarp();
+            Block<D> b;
+            read_block<D>(rawp + slot * RAW_BYTES<D>, b, lane);
+            __syncwarp();
+            const int ahead = blk + FS * FW;
+            fetch_block<D>(a, raws + slot * RAW_BYTES<D>, page, ahead * 16, ahead < bend ? end : 0, s.h, lane);
+            cp_async_commit();
+            page = page_of(ahead + FW);
+            slot = slot + 1 == FS ? 0 : slot + 1;
             // ---- S^T
             float st[NR][4];
 #pragma unroll
@@ -301,6 +338,7 @@ __global__ void __launch_bounds__(FT, NR == 1 ? 2 : 1) prompt_few_kernel(const F
                 }
             }
         }
+        cp_async_wait_all();  // (the last ones copy nothing, but into slots that come into use again)
         // ---- the warps' parts to shared memory: O row by row, (m, l)
 #pragma unroll
         for (int y = 0; y < NR; ++y)
@@ -358,13 +396,18 @@ __global__ void __launch_bounds__(FT, NR == 1 ? 2 : 1) prompt_few_kernel(const F
 }
 
 template <int D, int NR>
-cudaError_t launch_few(const FewArgs &f, int num_sms, cudaStream_t s)
+cudaError_t launch_few(const FewArgs &f, int dev, int num_sms, cudaStream_t s)
 {
-    constexpr int ROWS = 8 * NR, BYTES = FW * ROWS * (D * 4 + 8);
+    constexpr int ROWS = 8 * NR, BYTES = FW * (ROWS * (D * 4 + 8) + FS * RAW_BYTES<D>);
     static_assert(ROWS * 2 * 2 * PR_MAX_CTAS <= 2 * PR_MAX_CTAS * PR_ROWS, "partial slots");
-    cudaError_t e = cudaFuncSetAttribute(prompt_few_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
-    if (e != cudaSuccess)
-        return e;
+    static DeviceFlags ready;
+    cudaError_t e = cudaSuccess;
+    if (!ready.test(dev)) {
+        e = cudaFuncSetAttribute(prompt_few_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
+        if (e != cudaSuccess)
+            return e;
+        ready.set(dev);
+    }
     const int grid = (num_sms < PR_MAX_CTAS ? num_sms : PR_MAX_CTAS) * (NR == 1 ? 2 : 1);
     prompt_few_kernel<D, NR><<<grid, FT, BYTES, s>>>(f);
     e = cudaGetLastError();
@@ -382,6 +425,6 @@ cudaError_t launch_prompt_few(ddt_ctx *c, const PtArgs &a, const uint16_t *q, in
     f.q = q;
     f.q_stride = q_stride;
     if (c->cfg.d == 128)
-        return rows <= 8 ? launch_few<128, 1>(f, c->num_sms, s) : launch_few<128, 2>(f, c->num_sms, s);
-    return rows <= 8 ? launch_few<64, 1>(f, c->num_sms, s) : launch_few<64, 2>(f, c->num_sms, s);
+        return rows <= 8 ? launch_few<128, 1>(f, c->device, c->num_sms, s) : launch_few<128, 2>(f, c->device, c->num_sms, s);
+    return rows <= 8 ? launch_few<64, 1>(f, c->device, c->num_sms, s) : launch_few<64, 2>(f, c->device, c->num_sms, s);
 }

@@ -6,6 +6,7 @@ memory and streams); bf16 tensors may be torch.bfloat16 or int16/uint16
 views of the same bits. There is no fallback: if the library is missing or
 fails to load, loading raises.
 """
+import collections
 import ctypes
 import os
 
@@ -107,32 +108,38 @@ class Kv4Cache:
         self.k_scale, self.v_scale = float(k_scale), float(v_scale)
 
     def check(self, cfg):
-        for n in ("k", "v"):
-            _shaped(getattr(self, n + "_codes"), n + "_codes", (torch.uint8,),
-                    (cfg.num_pages, cfg.Hkv, cfg.page_size, cfg.d // 2))
-            _shaped(getattr(self, n + "_scales"), n + "_scales", (torch.uint8,),
-                    (cfg.num_pages, cfg.Hkv, cfg.page_size, cfg.d // 16))
+        p, h, s, d = cfg.num_pages, cfg.Hkv, cfg.page_size, cfg.d
+        for t, n in ((self.k_codes, "k_codes"), (self.v_codes, "v_codes")):
+            _shaped(t, n, _U8, (p, h, s, d // 2))
+        for t, n in ((self.k_scales, "k_scales"), (self.v_scales, "v_scales")):
+            _shaped(t, n, _U8, (p, h, s, d // 16))
 
+
+# what the packed-sequence calls look at, as plain values (a ctypes field is slow to read)
+Dims = collections.namedtuple("Dims", "R_max Hq Hkv d page_size max_pages_per_req num_pages")
 
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
 _I32 = (torch.int32,)
+_U8 = (torch.uint8,)
 
 
 def _shaped(t, name, dtypes, shape):
-    """Raise unless t has one of the types and the shape (None: any extent)."""
+    """Raise unless t has one of the types and the shape."""
     if t.dtype not in dtypes:
         raise ValueError("%s: expected %s, got %s" % (name, dtypes[0], t.dtype))
-    if t.dim() != len(shape) or any(w is not None and g != w for g, w in zip(t.shape, shape)):
-        raise ValueError("%s: expected shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.shape != shape:
+        raise ValueError("%s: expected shape %s, got %s" % (name, shape, tuple(t.shape)))
 
 
 def _rows(t, name, T, heads, d):
     """The token stride of packed rows [T, heads, d], each row dense."""
     _shaped(t, name, _BF16, (T, heads, d))
-    if t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != d)):
+    if t.is_contiguous():
+        return 0
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
         raise ValueError("%s: expected each token's heads and channels dense" % name)
     # (a single row has no next one)
-    return t.stride(0) if T > 1 else heads * d
+    return t.stride(0) if T > 1 else 0
 
 
 def check_append(cfg, q, k, v, q_start, ctx_lens, block_table, R, q_out, rotary, new_lens):
@@ -268,6 +275,8 @@ class Context:
         _check(lib.ddt_create(ctypes.byref(cfg), ctypes.byref(h)), "ddt_create")
         self._h = h
         self.device = torch.cuda.current_device()
+        self.dims = Dims(cfg.R_max, cfg.Hq, cfg.Hkv, cfg.d, cfg.page_size, cfg.max_pages_per_req,
+                         cfg.num_pages)
         self.K = cfg.K if cfg.K else min(cfg.B, cfg.V)
         self.P = cfg.B + 1
         self.W = (self.P + 31) // 32
@@ -357,40 +366,40 @@ class Context:
                "ddt_schedule_prefix")
 
     # -- packed sequences over the paged cache --------------------------------
-    def _on_device(self, *tensors, dense=True):
-        """Device pointers of tensors on this context's device (None: NULL)."""
-        out = []
-        for t in tensors:
-            if t is not None and (not t.is_cuda or t.device.index != self.device):
-                raise ValueError("expected a tensor on CUDA device %d" % self.device)
-            if t is not None and dense and not t.is_contiguous():
-                raise ValueError("expected a contiguous tensor")
-            out.append(None if t is None else ctypes.c_void_p(t.data_ptr()))
-        return out
+    # (a decoding step makes these calls once a layer: their checks are kept short)
+    def _at(self, t, dense=True):
+        """Device address of a tensor on this context's device (None: NULL)."""
+        if t is None:
+            return None
+        if t.get_device() != self.device:
+            raise ValueError("expected a tensor on CUDA device %d" % self.device)
+        if dense and not t.is_contiguous():
+            raise ValueError("expected a contiguous tensor")
+        return t.data_ptr()
 
     def _own_stream(self, stream):
         """The given stream, or the current one of this context's device."""
-        return _stream(torch.cuda.current_stream(self.device) if stream is None else stream)
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(self.device)
+        return stream.cuda_stream
 
     def _kv4(self, cache):
-        cache.check(self.cfg)
-        ptrs = self._on_device(cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales)
-        return Kv4(*ptrs, cache.k_scale, cache.v_scale)
+        cache.check(self.dims)
+        at = self._at
+        return Kv4(at(cache.k_codes), at(cache.v_codes), at(cache.k_scales), at(cache.v_scales),
+                   cache.k_scale, cache.v_scale)
 
     def _append_args(self, q, k, v, q_start, ctx_lens, block_table, R, q_out, rotary, new_lens):
-        qs, ks, vs = check_append(self.cfg, q, k, v, q_start, ctx_lens, block_table, R, q_out,
+        qs, ks, vs = check_append(self.dims, q, k, v, q_start, ctx_lens, block_table, R, q_out,
                                   rotary, new_lens)
-        a = AppendArgs()
-        a.R, a.T = R, k.shape[0]
-        a.q, a.k, a.v = self._on_device(q, k, v, dense=False)
-        a.q_stride, a.k_stride, a.v_stride = qs, ks, vs
-        a.q_start, a.ctx_lens, a.block_table, a.q_out, a.new_lens = self._on_device(
-            q_start, ctx_lens, block_table, q_out, new_lens)
+        at = self._at
+        table, dim, rows, inter = None, 0, 0, 0
         if rotary is not None:
-            a.cos_sin, = self._on_device(rotary.table)
-            a.rotary_dim, a.max_pos = rotary.dim, rotary.table.shape[0]
-            a.interleaved = int(rotary.interleaved)
-        return a
+            table, dim, rows = at(rotary.table), rotary.dim, rotary.table.shape[0]
+            inter = int(rotary.interleaved)
+        return AppendArgs(R, k.shape[0], at(q, False), at(k, False), at(v, False), qs, ks, vs,
+                          at(q_start), at(ctx_lens), at(block_table), table, dim, rows, inter,
+                          at(q_out), at(new_lens))
 
     def ddt_append_kv(self, q, k, v, q_start, ctx_lens, block_table, R, k_cache, v_cache,
                       q_out=None, rotary=None, new_lens=None, stream=None):
@@ -400,8 +409,8 @@ class Context:
         q_out may be q itself when q is dense. new_lens [R] i32 (optional):
         the lengths after the append; ctx_lens stays as it is."""
         a = self._append_args(q, k, v, q_start, ctx_lens, block_table, R, q_out, rotary, new_lens)
-        _cache_shapes(self.cfg, k_cache, v_cache)
-        _check(_lib.ddt_append_kv(self._h, ctypes.byref(a), *self._on_device(k_cache, v_cache),
+        _cache_shapes(self.dims, k_cache, v_cache)
+        _check(_lib.ddt_append_kv(self._h, ctypes.byref(a), self._at(k_cache), self._at(v_cache),
                                   self._own_stream(stream)), "ddt_append_kv")
 
     def ddt_append_kvq(self, q, k, v, q_start, ctx_lens, block_table, R, cache, q_out=None,
@@ -411,34 +420,32 @@ class Context:
         a = self._append_args(q, k, v, q_start, ctx_lens, block_table, R, q_out, rotary, new_lens)
         for t, n in ((k_held, "k_held"), (v_held, "v_held")):
             if t is not None:
-                _shaped(t, n, _BF16, (k.shape[0], self.cfg.Hkv, self.cfg.d))
+                _shaped(t, n, _BF16, (k.shape[0], self.dims.Hkv, self.dims.d))
         c = self._kv4(cache)
-        _check(_lib.ddt_append_kvq(self._h, ctypes.byref(a), ctypes.byref(c),
-                                   *self._on_device(k_held, v_held), self._own_stream(stream)),
-               "ddt_append_kvq")
+        _check(_lib.ddt_append_kvq(self._h, ctypes.byref(a), ctypes.byref(c), self._at(k_held),
+                                   self._at(v_held), self._own_stream(stream)), "ddt_append_kvq")
 
     def ddt_prompt_attention(self, q, q_start, ctx_lens, block_table, R, k_cache, v_cache, out,
                              stream=None):
         """Causal attention of R requests' packed queries q [T, Hq, d] bf16 over
         the paged cache that holds their keys and values (ctx_lens [R]: the
         lengths before these tokens) into out [T, Hq, d] bf16."""
-        qs = check_prompt(self.cfg, q, q_start, ctx_lens, block_table, R, out)
-        _cache_shapes(self.cfg, k_cache, v_cache)
-        pq, = self._on_device(q, dense=False)
-        ps, pc, pb, po, pk, pv = self._on_device(q_start, ctx_lens, block_table, out, k_cache, v_cache)
-        _check(_lib.ddt_prompt_attention(self._h, pq, qs, ps, pc, R, q.shape[0], pk, pv, pb, po,
-                                         self._own_stream(stream)), "ddt_prompt_attention")
+        qs = check_prompt(self.dims, q, q_start, ctx_lens, block_table, R, out)
+        _cache_shapes(self.dims, k_cache, v_cache)
+        at = self._at
+        _check(_lib.ddt_prompt_attention(self._h, at(q, False), qs, at(q_start), at(ctx_lens), R,
+                                         q.shape[0], at(k_cache), at(v_cache), at(block_table),
+                                         at(out), self._own_stream(stream)), "ddt_prompt_attention")
 
     def ddt_prompt_attention_kvq(self, q, q_start, ctx_lens, block_table, R, cache, out,
                                  stream=None):
         """The same over a Kv4Cache."""
-        qs = check_prompt(self.cfg, q, q_start, ctx_lens, block_table, R, out)
+        qs = check_prompt(self.dims, q, q_start, ctx_lens, block_table, R, out)
         c = self._kv4(cache)
-        pq, = self._on_device(q, dense=False)
-        ps, pc, pb, po = self._on_device(q_start, ctx_lens, block_table, out)
-        _check(_lib.ddt_prompt_attention_kvq(self._h, pq, qs, ps, pc, R, q.shape[0],
-                                             ctypes.byref(c), pb, po, self._own_stream(stream)),
-               "ddt_prompt_attention_kvq")
+        at = self._at
+        _check(_lib.ddt_prompt_attention_kvq(self._h, at(q, False), qs, at(q_start), at(ctx_lens), R,
+                                             q.shape[0], ctypes.byref(c), at(block_table), at(out),
+                                             self._own_stream(stream)), "ddt_prompt_attention_kvq")
 
     def alloc_kv4(self, k_scale=1.0, v_scale=1.0, device="cuda"):
         """An empty (all zero) Kv4Cache of this context's page pool."""
