@@ -11,8 +11,9 @@
 //     and i + 8, channels [c D/4, (c + 1) D/4) -- 16 bytes of codes of a key, whose
 //     pairs go to the products as they come; Q's are laid out alike, once an item;
 //   O^T (channels x 8 rows) += V^T P^T: lane (i, c) holds keys 2c, 2c + 1, 2c + 8,
-//     2c + 9, channels [i D/8, (i + 1) D/8); two keys' values of one channel are
-//     paired by a byte permutation, and P^T is transposed in the warp.
+//     2c + 9, channels [i D/8, (i + 1) D/8); two keys' codes of one channel are
+//     put into one byte, so that they come out as the pair the product takes, and
+//     P^T is transposed in the warp.
 // Eight warps of a CTA take the 16-key blocks of a segment in turn, each with its
 // own running maximum and sum, and meet at the segment's end; four blocks a warp
 // are in flight (cp.async into a ring of the warp's own). Shares of the work and the merge of
@@ -81,28 +82,56 @@ DDT_DEVINL uint32_t v_place(int key, int q)  // of 16-byte vector q of the key's
     return key * 32 + q * 16;
 }
 
-// start the copies of a block into dst; page: the block's (NO_PAGE: no rows); rows of
-// keys from `end` on become zeros
+// Where a lane's copies of a block begin: vectors lane, lane + 32 of the codes (of K
+// and V alike), and one vector of scales for the first lanes.
 template <int D>
-DDT_DEVINL void fetch_block(const PtArgs &a, uint32_t dst, int page, int key0, int end, int h, int lane)
-{
-    constexpr int CH = D / 32, RS = 256 / D;  // vectors of a key's codes; keys of a vector of scales
-    const bool ok = page_ok(a, page);
-    const int64_t row = (((int64_t)(ok ? page : 0) * a.Hkv + h) << a.page_shift) + (key0 & ((1 << a.page_shift) - 1));
-    const int n = ok ? end - key0 : 0;  // keys that count
+struct Copier {
+    static constexpr int CH = D / 32, RS = 256 / D, NS = 16 / RS;  // vectors of a key's codes; keys, vectors of scales
+    const uint8_t *k, *v, *s;  // the pools' bases, moved by the lane's place (s: K's or V's scales)
+    uint32_t vdst[16 * CH / 32], sdst;
+
+    DDT_DEVINL void begin(const PtArgs &a, int lane)
+    {
+        k = a.codes[0] + lane * 16;
+        v = a.codes[1] + lane * 16;
+        const int sv = lane / NS, first = lane % NS * RS;
+        s = (sv ? a.scales[1] : a.scales[0]) + first * (D / 16);
+        sdst = 2 * RAW_CODES<D> + sv * RAW_SCALES<D> + first * (D / 16);
 #pragma unroll
-    for (int x = 0; x < 16 * CH / 32; ++x) {
-        const int idx = x * 32 + lane, key = idx / CH, q = idx % CH;
-        const int64_t at = (key < n ? row * (D / 2) + idx * 16 : 0);
-        cp_async_16(dst + idx * 16, a.codes[0] + at, key < n ? 16u : 0u);
-        cp_async_16(dst + RAW_CODES<D> + v_place<D>(key, q), a.codes[1] + at, key < n ? 16u : 0u);
+        for (int x = 0; x < 16 * CH / 32; ++x)
+            vdst[x] = RAW_CODES<D> + v_place<D>((x * 32 + lane) / CH, (x * 32 + lane) % CH);
     }
-    if (lane < 2 * (16 / RS)) {
-        const int v = lane / (16 / RS), first = lane % (16 / RS) * RS, k = max(0, min(RS, n - first));
-        cp_async_16(dst + 2 * RAW_CODES<D> + v * RAW_SCALES<D> + first * (D / 16),
-                    (v ? a.scales[1] : a.scales[0]) + (k > 0 ? (row + first) * (D / 16) : 0), k * (D / 16));
+
+    // start the copies of a block into dst; page: the block's (NO_PAGE: no rows); rows
+    // of keys from `end` on become zeros
+    DDT_DEVINL void fetch(const PtArgs &a, uint32_t dst, int page, int key0, int end, int h, int lane) const
+    {
+        const bool ok = page_ok(a, page);
+        const int64_t row = (((int64_t)(ok ? page : 0) * a.Hkv + h) << a.page_shift) + (key0 & ((1 << a.page_shift) - 1));
+        const int n = ok ? end - key0 : 0;  // keys that count
+        const int64_t at = row * (D / 2);
+        if (n >= 16) {
+#pragma unroll
+            for (int x = 0; x < 16 * CH / 32; ++x) {
+                cp_async_16(dst + lane * 16 + x * 512, k + at + x * 512, 16);
+                cp_async_16(dst + vdst[x], v + at + x * 512, 16);
+            }
+            if (lane < 2 * NS)
+                cp_async_16(dst + sdst, s + (at >> 3), 16);
+            return;
+        }
+#pragma unroll
+        for (int x = 0; x < 16 * CH / 32; ++x) {
+            const bool in = (x * 32 + lane) / CH < n;
+            cp_async_16(dst + lane * 16 + x * 512, k + (in ? at + x * 512 : 0), in ? 16u : 0u);
+            cp_async_16(dst + vdst[x], v + (in ? at + x * 512 : 0), in ? 16u : 0u);
+        }
+        if (lane < 2 * NS) {
+            const int c = max(0, min(RS, n - lane % NS * RS));
+            cp_async_16(dst + sdst, s + (c > 0 ? at >> 3 : 0), c * (D / 16));
+        }
     }
-}
+};
 
 template <int D>
 DDT_DEVINL void read_block(const unsigned char *raw, Block<D> &b, int lane)
@@ -157,6 +186,8 @@ __global__ void __launch_bounds__(FT, NR == 1 ? 2 : 1) prompt_few_kernel(const F
         }
     pdl_trigger();  // (the merge stages itself; it waits for this grid before it reads)
     find_share(a, tq, gridDim.x, blockIdx.x, s_sums, s_found, tid, FT);
+    Copier<D> copier;
+    copier.begin(a, lane);
     ShareWalk walk;
     walk.begin(a, s_found, tq, gridDim.x, blockIdx.x);
     for (;;) {
@@ -172,8 +203,8 @@ __global__ void __launch_bounds__(FT, NR == 1 ? 2 : 1) prompt_few_kernel(const F
         auto page_of = [&](int b) { return b < bend ? __ldg(pages + ((b * 16) >> a.page_shift)) : NO_PAGE; };
 #pragma unroll
         for (int x = 0; x < FS; ++x) {
-            fetch_block<D>(a, raws + x * RAW_BYTES<D>, page_of(blk + x * FW), (blk + x * FW) * 16,
-                           blk + x * FW < bend ? end : 0, s.h, lane);
+            copier.fetch(a, raws + x * RAW_BYTES<D>, page_of(blk + x * FW), (blk + x * FW) * 16,
+                         blk + x * FW < bend ? end : 0, s.h, lane);
             cp_async_commit();
         }
         int page = page_of(blk + FS * FW), slot = 0;
@@ -181,6 +212,7 @@ __global__ void __launch_bounds__(FT, NR == 1 ? 2 : 1) prompt_few_kernel(const F
         //      row's largest magnitude, to fp16 in the order of the codes' pairs
         uint32_t qf[NR][2 * KS];
         float sc[NR][2], m[NR][2], l[NR][2], o[NR][KS][4];
+        float top[NR][2], off[NR][2];  // the score that moves the reference; what is added in the exponent
         int pos[NR][2];
 #pragma unroll
         for (int y = 0; y < NR; ++y) {
@@ -222,7 +254,8 @@ __global__ void __launch_bounds__(FT, NR == 1 ? 2 : 1) prompt_few_kernel(const F
 #pragma unroll
             for (int e = 0; e < 2; ++e) {  // this lane's columns of S^T: rows 8 y + 2 c, + 1
                 sc[y][e] = __shfl_sync(0xFFFFFFFFu, up, (2 * c + e) * 4);
-                m[y][e] = DDT_NEG_INF;
+                m[y][e] = top[y][e] = DDT_NEG_INF;
+                off[y][e] = PBIAS;
                 l[y][e] = 0.f;
                 pos[y][e] = s.pos0 + min((8 * y + 2 * c + e) >> a.g_shift, s.ntok - 1);
             }
@@ -239,15 +272,17 @@ __global__ void __launch_bounds__(FT, NR == 1 ? 2 : 1) prompt_few_kernel(const F
             read_block<D>(rawp + slot * RAW_BYTES<D>, b, lane);
             __syncwarp();
             const int ahead = blk + FS * FW;
-            fetch_block<D>(a, raws + slot * RAW_BYTES<D>, page, ahead * 16, ahead < bend ? end : 0, s.h, lane);
+            copier.fetch(a, raws + slot * RAW_BYTES<D>, page, ahead * 16, ahead < bend ? end : 0, s.h, lane);
             cp_async_commit();
             page = page_of(ahead + FW);
             slot = slot + 1 == FS ? 0 : slot + 1;
             // ---- S^T
-            float st[NR][4];
+            float st[NR][4], su[NR][4];  // (two sums: half the products wait for one another)
 #pragma unroll
             for (int y = 0; y < NR; ++y)
-                st[y][0] = st[y][1] = st[y][2] = st[y][3] = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    st[y][e] = su[y][e] = 0.f;
             uint32_t s2[2];
 #pragma unroll
             for (int x = 0; x < 2; ++x)
@@ -261,9 +296,14 @@ __global__ void __launch_bounds__(FT, NR == 1 ? 2 : 1) prompt_few_kernel(const F
 #pragma unroll
                 for (int y = 0; y < NR; ++y) {
                     mma_f16(st[y], x0.x, x1.x, x0.y, x1.y, qf[y][4 * w], qf[y][4 * w + 1]);
-                    mma_f16(st[y], x0.z, x1.z, x0.w, x1.w, qf[y][4 * w + 2], qf[y][4 * w + 3]);
+                    mma_f16(su[y], x0.z, x1.z, x0.w, x1.w, qf[y][4 * w + 2], qf[y][4 * w + 3]);
                 }
             }
+#pragma unroll
+            for (int y = 0; y < NR; ++y)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    st[y][e] += su[y][e];
             // ---- softmax: keys key0 + i and + 8, rows 2 c and 2 c + 1
             const int key0 = blk * 16;
             if (key0 + 15 > s.pos0) {
@@ -278,10 +318,8 @@ __global__ void __launch_bounds__(FT, NR == 1 ? 2 : 1) prompt_few_kernel(const F
 #pragma unroll
             for (int y = 0; y < NR; ++y)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    st[y][e] *= sc[y][e & 1];
-                    grow |= st[y][e] > m[y][e & 1] + TAU;
-                }
+                for (int e = 0; e < 2; ++e)
+                    grow |= fmaxf(st[y][e], st[y][e + 2]) > top[y][e];
             if (__any_sync(0xFFFFFFFFu, grow)) {
 #pragma unroll
                 for (int y = 0; y < NR; ++y)
@@ -291,9 +329,12 @@ __global__ void __launch_bounds__(FT, NR == 1 ? 2 : 1) prompt_few_kernel(const F
 #pragma unroll
                         for (int x = 4; x <= 16; x <<= 1)
                             mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, x));
+                        mx *= sc[y][e];
                         if (mx > m[y][e]) {
                             const float alpha = ex2(m[y][e] - mx);
                             m[y][e] = mx;
+                            off[y][e] = PBIAS - mx;
+                            top[y][e] = (mx + TAU) / sc[y][e];
                             l[y][e] *= alpha;
 #pragma unroll
                             for (int j = 0; j < KS; ++j) {
@@ -309,33 +350,35 @@ __global__ void __launch_bounds__(FT, NR == 1 ? 2 : 1) prompt_few_kernel(const F
                 float p[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    p[e] = ex2(st[y][e] + (PBIAS - (m[y][e & 1] == DDT_NEG_INF ? 0.f : m[y][e & 1])));
+                    p[e] = ex2(fmaf(st[y][e], sc[y][e & 1], off[y][e & 1]));
                     l[y][e & 1] += p[e];
                 }
                 pb[y][0] = transpose8(pack_f16x2(p[0], p[1]));
                 pb[y][1] = transpose8(pack_f16x2(p[2], p[3]));
             }
             // ---- O^T
-            uint32_t vsc[4];
+            // keys 2c, 2c + 1 (and + 8) pair up before they are converted: a byte takes one
+            // channel's code of either key
+            uint32_t vsc[2];
 #pragma unroll
-            for (int x = 0; x < 4; ++x)
-                vsc[x] = scales2(b.vs[x] * 0x0101u);
+            for (int x = 0; x < 2; ++x)
+                vsc[x] = scales2(b.vs[2 * x + 1] * 256u + b.vs[2 * x]);
 #pragma unroll
             for (int w = 0; w < KW / 2; ++w) {
-                uint4 x[4];
+                uint4 lo[2], hi[2];  // of either pair of keys: channels {0, 4, 1, 5}, and those + 2
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    x[e] = values8(b.v[e][w], vsc[e]);
-                const uint32_t u[4][4] = {{x[0].x, x[0].y, x[0].z, x[0].w}, {x[1].x, x[1].y, x[1].z, x[1].w},
-                                          {x[2].x, x[2].y, x[2].z, x[2].w}, {x[3].x, x[3].y, x[3].z, x[3].w}};
+                for (int x = 0; x < 2; ++x) {
+                    const uint32_t ka = b.v[2 * x][w], kb = b.v[2 * x + 1][w], mask = 0x0F0F0F0Fu;
+                    lo[x] = values8((ka & mask) | ((kb * 16u) & ~mask), vsc[x]);
+                    hi[x] = values8(((ka >> 4) & mask) | (kb & ~mask), vsc[x]);
+                }
+                const uint32_t l0[4] = {lo[0].x, lo[0].y, lo[0].z, lo[0].w}, h0[4] = {hi[0].x, hi[0].y, hi[0].z, hi[0].w};
+                const uint32_t l1[4] = {lo[1].x, lo[1].y, lo[1].z, lo[1].w}, h1[4] = {hi[1].x, hi[1].y, hi[1].z, hi[1].w};
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint32_t a0 = __byte_perm(u[0][q], u[1][q], 0x5410), a1 = __byte_perm(u[0][q], u[1][q], 0x7632);
-                    const uint32_t a2 = __byte_perm(u[2][q], u[3][q], 0x5410), a3 = __byte_perm(u[2][q], u[3][q], 0x7632);
+                for (int q = 0; q < 4; ++q)
 #pragma unroll
                     for (int y = 0; y < NR; ++y)
-                        mma_f16(o[y][4 * w + q], a0, a1, a2, a3, pb[y][0], pb[y][1]);
-                }
+                        mma_f16(o[y][4 * w + q], l0[q], h0[q], l1[q], h1[q], pb[y][0], pb[y][1]);
             }
         }
         cp_async_wait_all();  // (the last ones copy nothing, but into slots that come into use again)
