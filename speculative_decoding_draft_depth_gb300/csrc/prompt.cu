@@ -31,6 +31,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "ddt_device.cuh"
 #include "ddt_internal.h"
 #include "prompt_common.cuh"
@@ -93,7 +95,9 @@ constexpr uint32_t B_QFULL = 0, B_QEMPTY = 8, B_KFULL = 16, B_KEMPTY = 32, B_VFU
                    B_ML = 592,        // [128] float2: B's (m, l); before the roles start, the scan's sums
                    B_ROWSC = 1616;    // 4 bits: [2][256] floats: the row's factor, by item parity
 template <bool KV4>
-constexpr uint32_t B_END = KV4 ? B_ROWSC + 2048 : B_ROWSC;
+constexpr uint32_t B_TURN = B_ROWSC + (KV4 ? 2048 : 0);  // int: a group's issuer has its turn
+template <bool KV4>
+constexpr uint32_t B_END = B_TURN<KV4> + 8;
 template <bool KV4>
 constexpr uint32_t SM_ALLOC = SM_BAR<KV4> + B_END<KV4> + 1024;
 static_assert(SM_ALLOC<false> <= 232448 && SM_ALLOC<true> <= 232448, "shared memory of one CTA");
@@ -347,6 +351,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         mbar_init(bar + B_FINAL + 8, 1);
         mbar_init(bar + B_QREADY, NDQ);
         *abort_flag = 0;
+        *reinterpret_cast<volatile int *>(sgen + SM_BAR<KV4> + B_TURN<KV4>) = 0;
         fence_mbar_init();
     }
     if (warp == W_MMA) {
@@ -515,6 +520,19 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             // (after a wait that gave up, what the body still issues reads and writes
             // this CTA's own memory; the loop then ends)
             auto need = [&](uint32_t b, uint32_t parity) { ok &= wait_bar(b, parity, abort_flag, a.status); };
+            // 4 bits: one group's P V and next S go to the tensor cores together, or the
+            // groups' softmax fall into step and the tensor cores idle meanwhile (chunks of
+            // 1500..2048 tokens: 1030 us, so 900 us; the bf16 cache: 1376 and 1401 us, no turns)
+            volatile int *turn = reinterpret_cast<volatile int *>(sgen + SM_BAR<KV4> + B_TURN<KV4>);
+            auto turn_begin = [&]() {
+                const long long t0 = clock64();
+                while (ok && atomicCAS_block(const_cast<int *>(turn), 0, 1) != 0)
+                    if (*abort_flag || clock64() - t0 > WAIT_LIMIT) {
+                        *abort_flag = 1;
+                        atomicOr(a.status, DDT_DEV_TIMEOUT);
+                        ok = false;
+                    }
+            };
             for (int k = 0; ok; ++k) {
                 const int slot = k & (NRING - 1);
                 need(bar + B_RFULL + 8 * slot, (k / NRING) & 1);
@@ -543,6 +561,13 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         const uint32_t more = j > 1 ? 1u : 0u;
                         need(bar + B_PFULL + 8 * g, pph);
                         need(bar + B_VFULL + 8 * vs, (vbits >> vs) & 1);
+                        if (KV4 && !s.split) {
+                            // (all that another role has to bring is there before a turn
+                            // begins, so nobody waits for the one whose turn it is)
+                            if (j < steps)
+                                need(bar + B_KFULL + 8 * ks, kph);
+                            turn_begin();
+                        }
                         tc_fence_after();
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
@@ -559,8 +584,11 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         vbits ^= 1u << vs;
                         if (!s.split && ++vs == NV<KV4>)
                             vs = 0;
-                        if (j == steps)
+                        if (j == steps) {
                             mma_commit(bar + B_OFULL + 8 * g);
+                            if (KV4 && !s.split)
+                                *turn = 0;
+                        }
                     }
                     if (j < steps) {
                         const uint64_t kk = dK + (uint64_t)(ks * (32768u >> 4));
@@ -572,6 +600,8 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                             mma_bf16(sp, q + off, kk + off, IDESC_QK<KV4>, i > 0 ? 1u : 0u);
                         }
                         mma_commit(bar + B_SFULL + 8 * g);
+                        if (KV4 && !s.split && j > 0)
+                            *turn = 0;
                         mma_commit(bar + B_KEMPTY + 8 * ks);
                         if (s.split)
                             mbar_arrive(bar + B_KEMPTY + 8 * ks);
@@ -781,9 +811,9 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     if (lane == 0)
                         mbar_arrive(bar + b + 8 * g);
                 };
-                auto exps = [&](const uint32_t *x, uint32_t *pw) {  // 32 scores to 16 pairs
+                auto exps = [&](auto pairs, const uint32_t *x, uint32_t *pw) {  // scores to pairs of P
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
+                    for (int e = 0; e < decltype(pairs)::value; ++e) {
                         float x0, x1;
                         f2unpack(f2fma(f2pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sc2, nm2), x0, x1);
                         x0 = ex2(x0);
@@ -799,8 +829,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         uint32_t pw[32];
-                        exps(sv + 64 * c, pw);
-                        exps(sv + 64 * c + 32, pw + 16);
+                        exps(std::integral_constant<int, 32>(), sv + 64 * c, pw);
                         tmem_st32(s_addr + 32u * c, pw);
                         publish(c == 0 ? B_PFULL : B_PHALF);
                     }
@@ -819,7 +848,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                                         x[e] = __float_as_uint(DDT_NEG_INF);
                             }
                         }
-                        exps(x, pw);
+                        exps(std::integral_constant<int, 16>(), x, pw);
                         tmem_st16(s_addr + 16u * c, pw);
                         if (c & 1)
                             publish(c == 1 ? B_PFULL : B_PHALF);
