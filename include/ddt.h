@@ -475,8 +475,8 @@ typedef struct ddt_kv4 {
 
 /* The same append into a cache held in 4 bits: for each block, with g the
  * cache's k_scale or v_scale, scale = e4m3(min(amax * (1 / (6 g)), 448)) and
- * each channel's code the nearest magnitude of |x| / (scale g), ties to the
- * even code, 6 where it is larger. A block with a NaN gets a NaN scale and so
+ * each channel's code the magnitude nearest to the quotient |x| / (scale g) in
+ * fp32, ties to the even code, 6 where it is larger. A block with a NaN gets a NaN scale and so
  * reads as NaN. k_held, v_held ([T, Hkv, d] bf16, dense, both or neither NULL):
  * the values that the cache now holds for the new tokens. */
 ddt_status ddt_append_kvq(ddt_ctx *ctx, const ddt_append_args *args, const ddt_kv4 *cache,

@@ -6,6 +6,13 @@
 // thread: for paired halves (j, j + rd/2) the two 8-channel vectors that turn
 // into each other, otherwise 16 neighbouring channels. So every thread reads
 // and writes 2 x 16 bytes, holds both members of its pairs, and q_out may be q.
+//
+// Bound by memory: 24083 ragged tokens of 32/8 heads of 128 (593 MB with the angles)
+// take 98.5 us, 6.0 TB/s. Five CTAs of 256 threads an SM (48 registers) hide the
+// loads; four take 106 us, six 101, and a thread that keeps its piece over four
+// tokens, for more loads in flight, 115. Into 4 bits (16/16 heads of 64, 324 MB): 65
+// us, 5.0 TB/s, where the codes' arithmetic (three multiply-adds a channel for the
+// exact quotient, a conversion for two) and short stores cost the rest.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -16,7 +23,7 @@
 namespace {
 
 constexpr int AP_THREADS = 256;
-constexpr int AP_TOKENS = 4;  // tokens of one CTA
+constexpr int AP_TOKENS = 4;  // tokens of one CTA, at most
 
 struct ApArgs {
     ddt_append_args a;
@@ -27,6 +34,7 @@ struct ApArgs {
     int Hq, Hkv, page_shift, max_pages, cap;  // Hq: 0 when there are no queries
     int64_t num_pages;
     float k_inv6, v_inv6;  // 1 / (6 g)
+    int tokens;            // of a CTA
 };
 
 // x1' = x1 cos - x2 sin, x2' = x2 cos + x1 sin, every product and sum rounded
@@ -68,22 +76,43 @@ DDT_DEVINL float from_e4m3(uint32_t b)
     return f;
 }
 
-// nearest e2m1 code of |x| in units of s: the seven midpoints t s, which a
-// float holds exactly (s has four significant bits, t at most three; g = 1)
-DDT_DEVINL uint32_t to_e2m1(float x, float s)
+// two fp32 to a byte of e2m1 codes, to nearest even, at most 6 in magnitude
+DDT_DEVINL uint32_t to_e2m1x2(float lo, float hi)
 {
-    const float a = fabsf(x);
-    uint32_t m = (a > s * 0.25f) + (a >= s * 0.75f) + (a > s * 1.25f) + (a >= s * 1.75f) +
-                 (a > s * 2.5f) + (a >= s * 3.5f) + (a > s * 5.0f);
-    if (!(s > 0.f))
-        m = 0;
-    return m | ((__float_as_uint(x) >> 28) & 8u);
+    uint32_t r;
+    asm("{\n .reg .b8 b;\n cvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n cvt.u32.u8 %0, b;\n}\n" : "=r"(r) : "f"(lo), "f"(hi));
+    return r;
 }
-DDT_DEVINL float from_e2m1(uint32_t c)
+// and back: a byte's two values
+DDT_DEVINL void from_e2m1x2(uint32_t b, float &lo, float &hi)
 {
-    const uint32_t m = c & 7u;
-    const float f = m < 2 ? 0.5f * (float)m : __uint_as_float(((126u + (m >> 1)) << 23) | ((m & 1u) << 22));
-    return (c & 8u) ? -f : f;
+    uint32_t h2;
+    asm("{\n .reg .b8 b;\n cvt.u8.u32 b, %1;\n cvt.rn.f16x2.e2m1x2 %0, b;\n}\n" : "=r"(h2) : "r"(b));
+    asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.f32.f16 %0, l;\n cvt.f32.f16 %1, h;\n}\n"
+        : "=f"(lo), "=f"(hi)
+        : "r"(h2));
+}
+
+// A block's scale and what its codes need. With q = RN(x / s) the nearest code of q
+// (ties to even) is the nearest code of x / s for g = 1: a midpoint t and s have at
+// most three and four significant bits, so t s is an fp32 number, and an x next to it
+// is at least as far from it, in units of x / s, as half a step of q at t. q comes from
+// the correctly rounded reciprocal y by one residual, q0 + (x - q0 s) y with
+// q0 = RN(x y), which is RN(x / s) (Markstein).
+struct Scale {
+    uint32_t bits;  // e4m3
+    float s, y;     // scale * g; 1 / s
+    bool plain;     // neither zero, NaN nor saturated
+};
+DDT_DEVINL Scale make_scale(float amax, float inv6, float g)
+{
+    Scale r;
+    const float raw = __fmul_rn(amax, inv6);
+    r.bits = to_e4m3(min_nan(raw, 448.f));
+    r.s = __fmul_rn(from_e4m3(r.bits), g);
+    r.y = __frcp_rn(r.s);
+    r.plain = r.s > 0.f && raw <= 448.f;
+    return r;
 }
 
 DDT_DEVINL void unpack8(const uint4 &w, float *f)
@@ -96,32 +125,45 @@ DDT_DEVINL uint4 pack8(const float *f)
     return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
                       pack_bf16x2(f[6], f[7]));
 }
-// the codes of 8 neighbouring channels: even ones in the low half's nibbles,
-// odd ones in the high half's
-DDT_DEVINL uint32_t codes8(const float *f, float s)
+// the codes of 8 neighbouring channels: bytes of channels (0, 2), (4, 6), (1, 3), (5, 7)
+DDT_DEVINL uint32_t codes8(const float *f, const Scale &c)
 {
-    uint32_t w = 0;
+    float q[8];
+    if (c.plain) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        w |= to_e2m1(f[i], s) << ((i >> 1) * 4 + (i & 1) * 16);
-    return w;
+        for (int i = 0; i < 8; ++i) {
+            const float q0 = __fmul_rn(f[i], c.y);
+            q[i] = __fmaf_rn(__fmaf_rn(-q0, c.s, f[i]), c.y, q0);
+        }
+    } else {
+        // zero or NaN scale: zeros with their signs; saturated: the quotient may be
+        // beyond fp32
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            q[i] = c.s > 0.f ? __fdiv_rn(f[i], c.s) : copysignf(0.f, f[i]);
+    }
+    return to_e2m1x2(q[0], q[2]) | to_e2m1x2(q[4], q[6]) << 8 | to_e2m1x2(q[1], q[3]) << 16 | to_e2m1x2(q[5], q[7]) << 24;
 }
 DDT_DEVINL void held8(uint32_t w, float s, float *f)
 {
+    from_e2m1x2(w & 255u, f[0], f[2]);
+    from_e2m1x2((w >> 8) & 255u, f[4], f[6]);
+    from_e2m1x2((w >> 16) & 255u, f[1], f[3]);
+    from_e2m1x2(w >> 24, f[5], f[7]);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-        f[i] = from_e2m1((w >> ((i >> 1) * 4 + (i & 1) * 16)) & 15u) * s;
+        f[i] = __fmul_rn(f[i], s);
 }
 
 template <int D, bool KV4>
-__global__ void __launch_bounds__(AP_THREADS) append_kernel(const ApArgs p)
+__global__ void __launch_bounds__(AP_THREADS, 5) append_kernel(const ApArgs p)
 {
     constexpr int PIECES = D / 16;  // of a head
     __shared__ int s_r[AP_TOKENS], s_pos[AP_TOKENS];
     __shared__ int64_t s_row[AP_TOKENS];  // the token's row of the pool, -1: no slot
     const ddt_append_args &a = p.a;
-    const int tid = threadIdx.x, t0 = blockIdx.x * AP_TOKENS;
-    if (tid < AP_TOKENS)
+    const int tid = threadIdx.x, t0 = blockIdx.x * p.tokens;
+    if (tid < p.tokens)
         s_r[tid] = -1;
     __syncthreads();
     // every thread looks at some of the requests: one round of independent
@@ -137,13 +179,13 @@ __global__ void __launch_bounds__(AP_THREADS) append_kernel(const ApArgs p)
                 a.new_lens[r] = ok ? ctx + (q1 - q0) : ctx;
         }
         if (ok)
-            for (int t = max(q0, t0); t < min(q1, t0 + AP_TOKENS); ++t) {
+            for (int t = max(q0, t0); t < min(q1, t0 + p.tokens); ++t) {
                 s_r[t - t0] = r;
                 s_pos[t - t0] = ctx + (t - q0);
             }
     }
     __syncthreads();
-    if (tid < AP_TOKENS && s_r[tid] >= 0) {
+    if (tid < p.tokens && s_r[tid] >= 0) {
         const int pos = s_pos[tid];
         const int pg = __ldg(&a.block_table[(int64_t)s_r[tid] * p.max_pages + (pos >> p.page_shift)]);
         const bool ok = pg >= 0 && pg < p.num_pages;
@@ -155,28 +197,27 @@ __global__ void __launch_bounds__(AP_THREADS) append_kernel(const ApArgs p)
     }
     __syncthreads();
 
-    const int heads = p.Hq + 2 * p.Hkv, per_token = heads * PIECES;
-    const int n = min(AP_TOKENS, a.T - t0) * per_token;
-    const int half = a.rotary_dim / 2;
+    const int per_token = (p.Hq + 2 * p.Hkv) * PIECES, half = a.rotary_dim / 2;
+    const int n = min(p.tokens, a.T - t0) * per_token;
     // the last round is padded to whole warps: lanes exchange block maxima
     for (int e0 = 0; e0 < n; e0 += AP_THREADS) {
-        const int e = e0 + tid;
-        const int tk = min(e / per_token, AP_TOKENS - 1);
-        const int h = (e - tk * per_token) / PIECES, piece = e % PIECES;
-        const int t = t0 + tk;
-        const bool live = e < n && s_r[tk] >= 0;
+        const int e = min(e0 + tid, n - 1);
+        static_assert(AP_TOKENS == 4, "the token by comparison");
+        const int tk = (e >= per_token) + (e >= 2 * per_token) + (e >= 3 * per_token);
+        const int h = (e - tk * per_token) / PIECES, piece = e % PIECES;  // (whole heads: pieces stay aligned)
+        const bool live = e0 + tid < n && s_r[tk] >= 0;
         const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hkv;
         const int hk = is_q ? h : (h - p.Hq) - (is_k ? 0 : p.Hkv);
-        const bool turned = !(!is_q && !is_k) && piece * 16 < a.rotary_dim;
+        const bool turned = (is_q || is_k) && piece * 16 < a.rotary_dim;
         const bool halves = turned && !a.interleaved;
         const int o0 = halves ? piece * 8 : piece * 16, o1 = halves ? half + piece * 8 : piece * 16 + 8;
         float x[16];
         if (live) {
-            const uint16_t *src = is_q ? a.q + (int64_t)t * a.q_stride
-                                       : is_k ? a.k + (int64_t)t * a.k_stride : a.v + (int64_t)t * a.v_stride;
-            src += (int64_t)hk * D;
-            unpack8(*reinterpret_cast<const uint4 *>(src + o0), x);
-            unpack8(*reinterpret_cast<const uint4 *>(src + o1), x + 8);
+            const uint16_t *src = is_q ? a.q + (t0 + tk) * a.q_stride
+                                       : is_k ? a.k + (t0 + tk) * a.k_stride : a.v + (t0 + tk) * a.v_stride;
+            src += hk * D;
+            unpack8(__ldcs(reinterpret_cast<const uint4 *>(src + o0)), x);
+            unpack8(__ldcs(reinterpret_cast<const uint4 *>(src + o1)), x + 8);
         } else {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
@@ -199,56 +240,58 @@ __global__ void __launch_bounds__(AP_THREADS) append_kernel(const ApArgs p)
                     turn(x[2 * i], x[2 * i + 1], c[i], s[i]);
             }
         }
-        if (is_q || !KV4) {
-            if (live) {
-                uint16_t *dst = nullptr;
-                if (is_q)
-                    dst = a.q_out + ((int64_t)t * p.Hq + h) * D;
-                else if (s_row[tk] >= 0)
-                    dst = (is_k ? p.k_cache : p.v_cache) + (s_row[tk] * p.Hkv + hk) * D;
-                if (dst) {
-                    *reinterpret_cast<uint4 *>(dst + o0) = pack8(x);
-                    *reinterpret_cast<uint4 *>(dst + o1) = pack8(x + 8);
-                }
+        if ((is_q || !KV4) && live) {
+            uint16_t *dst = nullptr;
+            if (is_q)
+                dst = a.q_out + ((int64_t)(t0 + tk) * p.Hq + h) * D;
+            else if (s_row[tk] >= 0)
+                dst = (is_k ? p.k_cache : p.v_cache) + (s_row[tk] * p.Hkv + hk) * D;
+            if (dst) {
+                *reinterpret_cast<uint4 *>(dst + o0) = pack8(x);
+                *reinterpret_cast<uint4 *>(dst + o1) = pack8(x + 8);
             }
         }
         if (KV4) {
+            if (__all_sync(0xFFFFFFFFu, is_q))
+                continue;
             float m0 = 0.f, m1 = 0.f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 m0 = max_nan(m0, fabsf(x[i]));
                 m1 = max_nan(m1, fabsf(x[8 + i]));
             }
-            // a block's other 8 channels: the neighbour's vector when halves pair
-            // up (pieces 2i and 2i + 1 sit in lanes 2i and 2i + 1), else this
-            // thread's second one
+            // a block's other 8 channels: the neighbour's vector when halves pair up
+            // (pieces 2i and 2i + 1 sit in lanes 2i and 2i + 1), else this thread's
+            // second one
             const float u0 = __shfl_xor_sync(0xFFFFFFFFu, m0, 1), u1 = __shfl_xor_sync(0xFFFFFFFFu, m1, 1);
             const float b0 = max_nan(m0, halves ? u0 : m1), b1 = max_nan(m1, halves ? u1 : m0);
             if (live && !is_q) {
                 const float g = is_k ? p.kv4.k_scale : p.kv4.v_scale, inv6 = is_k ? p.k_inv6 : p.v_inv6;
-                const uint32_t e0b = to_e4m3(min_nan(__fmul_rn(b0, inv6), 448.f));
-                const uint32_t e1b = to_e4m3(min_nan(__fmul_rn(b1, inv6), 448.f));
-                const float s0 = __fmul_rn(from_e4m3(e0b), g), s1 = __fmul_rn(from_e4m3(e1b), g);
+                const Scale s0 = make_scale(b0, inv6, g);
+                const Scale s1 = halves ? make_scale(b1, inv6, g) : s0;
                 const uint32_t w0 = codes8(x, s0), w1 = codes8(x + 8, s1);
                 if (s_row[tk] >= 0) {
                     const int64_t row = s_row[tk] + ((int64_t)hk << p.page_shift);
                     uint8_t *cd = (is_k ? p.kv4.k_codes : p.kv4.v_codes) + row * (D / 2);
                     uint8_t *sc = (is_k ? p.kv4.k_scales : p.kv4.v_scales) + row * (D / 16);
-                    *reinterpret_cast<uint32_t *>(cd + o0 / 2) = w0;
-                    *reinterpret_cast<uint32_t *>(cd + o1 / 2) = w1;
                     if (!halves) {
-                        sc[piece] = (uint8_t)e0b;
-                    } else if ((piece & 1) == 0) {
-                        sc[o0 / 16] = (uint8_t)e0b;
-                        sc[o1 / 16] = (uint8_t)e1b;
+                        *reinterpret_cast<uint2 *>(cd + o0 / 2) = make_uint2(w0, w1);
+                        sc[piece] = (uint8_t)s0.bits;
+                    } else {
+                        *reinterpret_cast<uint32_t *>(cd + o0 / 2) = w0;
+                        *reinterpret_cast<uint32_t *>(cd + o1 / 2) = w1;
+                        if ((piece & 1) == 0) {
+                            sc[o0 / 16] = (uint8_t)s0.bits;
+                            sc[o1 / 16] = (uint8_t)s1.bits;
+                        }
                     }
                 }
                 if (p.k_held) {
-                    uint16_t *hd = (is_k ? p.k_held : p.v_held) + ((int64_t)t * p.Hkv + hk) * D;
+                    uint16_t *hd = (is_k ? p.k_held : p.v_held) + ((int64_t)(t0 + tk) * p.Hkv + hk) * D;
                     float y[8];
-                    held8(w0, s0, y);
+                    held8(w0, s0.s, y);
                     *reinterpret_cast<uint4 *>(hd + o0) = pack8(y);
-                    held8(w1, s1, y);
+                    held8(w1, s1.s, y);
                     *reinterpret_cast<uint4 *>(hd + o1) = pack8(y);
                 }
             }
@@ -285,7 +328,12 @@ cudaError_t launch_append(const ddt_ctx *c, const ddt_append_args &a, uint16_t *
         p.cap = a.max_pos;
     p.num_pages = cfg.num_pages;
     // (T = 0 still writes new_lens)
-    const int grid = a.T > 0 ? (a.T - 1) / AP_TOKENS + 1 : 1;
+    // Tokens of a CTA: each CTA first finds its requests and pages, which takes longer
+    // than one token's pieces; few tokens want all SMs all the same. Measured (32/8
+    // heads of 128, bf16; 1, 2, 4 tokens a CTA): 256 tokens 3.6, 4.0, 5.9 us; 1024
+    // 7.4, 6.5, 7.9; 4096 22.3, 18.3, 19.0; 8192 45.1, 38.4, 37.0.
+    p.tokens = a.T >= 40 * c->num_sms ? AP_TOKENS : a.T >= 3 * c->num_sms ? 2 : 1;
+    const int grid = a.T > 0 ? (a.T - 1) / p.tokens + 1 : 1;
     if (kv4) {
         if (cfg.d == 128)
             append_kernel<128, true><<<grid, AP_THREADS, 0, s>>>(p);

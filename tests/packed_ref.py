@@ -199,11 +199,9 @@ def quantise(x, g):
     inv6 = np.float32(1) / (np.float32(6) * g)
     sc = e4m3(np.minimum(amax * inv6, np.float32(448)))
     s = (e4m3_value(sc) * g)[..., None]
-    a = np.abs(b)
-    with np.errstate(invalid="ignore"):
-        m = ((a > s * np.float32(.25)).astype(np.uint8) + (a >= s * np.float32(.75)) + (a > s * np.float32(1.25)) +
-             (a >= s * np.float32(1.75)) + (a > s * np.float32(2.5)) + (a >= s * np.float32(3.5)) +
-             (a > s * np.float32(5)))
+    with np.errstate(invalid="ignore", divide="ignore", over="ignore"):
+        a = np.abs(b / s)  # rounded to nearest
+        m = ((a > .25).astype(np.uint8) + (a >= .75) + (a > 1.25) + (a >= 1.75) + (a > 2.5) + (a >= 3.5) + (a > 5))
         m = np.where(s > 0, m, 0).astype(np.uint8)
     val = MAGS[m] * s
     val = np.where(np.signbit(b), -val, val).reshape(x.shape)
