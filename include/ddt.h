@@ -477,16 +477,19 @@ typedef struct ddt_kv4 {
  * cache's k_scale or v_scale, scale = e4m3(min(amax * (1 / (6 g)), 448)) and
  * each channel's code the magnitude nearest to the quotient |x| / (scale g) in
  * fp32, ties to the even code, 6 where it is larger. A block with a NaN gets a NaN scale and so
- * reads as NaN. k_held, v_held ([T, Hkv, d] bf16, dense, both or neither NULL):
- * the values that the cache now holds for the new tokens. */
+ * reads as NaN. k_held, v_held ([T, Hkv, d] bf16, dense, both or neither NULL;
+ * overlapping no other tensor): the values that the cache now holds for the new
+ * tokens. */
 ddt_status ddt_append_kvq(ddt_ctx *ctx, const ddt_append_args *args, const ddt_kv4 *cache,
                           uint16_t *k_held, uint16_t *v_held, void *stream);
 
 /* Causal attention of the packed queries over the paged cache, to which the
  * same tokens' keys and values have been appended: the query at position p
  * attends, with scale 1/sqrt(d), to positions 0..p of its request and KV head
- * h / (Hq / Hkv); softmax and sums in fp32, probabilities rounded to bf16 for
- * the product with the values, one rounding of the result.
+ * h / (Hq / Hkv); softmax and sums in fp32, probabilities rounded to bf16 (over
+ * the 4-bit cache: to fp16, and a query's channels below 2^-14 of its largest to
+ * 2^-25 of that) for the product with the values, one rounding of the result.
+ * The result does not depend on what else runs (no atomics in its sums).
  *   q        [T, Hq, d] bf16 with q_stride elements from token to token (a
  *            multiple of 8, at least Hq * d; 0 = dense)
  *   out      [T, Hq, d] bf16, dense; must not overlap q
@@ -495,7 +498,10 @@ ddt_status ddt_append_kvq(ddt_ctx *ctx, const ddt_append_args *args, const ddt_k
  * a request's last token are never attended to, whatever they hold; a NaN or
  * an infinity among a request's own values can reach every query of the same
  * request from 255 positions before it on. One token per request is a decoding
- * step; a chain's tokens are its verification pass. */
+ * step; a chain's tokens are its verification pass. A bounded wait that gives up
+ * sets DDT_DEV_TIMEOUT; the output of that call is undefined. The call uses the
+ * context's workspace (as ddt_tree_attention does): calls on one context, and
+ * graphs captured from them, must not overlap. */
 ddt_status ddt_prompt_attention(ddt_ctx *ctx, const uint16_t *q, int64_t q_stride,
                                 const int32_t *q_start, const int32_t *ctx_lens, int32_t R,
                                 int32_t T, const uint16_t *k_cache, const uint16_t *v_cache,

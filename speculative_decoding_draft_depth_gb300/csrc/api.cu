@@ -914,6 +914,16 @@ ddt_status ddt_append_kvq(ddt_ctx *ctx, const ddt_append_args *args, const ddt_k
     if (a.R == 0)
         return DDT_OK;
     DDT_CHECK((k_held == nullptr) == (v_held == nullptr) && aligned16(k_held) && aligned16(v_held));
+    if (k_held) {
+        const int64_t nq = (int64_t)ctx->cfg.Hq * ctx->cfg.d, nk = (int64_t)ctx->cfg.Hkv * ctx->cfg.d;
+        const int64_t held = span_bytes(a.T, nk, nk);
+        DDT_CHECK(!overlap(k_held, held, v_held, held));
+        for (const uint16_t *h : {k_held, v_held})
+            DDT_CHECK(!overlap(h, held, a.k, span_bytes(a.T, a.k_stride, nk)) &&
+                      !overlap(h, held, a.v, span_bytes(a.T, a.v_stride, nk)) &&
+                      (!a.q || (!overlap(h, held, a.q, span_bytes(a.T, a.q_stride, nq)) &&
+                                !overlap(h, held, a.q_out, span_bytes(a.T, nq, nq)))));
+    }
     if ((st = set_device(ctx)) != DDT_OK)
         return st;
     DDT_TRY(launch_append(ctx, a, nullptr, nullptr, cache, k_held, v_held, (cudaStream_t)stream));

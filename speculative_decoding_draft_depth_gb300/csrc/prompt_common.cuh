@@ -5,6 +5,7 @@
 
 #include <stdint.h>
 
+#include <algorithm>
 #include <atomic>
 
 #include "ddt_device.cuh"
@@ -248,23 +249,31 @@ __global__ void __launch_bounds__(MG_THREADS) prompt_merge_kernel(const PtArgs a
     __shared__ long long s_sums[MG_THREADS / 32], s_found[3];
     const int tq = rows >> a.g_shift, tid = threadIdx.x, b = blockIdx.x + 1;
     find_share(a, tq, grid, b, s_sums, s_found, tid, MG_THREADS);
-    if (s_found[0] < 0)
-        return;  // no such share
     const long long total = s_found[2], base = s_found[1];
-    const int nc = pp_ctas(total, grid, MIN_UNITS);
-    const PpReq rq = load_req(a, (int)s_found[0]);
-    const long long at = pp_share(total, b, nc);
-    const PpItem it = pp_find(rq, at - base, tq, a.Hkv);
-    const long long i0 = base + it.start;
-    if (pp_tile_at(at - i0) == 0)
-        return;  // the item's tiles all lie behind this boundary
+    int nc = 0;
+    PpReq rq = {0, 0, 0};
+    PpItem it = {0, 0, 0, 0};
+    long long i0 = 0;
+    bool cuts = s_found[0] >= 0;  // (else no such share)
+    if (cuts) {
+        nc = pp_ctas(total, grid, MIN_UNITS);
+        rq = load_req(a, (int)s_found[0]);
+        const long long at = pp_share(total, b, nc);
+        it = pp_find(rq, at - base, tq, a.Hkv);
+        i0 = base + it.start;
+        cuts = pp_tile_at(at - i0) > 0;  // (else the item's tiles all lie behind this boundary)
+    }
+    // The main kernel let this one start early: every CTA waits for it, one without
+    // work too, or what comes next in the stream could begin before it has ended.
+    pdl_wait();
+    if (!cuts)
+        return;
     const int c0 = pp_cta_of(i0 + PP_ITEM, total, nc), c1 = pp_cta_of(i0 + PP_ITEM + it.n - 1, total, nc);
     const int ntok = min(tq, rq.len - it.qt * tq), nrows = ntok << a.g_shift, ns = c1 - c0 + 1;
     const int nb = ns - 1, j = b - c0 - 1;
     // of the boundary's rows, this CTA's part
     const int y = j * gridDim.y + blockIdx.y, ny = nb * gridDim.y;
     const int lo = (int)((long long)y * nrows / ny), hi = (int)((long long)(y + 1) * nrows / ny);
-    pdl_wait();  // the partials, once the main kernel has completed
     // a warp: eight rows by four float4 columns (the partials' rows lie side by
     // side, the output's columns do)
     constexpr int C4 = D / 4;
@@ -275,7 +284,7 @@ __global__ void __launch_bounds__(MG_THREADS) prompt_merge_kernel(const PtArgs a
             continue;
         float M = DDT_NEG_INF, L = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
         for (int s = 0; s < ns; ++s) {
             const int64_t slot = s == 0 ? 2 * c0 + 1 : 2 * (c0 + s);
             const float2 ml = __ldcg(&a.part_ml[slot * rows + row]);
@@ -316,7 +325,9 @@ template <int D>
 cudaError_t launch_merge(const PtArgs &a, int grid, int rows, cudaStream_t s)
 {
     cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3(grid - 1, rows >= 64 ? MG_SPLIT : 1);
+    // CTAs of a boundary: one for about 32 of the rows that an item can have
+    const int64_t most = std::min((int64_t)rows, (int64_t)a.T << a.g_shift);
+    lc.gridDim = dim3(grid - 1, (unsigned)std::max((int64_t)1, std::min((int64_t)MG_SPLIT, most / 32)));
     lc.blockDim = dim3(MG_THREADS);
     lc.stream = s;
     cudaLaunchAttribute at[1];

@@ -190,24 +190,37 @@ __global__ void __launch_bounds__(FT, NR == 1 ? 2 : 1) prompt_few_kernel(const F
     copier.begin(a, lane);
     ShareWalk walk;
     walk.begin(a, s_found, tq, gridDim.x, blockIdx.x);
-    for (;;) {
-        Seg s;
+    // this warp's blocks of a segment: the next one, their end, the page of the one FS
+    // turns ahead; their copies begin while the segment before is merged
+    int blk = 0, bend = 0, page = NO_PAGE;
+    Seg s = {};
+    auto page_of = [&](int b) {
+        return b < bend ? __ldg(a.block_table + (int64_t)s.r * a.max_pages + ((b * 16) >> a.page_shift)) : NO_PAGE;
+    };
+    auto fetch = [&](int b, int pg, int slot) {  // (nothing beyond the end: a slot has one copy under way)
+        if (b < bend)
+            copier.fetch(a, raws + slot * RAW_BYTES<D>, pg, b * 16, s.pos0 + s.ntok, s.h, lane);
+        cp_async_commit();
+    };
+    auto start = [&]() {
         walk.next(a, tq, 0, s);
         if (s.r < 0)
-            break;
-        const int end = s.pos0 + s.ntok, nrows = s.ntok << a.g_shift;
-        // ---- this warp's blocks: the first one's codes, the second one's page
-        const int bend = (min(end, s.t1 * PP_TILE) + 15) >> 4;
-        int blk = s.t0 * (PP_TILE / 16) + warp;
-        const int32_t *pages = a.block_table + (int64_t)s.r * a.max_pages;
-        auto page_of = [&](int b) { return b < bend ? __ldg(pages + ((b * 16) >> a.page_shift)) : NO_PAGE; };
+            return;
+        bend = (min(s.pos0 + s.ntok, s.t1 * PP_TILE) + 15) >> 4;
+        blk = s.t0 * (PP_TILE / 16) + warp;
+        int pg[FS];
 #pragma unroll
-        for (int x = 0; x < FS; ++x) {
-            copier.fetch(a, raws + x * RAW_BYTES<D>, page_of(blk + x * FW), (blk + x * FW) * 16,
-                         blk + x * FW < bend ? end : 0, s.h, lane);
-            cp_async_commit();
-        }
-        int page = page_of(blk + FS * FW), slot = 0;
+        for (int x = 0; x < FS; ++x)
+            pg[x] = page_of(blk + x * FW);
+        page = page_of(blk + FS * FW);
+#pragma unroll
+        for (int x = 0; x < FS; ++x)
+            fetch(blk + x * FW, pg[x], x);
+    };
+    start();
+    while (s.r >= 0) {
+        const int nrows = s.ntok << a.g_shift;
+        int slot = 0;
         // ---- Q: row 8 y + i, channels [c D/4, + D/4), divided by a power of two of the
         //      row's largest magnitude, to fp16 in the order of the codes' pairs
         uint32_t qf[NR][2 * KS];
@@ -271,10 +284,8 @@ __global__ void __launch_bounds__(FT, NR == 1 ? 2 : 1) prompt_few_kernel(const F
             Block<D> b;
             read_block<D>(rawp + slot * RAW_BYTES<D>, b, lane);
             __syncwarp();
-            const int ahead = blk + FS * FW;
-            copier.fetch(a, raws + slot * RAW_BYTES<D>, page, ahead * 16, ahead < bend ? end : 0, s.h, lane);
-            cp_async_commit();
-            page = page_of(ahead + FW);
+            fetch(blk + FS * FW, page, slot);
+            page = page_of(blk + (FS + 1) * FW);
             slot = slot + 1 == FS ? 0 : slot + 1;
             // ---- S^T
             float st[NR][4], su[NR][4];  // (two sums: half the products wait for one another)
@@ -381,7 +392,8 @@ __global__ void __launch_bounds__(FT, NR == 1 ? 2 : 1) prompt_few_kernel(const F
                         mma_f16(o[y][4 * w + q], l0[q], h0[q], l1[q], h1[q], pb[y][0], pb[y][1]);
             }
         }
-        cp_async_wait_all();  // (the last ones copy nothing, but into slots that come into use again)
+        const Seg was = s;
+        start();
         // ---- the warps' parts to shared memory: O row by row, (m, l)
 #pragma unroll
         for (int y = 0; y < NR; ++y)
@@ -422,20 +434,21 @@ __global__ void __launch_bounds__(FT, NR == 1 ? 2 : 1) prompt_few_kernel(const F
                 r.z += v.z * k;
                 r.w += v.w * k;
             }
-            if (s.whole) {
+            if (was.whole) {
                 const float inv = L > 0.f || L != L ? a.out_scale / L : 0.f;
                 uint32_t *dst = reinterpret_cast<uint32_t *>(
-                    a.out + ((int64_t)(s.row0 + (row >> a.g_shift)) * a.Hq + (s.h << a.g_shift) + (row & (G - 1))) * D) + 2 * c4;
+                    a.out + ((int64_t)(was.row0 + (row >> a.g_shift)) * a.Hq + (was.h << a.g_shift) + (row & (G - 1))) * D) + 2 * c4;
                 *reinterpret_cast<uint2 *>(dst) =
                     make_uint2(pack_bf16x2(r.x * inv, r.y * inv), pack_bf16x2(r.z * inv, r.w * inv));
             } else {
-                reinterpret_cast<float4 *>(a.part_o + (int64_t)s.slot * ROWS * D)[c4 * ROWS + row] = r;
+                reinterpret_cast<float4 *>(a.part_o + (int64_t)was.slot * ROWS * D)[c4 * ROWS + row] = r;
                 if (c4 == 0)
-                    a.part_ml[(int64_t)s.slot * ROWS + row] = make_float2(M, L);
+                    a.part_ml[(int64_t)was.slot * ROWS + row] = make_float2(M, L);
             }
         }
         __syncthreads();
     }
+    cp_async_wait_all();
 }
 
 template <int D, int NR>

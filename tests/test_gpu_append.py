@@ -237,6 +237,19 @@ def test_refusals():
         bad = p.h._kv4(fake)
         setattr(bad, name, v)
         assert call(cache=bad) == ddt.EINVAL, (name, v)
+    # what the cache holds is written apart from every other tensor
+    qo = torch.empty_like(p.q)
+    args = p.h._append_args(p.q, p.k, p.v, p.q_start, p.ctx_lens, p.table, p.R, qo, None, None)
+    kh, vh = torch.empty_like(p.k), torch.empty_like(p.v)
+
+    def held(k, v):
+        return lib.ddt_append_kvq(p.h._h, ctypes.byref(args), ctypes.byref(k4), k, v, None)
+
+    assert held(kh.data_ptr(), vh.data_ptr()) == ddt.OK
+    for k, v in ((kh.data_ptr(), None), (kh.data_ptr(), kh.data_ptr()), (p.k.data_ptr(), vh.data_ptr()),
+                 (kh.data_ptr(), p.v.data_ptr()), (kh.data_ptr(), args.q_out), (p.q.data_ptr(), vh.data_ptr()),
+                 (kh.data_ptr() + 8, vh.data_ptr())):
+        assert held(k, v) == ddt.EINVAL
     with pytest.raises(ValueError):
         p.append(k=p.k.cpu())
     torch.cuda.synchronize()

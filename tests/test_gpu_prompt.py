@@ -215,6 +215,40 @@ def test_another_stream_and_repeats_agree():
 
 
 @pytest.mark.parametrize("bits", [16, 4])
+@pytest.mark.parametrize("lens,ctx", [([1], [10]), ([1, 1, 1], [10, 700, 0]), ([20], [3000])])
+def test_what_comes_next_sees_the_whole_output(bits, lens, ctx):
+    """Work right behind the call on its stream, with and without items that share
+    boundaries cut (whose merge is staged while the attention still runs)."""
+    p = Packed(lens, ctx, 32, 8, 128, 16, bits, seed=47)
+    first = run(p)
+    out, copies = torch.empty_like(first), []
+    for _ in range(50):
+        out.fill_(SENTINEL)
+        p.attend(out=out)
+        copies.append(out.clone())
+    for c in copies:
+        assert torch.equal(c.view(torch.int16), first.view(torch.int16))
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_two_contexts_at_once(bits):
+    """Two contexts on two streams share nothing."""
+    a = Packed([1, 40], [2000, 300], 16, 2, 128, 16, bits, seed=48)
+    b = Packed([3, 1], [900, 4000], 8, 8, 64, 16, bits, seed=49)
+    want = [run(a), run(b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    outs = [[torch.empty_like(w) for _ in range(20)] for w in want]
+    for i in range(20):
+        for p, s, o in zip((a, b), streams, outs):
+            p.attend(out=o[i], stream=s)
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        for x in o:
+            assert torch.equal(x.view(torch.int16), w.view(torch.int16))
+
+
+@pytest.mark.parametrize("bits", [16, 4])
 def test_captured_steps_follow_the_lengths(bits):
     """An append and its attention captured once; the replays read the lengths,
     pages and tokens of their own time."""
