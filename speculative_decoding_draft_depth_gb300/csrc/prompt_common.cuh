@@ -241,7 +241,7 @@ DDT_DEVINL uint32_t pack_f16x2(float lo, float hi)
 // Merge of a cut item: boundary b (between CTAs b - 1 and b) takes the j-th of
 // the nb row blocks of the item that it cuts, if it lies among the item's tiles
 // (nb: the boundaries that do).
-constexpr int MG_THREADS = 256, MG_SPLIT = 8;
+constexpr int MG_THREADS = 256, MG_SPLIT = 4;
 
 template <int D>
 __global__ void __launch_bounds__(MG_THREADS) prompt_merge_kernel(const PtArgs a, int grid, int rows)
