@@ -1,5 +1,9 @@
-// prompt_tc.cu -- causal attention of packed sequences over the paged cache on
-// the 5th-generation tensor cores (tcgen05 + TMEM + TMA), D = 128 and 64.
+// prompt.cu -- causal attention of packed sequences over the paged cache on the
+// 5th-generation tensor cores (tcgen05 + TMEM + TMA), D = 128 and 64.
+//
+//   O = softmax(scale Q K^T + mask) V, one pass over the keys: with a running m and
+//   P = exp2(scale log2(e) S - m), O and l (the row's sum) are sums over the keys,
+//   multiplied by exp2(m_old - m_new) when m moves.
 //
 // Work split (prompt_plan.h): an item is up to 256 rows (256 / G tokens of a
 // request with the G heads of one KV head) against the request's key tiles of
@@ -9,23 +13,46 @@
 // per CTA), merged by prompt_merge_kernel.
 //
 // Inside a CTA:
-//  * two groups, A and B, of 128 rows each (rows in TMEM lanes): S = Q K^T into
-//    the group's 128 TMEM columns, softmax by the group's four warps (one row
-//    per thread, no exchange between threads), P (bf16) over the first 64 of the same
-//    columns, O += P V from there. While one group's softmax runs, the tensor
-//    cores work for the other. An item of at most 128 rows (a token or a chain
-//    of a few) gives both groups the same rows and alternate key tiles; group A
-//    merges the two at the end, reading B's O from TMEM.
-//  * K and V tiles of 128 tokens arrive by TMA in a 2-deep K ring and a 3-deep V
-//    ring, one box per 16-token page run and 64-channel half.
-//  * the running maximum is followed lazily: O and the sum are rescaled only when
-//    a row's maximum grows by more than 2^8. P V of the tile before has then
-//    completed, since the tile's S was issued behind it.
-//  * warps 0-3: group A; 4-7: group B; 8: MMA issuer; 9: walks the share, loads Q
-//    and K; 10: loads V, with the rows past the item's last key zeroed (whatever
-//    the page holds there must not meet a probability of zero).
+//  * two groups, A and B, of 128 rows each (rows in TMEM lanes), worked on in steps
+//    of 64 keys: S = Q K^T into one of the group's two buffers of 64 TMEM columns,
+//    softmax by the group's four warps (one row per thread, no exchange between
+//    threads), P (bf16; fp16 for the 4-bit cache) over the buffer's first 32 columns,
+//    O += P V from there. S of the next step is issued before P of this one is
+//    waited for, so the softmax warps find their next S ready. An item of at most
+//    128 rows (a token or a chain of a few) gives both groups the same rows and
+//    alternate key tiles; group A merges the two at the end, reading B's O from TMEM.
+//  * m is followed loosely. The common step looks for no maximum: while a row's
+//    weights of a step add up to no more than a limit, none of them can overflow or
+//    swamp the sums, and m stays. The first step, steps with masked keys and those
+//    above the limit read S once more and take the maximum.
+//  * bf16 cache: K and V tiles of 128 tokens arrive by TMA in a ring of two K and of
+//    three V tiles, one box per 16 tokens and 64 channels.
+//  * 4-bit cache: codes and scales arrive by cp.async; eight warps turn them into
+//    fp16 tiles (exact) in the same places. Q goes to fp16 by a power of two for
+//    each row, in the channel order that the codes' pairs come out in.
+//  * warps 0-3: group A; 4-7: group B; 8 and 11: MMA issuers of A and of B; 9: walks
+//    the share, loads Q and K; 10: loads V, with the rows past the item's last key
+//    zeroed (whatever the page holds there must not meet a probability of zero).
+//    4 bits: 9 walks, 10 loads Q, 12-15 make K's tiles and 16-19 V's.
 //  * every wait is bounded; on timeout the CTA raises DDT_DEV_TIMEOUT, waits
 //    (bounded) for its own copies and MMAs, frees its TMEM and returns.
+//
+// Measured (GB300; a step of both groups is 2 x 128 rows x 64 keys):
+//  * 16384 tokens, 32 heads of 128 over 8 KV heads: 1.34 to 1.40 ms, 1570 to 1640
+//    TFLOP/s. Alone, a launch takes 1300 cycles a step, and the tensor pipe 1286 of
+//    them (8 MMAs of N = 64 for S, bound by shared memory at 48 cycles each, and 4 of
+//    N = 128 for P V, both groups); repeated, the board's power limit lowers the
+//    clock, and the rate is that of a large bf16 matrix product in the same state
+//    (1740) but for 6 to 10%.
+//    S of a whole tile at once (N = 128, 32 cycles per 64 keys) needs both buffers, so
+//    a group has no next S while its softmax runs: 1.66 ms.
+//  * 32 prompts of up to 2047 tokens, 8 heads of 64: 119 us. Softmax bound: a step
+//    takes two warps of each scheduler 900 cycles, of which 512 are exponentials.
+//    With the maximum in every step it was 127 us; with the mask and the maximum as
+//    branches of one path (registers copied at their joins) 137.
+//  * 64 tokens behind 512 to 16384 cached: 361 us, 6.7 TB/s.
+//  * 4-bit cache, four chunks of 1500 to 2048 tokens behind 4000 to 16000: 0.90 ms,
+//    1320 TFLOP/s. Bound by the instructions of softmax and conversion together.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -60,13 +87,17 @@ constexpr int NRING = 8;
 template <bool KV4>
 constexpr int RING_CONSUMERS = 8 + 2 + 1 + (KV4 ? 2 * NDQ : 0);  // softmax warps, MMA issuers, V or Q loader, ...
 constexpr uint32_t TMEM_COLS = 512;
-constexpr uint32_t TM_S = 0;    // S (and P) of A, B: 128 columns each
+constexpr uint32_t TM_S = 0;    // S (and P) of A, B: two buffers of SUB columns each
 constexpr uint32_t TM_O = 256;  // O of A, B: 128 columns each
 constexpr long long WAIT_LIMIT = 4000000000LL;  // cycles (about 2 s)
 constexpr long long DRAIN_LIMIT = 200000000LL;
 
 // shared memory (offsets from a 1024-byte aligned base)
 constexpr int NK = 2;
+constexpr int SUB = 64;  // keys of a softmax step: half a tile
+// what a step's weights of a row may add up to before the maximum is looked for again
+template <bool KV4>
+constexpr float LIMIT = KV4 ? 32768.f : 256.f;
 template <bool KV4>
 constexpr int NV = KV4 ? 2 : 3;
 constexpr int NRK = 2, NRV = 1;  // 4-bit cache: tiles of K's and of V's codes and scales in flight
@@ -79,31 +110,29 @@ constexpr uint32_t SM_RAW = SM_V + NV<KV4> * 32768;
 template <bool KV4>
 constexpr uint32_t SM_BAR = SM_RAW<KV4> + (KV4 ? (NRK + NRV) * RAW : 0);
 constexpr uint32_t B_QFULL = 0, B_QEMPTY = 8, B_KFULL = 16, B_KEMPTY = 32, B_VFULL = 48, B_VEMPTY = 72,
-                   B_SFULL = 96,   // [2 groups]
-                   B_PFULL = 112,  // [2] 4 arrivals (the group's warps): P of keys 0..63 is there
-                   B_OFULL = 128,  // [2]
-                   B_XB = 144,     // B's (m, l) published and its O complete (4 arrivals)
-                   B_XA = 152,     // A has read them (4 arrivals)
-                   B_FINAL = 160,  // [2]
-                   B_PHALF = 176,  // [2] 4 arrivals: P of keys 64..127
-                   B_TMEM = 192, B_ABORT = 196,
-                   B_QREADY = 200,    // 4 bits: Q is fp16 (NDQ arrivals)
-                   B_RFULL = 208,     // [NRING]
-                   B_REMPTY = 272,    // [NRING]
-                   B_RING = 336,      // [NRING][8] ints
+                   B_SFULL = 96,   // [2 groups][2 buffers]
+                   B_PFULL = 128,  // [2][2] 4 arrivals (the group's warps)
+                   B_ODONE = 160,  // [2] every P V of the group
+                   B_XB = 176,     // B's (m, l) published and its O complete (4 arrivals)
+                   B_XA = 184,     // A has read them (4 arrivals)
+                   B_FINAL = 192,  // [2]
+                   B_OFULL = 208,  // [2] the last P V of an item
+                   B_TMEM = 224, B_ABORT = 228,
+                   B_QREADY = 232,    // 4 bits: Q is fp16 (NDQ arrivals)
+                   B_RFULL = 240,     // [NRING]
+                   B_REMPTY = 304,    // [NRING]
+                   B_RING = 368,      // [NRING][8] ints
                    B_FOUND = B_RING,  // three 64-bit words, before the walk begins
-                   B_ML = 592,        // [128] float2: B's (m, l); before the roles start, the scan's sums
-                   B_ROWSC = 1616;    // 4 bits: [2][256] floats: the row's factor, by item parity
+                   B_ML = 624,        // [128] float2: B's (m, l); before the roles start, the scan's sums
+                   B_ROWSC = 1648;    // 4 bits: [2][256] floats: the row's factor, by item parity
 template <bool KV4>
-constexpr uint32_t B_TURN = B_ROWSC + (KV4 ? 2048 : 0);  // int: a group's issuer has its turn
-template <bool KV4>
-constexpr uint32_t B_END = B_TURN<KV4> + 8;
+constexpr uint32_t B_END = B_ROWSC + (KV4 ? 2048 : 0);
 template <bool KV4>
 constexpr uint32_t SM_ALLOC = SM_BAR<KV4> + B_END<KV4> + 1024;
 static_assert(SM_ALLOC<false> <= 232448 && SM_ALLOC<true> <= 232448, "shared memory of one CTA");
 
 template <bool KV4>
-constexpr uint32_t IDESC_QK = KV4 ? idesc_f16(128, 128, false, false) : idesc_bf16(128, 128, false, false);
+constexpr uint32_t IDESC_QK = KV4 ? idesc_f16(128, SUB, false, false) : idesc_bf16(128, SUB, false, false);
 template <int D, bool KV4>
 constexpr uint32_t IDESC_PV = KV4 ? idesc_f16(128, D, false, true) : idesc_bf16(128, D, false, true);
 
@@ -336,9 +365,11 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             mbar_init(bar + B_VEMPTY + 8 * i, 2);
         }
         for (int g = 0; g < 2; ++g) {
-            mbar_init(bar + B_SFULL + 8 * g, 1);
-            mbar_init(bar + B_PFULL + 8 * g, 4);
-            mbar_init(bar + B_PHALF + 8 * g, 4);
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(bar + B_SFULL + 16 * g + 8 * b, 1);
+                mbar_init(bar + B_PFULL + 16 * g + 8 * b, 4);
+            }
+            mbar_init(bar + B_ODONE + 8 * g, 1);
             mbar_init(bar + B_OFULL + 8 * g, 1);
         }
         mbar_init(bar + B_XB, 4);
@@ -351,7 +382,6 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         mbar_init(bar + B_FINAL + 8, 1);
         mbar_init(bar + B_QREADY, NDQ);
         *abort_flag = 0;
-        *reinterpret_cast<volatile int *>(sgen + SM_BAR<KV4> + B_TURN<KV4>) = 0;
         fence_mbar_init();
     }
     if (warp == W_MMA) {
@@ -514,25 +544,12 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             // earlier items are complete once this item's Q is there (it waited for both
             // groups' last S), V's once the group's P is (its softmax has finished the
             // item before, with the other group's last product): P is waited for first.
-            uint32_t base = 0, pph = 0;  // tiles before the item; phase of the group's next P
+            uint32_t base = 0, n = 0;    // tiles before the item; the group's steps so far
             uint32_t vfill = 0;          // phase of each V slot's next fill, at the item's start
             bool ok = true;
             // (after a wait that gave up, what the body still issues reads and writes
             // this CTA's own memory; the loop then ends)
             auto need = [&](uint32_t b, uint32_t parity) { ok &= wait_bar(b, parity, abort_flag, a.status); };
-            // 4 bits: one group's P V and next S go to the tensor cores together, or the
-            // groups' softmax fall into step and the tensor cores idle meanwhile (chunks of
-            // 1500..2048 tokens: 1030 us, so 900 us; the bf16 cache: 1376 and 1401 us, no turns)
-            volatile int *turn = reinterpret_cast<volatile int *>(sgen + SM_BAR<KV4> + B_TURN<KV4>);
-            auto turn_begin = [&]() {
-                const long long t0 = clock64();
-                while (ok && atomicCAS_block(const_cast<int *>(turn), 0, 1) != 0)
-                    if (*abort_flag || clock64() - t0 > WAIT_LIMIT) {
-                        *abort_flag = 1;
-                        atomicOr(a.status, DDT_DEV_TIMEOUT);
-                        ok = false;
-                    }
-            };
             for (int k = 0; ok; ++k) {
                 const int slot = k & (NRING - 1);
                 need(bar + B_RFULL + 8 * slot, (k / NRING) & 1);
@@ -546,79 +563,73 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 seg_decode(w, s);
                 if (s.r < 0)
                     break;
-                const int steps = s.steps(g);
+                const int steps = 2 * s.steps(g);
                 // the group's first tile and its slots; then every tile, or every second
                 const uint32_t first = base + (s.split ? g : 0u), by = s.split ? 2u : 1u;
                 uint32_t ks = first % NK, kph = (first / NK) & 1;
                 uint32_t vs = s.split ? g : 0u, vbits = vfill;
                 const uint64_t q = dQ + (uint64_t)((!s.split && g) ? (32768u >> 4) : 0u);
                 need(bar + (KV4 ? B_QREADY : B_QFULL), k & 1);
-                // S of tile j behind P V of tile j - 1, whose P lies in the same columns
+                // S of step u (into the buffer that P of step u - 2 has left), then P V of
+                // step u - 1
 #pragma unroll 1
-                for (int j = 0; j <= steps && ok; ++j) {
-                    if (j > 0) {
-                        const uint64_t v = dV + (uint64_t)(vs * (32768u >> 4));
-                        const uint32_t more = j > 1 ? 1u : 0u;
-                        need(bar + B_PFULL + 8 * g, pph);
-                        need(bar + B_VFULL + 8 * vs, (vbits >> vs) & 1);
-                        if (KV4 && !s.split) {
-                            // (all that another role has to bring is there before a turn
-                            // begins, so nobody waits for the one whose turn it is)
-                            if (j < steps)
-                                need(bar + B_KFULL + 8 * ks, kph);
-                            turn_begin();
-                        }
-                        tc_fence_after();
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            mma_bf16_ts(o, sp + 8u * i, v + i * (2048u >> 4), IDESC_PV<D, KV4>, i > 0 ? 1u : more);
-                        need(bar + B_PHALF + 8 * g, pph);
-                        tc_fence_after();
-#pragma unroll
-                        for (int i = 4; i < 8; ++i)
-                            mma_bf16_ts(o, sp + 8u * i, v + i * (2048u >> 4), IDESC_PV<D, KV4>, 1u);
-                        pph ^= 1;
-                        mma_commit(bar + B_VEMPTY + 8 * vs);
-                        if (s.split)  // (a slot counts two releases: of both groups, or two of its one)
-                            mbar_arrive(bar + B_VEMPTY + 8 * vs);
-                        vbits ^= 1u << vs;
-                        if (!s.split && ++vs == NV<KV4>)
-                            vs = 0;
-                        if (j == steps) {
-                            mma_commit(bar + B_OFULL + 8 * g);
-                            if (KV4 && !s.split)
-                                *turn = 0;
-                        }
-                    }
-                    if (j < steps) {
-                        const uint64_t kk = dK + (uint64_t)(ks * (32768u >> 4));
-                        need(bar + B_KFULL + 8 * ks, kph);
+                for (int u = 0; u <= steps && ok; ++u) {
+                    const uint32_t b = (n + u) & 1;
+                    if (u < steps) {
+                        const uint64_t kk = dK + (uint64_t)(ks * (32768u >> 4) + (u & 1) * (SUB * 128u >> 4));
+                        const uint32_t d = sp + SUB * b;
+                        if ((u & 1) == 0)
+                            need(bar + B_KFULL + 8 * ks, kph);
                         tc_fence_after();
 #pragma unroll
                         for (int i = 0; i < D / 16; ++i) {
                             const uint32_t off = ((i >> 2) * 16384u + (i & 3) * 32u) >> 4;
-                            mma_bf16(sp, q + off, kk + off, IDESC_QK<KV4>, i > 0 ? 1u : 0u);
+                            mma_bf16(d, q + off, kk + off, IDESC_QK<KV4>, i > 0 ? 1u : 0u);
                         }
-                        mma_commit(bar + B_SFULL + 8 * g);
-                        if (KV4 && !s.split && j > 0)
-                            *turn = 0;
-                        mma_commit(bar + B_KEMPTY + 8 * ks);
-                        if (s.split)
-                            mbar_arrive(bar + B_KEMPTY + 8 * ks);
-                        ks += by;
-                        if (ks >= NK) {
-                            ks -= NK;
-                            kph ^= 1;
+                        mma_commit(bar + B_SFULL + 16 * g + 8 * b);
+                        if (u & 1) {
+                            mma_commit(bar + B_KEMPTY + 8 * ks);
+                            if (s.split)  // (a slot counts two releases: of both groups, or two of its one)
+                                mbar_arrive(bar + B_KEMPTY + 8 * ks);
+                            ks += by;
+                            if (ks >= NK) {
+                                ks -= NK;
+                                kph ^= 1;
+                            }
+                            if (u == steps - 1)  // the group is done with the item's Q
+                                mma_commit(bar + B_QEMPTY);
                         }
-                        if (j == steps - 1)  // the group is done with the item's Q
-                            mma_commit(bar + B_QEMPTY);
+                    }
+                    if (u > 0) {
+                        const uint32_t m = n + u - 1, h = (u - 1) & 1, pp = sp + SUB * (m & 1);
+                        const uint64_t v = dV + (uint64_t)(vs * (32768u >> 4) + h * (SUB * 128u >> 4));
+                        const uint32_t more = u > 1 ? 1u : 0u;
+                        need(bar + B_PFULL + 16 * g + 8 * (m & 1), (m >> 1) & 1);
+                        if (h == 0)
+                            need(bar + B_VFULL + 8 * vs, (vbits >> vs) & 1);
+                        tc_fence_after();
+#pragma unroll
+                        for (int i = 0; i < SUB / 16; ++i)
+                            mma_bf16_ts(o, pp + 8u * i, v + i * (2048u >> 4), IDESC_PV<D, KV4>, i > 0 ? 1u : more);
+                        mma_commit(bar + B_ODONE + 8 * g);
+                        if (u == steps)
+                            mma_commit(bar + B_OFULL + 8 * g);
+                        if (h) {
+                            mma_commit(bar + B_VEMPTY + 8 * vs);
+                            if (s.split)
+                                mbar_arrive(bar + B_VEMPTY + 8 * vs);
+                            vbits ^= 1u << vs;
+                            if (!s.split && ++vs == NV<KV4>)
+                                vs = 0;
+                        }
                     }
                 }
                 if (steps == 0)  // (the wait for this item's Q keeps this arrival in its phase)
                     mbar_arrive(bar + B_QEMPTY);
-                const uint32_t n = s.t1 - s.t0;
-                base += n;
-                vfill = s.split ? vfill ^ (((n + 1) >> 1) & 1u) ^ (((n >> 1) & 1u) << 1) : vbits;
+                n += steps;
+                const uint32_t tiles = s.t1 - s.t0;
+                base += tiles;
+                vfill = s.split ? vfill ^ (((tiles + 1) >> 1) & 1u) ^ (((tiles >> 1) & 1u) << 1) : vbits;
             }
             // wind down: every MMA issued here has completed
             mma_commit(bar + B_FINAL + 8 * g);
@@ -714,108 +725,42 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const uint32_t s_addr = tmem + lane_addr + TM_S + 128u * g;
         const uint32_t o_addr = tmem + lane_addr + TM_O + 128u * g;
         float2 *ml = reinterpret_cast<float2 *>(sgen + SM_BAR<KV4> + B_ML);
-        int n = 0, no = 0, nx = 0;  // tiles, items with tiles, split items so far
+        int n = 0, no = 0, nx = 0;  // the group's steps, items with steps, split items so far
         for (int k = 0;; ++k) {
             Seg s;
             if (!ring_get(a, bar, ring, k, lane, abort_flag, s))
                 break;
-            const int steps = s.steps(g);
+            const int steps = 2 * s.steps(g);
             // this row's token, head and last key (rows without a token: the last one's)
             const int tok = ((s.split ? 0 : 128 * g) + row) >> a.g_shift, hl = row & ((1 << a.g_shift) - 1);
             const int pos = s.pos0 + min(tok, s.ntok - 1);
-            const int pos_warp = __shfl_sync(0xFFFFFFFFu, pos, 0);  // the warp's least
+            const int pos_warp = __shfl_sync(0xFFFFFFFFu, pos, 0);  // the warp's least and greatest
+            const int pos_top = __shfl_sync(0xFFFFFFFFu, pos, 31);
             float m_used = DDT_NEG_INF, l = 0.f;
             float scale = a.scale_log2;
             bool alive = true;
             for (int j = 0; j < steps; ++j, ++n) {
-                if (!wait_warp(bar + B_SFULL + 8 * g, n & 1, abort_flag, a.status)) {
+                const uint32_t buf = s_addr + SUB * (n & 1);
+                if (!wait_warp(bar + B_SFULL + 16 * g + 8 * (n & 1), (n >> 1) & 1, abort_flag, a.status)) {
                     alive = false;
                     break;
                 }
                 tc_fence_after();
                 if (KV4 && j == 0)
-                    scale = a.scale_log2 * reinterpret_cast<const volatile float *>(sgen + SM_BAR<KV4> + B_ROWSC)[(k & 1) * 256 + (s.split ? 0 : 128 * g) + row];
-                const int lim = pos - s.tile(g, j) * PP_TILE;  // the row's last key, in this tile's columns
-                // The scores stay in registers; the 4-bit form has fewer (two warpgroups make
-                // tiles) and loads keys 64..127 again for their exponentials.
-                constexpr bool KEEP = !KV4;
-                const bool cut = s.tile(g, j) * PP_TILE + PP_TILE - 1 > pos_warp;
-                uint32_t sv[KEEP ? 128 : 64];
-                auto load = [&](int c0, uint32_t *x) {  // 64 columns, masked once waited for
-                    tmem_ld32(s_addr + c0, x);
-                    tmem_ld32(s_addr + c0 + 32u, x + 32);
-                };
-                auto mask = [&](int c0, uint32_t *x) {
-                    if (cut) {
+                    scale = a.scale_log2 *
+                            reinterpret_cast<const volatile float *>(sgen + SM_BAR<KV4> + B_ROWSC)[(k & 1) * 256 + (s.split ? 0 : 128 * g) + row];
+                const int key0 = s.tile(g, j >> 1) * PP_TILE + SUB * (j & 1);
+                // P = exp2(scale S - m), rounded to bf16 (fp16 with its range moved up) for
+                // the tensor cores; the sum takes the unrounded values. A row with nothing
+                // yet has m = -inf.
+                auto weigh = [&](const uint32_t (&sv)[SUB], uint32_t (&pw)[SUB / 2]) {
+                    const float off = (KV4 ? PBIAS : 0.f) - (m_used == DDT_NEG_INF ? 0.f : m_used);
+                    const uint64_t sc2 = f2pack(scale, scale), nm2 = f2pack(off, off);
+                    uint64_t sum0 = f2pack(0.f, 0.f), sum1 = sum0;
 #pragma unroll
-                        for (int c = 0; c < 64; ++c)
-                            if (c0 + c > lim)
-                                x[c] = __float_as_uint(DDT_NEG_INF);
-                    }
-                };
-                float m4[4] = {DDT_NEG_INF, DDT_NEG_INF, DDT_NEG_INF, DDT_NEG_INF};
-                auto largest = [&](const uint32_t *x) {
-#pragma unroll
-                    for (int c = 0; c < 64; c += 8)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            m4[e] = fmaxf(m4[e], fmaxf(__uint_as_float(x[c + 2 * e]), __uint_as_float(x[c + 2 * e + 1])));
-                };
-                if constexpr (KEEP) {
-                    load(0, sv);
-                    load(64, sv + 64);
-                    tmem_wait_ld();
-                    mask(0, sv);
-                    mask(64, sv + 64);
-                    largest(sv);
-                    largest(sv + 64);
-                } else {
-#pragma unroll
-                    for (int h = 1; h >= 0; --h) {
-                        load(64 * h, sv);
-                        tmem_wait_ld();
-                        mask(64 * h, sv);
-                        largest(sv);
-                    }
-                }
-                const float mcand = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * scale;
-                float alpha = 1.f;
-                const bool grow = mcand > m_used + TAU;
-                if (grow) {
-                    alpha = ex2(m_used - mcand);  // 0 while m_used is -inf
-                    m_used = mcand;
-                }
-                // O rescale (rare): P V of the tile before completed before this S did
-                if (__any_sync(0xFFFFFFFFu, grow && j > 0)) {
-#pragma unroll 1
-                    for (int c = 0; c < D / 32; ++c) {
-                        uint32_t ov[32];
-                        tmem_ld32(o_addr + 32u * c, ov);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
-                        tmem_st32(o_addr + 32u * c, ov);
-                    }
-                }
-                // P = exp2(scale S - m), rounded to bf16 for the tensor cores (the sum
-                // takes the unrounded values); a row with nothing yet has m = -inf
-                const float off = (KV4 ? PBIAS : 0.f) - (m_used == DDT_NEG_INF ? 0.f : m_used);
-                const uint64_t sc2 = f2pack(scale, scale), nm2 = f2pack(off, off);
-                uint64_t sum0 = f2pack(0.f, 0.f), sum1 = sum0;
-                // the first half's products may begin while the second is computed
-                auto publish = [&](uint32_t b) {
-                    tmem_wait_st();
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(bar + b + 8 * g);
-                };
-                auto exps = [&](auto pairs, const uint32_t *x, uint32_t *pw) {  // scores to pairs of P
-#pragma unroll
-                    for (int e = 0; e < decltype(pairs)::value; ++e) {
+                    for (int e = 0; e < SUB / 2; ++e) {
                         float x0, x1;
-                        f2unpack(f2fma(f2pack(__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])), sc2, nm2), x0, x1);
+                        f2unpack(f2fma(f2pack(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), sc2, nm2), x0, x1);
                         x0 = ex2(x0);
                         x1 = ex2(x1);
                         pw[e] = KV4 ? pack_f16x2(x0, x1) : pack_bf16x2(x0, x1);
@@ -824,39 +769,91 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         else
                             sum0 = f2add(sum0, f2pack(x0, x1));
                     }
+                    float r0, r1;
+                    f2unpack(f2add(sum0, sum1), r0, r1);
+                    return r0 + r1;
                 };
-                if constexpr (KEEP) {
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t pw[32];
-                        exps(std::integral_constant<int, 32>(), sv + 64 * c, pw);
-                        tmem_st32(s_addr + 32u * c, pw);
-                        publish(c == 0 ? B_PFULL : B_PHALF);
-                    }
-                } else {
-                    // (P's 16 columns never reach scores that are still to be loaded)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t *x = sv + 32 * (c & 1), pw[16];
-                        if (c >= 2) {
-                            tmem_ld32(s_addr + 32u * c, x);
-                            tmem_wait_ld();
-                            if (cut) {
-#pragma unroll
-                                for (int e = 0; e < 32; ++e)
-                                    if (32 * c + e > lim)
-                                        x[e] = __float_as_uint(DDT_NEG_INF);
-                            }
-                        }
-                        exps(std::integral_constant<int, 16>(), x, pw);
-                        tmem_st16(s_addr + 16u * c, pw);
-                        if (c & 1)
-                            publish(c == 1 ? B_PFULL : B_PHALF);
+                // m need not be the row's maximum, only near enough to it: while a step's
+                // weights add up to no more than LIMIT, none of them is larger. So the
+                // maximum is looked for on the item's first step, with the mask, and when
+                // a sum says so (NaN does); S is then read anew, so that no register of
+                // the common path outlives a branch (that cost 250 cycles of 1000 a step).
+                bool done = false;
+                const bool common = j > 0 && key0 + SUB - 1 <= pos_warp;
+                if (common) {
+                    uint32_t sv[SUB], pw[SUB / 2];
+                    tmem_ld32(buf, sv);
+                    tmem_ld32(buf + 32u, sv + 32);
+                    tmem_wait_ld();
+                    const float sum = weigh(sv, pw);
+                    done = __all_sync(0xFFFFFFFFu, sum <= LIMIT<KV4> && m_used != DDT_NEG_INF);
+                    if (done) {
+                        l += sum;
+                        tmem_st32(buf, pw);
                     }
                 }
-                float r0, r1;
-                f2unpack(f2add(sum0, sum1), r0, r1);
-                l = l * alpha + (r0 + r1);
+                if (!KV4 && !common && key0 > pos_top) {
+                    // nothing for these rows
+                    uint32_t pw[SUB / 2];
+#pragma unroll
+                    for (int e = 0; e < SUB / 2; ++e)
+                        pw[e] = 0;
+                    tmem_st32(buf, pw);
+                } else if (!done) {
+                    uint32_t sv[SUB], pw[SUB / 2];
+                    tmem_ld32(buf, sv);
+                    tmem_ld32(buf + 32u, sv + 32);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int w = 0; w < SUB / 32; ++w) {
+                        const int last = pos - key0 - 32 * w;  // the row's last key, in these columns
+                        const uint32_t mk = last < 0 ? 0u : last >= 31 ? 0xFFFFFFFFu : (2u << last) - 1u;
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (!(mk & (1u << c)))
+                                sv[32 * w + c] = __float_as_uint(DDT_NEG_INF);
+                    }
+                    float m4[4] = {DDT_NEG_INF, DDT_NEG_INF, DDT_NEG_INF, DDT_NEG_INF};
+#pragma unroll
+                    for (int c = 0; c < SUB; c += 8)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            m4[e] = fmaxf(m4[e], fmaxf(__uint_as_float(sv[c + 2 * e]), __uint_as_float(sv[c + 2 * e + 1])));
+                    const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * scale;
+                    // (a sum above the limit moves m even by less than TAU: the next one
+                    // would be above it again)
+                    if (__any_sync(0xFFFFFFFFu, top > m_used + (common ? 0.f : TAU))) {
+                        const float m = fmaxf(m_used, top), alpha = m == m_used ? 1.f : ex2(m_used - m);  // 0 from -inf
+                        m_used = m;
+                        l *= alpha;
+                        if (j > 0) {
+                            // O must not have P V of the step before under way (that of the one
+                            // before it is complete: this S was issued behind it)
+                            if (!wait_warp(bar + B_ODONE + 8 * g, (n - 1) & 1, abort_flag, a.status)) {
+                                alive = false;
+                                break;
+                            }
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < D / 32; ++c) {
+                                uint32_t ov[32];
+                                tmem_ld32(o_addr + 32u * c, ov);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    ov[e] = __float_as_uint(__uint_as_float(ov[e]) * alpha);
+                                tmem_st32(o_addr + 32u * c, ov);
+                            }
+                        }
+                    }
+                    l += weigh(sv, pw);
+                    tmem_st32(buf, pw);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(bar + B_PFULL + 16 * g + 8 * (n & 1));
             }
             if (!alive)
                 break;

@@ -32,8 +32,10 @@ cudaError_t launch_prompt_few(ddt_ctx *c, const PtArgs &a, const uint16_t *q, in
 
 namespace {
 
-constexpr int MIN_UNITS = 4;  // of a share
-constexpr float TAU = 8.0f;   // lazy-rescale threshold (log2 units)
+// Units of a share at least: an item of one tile is not cut (one token behind 10 takes
+// 9 us; cut, 11.5).
+constexpr int MIN_UNITS = 1 + PP_ITEM;
+constexpr float TAU = 8.0f;   // growth of a maximum that the running one may lag behind (log2 units)
 // 4-bit cache: probabilities are held times 2^7, at most 2^(7 + TAU) (fp16 ends at
 // 65504), so that what fp16 cannot hold lies 2^-32 below the row's largest
 constexpr float PBIAS = 7.0f;

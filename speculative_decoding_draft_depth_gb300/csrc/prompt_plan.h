@@ -18,7 +18,7 @@
 
 constexpr int PP_TILE = 128;   // keys of a tile
 constexpr int PP_ROWS = 256;   // rows of a query tile
-constexpr int PP_ITEM = 4;     // units of an item besides its tiles
+constexpr int PP_ITEM = 3;     // units of an item besides its tiles
 
 struct PpReq {   // one request, and where its units begin
     int q0, len, ctx;  // first packed row, tokens (0: none, or skipped), cached tokens

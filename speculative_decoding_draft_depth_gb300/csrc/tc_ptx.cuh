@@ -115,17 +115,6 @@ TC_DEVINL void cp_async_16(uint32_t dst, const void *src, uint32_t src_bytes)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes)
                  : "memory");
 }
-// 8- and 4-byte forms
-TC_DEVINL void cp_async_8(uint32_t dst, const void *src, uint32_t src_bytes)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(src_bytes)
-                 : "memory");
-}
-TC_DEVINL void cp_async_4(uint32_t dst, const void *src, uint32_t src_bytes)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes)
-                 : "memory");
-}
 // close this thread's group of copies; wait until at most N younger groups are open
 TC_DEVINL void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>

@@ -131,7 +131,13 @@ class Packed:
         most e = 2^-22 (d/16) sum |q_i k_i| / sqrt(d) (the products are exact, a
         partial sum of 16 is rounded each time, to two bits less than fp32 has),
         plus 2^-22 |s| for its scaling, which moves p_j by a factor within
-        exp(+-2e) through numerator and sum; exp2 and the fp32 sums add 2^-20."""
+        exp(+-2e) through numerator and sum; exp2 and the fp32 sums add 2^-20.
+        Over the 4-bit cache a probability is an fp16 number: the weight
+        w = 2^7 2^(s - m), with m no more than the row's largest score, is rounded
+        to 11 bits or, below 2^-14, to a multiple of 2^-24. The second error is at
+        most 2^-25, so 2^-32 of a weight at m, and the sum of weights is at least
+        one weight at the row's largest score: it moves the result by at most
+        2^-32 sum_j |v_j| over the row's keys."""
         q = self.q if q is None else q
         out = torch.full((self.T, self.Hq, self.d), SENTINEL, dtype=torch.float64, device="cuda")
         tol = torch.zeros_like(out)
@@ -155,6 +161,9 @@ class Packed:
             out[s0:s0 + n] = o.reshape(n, self.Hq, self.d)
             # 1.01: products of two of these errors
             tol[s0:s0 + n] = (1.01 * (2.0 ** -8 * o.abs() + rel * A)).reshape(n, self.Hq, self.d)
+            if self.bits == 4:
+                seen = torch.einsum("mn,nhd->mhd", (~ahead).double(), v.abs())
+                tol[s0:s0 + n] += (1.01 * 2.0 ** -32 * seen).repeat_interleave(self.Hq // self.Hkv, 1)
         return out, tol
 
 

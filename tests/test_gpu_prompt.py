@@ -103,6 +103,33 @@ def test_growing_scores():
     check_close(got, want, tol)
 
 
+@pytest.mark.parametrize("kind", ["creep", "leap", "fall", "flat"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("bits", [16, 4])
+def test_scores_that_change_along_the_keys(bits, d, kind):
+    """Keys whose first channel, which every query weighs by 4, moves the scores in
+    64-key steps that no mask touches: up by some three bits a step, by far at two
+    keys, down from the first on, or not at all (every key equal)."""
+    p = Packed([1, 300, 40], [1500, 900, 1300], 8, 2, d, 16, bits, seed=36)
+    p.q[..., 0] = 4
+    p.fill_context()
+    p.fill_new()
+    for r, (n, c) in enumerate(zip(p.lens, p.ctx)):
+        k, v = p._normal(n + c, 2, d).bfloat16(), p._normal(n + c, 2, d).bfloat16()
+        at = torch.arange(n + c, device="cuda")
+        if kind == "flat":
+            k.zero_()
+        else:
+            h = {"creep": at / 64 * (d ** 0.5 / 2), "leap": ((at == 700) | (at == 1203)) * 60.0,
+                 "fall": (n + c - at) / 20.0}[kind]
+            k[..., 0] = h[:, None].bfloat16()
+        p.put(r, 0, n + c, k, v)
+    got = p.attend()
+    want, tol = p.attention64()
+    check_close(got, want, tol)
+    assert p.h.ddt_device_status() == 0
+
+
 def test_global_scales():
     run(Packed([3, 40, 1], [90, 200, 400], 8, 2, 128, 16, 4, seed=27, k_scale=0.37, v_scale=1.0 / 1024, v_gain=1e-3))
 
