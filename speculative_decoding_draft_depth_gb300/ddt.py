@@ -138,8 +138,11 @@ def _rows(t, name, T, heads, d):
         return 0
     if t.stride(2) != 1 or (heads > 1 and t.stride(1) != d):
         raise ValueError("%s: expected each token's heads and channels dense" % name)
-    # (a single row has no next one)
-    return t.stride(0) if T > 1 else 0
+    if T <= 1:  # (a single row has no next one)
+        return 0
+    if t.stride(0) < heads * d:  # (an expanded or unfolded tensor: its rows share memory)
+        raise ValueError("%s: expected tokens that do not overlap" % name)
+    return t.stride(0)
 
 
 def check_append(cfg, q, k, v, q_start, ctx_lens, block_table, R, q_out, rotary, new_lens):

@@ -110,6 +110,24 @@ def test_prompt_shapes_are_checked(name, value):
         ddt.check_prompt(_cfg(), **t)
 
 
+@pytest.mark.parametrize("name", ["q", "k", "v"])
+def test_rows_that_share_memory_are_refused(name):
+    """One row expanded over the tokens, and rows that begin inside the last one:
+    a stride of 0 would otherwise stand for dense rows."""
+    heads = 8 if name == "q" else 2
+    row = torch.zeros(1, heads, 64, dtype=torch.bfloat16)
+    half = torch.zeros(7 * heads * 32, dtype=torch.bfloat16).as_strided((6, heads, 64), (heads * 32, 64, 1))
+    for bad in (row.expand(6, heads, 64), half):
+        t = _tensors()
+        t[name] = bad
+        with pytest.raises(ValueError):
+            ddt.check_append(_cfg(), **t)
+        if name == "q":
+            p = {k: v for k, v in t.items() if k in ("q", "q_start", "ctx_lens", "block_table", "R")}
+            with pytest.raises(ValueError):
+                ddt.check_prompt(_cfg(), out=torch.zeros(6, 8, 64, dtype=torch.bfloat16), **p)
+
+
 def test_cache_shapes_are_checked():
     def u8(*s):
         return torch.zeros(*s, dtype=torch.uint8)
