@@ -50,9 +50,9 @@
 //    takes two warps of each scheduler 900 cycles, of which 512 are exponentials.
 //    With the maximum in every step it was 127 us; with the mask and the maximum as
 //    branches of one path (registers copied at their joins) 137.
-//  * 64 tokens behind 512 to 16384 cached: 361 us, 6.7 TB/s.
-//  * 4-bit cache, four chunks of 1500 to 2048 tokens behind 4000 to 16000: 0.90 ms,
-//    1320 TFLOP/s. Bound by the instructions of softmax and conversion together.
+//  * 64 tokens behind 512 to 16384 cached: 361 to 371 us, 6.5 to 6.7 TB/s.
+//  * 4-bit cache, four chunks of 1500 to 2048 tokens behind 4000 to 16000: 0.88 ms,
+//    1350 TFLOP/s. Bound by the instructions of softmax and conversion together.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -95,6 +95,10 @@ constexpr long long DRAIN_LIMIT = 200000000LL;
 // shared memory (offsets from a 1024-byte aligned base)
 constexpr int NK = 2;
 constexpr int SUB = 64;  // keys of a softmax step: half a tile
+// scores of a step that a thread holds at a time (64 of them spill beside the 4-bit
+// cache's 112 registers: 0.90 ms for four chunks of prompts, in halves 0.88)
+template <bool KV4>
+constexpr int CHUNK = KV4 ? 32 : SUB;
 // what a step's weights of a row may add up to before the maximum is looked for again
 template <bool KV4>
 constexpr float LIMIT = KV4 ? 32768.f : 256.f;
@@ -724,6 +728,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         const uint32_t lane_addr = (uint32_t)(qw * 32) << 16;
         const uint32_t s_addr = tmem + lane_addr + TM_S + 128u * g;
         const uint32_t o_addr = tmem + lane_addr + TM_O + 128u * g;
+        constexpr int CH = CHUNK<KV4>;
         float2 *ml = reinterpret_cast<float2 *>(sgen + SM_BAR<KV4> + B_ML);
         int n = 0, no = 0, nx = 0;  // the group's steps, items with steps, split items so far
         for (int k = 0;; ++k) {
@@ -753,12 +758,12 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 // P = exp2(scale S - m), rounded to bf16 (fp16 with its range moved up) for
                 // the tensor cores; the sum takes the unrounded values. A row with nothing
                 // yet has m = -inf.
-                auto weigh = [&](const uint32_t (&sv)[SUB], uint32_t (&pw)[SUB / 2]) {
+                auto weigh = [&](const uint32_t (&sv)[CH], uint32_t *pw) {
                     const float off = (KV4 ? PBIAS : 0.f) - (m_used == DDT_NEG_INF ? 0.f : m_used);
                     const uint64_t sc2 = f2pack(scale, scale), nm2 = f2pack(off, off);
                     uint64_t sum0 = f2pack(0.f, 0.f), sum1 = sum0;
 #pragma unroll
-                    for (int e = 0; e < SUB / 2; ++e) {
+                    for (int e = 0; e < CH / 2; ++e) {
                         float x0, x1;
                         f2unpack(f2fma(f2pack(__uint_as_float(sv[2 * e]), __uint_as_float(sv[2 * e + 1])), sc2, nm2), x0, x1);
                         x0 = ex2(x0);
@@ -773,6 +778,24 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     f2unpack(f2add(sum0, sum1), r0, r1);
                     return r0 + r1;
                 };
+                auto load = [&](int c, uint32_t (&sv)[CH]) {  // CH columns from c on
+#pragma unroll
+                    for (int x = 0; x < CH; x += 32)
+                        tmem_ld32(buf + c + x, sv + x);
+                    tmem_wait_ld();
+                };
+                auto load_masked = [&](int c, uint32_t (&sv)[CH]) {
+                    load(c, sv);
+#pragma unroll
+                    for (int w = 0; w < CH / 32; ++w) {
+                        const int last = pos - key0 - c - 32 * w;  // the row's last key, in these columns
+                        const uint32_t mk = last < 0 ? 0u : last >= 31 ? 0xFFFFFFFFu : (2u << last) - 1u;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (!(mk & (1u << e)))
+                                sv[32 * w + e] = __float_as_uint(DDT_NEG_INF);
+                    }
+                };
                 // m need not be the row's maximum, only near enough to it: while a step's
                 // weights add up to no more than LIMIT, none of them is larger. So the
                 // maximum is looked for on the item's first step, with the mask, and when
@@ -781,11 +804,13 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 bool done = false;
                 const bool common = j > 0 && key0 + SUB - 1 <= pos_warp;
                 if (common) {
-                    uint32_t sv[SUB], pw[SUB / 2];
-                    tmem_ld32(buf, sv);
-                    tmem_ld32(buf + 32u, sv + 32);
-                    tmem_wait_ld();
-                    const float sum = weigh(sv, pw);
+                    uint32_t sv[CH], pw[SUB / 2];
+                    float sum = 0.f;
+#pragma unroll
+                    for (int c = 0; c < SUB; c += CH) {
+                        load(c, sv);
+                        sum += weigh(sv, pw + c / 2);
+                    }
                     done = __all_sync(0xFFFFFFFFu, sum <= LIMIT<KV4> && m_used != DDT_NEG_INF);
                     if (done) {
                         l += sum;
@@ -800,26 +825,20 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         pw[e] = 0;
                     tmem_st32(buf, pw);
                 } else if (!done) {
-                    uint32_t sv[SUB], pw[SUB / 2];
-                    tmem_ld32(buf, sv);
-                    tmem_ld32(buf + 32u, sv + 32);
-                    tmem_wait_ld();
+                    uint32_t sv[CH], pw[SUB / 2];
+                    float top = DDT_NEG_INF;
 #pragma unroll
-                    for (int w = 0; w < SUB / 32; ++w) {
-                        const int last = pos - key0 - 32 * w;  // the row's last key, in these columns
-                        const uint32_t mk = last < 0 ? 0u : last >= 31 ? 0xFFFFFFFFu : (2u << last) - 1u;
+                    for (int c = 0; c < SUB; c += CH) {
+                        load_masked(c, sv);
+                        float m4[4] = {DDT_NEG_INF, DDT_NEG_INF, DDT_NEG_INF, DDT_NEG_INF};
 #pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (!(mk & (1u << c)))
-                                sv[32 * w + c] = __float_as_uint(DDT_NEG_INF);
+                        for (int x = 0; x < CH; x += 8)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                m4[e] = fmaxf(m4[e], fmaxf(__uint_as_float(sv[x + 2 * e]), __uint_as_float(sv[x + 2 * e + 1])));
+                        top = fmaxf(top, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])));
                     }
-                    float m4[4] = {DDT_NEG_INF, DDT_NEG_INF, DDT_NEG_INF, DDT_NEG_INF};
-#pragma unroll
-                    for (int c = 0; c < SUB; c += 8)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            m4[e] = fmaxf(m4[e], fmaxf(__uint_as_float(sv[c + 2 * e]), __uint_as_float(sv[c + 2 * e + 1])));
-                    const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * scale;
+                    top *= scale;
                     // (a sum above the limit moves m even by less than TAU: the next one
                     // would be above it again)
                     if (__any_sync(0xFFFFFFFFu, top > m_used + (common ? 0.f : TAU))) {
@@ -846,7 +865,15 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                             }
                         }
                     }
-                    l += weigh(sv, pw);
+                    if (CH == SUB) {
+                        l += weigh(sv, pw);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < SUB; c += CH) {
+                            load_masked(c, sv);
+                            l += weigh(sv, pw + c / 2);
+                        }
+                    }
                     tmem_st32(buf, pw);
                 }
                 tmem_wait_st();
@@ -1065,7 +1092,9 @@ cudaError_t launch_prompt_attention(ddt_ctx *c, const uint16_t *q, int64_t q_str
         a.out_scale = kv4->v_scale;
     }
     // Few rows of a request (on average: lengths are the device's) over the 4-bit
-    // cache have a kernel of their own.
+    // cache have a kernel of their own. 64 requests behind 8000, 32/8 heads of 128, this
+    // kernel and that one: one token (4 rows) 363 and 140 us, two 364 and 142, four (16
+    // rows) 366 and 197, eight (32: it reads the cache twice) 370 and 377.
     if (kv4 && (int64_t)T * G <= (int64_t)R * 16)
         return launch_prompt_few(c, a, q, q_stride, G <= 8 && (int64_t)T * G <= (int64_t)R * 8 ? 8 : 16, s);
     CUtensorMap tq, tk = {}, tv = {};

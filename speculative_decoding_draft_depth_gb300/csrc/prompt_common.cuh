@@ -242,7 +242,10 @@ DDT_DEVINL uint32_t pack_f16x2(float lo, float hi)
 
 // Merge of a cut item: boundary b (between CTAs b - 1 and b) takes the j-th of
 // the nb row blocks of the item that it cuts, if it lies among the item's tiles
-// (nb: the boundaries that do).
+// (nb: the boundaries that do). Partials come from L2; what counts is how many CTAs
+// read them: with up to 1, 2, 4, 8 CTAs a boundary 32 packed prompts take 134, 123, 119,
+// 122 us, one prompt of 512 tokens 50, 34, 30, 28, and 64 tokens behind a thousand
+// cached 56, 56, 57, 61 (many CTAs of few rows).
 constexpr int MG_THREADS = 256, MG_SPLIT = 4;
 
 template <int D>
