@@ -199,9 +199,13 @@ struct ShareWalk {
                         base += it.start;
                         it.start = 0;
                         it.qt = 0;
-                        do
-                            rq = load_req(a, ++r);  // (units remain, so a request with tokens follows)
-                        while (rq.len == 0);
+                        do {  // (units remain, so a request with tokens follows)
+                            if (++r >= a.R) {
+                                cur = hi;  // (not so: lengths that changed under the call)
+                                break;
+                            }
+                            rq = load_req(a, r);
+                        } while (rq.len == 0);
                     }
                     it.n = pp_tiles(rq, it.qt, tq);
                 }
