@@ -422,7 +422,8 @@ ddt_status ddt_schedule_prefix(ddt_ctx *ctx, const float *conf, int32_t R, const
  * when q_start[r] > q_start[r+1], either lies outside [0, T], ctx_lens[r] < 0,
  * or its last slot passes max_pages_per_req * page_size (for the append with a
  * rotation: or its last position passes max_pos). Rows of no request (before
- * q_start[0], behind q_start[R]) are neither read for a result nor written. */
+ * q_start[0], behind q_start[R]) are neither read for a result nor written;
+ * rows that two requests name (q_start fell between them) get either's. */
 typedef struct ddt_append_args {
     int32_t R;                  /* requests, at most R_max */
     int32_t T;                  /* rows of q, k, v and q_out */

@@ -196,6 +196,51 @@ def test_bad_lengths_skip_their_request(kind):
     assert p.h.ddt_device_status() == ddt.DEV_BAD_LENGTH
 
 
+@pytest.mark.parametrize("bits", [16, 4])
+def test_the_last_slot_of_the_table(bits):
+    """A request whose tokens end with the block table's last page."""
+    p = Packed([5, 130], [40, 300], 8, 2, 64, 16, bits, seed=37)
+    free = sorted(set(range(p.num_pages)) - set(p.table.flatten().tolist()))
+    assert int(p.table[1, -1]) < 0 and bool((p.table[1, :-1] >= 0).all())
+    p.table[1, -1] = free[0]
+    p.ctx[1] = p.max_pages * 16 - 130
+    p.ctx_lens.copy_(torch.tensor(p.ctx, dtype=torch.int32))
+    run(p)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_requests_that_share_pages(bits):
+    """A prefix held once: both tables begin with the same pages."""
+    p = Packed([3, 70], [200, 260], 8, 2, 128, 16, bits, seed=38)
+    p.table[1, :12] = p.table[0, :12]
+    run(p)
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_rows_of_no_request(bits):
+    """Rows, but not a token of any request: nothing is written."""
+    p = Packed([0, 0, 0], [5, 0, 90], 8, 2, 64, 16, bits, seed=39, lead=2, tail=40)
+    p.fill_context()
+    assert bool((p.attend() == SENTINEL).all())
+    assert p.h.ddt_device_status() == 0
+
+
+@pytest.mark.parametrize("bits", [16, 4])
+def test_rows_that_two_requests_name(bits):
+    """q_start that falls: the request with the fall is skipped, and rows that the
+    two around it both name hold the result of either."""
+    p = Packed([6, 3, 7], [30, 4, 50], 8, 2, 64, 16, bits, seed=40)
+    p.fill_context()
+    p.fill_new()
+    want, tol = p.attention64()
+    p.q_start.copy_(torch.tensor([0, 6, 2, 9], dtype=torch.int32))
+    got = p.attend()
+    assert p.h.ddt_device_status() == ddt.DEV_BAD_LENGTH
+    check_close(got[:2], want[:2], tol[:2])
+    assert bool((got[9:] == SENTINEL).all())
+    assert bool(got[:9].isfinite().all()) and not bool((got[:9] == SENTINEL).all(-1).any())
+
+
 def test_refusals():
     p = Packed([4, 4], [0, 3], 4, 2, 64, 16, 16, seed=32)
     lib = ddt.load()
