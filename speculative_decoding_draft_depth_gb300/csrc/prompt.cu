@@ -46,8 +46,10 @@
 //    (1740) but for 6 to 10%.
 //    S of a whole tile at once (N = 128, 32 cycles per 64 keys) needs both buffers, so
 //    a group has no next S while its softmax runs: 1.66 ms.
-//  * 32 prompts of up to 2047 tokens, 8 heads of 64: 119 us. Softmax bound: a step
-//    takes two warps of each scheduler 900 cycles, of which 512 are exponentials.
+//  * 32 prompts of up to 2047 tokens, 8 heads of 64: 119 us. A step takes 1080 cycles:
+//    the softmax of two warps a scheduler (700 to 900, of which 512 are exponentials) and
+//    the chain from P over P V to the next S are about as long, so that sixteen softmax
+//    warps, a third buffer of S, or sums made by the tensor core each gave 1% or nothing.
 //    With the mask and the maximum as branches of one path (registers copied at their
 //    joins) 137; the common path by itself 127; zeros at once where a warp's rows have
 //    no key 123; an item at three units in the shares 119.
