@@ -423,7 +423,9 @@ ddt_status ddt_schedule_prefix(ddt_ctx *ctx, const float *conf, int32_t R, const
  * or its last slot passes max_pages_per_req * page_size (for the append with a
  * rotation: or its last position passes max_pos). Rows of no request (before
  * q_start[0], behind q_start[R]) are neither read for a result nor written;
- * rows that two requests name (q_start fell between them) get either's. */
+ * rows that two requests name (q_start fell between them) belong to the later
+ * one in an append, and get either's result, element by element, from an
+ * attention. */
 typedef struct ddt_append_args {
     int32_t R;                  /* requests, at most R_max */
     int32_t T;                  /* rows of q, k, v and q_out */
