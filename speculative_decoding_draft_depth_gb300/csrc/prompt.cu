@@ -127,13 +127,16 @@ constexpr uint32_t B_QFULL = 0, B_QEMPTY = 8, B_KFULL = 16, B_KEMPTY = 32, B_VFU
                    B_RFULL = 240,     // [NRING]
                    B_REMPTY = 304,    // [NRING]
                    B_RING = 368,      // [NRING][8] ints
-                   B_FOUND = B_RING,  // three 64-bit words, before the walk begins
-                   B_ML = 624,        // [128] float2: B's (m, l); before the roles start, the scan's sums
-                   B_ROWSC = 1648;    // 4 bits: [2][256] floats: the row's factor, by item parity
+                   B_FOUND = 624,     // three 64-bit words of the share search: apart from the ring, whose first
+                                      // entry one lane of the walker writes while others may still read them
+                   B_ML = 648,        // [128] float2: B's (m, l); before the roles start, the scan's sums
+                   B_ROWSC = 1672;    // 4 bits: [2][256] floats: the row's factor, by item parity
 template <bool KV4>
 constexpr uint32_t B_END = B_ROWSC + (KV4 ? 2048 : 0);
 template <bool KV4>
 constexpr uint32_t SM_ALLOC = SM_BAR<KV4> + B_END<KV4> + 1024;
+static_assert(B_FOUND >= B_RING + NRING * 8 * 4 && B_ML >= B_FOUND + 3 * 8, "the share search's words are their own");
+static_assert(B_ML % 8 == 0 && B_ROWSC >= B_ML + 128 * 8, "(m, l) pairs");
 static_assert(SM_ALLOC<false> <= 232448 && SM_ALLOC<true> <= 232448, "shared memory of one CTA");
 
 template <bool KV4>
