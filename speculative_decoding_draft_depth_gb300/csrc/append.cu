@@ -159,13 +159,12 @@ template <int D, bool KV4>
 __global__ void __launch_bounds__(AP_THREADS, 5) append_kernel(const ApArgs p)
 {
     constexpr int PIECES = D / 16;  // of a head
-    // the token's request + 1 in the high half, its position in the low one (0: no request)
-    __shared__ unsigned long long s_own[AP_TOKENS];
+    __shared__ int s_r[AP_TOKENS], s_pos[AP_TOKENS];  // the token's request and position, -1: no request
     __shared__ int64_t s_row[AP_TOKENS];  // the token's row of the pool, -1: no slot
     const ddt_append_args &a = p.a;
     const int tid = threadIdx.x, t0 = blockIdx.x * p.tokens;
     if (tid < p.tokens)
-        s_own[tid] = 0;
+        s_r[tid] = -1;
     __syncthreads();
     // every thread looks at some of the requests: one round of independent
     // loads instead of a chain of dependent ones
@@ -179,15 +178,19 @@ __global__ void __launch_bounds__(AP_THREADS, 5) append_kernel(const ApArgs p)
             if (a.new_lens)
                 a.new_lens[r] = ok ? ctx + (q1 - q0) : ctx;
         }
-        // One word, so that request and position belong together; of two requests that
-        // name the row (q_start fell between them) the later one has it.
+        // Of two requests that name the row (q_start fell between them) the later one has
+        // it; the position follows from the owner, so that the two belong together.
         if (ok)
             for (int t = max(q0, t0); t < min(q1, t0 + p.tokens); ++t)
-                atomicMax(&s_own[t - t0], (unsigned long long)(r + 1) << 32 | (unsigned)(ctx + (t - q0)));
+                atomicMax(&s_r[t - t0], r);
     }
     __syncthreads();
-    if (tid < p.tokens && s_own[tid] != 0) {
-        const int pos = (int)(uint32_t)s_own[tid], r = (int)(s_own[tid] >> 32) - 1;
+    if (tid < p.tokens) {
+        const int r = s_r[tid];
+        s_pos[tid] = r < 0 ? -1 : __ldg(&a.ctx_lens[r]) + (t0 + tid - __ldg(&a.q_start[r]));
+    }
+    if (tid < p.tokens && s_r[tid] >= 0) {
+        const int pos = s_pos[tid], r = s_r[tid];
         const int pg = __ldg(&a.block_table[(int64_t)r * p.max_pages + (pos >> p.page_shift)]);
         const bool ok = pg >= 0 && pg < p.num_pages;
         if (!ok)
@@ -206,7 +209,7 @@ __global__ void __launch_bounds__(AP_THREADS, 5) append_kernel(const ApArgs p)
         static_assert(AP_TOKENS == 4, "the token by comparison");
         const int tk = (e >= per_token) + (e >= 2 * per_token) + (e >= 3 * per_token);
         const int h = (e - tk * per_token) / PIECES, piece = e % PIECES;  // (whole heads: pieces stay aligned)
-        const bool live = e0 + tid < n && s_own[tk] != 0;
+        const bool live = e0 + tid < n && s_r[tk] >= 0;
         const bool is_q = h < p.Hq, is_k = !is_q && h < p.Hq + p.Hkv;
         const int hk = is_q ? h : (h - p.Hq) - (is_k ? 0 : p.Hkv);
         const bool turned = (is_q || is_k) && piece * 16 < a.rotary_dim;
@@ -225,7 +228,7 @@ __global__ void __launch_bounds__(AP_THREADS, 5) append_kernel(const ApArgs p)
                 x[i] = 0.f;
         }
         if (live && turned) {
-            const float4 *row = reinterpret_cast<const float4 *>(a.cos_sin + (int64_t)(uint32_t)s_own[tk] * a.rotary_dim +
+            const float4 *row = reinterpret_cast<const float4 *>(a.cos_sin + (int64_t)s_pos[tk] * a.rotary_dim +
                                                                  piece * 8);
             const float4 c0 = __ldg(row), c1 = __ldg(row + 1);
             const float4 n0 = __ldg(row + half / 4), n1 = __ldg(row + half / 4 + 1);
