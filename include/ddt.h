@@ -477,7 +477,8 @@ typedef struct ddt_kv4 {
 } ddt_kv4;
 
 /* The same append into a cache held in 4 bits: for each block, with g the
- * cache's k_scale or v_scale, scale = e4m3(min(amax * (1 / (6 g)), 448)) and
+ * cache's k_scale or v_scale, scale = e4m3(min(amax / (6 g), 448)) (6 g and the
+ * quotient rounded to fp32) and
  * each channel's code the magnitude nearest to the quotient |x| / (scale g) in
  * fp32, ties to the even code, 6 where it is larger. A block with a NaN gets a NaN scale and so
  * reads as NaN. k_held, v_held ([T, Hkv, d] bf16, dense, both or neither NULL;

@@ -93,7 +93,9 @@ DDT_DEVINL void from_e2m1x2(uint32_t b, float &lo, float &hi)
         : "r"(h2));
 }
 
-// A block's scale and what its codes need. With q = RN(x / s) the nearest code of q
+// A block's scale and what its codes need. The scale is the e4m3 number nearest to
+// RN(amax / (6 g)): the product amax RN(1 / (6 g)) alone can be a midpoint of e4m3 where
+// the quotient is one step below it, so it gets one residual as the codes' do. With q = RN(x / s) the nearest code of q
 // (ties to even) is the nearest code of x / s for g = 1: a midpoint t and s have at
 // most three and four significant bits, so t s is an fp32 number, and an x next to it
 // is at least as far from it, in units of x / s, as half a step of q at t. q comes from
@@ -107,7 +109,9 @@ struct Scale {
 DDT_DEVINL Scale make_scale(float amax, float inv6, float g)
 {
     Scale r;
-    const float raw = __fmul_rn(amax, inv6);
+    const float raw0 = __fmul_rn(amax, inv6);
+    // (beyond e4m3 the product will do: infinity would have no residual)
+    const float raw = raw0 <= 512.f ? __fmaf_rn(__fmaf_rn(-raw0, __fmul_rn(6.f, g), amax), inv6, raw0) : raw0;
     r.bits = to_e4m3(min_nan(raw, 448.f));
     r.s = __fmul_rn(from_e4m3(r.bits), g);
     r.y = __frcp_rn(r.s);
