@@ -425,7 +425,9 @@ ddt_status ddt_schedule_prefix(ddt_ctx *ctx, const float *conf, int32_t R, const
  * q_start[0], behind q_start[R]) are neither read for a result nor written;
  * rows that two requests name (q_start fell between them) belong to the later
  * one in an append, and get either's result, element by element, from an
- * attention. */
+ * attention. A tensor that a call writes (the pools of an append among them)
+ * that shares memory with another one it reads or writes is DDT_EINVAL, but for
+ * queries turned in place (q_out == q, dense). */
 typedef struct ddt_append_args {
     int32_t R;                  /* requests, at most R_max */
     int32_t T;                  /* rows of q, k, v and q_out */
@@ -444,9 +446,9 @@ typedef struct ddt_append_args {
     int32_t max_pos;            /* rows of cos_sin */
     int32_t interleaved;        /* 0: channels (j, j + rotary_dim / 2) form a pair; 1: (2j, 2j + 1) */
     uint16_t *q_out;            /* [T, Hq, d] bf16, dense: the turned queries; may be q itself when
-                                   q is dense (any other overlap is DDT_EINVAL) */
+                                   q is dense */
     int32_t *new_lens;          /* [R] or NULL: ctx_lens[r] + the request's tokens (ctx_lens[r] for
-                                   a skipped request); must not overlap ctx_lens */
+                                   a skipped request) */
 } ddt_append_args;
 
 /* Append: q and k of every new token turned by its position,
@@ -481,9 +483,8 @@ typedef struct ddt_kv4 {
  * quotient rounded to fp32) and
  * each channel's code the magnitude nearest to the quotient |x| / (scale g) in
  * fp32, ties to the even code, 6 where it is larger. A block with a NaN gets a NaN scale and so
- * reads as NaN. k_held, v_held ([T, Hkv, d] bf16, dense, both or neither NULL;
- * overlapping no other tensor): the values that the cache now holds for the new
- * tokens. */
+ * reads as NaN. k_held, v_held ([T, Hkv, d] bf16, dense, both or neither NULL):
+ * the values that the cache now holds for the new tokens. */
 ddt_status ddt_append_kvq(ddt_ctx *ctx, const ddt_append_args *args, const ddt_kv4 *cache,
                           uint16_t *k_held, uint16_t *v_held, void *stream);
 
@@ -496,7 +497,7 @@ ddt_status ddt_append_kvq(ddt_ctx *ctx, const ddt_append_args *args, const ddt_k
  * The result does not depend on what else runs (no atomics in its sums).
  *   q        [T, Hq, d] bf16 with q_stride elements from token to token (a
  *            multiple of 8, at least Hq * d; 0 = dense)
- *   out      [T, Hq, d] bf16, dense; must not overlap q
+ *   out      [T, Hq, d] bf16, dense
  *   k_cache, v_cache, block_table, ctx_lens, q_start: as above
  * Page ids out of range set DDT_DEV_BAD_PAGE and are read as zeros. Slots past
  * a request's last token are never attended to, whatever they hold; a NaN or

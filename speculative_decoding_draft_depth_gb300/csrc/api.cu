@@ -7,6 +7,7 @@
 #include <string.h>
 
 #include "ddt_internal.h"
+#include "packed_seq.h"
 
 namespace {
 
@@ -224,13 +225,6 @@ ddt_status chk_compact(const uint16_t *kc, const uint16_t *vc, const int32_t *bt
     return DDT_OK;
 }
 
-// byte ranges [a, a + na) and [b, b + nb) share a byte
-bool overlap(const void *a, int64_t na, const void *b, int64_t nb)
-{
-    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
-    return na > 0 && nb > 0 && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
-}
-
 // packed rows a call may carry (row indices plus a tile stay within 31 bits)
 const int32_t MAX_PACKED = 0x7fff0000;
 
@@ -259,6 +253,52 @@ ddt_status chk_kv4(const ddt_kv4 *c)
     return DDT_OK;
 }
 
+// the bytes of a bf16 pool; of a 4-bit one's codes, and an eighth of them its scales'
+int64_t pool_bytes(const ddt_ctx *ctx)
+{
+    return ctx->cfg.num_pages * ctx->cfg.page_size * ctx->cfg.Hkv * ctx->cfg.d * 2;
+}
+int64_t code_bytes(const ddt_ctx *ctx) { return pool_bytes(ctx) / 4; }
+
+int64_t table_bytes(const ddt_ctx *ctx, int32_t R) { return 4 * (int64_t)R * ctx->cfg.max_pages_per_req; }
+
+// what an append writes (the pools among it) lies apart from all else that it touches,
+// but for queries turned in place
+bool append_apart(const ddt_ctx *ctx, const ddt_append_args &a, const PsBytes *pools, int npools,
+                  const uint16_t *k_held, const uint16_t *v_held)
+{
+    const int64_t nq = (int64_t)ctx->cfg.Hq * ctx->cfg.d, nk = (int64_t)ctx->cfg.Hkv * ctx->cfg.d;
+    PsBytes w[8] = {{a.q_out, span_bytes(a.T, nq, nq)},
+                    {a.new_lens, 4 * (int64_t)a.R},
+                    {k_held, span_bytes(a.T, nk, nk)},
+                    {v_held, span_bytes(a.T, nk, nk)}};
+    for (int i = 0; i < npools; ++i)
+        w[4 + i] = pools[i];
+    const PsBytes q = {a.q, span_bytes(a.T, a.q_stride, nq)};
+    const PsBytes r[] = {{a.k, span_bytes(a.T, a.k_stride, nk)},
+                         {a.v, span_bytes(a.T, a.v_stride, nk)},
+                         {a.q_start, 4 * ((int64_t)a.R + 1)},
+                         {a.ctx_lens, 4 * (int64_t)a.R},
+                         {a.block_table, table_bytes(ctx, a.R)},
+                         {a.cos_sin, a.cos_sin ? 4 * (int64_t)a.max_pos * a.rotary_dim : 0}};
+    const int in_place = a.q == a.q_out && a.q_stride == nq ? 1 : 0;
+    return ps_apart(w, 4 + npools, r, 6) && ps_apart(w + in_place, 4 + npools - in_place, &q, 1);
+}
+
+// the same for an attention: out and what it reads (pools: n of them)
+bool prompt_apart(const ddt_ctx *ctx, const uint16_t *q, int64_t q_stride, const int32_t *q_start,
+                  const int32_t *ctx_lens, int32_t R, int32_t T, const int32_t *block_table,
+                  const PsBytes *pools, int n, const uint16_t *out)
+{
+    const int64_t nq = (int64_t)ctx->cfg.Hq * ctx->cfg.d;
+    const PsBytes w = {out, span_bytes(T, nq, nq)};
+    const PsBytes r[] = {{q, span_bytes(T, q_stride, nq)},
+                         {q_start, 4 * ((int64_t)R + 1)},
+                         {ctx_lens, 4 * (int64_t)R},
+                         {block_table, table_bytes(ctx, R)}};
+    return ps_apart(&w, 1, r, 4) && ps_apart(&w, 1, pools, n);
+}
+
 // the checks that both caches' appends share; *out: the arguments with strides resolved
 ddt_status chk_append(const ddt_ctx *ctx, const ddt_append_args *in, ddt_append_args *out)
 {
@@ -275,20 +315,12 @@ ddt_status chk_append(const ddt_ctx *ctx, const ddt_append_args *in, ddt_append_
     }
     DDT_CHECK(a.q_start && a.ctx_lens && a.block_table && aligned4(a.q_start) &&
               aligned4(a.ctx_lens) && aligned4(a.block_table));
-    DDT_CHECK(!a.new_lens || (aligned4(a.new_lens) &&
-                              !overlap(a.new_lens, 4 * (int64_t)a.R, a.ctx_lens, 4 * (int64_t)a.R)));
+    DDT_CHECK(aligned4(a.new_lens));
     DDT_CHECK((a.q == nullptr) == (a.q_out == nullptr));
     DDT_CHECK(good_stride(&a.q_stride, nq) && good_stride(&a.k_stride, nk) &&
               good_stride(&a.v_stride, nk));
     DDT_CHECK(a.T == 0 || (a.k && a.v));
     DDT_CHECK(aligned16(a.q) && aligned16(a.k) && aligned16(a.v) && aligned16(a.q_out));
-    if (a.q) {
-        const bool in_place = a.q == a.q_out && a.q_stride == nq;
-        const int64_t out_bytes = span_bytes(a.T, nq, nq);
-        DDT_CHECK(in_place || !overlap(a.q, span_bytes(a.T, a.q_stride, nq), a.q_out, out_bytes));
-        DDT_CHECK(!overlap(a.k, span_bytes(a.T, a.k_stride, nk), a.q_out, out_bytes) &&
-                  !overlap(a.v, span_bytes(a.T, a.v_stride, nk), a.q_out, out_bytes));
-    }
     if (a.cos_sin) {
         DDT_CHECK(aligned16(a.cos_sin) && a.max_pos >= 1 && a.rotary_dim >= 32 &&
                   a.rotary_dim % 32 == 0 && a.rotary_dim <= ctx->cfg.d);
@@ -315,7 +347,6 @@ ddt_status chk_prompt(const ddt_ctx *ctx, const uint16_t *q, int64_t *q_stride,
     DDT_CHECK(q && q_start && ctx_lens && block_table && out && good_stride(q_stride, nq));
     DDT_CHECK(aligned16(q) && aligned16(out) && aligned4(q_start) && aligned4(ctx_lens) &&
               aligned4(block_table));
-    DDT_CHECK(!overlap(q, span_bytes(T, *q_stride, nq), out, span_bytes(T, nq, nq)));
     return DDT_OK;
 }
 
@@ -897,6 +928,8 @@ ddt_status ddt_append_kv(ddt_ctx *ctx, const ddt_append_args *args, uint16_t *k_
     if (a.R == 0)
         return DDT_OK;
     DDT_CHECK(k_cache && v_cache && aligned16(k_cache) && aligned16(v_cache));
+    const PsBytes pools[] = {{k_cache, pool_bytes(ctx)}, {v_cache, pool_bytes(ctx)}};
+    DDT_CHECK(append_apart(ctx, a, pools, 2, nullptr, nullptr));
     if ((st = set_device(ctx)) != DDT_OK)
         return st;
     DDT_TRY(launch_append(ctx, a, k_cache, v_cache, nullptr, nullptr, nullptr,
@@ -914,16 +947,10 @@ ddt_status ddt_append_kvq(ddt_ctx *ctx, const ddt_append_args *args, const ddt_k
     if (a.R == 0)
         return DDT_OK;
     DDT_CHECK((k_held == nullptr) == (v_held == nullptr) && aligned16(k_held) && aligned16(v_held));
-    if (k_held) {
-        const int64_t nq = (int64_t)ctx->cfg.Hq * ctx->cfg.d, nk = (int64_t)ctx->cfg.Hkv * ctx->cfg.d;
-        const int64_t held = span_bytes(a.T, nk, nk);
-        DDT_CHECK(!overlap(k_held, held, v_held, held));
-        for (const uint16_t *h : {k_held, v_held})
-            DDT_CHECK(!overlap(h, held, a.k, span_bytes(a.T, a.k_stride, nk)) &&
-                      !overlap(h, held, a.v, span_bytes(a.T, a.v_stride, nk)) &&
-                      (!a.q || (!overlap(h, held, a.q, span_bytes(a.T, a.q_stride, nq)) &&
-                                !overlap(h, held, a.q_out, span_bytes(a.T, nq, nq)))));
-    }
+    const int64_t codes = code_bytes(ctx);
+    const PsBytes pools[] = {{cache->k_codes, codes}, {cache->v_codes, codes}, {cache->k_scales, codes / 8},
+                             {cache->v_scales, codes / 8}};
+    DDT_CHECK(append_apart(ctx, a, pools, 4, k_held, v_held));
     if ((st = set_device(ctx)) != DDT_OK)
         return st;
     DDT_TRY(launch_append(ctx, a, nullptr, nullptr, cache, k_held, v_held, (cudaStream_t)stream));
@@ -939,6 +966,8 @@ ddt_status ddt_prompt_attention(ddt_ctx *ctx, const uint16_t *q, int64_t q_strid
     if (st != DDT_OK || R == 0 || T == 0)
         return st;
     DDT_CHECK(k_cache && v_cache && aligned16(k_cache) && aligned16(v_cache));
+    const PsBytes pools[] = {{k_cache, pool_bytes(ctx)}, {v_cache, pool_bytes(ctx)}};
+    DDT_CHECK(prompt_apart(ctx, q, q_stride, q_start, ctx_lens, R, T, block_table, pools, 2, out));
     if ((st = set_device(ctx)) != DDT_OK)
         return st;
     DDT_TRY(launch_prompt_attention(ctx, q, q_stride, q_start, ctx_lens, R, T, k_cache, v_cache,
@@ -954,6 +983,10 @@ ddt_status ddt_prompt_attention_kvq(ddt_ctx *ctx, const uint16_t *q, int64_t q_s
     ddt_status st = chk_prompt(ctx, q, &q_stride, q_start, ctx_lens, R, T, block_table, out);
     if (st != DDT_OK || (st = chk_kv4(cache)) != DDT_OK || R == 0 || T == 0)
         return st;
+    const int64_t codes = code_bytes(ctx);
+    const PsBytes pools[] = {{cache->k_codes, codes}, {cache->v_codes, codes}, {cache->k_scales, codes / 8},
+                             {cache->v_scales, codes / 8}};
+    DDT_CHECK(prompt_apart(ctx, q, q_stride, q_start, ctx_lens, R, T, block_table, pools, 4, out));
     if ((st = set_device(ctx)) != DDT_OK)
         return st;
     DDT_TRY(launch_prompt_attention(ctx, q, q_stride, q_start, ctx_lens, R, T, nullptr, nullptr,
