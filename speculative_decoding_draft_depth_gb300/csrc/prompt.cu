@@ -467,8 +467,10 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             ++k;
             if constexpr (KV4)
                 continue;
-            if (!load_q(s, k - 1))
+            if (!load_q(s, k - 1)) {
+                --k;  // (k counts the loads of Q under way or over; the parity of one more would pass at once)
                 break;
+            }
             for (int j = s.t0; j < s.t1; ++j, ++kn) {
                 const int sl = kn % NK;
                 const int z = lane < 8 ? group_row(a, s, j, lane) : 0;
