@@ -25,7 +25,7 @@ EXPORTS = ("ddt_create", "ddt_destroy", "ddt_workspace_bytes", "ddt_topk_logprob
            "ddt_markov_table", "ddt_build_tree_markov", "ddt_round_markov",
            "ddt_accept_stochastic", "ddt_schedule_prefix", "ddt_append_kv", "ddt_append_kvq",
            "ddt_prompt_attention", "ddt_prompt_attention_kvq", "ddt_device_status", "ddt_strerror",
-           "ddt_last_cuda_error", "ddt_debug_arm_attention_timeout")
+           "ddt_last_cuda_error", "ddt_debug_arm_attention_timeout", "ddt_debug_arm_prompt_timeout")
 
 
 class DdtError(RuntimeError):
@@ -226,6 +226,7 @@ def load(path=LIB_PATH):
                                       _P], i32),
         "ddt_device_status": ([_P, ctypes.POINTER(i32)], i32),
         "ddt_debug_arm_attention_timeout": ([_P, i64], i32),
+        "ddt_debug_arm_prompt_timeout": ([_P, i64], i32),
         "ddt_strerror": ([i32], ctypes.c_char_p),
         "ddt_last_cuda_error": ([], i32),
     }
@@ -516,6 +517,11 @@ class Context:
         out after wait_cycles SM cycles (see include/ddt.h)."""
         _check(_lib.ddt_debug_arm_attention_timeout(self._h, int(wait_cycles)),
                "ddt_debug_arm_attention_timeout")
+
+    def ddt_debug_arm_prompt_timeout(self, wait_cycles):
+        """Test only: the waits of the next tensor-core prompt attention run out
+        after wait_cycles SM cycles (see include/ddt.h)."""
+        _check(_lib.ddt_debug_arm_prompt_timeout(self._h, int(wait_cycles)), "ddt_debug_arm_prompt_timeout")
 
     # -- allocation helper (plumbing) ----------------------------------------
     def alloc_outputs(self, R, device="cuda"):
