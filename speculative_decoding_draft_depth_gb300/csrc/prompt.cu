@@ -330,7 +330,7 @@ DDT_DEVINL float halve_row(unsigned char *q, int row)
             amax = max(amax, max(v[i] & 0x7FFFu, (v[i] >> 16) & 0x7FFFu));
     }
     int e = (int)(amax >> 7) - 127;
-    e = amax >= 0x7F80u ? 0 : max(-100, min(100, e));  // (rows with NaN or inf as they are)
+    e = amax >= 0x7F80u ? 0 : max(-100, min(126, e));  // (rows with NaN or inf as they are; 2^-126 is normal)
     const float f = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll 4
     for (int c = 0; c < D / 8; ++c) {
@@ -758,8 +758,8 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 }
                 tc_fence_after();
                 if (KV4 && j == 0)
-                    scale = a.scale_log2 *
-                            reinterpret_cast<const volatile float *>(sgen + SM_BAR<KV4> + B_ROWSC)[(k & 1) * 256 + (s.split ? 0 : 128 * g) + row];
+                    scale = row_scale(a, reinterpret_cast<const volatile float *>(
+                                             sgen + SM_BAR<KV4> + B_ROWSC)[(k & 1) * 256 + (s.split ? 0 : 128 * g) + row]);
                 const int key0 = s.tile(g, j >> 1) * PP_TILE + SUB * (j & 1);
                 // P = exp2(scale S - m), rounded to bf16 (fp16 with its range moved up) for
                 // the tensor cores; the sum takes the unrounded values. A row with nothing

@@ -70,6 +70,10 @@ DDT_DEVINL void seg_decode(const int *w, Seg &s)
     s.t1 = w[6];
 }
 
+// 4-bit cache: what a score is multiplied by whose query was divided by `power`. Finite:
+// an infinity would make a score of zero NaN.
+DDT_DEVINL float row_scale(const PtArgs &a, float power) { return fminf(a.scale_log2 * power, 3.402823466e38f); }
+
 DDT_DEVINL PpReq load_req(const PtArgs &a, int r)
 {
     const int s0 = __ldg(&a.q_start[r]), s1 = __ldg(&a.q_start[r + 1]), c = __ldg(&a.ctx_lens[r]);

@@ -257,9 +257,9 @@ __global__ void __launch_bounds__(FT, NR == 1 ? 2 : 1) prompt_few_kernel(const F
             amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
             amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
             int e2 = (int)(amax >> 7) - 127;
-            e2 = amax >= 0x7F80u ? 0 : max(-100, min(100, e2));  // (rows with NaN or inf as they are)
+            e2 = amax >= 0x7F80u ? 0 : max(-100, min(126, e2));  // (rows with NaN or inf as they are; 2^-126 is normal)
             const float down = __uint_as_float((uint32_t)(127 - e2) << 23);
-            const float up = __uint_as_float((uint32_t)(127 + e2) << 23) * a.scale_log2;
+            const float up = row_scale(a, __uint_as_float((uint32_t)(127 + e2) << 23));
 #pragma unroll
             for (int x = 0; x < D / 32; ++x) {
                 const float v[8] = {bf16lo(w[x].x), bf16hi(w[x].x), bf16lo(w[x].y), bf16hi(w[x].y),
