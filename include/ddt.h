@@ -495,6 +495,10 @@ ddt_status ddt_append_kvq(ddt_ctx *ctx, const ddt_append_args *args, const ddt_k
  * the 4-bit cache: to fp16, and a query's channels below 2^-14 of its largest to
  * 2^-25 of that) for the product with the values, one rounding of the result.
  * The result does not depend on what else runs (no atomics in its sums).
+ * Scores q . k / sqrt(d) may be as large as 2^20: a row's maximum is an fp32
+ * number, and what its rounding leaves in the exponent (2^-4 there) has to stay
+ * within what a probability can hold; far beyond, a row may come out as zeros or
+ * NaN. A row whose scores are all -infinity gives zeros.
  *   q        [T, Hq, d] bf16 with q_stride elements from token to token (a
  *            multiple of 8, at least Hq * d; 0 = dense)
  *   out      [T, Hq, d] bf16, dense
