@@ -196,7 +196,7 @@ def prepare(case, seed):
         st["out"] = torch.empty_like(st["q"])
     if own:
         from speculative_decoding_draft_depth_gb300 import ddt
-        st["ctx"] = ddt.Context(ddt.make_config(
+        st["handle"] = ddt.Context(ddt.make_config(
             R_max=R, L=4, V=32, B=8, Hq=Hq, Hkv=Hkv, d=d, page_size=page, max_pages_per_req=max_pages,
             num_pages=num_pages))
         if case["kind"] == "append":
@@ -221,7 +221,7 @@ def run(st):
 
 
 def _run_own(st, case):
-    h, R = st["ctx"], case["R"]
+    h, R = st["handle"], case["R"]
     if case["kind"] == "append" and case["bits"] == 16:
         h.ddt_append_kv(st["q"], st["k"], st["v"], st["q_start"], st["ctx_lens"], st["table"], R, st["k_cache"],
                         st["v_cache"], q_out=st["q_out"], rotary=st["rotary"])
