@@ -427,7 +427,9 @@ ddt_status ddt_schedule_prefix(ddt_ctx *ctx, const float *conf, int32_t R, const
  * one in an append, and get either's result, element by element, from an
  * attention. A tensor that a call writes (the pools of an append among them)
  * that shares memory with another one it reads or writes is DDT_EINVAL, but for
- * queries turned in place (q_out == q, dense). */
+ * queries turned in place (q_out == q, dense). The calls run on the
+ * context's device, whichever is current, and leave the calling thread's current
+ * device as it was. */
 typedef struct ddt_append_args {
     int32_t R;                  /* requests, at most R_max */
     int32_t T;                  /* rows of q, k, v and q_out */

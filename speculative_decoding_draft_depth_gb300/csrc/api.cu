@@ -7,6 +7,7 @@
 #include <string.h>
 
 #include "ddt_internal.h"
+#include "device_scope.h"
 #include "packed_seq.h"
 
 namespace {
@@ -167,6 +168,17 @@ ddt_status set_device(const ddt_ctx *ctx)
     }
     return DDT_OK;
 }
+
+struct CudaDevice {
+    static int get(int *device) { return (int)cudaGetDevice(device); }
+    static int set(int device) { return (int)cudaSetDevice(device); }
+};
+
+// the context's device for the rest of the function; the caller's own afterwards
+#define DDT_ON_DEVICE(ctx)                                                                         \
+    const DeviceScope<CudaDevice> on_device((ctx)->device);                                        \
+    if (on_device.err != 0)                                                                        \
+        return cuda_fail((cudaError_t)on_device.err);
 
 #define DDT_TRY(expr)                                                                              \
     do {                                                                                           \
@@ -930,8 +942,7 @@ ddt_status ddt_append_kv(ddt_ctx *ctx, const ddt_append_args *args, uint16_t *k_
     DDT_CHECK(k_cache && v_cache && aligned16(k_cache) && aligned16(v_cache));
     const PsBytes pools[] = {{k_cache, pool_bytes(ctx)}, {v_cache, pool_bytes(ctx)}};
     DDT_CHECK(append_apart(ctx, a, pools, 2, nullptr, nullptr));
-    if ((st = set_device(ctx)) != DDT_OK)
-        return st;
+    DDT_ON_DEVICE(ctx)
     DDT_TRY(launch_append(ctx, a, k_cache, v_cache, nullptr, nullptr, nullptr,
                           (cudaStream_t)stream));
     return DDT_OK;
@@ -951,8 +962,7 @@ ddt_status ddt_append_kvq(ddt_ctx *ctx, const ddt_append_args *args, const ddt_k
     const PsBytes pools[] = {{cache->k_codes, codes}, {cache->v_codes, codes}, {cache->k_scales, codes / 8},
                              {cache->v_scales, codes / 8}};
     DDT_CHECK(append_apart(ctx, a, pools, 4, k_held, v_held));
-    if ((st = set_device(ctx)) != DDT_OK)
-        return st;
+    DDT_ON_DEVICE(ctx)
     DDT_TRY(launch_append(ctx, a, nullptr, nullptr, cache, k_held, v_held, (cudaStream_t)stream));
     return DDT_OK;
 }
@@ -968,8 +978,7 @@ ddt_status ddt_prompt_attention(ddt_ctx *ctx, const uint16_t *q, int64_t q_strid
     DDT_CHECK(k_cache && v_cache && aligned16(k_cache) && aligned16(v_cache));
     const PsBytes pools[] = {{k_cache, pool_bytes(ctx)}, {v_cache, pool_bytes(ctx)}};
     DDT_CHECK(prompt_apart(ctx, q, q_stride, q_start, ctx_lens, R, T, block_table, pools, 2, out));
-    if ((st = set_device(ctx)) != DDT_OK)
-        return st;
+    DDT_ON_DEVICE(ctx)
     DDT_TRY(launch_prompt_attention(ctx, q, q_stride, q_start, ctx_lens, R, T, k_cache, v_cache,
                                     nullptr, block_table, out, (cudaStream_t)stream));
     return DDT_OK;
@@ -987,8 +996,7 @@ ddt_status ddt_prompt_attention_kvq(ddt_ctx *ctx, const uint16_t *q, int64_t q_s
     const PsBytes pools[] = {{cache->k_codes, codes}, {cache->v_codes, codes}, {cache->k_scales, codes / 8},
                              {cache->v_scales, codes / 8}};
     DDT_CHECK(prompt_apart(ctx, q, q_stride, q_start, ctx_lens, R, T, block_table, pools, 4, out));
-    if ((st = set_device(ctx)) != DDT_OK)
-        return st;
+    DDT_ON_DEVICE(ctx)
     DDT_TRY(launch_prompt_attention(ctx, q, q_stride, q_start, ctx_lens, R, T, nullptr, nullptr,
                                     cache, block_table, out, (cudaStream_t)stream));
     return DDT_OK;
