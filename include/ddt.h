@@ -545,10 +545,10 @@ ddt_status ddt_debug_arm_attention_timeout(ddt_ctx *ctx, int64_t wait_cycles);
 
 /* The same for prompt attention's tensor-core kernel (that of few rows over a
  * 4-bit cache has no such waits and leaves the setting armed): in the next
- * launch of it, once, each CTA's share of the work is not announced to the
- * CTA's other warps, so the first wait of each runs out after wait_cycles SM
- * clock cycles, before any copy or MMA was issued; DDT_DEV_TIMEOUT is raised,
- * every role winds down, and that launch's output is undefined. */
+ * launch of it, once, the warp that announces a CTA's work to its other warps
+ * starts with a wait that nothing ends. It runs out after wait_cycles SM clock
+ * cycles, before any copy or MMA was issued; DDT_DEV_TIMEOUT is raised, every
+ * role winds down, and that launch's output is undefined. */
 ddt_status ddt_debug_arm_prompt_timeout(ddt_ctx *ctx, int64_t wait_cycles);
 
 /* a1 without a context, for callers that cannot allocate device memory.

@@ -51,7 +51,7 @@ struct ddt_ctx {
     cudaEvent_t ev_fork, ev_tree, ev_join, ev_walk;
     int32_t *status;         // device status word
     int64_t debug_att_wait;  // > 0: the next attention launch starts with a wait that runs out (test only)
-    int64_t debug_pr_wait;   // > 0: the next tensor-core prompt attention starts with waits that run out (test only)
+    int64_t debug_pr_wait;   // > 0: the next tensor-core prompt attention starts with a wait that runs out (test only)
     // a1 partials
     int tk_nch;              // chunks per row
     uint16_t *tk_gkey;       // [R_max * L, nch * TOPK_THREADS] each group's max (ordered key)

@@ -145,7 +145,7 @@ template <int D, bool KV4>
 constexpr uint32_t IDESC_PV = KV4 ? idesc_f16(128, D, false, true) : idesc_bf16(128, D, false, true);
 
 // bounded mbarrier wait; false (and the abort flag raised) on timeout
-DDT_DEVINL bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag, const PtArgs &a)
+DDT_DEVINL bool wait_bar_for(uint32_t bar, uint32_t parity, volatile int *abort_flag, int32_t *status, long long limit)
 {
     if (mbar_try_wait(bar, parity))
         return true;
@@ -153,17 +153,21 @@ DDT_DEVINL bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag
     while (!mbar_try_wait(bar, parity)) {
         if (*abort_flag)
             return false;
-        if (clock64() - t0 > a.wait_limit) {
+        if (clock64() - t0 > limit) {
             *abort_flag = 1;
-            atomicOr(a.status, DDT_DEV_TIMEOUT);
+            atomicOr(status, DDT_DEV_TIMEOUT);
             return false;
         }
     }
     return true;
 }
-DDT_DEVINL bool wait_warp(uint32_t bar, uint32_t parity, volatile int *abort_flag, const PtArgs &a)
+DDT_DEVINL bool wait_bar(uint32_t bar, uint32_t parity, volatile int *abort_flag, int32_t *status)
 {
-    return __all_sync(0xFFFFFFFFu, wait_bar(bar, parity, abort_flag, a));
+    return wait_bar_for(bar, parity, abort_flag, status, WAIT_LIMIT);
+}
+DDT_DEVINL bool wait_warp(uint32_t bar, uint32_t parity, volatile int *abort_flag, int32_t *status)
+{
+    return __all_sync(0xFFFFFFFFu, wait_bar(bar, parity, abort_flag, status));
 }
 DDT_DEVINL void drain_bar(uint32_t bar, uint32_t parity)
 {
@@ -178,7 +182,7 @@ DDT_DEVINL bool ring_get(const PtArgs &a, uint32_t bar, const volatile int *ring
                          volatile int *abort_flag, Seg &s)
 {
     const int slot = k & (NRING - 1);
-    if (!wait_warp(bar + B_RFULL + 8 * slot, (k / NRING) & 1, abort_flag, a))
+    if (!wait_warp(bar + B_RFULL + 8 * slot, (k / NRING) & 1, abort_flag, a.status))
         return false;
     int w[7];
 #pragma unroll
@@ -413,7 +417,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 
     // a whole warp: Q of item k, once the item before is done with its own
     auto load_q = [&](const Seg &s, int k) {
-        if (k >= 1 && !wait_warp(bar + B_QEMPTY, (k - 1) & 1, abort_flag, a))
+        if (k >= 1 && !wait_warp(bar + B_QEMPTY, (k - 1) & 1, abort_flag, a.status))
             return false;
         if (elect_one()) {
             mbar_arrive_expect_tx(bar + B_QFULL, 16384u * (D / 64) * (s.split ? 1 : 2));
@@ -442,12 +446,14 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         ShareWalk walk;
         walk.begin(a, found, tq, gridDim.x, blockIdx.x);
         int k = 0, kn = 0;
-        bool ok = !a.unannounced;  // (armed by a test: nothing is announced, so every other role's wait runs out)
+        bool ok = true;
+        if (a.debug_wait > 0)  // (armed by a test) nothing is announced: this wait runs out, and the other roles give up
+            ok = __all_sync(0xFFFFFFFFu, wait_bar_for(bar + B_RFULL, 0, abort_flag, a.status, a.debug_wait));
         while (ok) {
             Seg s;
             walk.next(a, tq, 128, s);
             const int slot = k & (NRING - 1);
-            if (k >= NRING && !wait_warp(bar + B_REMPTY + 8 * slot, ((k / NRING) - 1) & 1, abort_flag, a))
+            if (k >= NRING && !wait_warp(bar + B_REMPTY + 8 * slot, ((k / NRING) - 1) & 1, abort_flag, a.status))
                 break;
             if (lane == 0) {
                 volatile int *w = ring + 8 * slot;
@@ -474,7 +480,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             for (int j = s.t0; j < s.t1; ++j, ++kn) {
                 const int sl = kn % NK;
                 const int z = lane < 8 ? group_row(a, s, j, lane) : 0;
-                if (kn >= NK && !wait_warp(bar + B_KEMPTY + 8 * sl, ((kn / NK) - 1) & 1, abort_flag, a)) {
+                if (kn >= NK && !wait_warp(bar + B_KEMPTY + 8 * sl, ((kn / NK) - 1) & 1, abort_flag, a.status)) {
                     ok = false;
                     break;
                 }
@@ -510,7 +516,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             for (int j = s.t0; j < s.t1; ++j) {
                 const int z = lane < 8 ? group_row(a, s, j, lane) : 0;
                 // (a slot never filled passes: its phase "before" is complete)
-                if (!wait_warp(bar + B_VEMPTY + 8 * sl, ((vfill >> sl) & 1) ^ 1, abort_flag, a)) {
+                if (!wait_warp(bar + B_VEMPTY + 8 * sl, ((vfill >> sl) & 1) ^ 1, abort_flag, a.status)) {
                     ok = false;
                     break;
                 }
@@ -559,7 +565,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             bool ok = true;
             // (after a wait that gave up, what the body still issues reads and writes
             // this CTA's own memory; the loop then ends)
-            auto need = [&](uint32_t b, uint32_t parity) { ok &= wait_bar(b, parity, abort_flag, a); };
+            auto need = [&](uint32_t b, uint32_t parity) { ok &= wait_bar(b, parity, abort_flag, a.status); };
             for (int k = 0; ok; ++k) {
                 const int slot = k & (NRING - 1);
                 need(bar + B_RFULL + 8 * slot, (k / NRING) & 1);
@@ -701,7 +707,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 if (v) {
                     sl = 0;  // (V's slots begin anew with each item)
                 } else {
-                    if (!wait_warp(bar + B_QFULL, qn & 1, abort_flag, a))
+                    if (!wait_warp(bar + B_QFULL, qn & 1, abort_flag, a.status))
                         break;
                     float *rowsc = reinterpret_cast<float *>(sgen + SM_BAR<KV4> + B_ROWSC) + (qn & 1) * 256;
                     for (int g = 0; g < ((now & 2) ? 2 : 1); ++g)
@@ -714,7 +720,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 }
             }
             // (a slot never filled passes: its phase "before" is complete)
-            if (!wait_warp(empty + 8 * sl, ((fill >> sl) & 1) ^ 1, abort_flag, a))
+            if (!wait_warp(empty + 8 * sl, ((fill >> sl) & 1) ^ 1, abort_flag, a.status))
                 break;
             fill ^= 1u << sl;
             dequant_part<D>(sgen + raws + raw * RAW, sgen + tiles + sl * 32768u, wq, lane);
@@ -752,7 +758,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             bool alive = true;
             for (int j = 0; j < steps; ++j, ++n) {
                 const uint32_t buf = s_addr + SUB * (n & 1);
-                if (!wait_warp(bar + B_SFULL + 16 * g + 8 * (n & 1), (n >> 1) & 1, abort_flag, a)) {
+                if (!wait_warp(bar + B_SFULL + 16 * g + 8 * (n & 1), (n >> 1) & 1, abort_flag, a.status)) {
                     alive = false;
                     break;
                 }
@@ -854,7 +860,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                         if (j > 0) {
                             // O must not have P V of the step before under way (that of the one
                             // before it is complete: this S was issued behind it)
-                            if (!wait_warp(bar + B_ODONE + 8 * g, (n - 1) & 1, abort_flag, a)) {
+                            if (!wait_warp(bar + B_ODONE + 8 * g, (n - 1) & 1, abort_flag, a.status)) {
                                 alive = false;
                                 break;
                             }
@@ -892,7 +898,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 break;
             // ---- epilogue
             if (steps > 0) {
-                if (!wait_warp(bar + B_OFULL + 8 * g, no & 1, abort_flag, a))
+                if (!wait_warp(bar + B_OFULL + 8 * g, no & 1, abort_flag, a.status))
                     break;
                 ++no;
                 tc_fence_after();
@@ -907,12 +913,12 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(bar + B_XB);
-                    if (!wait_warp(bar + B_XA, nx & 1, abort_flag, a))
+                    if (!wait_warp(bar + B_XA, nx & 1, abort_flag, a.status))
                         break;
                     ++nx;
                     continue;
                 }
-                if (!wait_warp(bar + B_XB, nx & 1, abort_flag, a))
+                if (!wait_warp(bar + B_XB, nx & 1, abort_flag, a.status))
                     break;
                 ++nx;
                 tc_fence_after();
@@ -1110,8 +1116,7 @@ cudaError_t launch_prompt_attention(ddt_ctx *c, const uint16_t *q, int64_t q_str
                  !make_map(&tv, v_cache, d, cfg.Hkv, rows, dense, 1, 16)))
         return cudaErrorInvalidValue;
     const int grid = c->num_sms < PR_MAX_CTAS ? c->num_sms : PR_MAX_CTAS;
-    a.unannounced = c->debug_pr_wait > 0;  // one-shot test setting
-    a.wait_limit = a.unannounced ? c->debug_pr_wait : WAIT_LIMIT;
+    a.debug_wait = c->debug_pr_wait;  // one-shot test setting
     c->debug_pr_wait = 0;
     if (kv4)
         return d == 128 ? launch_d<128, true>(c->device, grid, tq, tk, tv, a, s) : launch_d<64, true>(c->device, grid, tq, tk, tv, a, s);

@@ -23,8 +23,7 @@ struct PtArgs {
     int R, T, Hq, Hkv, g_shift, page_shift, max_pages, cap;
     int64_t num_pages;
     float scale_log2, out_scale;
-    long long wait_limit;  // of a bounded wait, in cycles
-    bool unannounced;      // (tests only) no CTA's work is announced to its warps: their first waits run out
+    long long debug_wait;  // > 0 (tests only): each CTA starts with a wait that runs out after this many cycles
 };
 
 // few rows of each request over the 4-bit cache (prompt_few.cu): items of up to 8

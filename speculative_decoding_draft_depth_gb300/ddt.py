@@ -519,8 +519,8 @@ class Context:
                "ddt_debug_arm_attention_timeout")
 
     def ddt_debug_arm_prompt_timeout(self, wait_cycles):
-        """Test only: the waits of the next tensor-core prompt attention run out
-        after wait_cycles SM cycles (see include/ddt.h)."""
+        """Test only: the next tensor-core prompt attention starts with a bounded
+        wait that runs out after wait_cycles SM cycles (see include/ddt.h)."""
         _check(_lib.ddt_debug_arm_prompt_timeout(self._h, int(wait_cycles)), "ddt_debug_arm_prompt_timeout")
 
     # -- allocation helper (plumbing) ----------------------------------------

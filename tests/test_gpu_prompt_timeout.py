@@ -1,8 +1,9 @@
-"""Prompt attention's bounded waits, without a fault: a test-only setting keeps each
-CTA's work from being announced to its warps, so the first wait of every role (the
-loaders, both issuers, the softmax warps, for the 4-bit cache the warps that make
-its tiles) runs out after a short limit. The call must report DDT_DEV_TIMEOUT and
-end by itself, and the context's next call must be normal."""
+"""Prompt attention's bounded waits, without a fault: a test-only setting makes the
+warp that announces each CTA's work start with a wait that nothing ends. It runs
+out after a short limit, and every other role (the loaders, both issuers, the
+softmax warps, for the 4-bit cache the warps that make its tiles) gives up in its
+own first wait. The call must report DDT_DEV_TIMEOUT and end by itself, and the
+context's next call must be normal."""
 import pytest
 import torch
 
