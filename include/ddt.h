@@ -420,11 +420,11 @@ ddt_status ddt_schedule_prefix(ddt_ctx *ctx, const float *conf, int32_t R, const
  * model of several layers appends and attends in each and moves its lengths on
  * afterwards (see new_lens). A request is skipped, and DDT_DEV_BAD_LENGTH set,
  * when q_start[r] > q_start[r+1], either lies outside [0, T], ctx_lens[r] < 0,
- * or its last slot passes max_pages_per_req * page_size (for the append with a
- * rotation: or its last position passes max_pos). Rows of no request (before
- * q_start[0], behind q_start[R]) are neither read for a result nor written;
- * rows that two requests name (q_start fell between them) belong to the later
- * one in an append, and get either's result, element by element, from an
+ * or ctx_lens[r] and its tokens (none, too) together pass max_pages_per_req *
+ * page_size (for the append with a rotation: or max_pos). Rows of no request
+ * (before q_start[0], behind q_start[R]) are neither read for a result nor
+ * written; rows that two requests name (q_start fell between them) belong to the
+ * later one in an append, and get either's result, element by element, from an
  * attention. A tensor that a call writes (the pools of an append among them)
  * that shares memory with another one it reads or writes is DDT_EINVAL, but for
  * queries turned in place (q_out == q, dense). The calls run on the
@@ -458,8 +458,9 @@ typedef struct ddt_append_args {
  * (fp32, each product and sum rounded to nearest, one rounding to bf16), the
  * queries to q_out, keys and values to the token's cache slot. Nothing else of
  * the cache is written. Page ids out of range set DDT_DEV_BAD_PAGE and that
- * row's keys and values are dropped. Two requests that append to one and the
- * same slot leave either's row there. T = 0 or R = 0 writes only new_lens. */
+ * row's keys and values are dropped. Two rows appended to one and the same slot
+ * leave a mixture there unless they are equal (a prefix that both requests
+ * hold). T = 0 or R = 0 writes only new_lens. */
 ddt_status ddt_append_kv(ddt_ctx *ctx, const ddt_append_args *args, uint16_t *k_cache,
                          uint16_t *v_cache, void *stream);
 
@@ -482,10 +483,9 @@ typedef struct ddt_kv4 {
 
 /* The same append into a cache held in 4 bits: for each block, with g the
  * cache's k_scale or v_scale, scale = e4m3(min(amax / (6 g), 448)) (6 g and the
- * quotient rounded to fp32) and
- * each channel's code the magnitude nearest to the quotient |x| / (scale g) in
- * fp32, ties to the even code, 6 where it is larger. A block with a NaN gets a NaN scale and so
- * reads as NaN. k_held, v_held ([T, Hkv, d] bf16, dense, both or neither NULL):
+ * quotient rounded to fp32) and each channel's code the magnitude nearest to the
+ * quotient |x| / (scale g) in fp32, ties to the even code, 6 where it is larger.
+ * A block with a NaN gets a NaN scale and so reads as NaN. k_held, v_held ([T, Hkv, d] bf16, dense, both or neither NULL):
  * the values that the cache now holds for the new tokens. */
 ddt_status ddt_append_kvq(ddt_ctx *ctx, const ddt_append_args *args, const ddt_kv4 *cache,
                           uint16_t *k_held, uint16_t *v_held, void *stream);

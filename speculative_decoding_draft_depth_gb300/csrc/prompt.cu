@@ -38,15 +38,17 @@
 //    (bounded) for its own copies and MMAs, frees its TMEM and returns.
 //
 // Measured (GB300; a step of both groups is 2 x 128 rows x 64 keys):
-//  * 16384 tokens, 32 heads of 128 over 8 KV heads: 1.34 to 1.40 ms, 1570 to 1640
-//    TFLOP/s. Alone, a launch takes 1300 cycles a step, and the tensor pipe 1286 of
-//    them (8 MMAs of N = 64 for S, bound by shared memory at 48 cycles each, and 4 of
-//    N = 128 for P V, both groups); repeated, the board's power limit lowers the
-//    clock, and the rate is that of a large bf16 matrix product in the same state
-//    (1740) but for 6 to 10%.
+//  * 16384 tokens, 32 heads of 128 over 8 KV heads: 1.34 to 1.50 ms by board and
+//    temperature, 1470 to 1640 TFLOP/s. Alone, a launch takes 1300 cycles a step, and the
+//    tensor pipe 1286 of them (8 MMAs of N = 64 for S, bound by shared memory at 48
+//    cycles each, and 4 of N = 128 for P V, both groups); repeated, the board's power
+//    limit lowers the clock (a large bf16 matrix product repeated for seconds: 1740).
 //    S of a whole tile at once (N = 128, 32 cycles per 64 keys) needs both buffers, so
 //    a group has no next S while its softmax runs: 1.66 ms.
-//  * 32 prompts of up to 2047 tokens, 8 heads of 64: 119 us. A step takes 1080 cycles:
+//  * 32 prompts of up to 2047 tokens, 8 heads of 64: 119 to 121 us, of which 132 steps a
+//    CTA and its items' outputs account for about 84 (the rest, a quarter, has not been
+//    taken apart: first scores of an item, its queries' way, the shares' ends). A step
+//    takes 1080 cycles:
 //    the softmax of two warps a scheduler (700 to 900, of which 512 are exponentials) and
 //    the chain from P over P V to the next S are about as long, so that sixteen softmax
 //    warps, a third buffer of S, or sums made by the tensor core each gave 1% or nothing.
@@ -54,8 +56,9 @@
 //    joins) 137; the common path by itself 127; zeros at once where a warp's rows have
 //    no key 123; an item at three units in the shares 119.
 //  * 64 tokens behind 512 to 16384 cached: 361 to 371 us, 6.5 to 6.7 TB/s.
-//  * 4-bit cache, four chunks of 1500 to 2048 tokens behind 4000 to 16000: 0.88 ms,
-//    1350 TFLOP/s. Bound by the instructions of softmax and conversion together.
+//  * 4-bit cache, four chunks of 1500 to 2048 tokens behind 4000 to 16000: 0.88 to 0.90
+//    ms, 1320 to 1350 TFLOP/s; issue slots 60% and the tensor core 65% busy. Each query
+//    tile turns the codes into fp16 anew.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -1106,7 +1109,10 @@ cudaError_t launch_prompt_attention(ddt_ctx *c, const uint16_t *q, int64_t q_str
     // Few rows of a request (on average: lengths are the device's) over the 4-bit
     // cache have a kernel of their own. 64 requests behind 8000, 32/8 heads of 128, this
     // kernel and that one: one token (4 rows) 363 and 140 us, two 364 and 142, four (16
-    // rows) 366 and 197, eight (32: it reads the cache twice) 370 and 377.
+    // rows) 366 and 197, eight (32: it reads the cache twice) 370 and 377. Uneven lengths
+    // can lose by it: 63 single tokens and a chunk of 190 behind 8000 171 and 203, 16
+    // chains of 16 among 48 empty requests 113 and 194; and 16 single tokens among 48
+    // empty requests 109 and 48.
     if (kv4 && (int64_t)T * G <= (int64_t)R * 16)
         return launch_prompt_few(c, a, q, q_stride, G <= 8 && (int64_t)T * G <= (int64_t)R * 8 ? 8 : 16, s);
     CUtensorMap tq, tk = {}, tv = {};

@@ -19,10 +19,12 @@
 // are in flight (cp.async into a ring of the warp's own). Shares of the work and the merge of
 // cut items as in prompt.cu.
 //
-// Measured (64 tokens behind 512 to 16384, 32/8 heads of 128, 680 MB): 159 us, 4.3 TB/s.
-// The codes' way to fp16 fills the ALU pipe (a conversion for two values at half rate,
-// shuffles of bytes for V) before HBM, whose time for the bytes is 101 us. Two CTAs of 8 rows an
-// SM; 16 rows (four tokens) need twice the registers and go one to an SM.
+// Measured (64 tokens behind 512 to 16384, 32/8 heads of 128, 680 MB): 160 us, 4.25 TB/s;
+// the bytes alone would take 101. No pipe is full: issue slots 63%, the ALU pipe (half of
+// it the codes' way to fp16 and the byte shuffles for V) 56%, HBM 50%. Four warps a
+// scheduler are what hides the dependent chains, and in 37% of the cycles none of them can
+// issue. Two CTAs of 8 rows an SM (registers and shared memory); 16 rows (four tokens)
+// need twice the registers and go one to an SM.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
