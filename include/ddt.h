@@ -22,6 +22,11 @@
  *   ddt_accept_stochastic
  *       stochastic verification of drafted chains at temperature 1, of
  *       every guess or of a per-request prefix
+ *   ddt_sample
+ *       a token of each logit row under temperature, top-k, top-p and min-p
+ *   ddt_accept_sampled
+ *       the same verification of chains whose drafter and target sample under
+ *       such settings
  *   ddt_schedule_prefix
  *       the hardware-aware prefix scheduler (guesses to verify per request;
  *       its output is ddt_accept_stochastic's prefix lengths)
@@ -104,6 +109,7 @@ typedef enum ddt_dtype { DDT_BF16 = 0, DDT_F32 = 1 } ddt_dtype;
 #define DDT_DEV_BAD_TREE 0x4   /* parents/n_nodes/acc arrays out of range */
 #define DDT_DEV_TIMEOUT 0x8    /* a bounded on-device wait gave up (the kernel wound down) */
 #define DDT_DEV_BAD_LENGTH 0x10 /* q_start or ctx_lens out of range (that request was skipped) */
+#define DDT_DEV_BAD_SETTING 0x20 /* a sampling setting out of range (that row or request has no token) */
 
 typedef struct ddt_config {
     int32_t R_max;             /* most requests a call may carry (1..2048) */
@@ -381,6 +387,64 @@ ddt_status ddt_accept_stochastic(ddt_ctx *ctx, const void *draft_logits,
                                  const void *target_logits, const int32_t *draft_tokens,
                                  const float *u, const float *r, int32_t R, int32_t *acc_len,
                                  int32_t *acc_tokens, const int32_t *n_guess, void *stream);
+
+/* Sampling settings of n rows (or requests): device arrays of n, each may be NULL.
+ *   temperature  f32, 0 or positive, finite (NULL: 1). 0 is greedy: the largest
+ *                logit, the lowest index of equal ones (the other settings then
+ *                change nothing). Below 2^-90 it counts as 2^-90.
+ *   top_k        i32, 0 or less: off (NULL: off)
+ *   top_p        f32 in [0, 1], 1: off (NULL: off); 0 keeps one token
+ *   min_p        f32 in [0, 1], 0: off (NULL: off)
+ * A value outside these (NaN among them) sets DDT_DEV_BAD_SETTING.
+ * With z_max a row's largest logit, token i has the weight w_i = exp((z_i -
+ * z_max) / temperature). In the order z descending, index ascending, the kept
+ * tokens are a front part: the tokens with w_i >= min_p; of these the first
+ * top_k; of these the fewest whose weights reach top_p times their sum, one at
+ * least. The row's distribution is w over the kept tokens, divided by their sum.
+ * Logits below 2^-90 in magnitude count as 0, NaN as -infinity (and set
+ * DDT_DEV_NAN_LOGITS), weights below 2^-64 as 0. Tokens with +infinity share the
+ * whole weight equally. Sums decide to about 2^-40: weights and their running
+ * sums are 64-bit integers in units of 2^-44, and do not depend on what else runs. */
+typedef struct ddt_filter {
+    const float *temperature;
+    const int32_t *top_k;
+    const float *top_p;
+    const float *min_p;
+} ddt_filter;
+
+/* A token of each of N logit rows (any N >= 0), drawn from the row's distribution.
+ *   logits    [N, V] of the given dtype, V the config's, rows contiguous
+ *   filter    the rows' settings ([N] each); NULL: none
+ *   u         [N] f32 in [0, 1) (what lies outside counts as the nearer end, NaN as
+ *             0): the token is the first kept index (ascending) whose running sum of
+ *             weights exceeds u times the kept weights' sum
+ *   tokens    [N] i32
+ *   logprobs  [N] f32 or NULL: log of the token's probability in the row's
+ *             distribution
+ * A row without weights (every logit -infinity or NaN) and a row with a bad setting
+ * get token -1 and log-probability -infinity. One kernel is enqueued; it uses no
+ * workspace, so calls on several streams may overlap. tokens and logprobs may not
+ * share memory with what the call reads, nor with each other. The calling thread's
+ * current device stays as it was. */
+ddt_status ddt_sample(ddt_ctx *ctx, const void *logits, int32_t dtype, int32_t N,
+                      const ddt_filter *filter, const float *u, int32_t *tokens, float *logprobs,
+                      void *stream);
+
+/* ddt_accept_stochastic where the drafter drew its guesses under draft_filter and the
+ * target samples under target_filter ([R] each, a request's settings for all of its
+ * rows; NULL: none): p_k and q_k are the rows' distributions as ddt_filter defines
+ * them. All other arguments, shapes and outputs as there; guess k is kept iff u[k] <
+ * min(1, p_k(x_k) / q_k(x_k)), q_k(x_k) = 0 counting as ratio 1. A request with a bad
+ * setting, or whose drawn row has no weights, gets -1 as its drawn token (with a bad
+ * setting no guess is kept either: acc_len 1). The call uses the context's workspace:
+ * calls on one context, and graphs captured from them, must not overlap. Outputs may
+ * not share memory with what the call reads, nor with each other. The calling thread's
+ * current device stays as it was. */
+ddt_status ddt_accept_sampled(ddt_ctx *ctx, const void *draft_logits, const void *target_logits,
+                              const int32_t *draft_tokens, const float *u, const float *r, int32_t R,
+                              const ddt_filter *draft_filter, const ddt_filter *target_filter,
+                              int32_t *acc_len, int32_t *acc_tokens, const int32_t *n_guess,
+                              void *stream);
 
 /* The hardware-aware prefix scheduler -- "DSpark Speculative Decoding
  * Explained: Block Drafting and Confidence Checks", sections "Survival

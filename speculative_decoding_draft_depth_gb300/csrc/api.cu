@@ -74,7 +74,7 @@ ddt_status check_config(const ddt_config *in, ddt_config *out)
 struct Layout {
     size_t status, tk_gkey, tk_wtop, tk_ms, am_val, am_idx, att_part_o, att_part_ml, cg_part_ms, cg_part_top, cg_fr_tok, cg_fr_cand,
         cg_fr_n, cg_fr_S, cg_c_S, cg_c_meta, cg_thr, cg_seed_lp, cg_seed_ids, mk_cand, mk_tab,
-        sv_part_d, sv_part_t, sv_cnt, sv_part_w, ps_rk, ps_rid, ps_arrive, total;
+        sv_part_d, sv_part_t, sv_cnt, sv_part_w, sm_rows, ps_rk, ps_rid, ps_arrive, total;
     int tk_nch, am_nch, max_items, sv_nch_d, sv_nch_t, sv_nch_w;
 };
 
@@ -136,6 +136,8 @@ Layout layout_for(const ddt_config &c)
     L.sv_part_t = take((size_t)c.R_max * (c.L + 1) * L.sv_nch_t * sizeof(float2));
     L.sv_cnt = take((size_t)c.R_max * sizeof(unsigned));
     L.sv_part_w = take((size_t)c.R_max * L.sv_nch_w * sizeof(float));
+    // sampled chain verification: 32 bytes a row
+    L.sm_rows = take((size_t)c.R_max * (2 * c.L + 1) * sample_row_bytes());
     // prefix scheduler: the ranking of up to DDT_SCHED_MAX_SLOTS slots
     L.ps_rk = take((size_t)DDT_SCHED_MAX_SLOTS * sizeof(uint64_t));
     L.ps_rid = take((size_t)DDT_SCHED_MAX_SLOTS * sizeof(int32_t));
@@ -443,6 +445,7 @@ ddt_status ddt_create(const ddt_config *cfg, ddt_ctx **out)
     ctx->sv_part_t = (float2 *)(w + L.sv_part_t);
     ctx->sv_cnt = (unsigned *)(w + L.sv_cnt);
     ctx->sv_part_w = (float *)(w + L.sv_part_w);
+    ctx->sm_rows = w + L.sm_rows;
     ctx->ps_rk = (uint64_t *)(w + L.ps_rk);
     ctx->ps_rid = (int32_t *)(w + L.ps_rid);
     ctx->ps_arrive = (unsigned *)(w + L.ps_arrive);
@@ -712,6 +715,71 @@ ddt_status ddt_accept_stochastic(ddt_ctx *ctx, const void *draft_logits,
         return st;
     DDT_TRY(launch_accept_stochastic(ctx, draft_logits, target_logits, draft_tokens, u, r, R,
                                      n_guess, acc_len, acc_tokens, (cudaStream_t)stream));
+    return DDT_OK;
+}
+
+// a filter's arrays of n, as tensors that a call reads; false: one is misaligned
+static bool filter_bytes(const ddt_filter &f, int64_t n, PsBytes *r)
+{
+    const void *at[4] = {f.temperature, f.top_k, f.top_p, f.min_p};
+    for (int i = 0; i < 4; ++i) {
+        if (!aligned4(at[i]))
+            return false;
+        r[i] = {at[i], 4 * n};
+    }
+    return true;
+}
+
+ddt_status ddt_sample(ddt_ctx *ctx, const void *logits, int32_t dtype, int32_t N,
+                      const ddt_filter *filter, const float *u, int32_t *tokens, float *logprobs,
+                      void *stream)
+{
+    DDT_CHECK(ctx && N >= 0 && (dtype == DDT_BF16 || dtype == DDT_F32));
+    if (N == 0)
+        return DDT_OK;
+    DDT_CHECK(logits && u && tokens && aligned16(logits) && aligned4(u) && aligned4(tokens) &&
+              aligned4(logprobs));
+    const ddt_filter f = filter ? *filter : ddt_filter{};
+    const int64_t n = 4 * (int64_t)N;
+    PsBytes r[6] = {{logits, (int64_t)N * ctx->cfg.V * (dtype == DDT_BF16 ? 2 : 4)}, {u, n}};
+    DDT_CHECK(filter_bytes(f, N, r + 2));
+    const PsBytes w[2] = {{tokens, n}, {logprobs, n}};
+    DDT_CHECK(ps_apart(w, 2, r, 6));
+    DDT_ON_DEVICE(ctx);
+    DDT_TRY(launch_sample(ctx, logits, dtype, N, f, u, tokens, logprobs, (cudaStream_t)stream));
+    return DDT_OK;
+}
+
+ddt_status ddt_accept_sampled(ddt_ctx *ctx, const void *draft_logits, const void *target_logits,
+                              const int32_t *draft_tokens, const float *u, const float *r, int32_t R,
+                              const ddt_filter *draft_filter, const ddt_filter *target_filter,
+                              int32_t *acc_len, int32_t *acc_tokens, const int32_t *n_guess,
+                              void *stream)
+{
+    const ddt_status st = check_R(ctx, R);
+    if (st != DDT_OK)
+        return st;
+    if (R == 0)
+        return DDT_OK;
+    DDT_CHECK(draft_logits && target_logits && draft_tokens && u && r && acc_len && acc_tokens);
+    DDT_CHECK(aligned16(draft_logits) && aligned16(target_logits) && aligned4(draft_tokens) &&
+              aligned4(u) && aligned4(r) && aligned4(acc_len) && aligned4(acc_tokens) &&
+              aligned4(n_guess));
+    const ddt_filter fd = draft_filter ? *draft_filter : ddt_filter{};
+    const ddt_filter ft = target_filter ? *target_filter : ddt_filter{};
+    const int64_t L = ctx->cfg.L, V = ctx->cfg.V, n = 4 * (int64_t)R;
+    PsBytes rd[14] = {{draft_logits, R * L * V * (ctx->cfg.draft_dtype == DDT_BF16 ? 2 : 4)},
+                      {target_logits, R * (L + 1) * V * (ctx->cfg.target_dtype == DDT_BF16 ? 2 : 4)},
+                      {draft_tokens, n * L},
+                      {u, n * L},
+                      {r, n},
+                      {n_guess, n}};
+    DDT_CHECK(filter_bytes(fd, R, rd + 6) && filter_bytes(ft, R, rd + 10));
+    const PsBytes w[2] = {{acc_len, n}, {acc_tokens, n * (L + 1)}};
+    DDT_CHECK(ps_apart(w, 2, rd, 14));
+    DDT_ON_DEVICE(ctx);
+    DDT_TRY(launch_accept_sampled(ctx, draft_logits, target_logits, fd, ft, draft_tokens, u, r, R,
+                                  n_guess, acc_len, acc_tokens, (cudaStream_t)stream));
     return DDT_OK;
 }
 

@@ -85,6 +85,8 @@ struct ddt_ctx {
     float2 *sv_part_t;       // [R_max * (L + 1), sv_nch_t]
     unsigned *sv_cnt;        // [R_max] arrival counters of the draw (self-resetting)
     float *sv_part_w;        // [R_max, sv_nch_w] chunk totals of the draw's weights
+    // sampled chain verification
+    void *sm_rows;           // [R_max, 2 L + 1] what the settings keep of each row
     // prefix scheduler (rank-counting grid)
     uint64_t *ps_rk;         // [DDT_SCHED_MAX_SLOTS] survival bits in ranking order
     int32_t *ps_rid;         // [DDT_SCHED_MAX_SLOTS] their tie ids
@@ -146,6 +148,14 @@ cudaError_t launch_accept_stochastic(const ddt_ctx *c, const void *draft, const 
                                      const int32_t *tokens, const float *u, const float *r, int R,
                                      const int32_t *n_guess, int32_t *acc_len, int32_t *acc_tokens,
                                      cudaStream_t s);
+
+// sampling under settings, and chain verification with them (sample.cu)
+size_t sample_row_bytes();
+cudaError_t launch_sample(const ddt_ctx *c, const void *logits, int dtype, int N, const ddt_filter &f, const float *u,
+                          int32_t *tokens, float *logprobs, cudaStream_t s);
+cudaError_t launch_accept_sampled(const ddt_ctx *c, const void *draft, const void *target, const ddt_filter &fd,
+                                  const ddt_filter &ft, const int32_t *tokens, const float *u, const float *r, int R,
+                                  const int32_t *n_guess, int32_t *acc_len, int32_t *acc_tokens, cudaStream_t s);
 
 // the hardware-aware prefix scheduler (sched.cu)
 int schedule_smem_bytes(int R, int L);

@@ -6,10 +6,10 @@
 #include <stdint.h>
 
 #include <algorithm>
-#include <atomic>
 
 #include "ddt_device.cuh"
 #include "ddt_internal.h"
+#include "device_flags.h"
 #include "prompt_plan.h"
 
 struct PtArgs {
@@ -320,18 +320,6 @@ __global__ void __launch_bounds__(MG_THREADS) prompt_merge_kernel(const PtArgs a
             make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
     }
 }
-
-// devices for which a kernel's attributes have been set (setting them twice does no
-// harm, so two threads may come at once)
-struct DeviceFlags {
-    std::atomic<uint64_t> bits{0};
-    bool test(int dev) const { return dev < 64 && ((bits.load(std::memory_order_relaxed) >> dev) & 1); }
-    void set(int dev)
-    {
-        if (dev < 64)
-            bits.fetch_or((uint64_t)1 << dev, std::memory_order_relaxed);
-    }
-};
 
 // the merge as a programmatic dependent of the main kernel (which lets it stage
 // itself at once); grid: the main kernel's

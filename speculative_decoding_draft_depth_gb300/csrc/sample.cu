@@ -1,0 +1,533 @@
+// sample.cu -- sampled decoding: a token of each logit row under temperature, top-k,
+// top-p and min-p (sample_kernel), and the probability rule on drafted chains whose
+// drafter and target both sample under such settings (keep_kernel, chain_kernel).
+// The mathematics and the work on one row are in sample_row.cuh.
+//
+//  * sample_kernel: one cluster a row: read once, the border of the kept tokens, their
+//    weights' running sums, the drawn token.
+//  * keep_kernel: one cluster for each draft and target row that a chain verifies: the
+//    border, the kept weights' sum and the guess's weight, 32 bytes a row.
+//  * chain_kernel (a dependent launch): one cluster a request. Each CTA takes the
+//    request's decisions itself, u < (w_p(x) / W_p) / (w_q(x) / W_q), and the cluster draws
+//    from max(0, w_p - (W_p / W_q) w_q) over the first rejected row, or from w_p behind the
+//    last guess, in 64-bit integers.
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "device_flags.h"
+#include "sample_row.cuh"
+
+namespace {
+
+template <typename T>
+struct SampleArgs {
+    const T *logits;  // [N, V]
+    ddt_filter f;
+    const float *u;
+    int32_t *tokens;
+    float *logprobs;  // or null
+    int32_t *status;
+    int V, subs;      // subs: sub-chunks that a CTA has room for
+};
+
+extern __shared__ __align__(16) unsigned char sr_smem[];
+
+// the row's top value and scale, and the border under the row's settings (a row in place
+// in shared memory). false: no token has a weight
+template <typename T>
+DDT_DEVINL bool row_border(Row<T> &row, const Settings &set, uint64_t *sub, int32_t *status, Scale &sc,
+                           typename Row<T>::Cut &cut, bool &infinite)
+{
+    typename Row<T>::Top t = row.top();
+    if (t.nan && row.rank == 0 && row.tid == 0)
+        set_status(status, DDT_DEV_NAN_LOGITS);
+    if (t.zmax == DDT_NEG_INF)
+        return false;
+    infinite = t.zmax == -DDT_NEG_INF;
+    if (infinite)
+        row.only_infinite(t);
+    sc = make_scale(t.zmax, set.T);
+    const float min_z = set.m > 0.f ? min_value(t.zmax, row.sh->off) : DDT_NEG_INF;
+    cut = row.border(t, sc, set.k, set.p, min_z, sub);
+    return true;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(SR_THREADS) sample_kernel(const SampleArgs<T> a)
+{
+    __shared__ RowShared sh;
+    Row<T> row;
+    row.begin(&sh);
+    const int64_t n = blockIdx.x / row.cl;
+    const Settings set = load_settings(a.f, (int)n);
+    if (!set.good) {
+        if (row.rank == 0 && row.tid == 0) {
+            a.tokens[n] = -1;
+            if (a.logprobs)
+                a.logprobs[n] = DDT_NEG_INF;
+            set_status(a.status, DDT_DEV_BAD_SETTING);
+        }
+        return;
+    }
+    uint64_t *sub = reinterpret_cast<uint64_t *>(sr_smem + a.subs * SR_SUB);
+    row.load(sr_smem, a.logits + n * a.V, a.V);
+    if (row.tid == 0 && set.m > 0.f)
+        sh.off = min_offset(set);
+    row.loaded();
+    Scale sc;
+    typename Row<T>::Cut cut;
+    bool infinite;
+    if (!row_border(row, set, sub, a.status, sc, cut, infinite)) {
+        if (row.rank == 0 && row.tid == 0) {
+            a.tokens[n] = -1;
+            if (a.logprobs)
+                a.logprobs[n] = DDT_NEG_INF;
+        }
+        return;
+    }
+    const uint64_t(*all)[4];
+    const uint64_t mass = row.mass(sc, cut.b, sub, &all);
+    const typename Row<T>::Weight w = {sc, cut.b, sh.tab};
+    const int i = row.locate(sub, all, draw_target(__ldg(a.u + n), mass), w);
+    if (i >= 0) {
+        a.tokens[n] = i;
+        if (a.logprobs) {
+            // (the largest weight is 2^44, so the sum is at least that)
+            a.logprobs[n] = (row.value(i) - sc.zmax) / set.T - log1pf((float)(mass - (1ull << SR_ONE)) * 5.684341886e-14f);
+        }
+    }
+}
+
+// what keep_kernel leaves of a row
+struct __align__(16) KeptRow {
+    float zmax;
+    Border b;
+    int flags;
+    uint64_t mass, guess;  // the kept weights' sum; the guess's weight (0: not kept)
+};
+constexpr int KR_BAD = 1, KR_INF = 2;
+
+template <typename T>
+struct KeepArgs {
+    const T *draft, *target;  // [R, L, V], [R, L + 1, V]; either may be null (then none of its rows is done here)
+    ddt_filter fd, ft;
+    const int32_t *tokens, *n_guess;
+    KeptRow *rows;  // [R, 2 L + 1]
+    int32_t *status;
+    int L, V, subs;
+};
+
+DDT_DEVINL int guess_count(const int32_t *n_guess, int i, int L)
+{
+    return n_guess ? max(0, min(L, __ldg(n_guess + i))) : L;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(SR_THREADS) keep_kernel(const KeepArgs<T> a)
+{
+    __shared__ RowShared sh;
+    Row<T> row;
+    row.begin(&sh);
+    pdl_trigger();
+    const int L = a.L, per = (a.draft ? L : 0) + (a.target ? L + 1 : 0);
+    const int64_t n = blockIdx.x / row.cl;
+    const int i = (int)(n / per), j = (int)(n % per);
+    const bool isd = a.draft && j < L;
+    const int k = isd || !a.draft ? j : j - L;
+    const int guesses = guess_count(a.n_guess, i, L);
+    if (isd ? k >= guesses : k > guesses) {
+        pdl_wait();
+        return;
+    }
+    KeptRow *to = a.rows + (int64_t)i * (2 * L + 1) + (isd ? k : L + k);
+    const T *z = isd ? a.draft + ((int64_t)i * L + k) * a.V : a.target + ((int64_t)i * (L + 1) + k) * a.V;
+    const Settings set = load_settings(isd ? a.fd : a.ft, i);
+    KeptRow r = {0.f, {0.f, 0}, 0, 0, 0};
+    if (!set.good) {
+        r.flags = KR_BAD;
+    } else {
+        uint64_t *sub = reinterpret_cast<uint64_t *>(sr_smem + a.subs * SR_SUB);
+        row.load(sr_smem, z, a.V);
+        if (row.tid == 0 && set.m > 0.f)
+            sh.off = min_offset(set);
+        row.loaded();
+        Scale sc;
+        typename Row<T>::Cut cut;
+        bool infinite;
+        if (row_border(row, set, sub, a.status, sc, cut, infinite)) {
+            r.zmax = sc.zmax;
+            r.b = cut.b;
+            r.flags = infinite ? KR_INF : 0;
+            r.mass = cut.mass ? cut.mass : row.mass(sc, cut.b, nullptr, nullptr);
+            const int x = k < L ? __ldg(a.tokens + (int64_t)i * L + k) : -1;
+            if (row.rank == 0 && row.tid == 0 && x >= 0 && x < a.V) {
+                const float v = held_value(logit_value(z, x), infinite);
+                if (kept(r.b, v, x))
+                    r.guess = weight_of<Row<T>::EXACT>(sc, sh.tab, v);
+            }
+        }
+    }
+    if (row.rank == 0 && row.tid == 0)
+        *to = r;
+    pdl_wait();  // (rows of the other type may be done by the launch before; what follows waits for both)
+}
+
+template <typename TD, typename TT>
+struct ChainArgs {
+    const TD *draft;
+    const TT *target;
+    ddt_filter fd, ft;
+    const int32_t *tokens, *n_guess;
+    const float *u, *r;
+    const KeptRow *rows;
+    int32_t *acc_len, *acc_tokens, *status;
+    int L, V, subs;
+};
+
+// 64 x 64 -> a quotient's product: x * (num / den) in integers, x and the result in units
+// of 2^-44; what does not fit becomes the largest number
+struct Ratio {
+    uint64_t m;  // num / den = m 2^-64 2^e, 2^63 <= m
+    int e;
+    DDT_DEVINL uint64_t times(uint64_t x) const
+    {
+        const uint64_t h = __umul64hi(x << 16, m);  // (x < 2^45)
+        const int sh = 16 - e;
+        if (sh >= 0)
+            return sh < 64 ? h >> sh : 0;
+        return -sh < 64 && h <= (~0ull >> -sh) ? h << -sh : ~0ull;
+    }
+};
+// (one thread: a quotient of up to 2^64 by long division)
+DDT_DEVINL Ratio make_ratio(uint64_t num, uint64_t den)
+{
+    Ratio r;
+    const int a = __clzll(num), b = __clzll(den);
+    num <<= a;
+    den <<= b;
+    r.e = b - a;
+    // num / den in (1/2, 2): 2^63 <= m < 2^64
+    const bool big = num >= den;
+    uint64_t rem = big ? num - den : num, q = big ? 1 : 0;
+    for (int k = 0; k < (big ? 63 : 64); ++k) {
+        const bool carry = rem >> 63;
+        rem <<= 1;
+        q <<= 1;
+        if (carry || rem >= den) {
+            rem -= den;
+            q |= 1;
+        }
+    }
+    r.m = q;
+    r.e += big ? 1 : 0;
+    return r;
+}
+
+// two weights in fixed point
+template <bool EXACT>
+DDT_DEVINL void fixed_pair(const Scale &sc, const float2 *tab, float x0, float x1, bool k0, bool k1, uint64_t &w0,
+                           uint64_t &w1)
+{
+    Sum2 s = {0, 0};
+    add_weights<EXACT>(sc, tab, x0, x1, k0, k1, s);
+    float h0, h1, l0, l1;
+    f2unpack(s.hi, h0, h1);
+    f2unpack(s.lo, l0, l1);
+    w0 = to_fixed(h0, l0);
+    w1 = to_fixed(h1, l1);
+}
+
+// weights of the draw: p's, less p's share of q's where there is a q
+template <typename TD, typename TT>
+struct Leftover {
+    static constexpr int E = Vec<TT>::E;
+    Scale p, q;
+    Border bp, bq;
+    const float2 *tab;
+    const TD *zq;  // shared memory: element i of q's row is zq[i]
+    Ratio ratio;
+    bool two, inf_p, inf_q;
+
+    DDT_DEVINL uint64_t sum_to(const float *z, int i0, int last) const
+    {
+        uint64_t t = 0;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+            const float x0 = held_value(z[e], inf_p), x1 = held_value(z[e + 1], inf_p);
+            const bool k0 = e <= last && kept(bp, x0, i0 + e), k1 = e + 1 <= last && kept(bp, x1, i0 + e + 1);
+            if (!(k0 || k1))
+                continue;
+            uint64_t w0, w1;
+            fixed_pair<Vec<TT>::EXACT>(p, tab, x0, x1, k0, k1, w0, w1);
+            if (two) {
+                // (a kept index lies within the row, and so within q's part)
+                const float y0 = k0 ? held_value(value(i0 + e), inf_q) : 0.f, y1 = k1 ? held_value(value(i0 + e + 1), inf_q) : 0.f;
+                const bool j0 = k0 && kept(bq, y0, i0 + e), j1 = k1 && kept(bq, y1, i0 + e + 1);
+                if (j0 || j1) {
+                    uint64_t v0, v1;
+                    fixed_pair<Vec<TD>::EXACT>(q, tab, y0, y1, j0, j1, v0, v1);
+                    v0 = ratio.times(v0);
+                    v1 = ratio.times(v1);
+                    w0 = w0 > v0 ? w0 - v0 : 0;
+                    w1 = w1 > v1 ? w1 - v1 : 0;
+                }
+            }
+            t += w0 + w1;
+        }
+        return t;
+    }
+    DDT_DEVINL uint64_t lane_sum(const float *z, int i0) const { return sum_to(z, i0, E - 1); }
+    DDT_DEVINL float value(int i) const
+    {
+        if constexpr (sizeof(TD) == 2)
+            return bf16_to_f32(zq[i]);
+        else
+            return zq[i];
+    }
+};
+
+// Start this thread's copies of elements [lo, hi) of a row of V (whole 16-byte vectors
+// around them, within the tensor); returns where element 0 of the row would lie.
+template <typename T>
+DDT_DEVINL const T *fetch_range(unsigned char *smem, const T *row, int V, int lo, int hi, int tid)
+{
+    constexpr int E = Vec<T>::E;
+    const int skip = (int)(((uintptr_t)(row + lo) & 15) / sizeof(T));
+    const T *from = row + lo - skip;
+    const uint32_t dst = (uint32_t)__cvta_generic_to_shared(smem);
+    for (int v = tid; v * E < hi - lo + skip; v += SR_THREADS) {
+        if (lo - skip + (v + 1) * E <= V) {
+            cp16(dst + v * 16, from + v * E);
+        } else {
+            T *d = reinterpret_cast<T *>(smem + v * 16);
+            for (int e = 0; e < E && lo - skip + v * E + e < V; ++e)
+                d[e] = from[v * E + e];
+        }
+    }
+    return reinterpret_cast<const T *>(smem) + skip - lo;
+}
+
+template <typename TD, typename TT>
+__global__ void __launch_bounds__(SR_THREADS) chain_kernel(const ChainArgs<TD, TT> a)
+{
+    __shared__ RowShared sh;
+    __shared__ Ratio s_ratio;
+    __shared__ int s_first, s_bad;
+    Row<TT> row;
+    row.begin(&sh);
+    const int L = a.L, V = a.V, i = blockIdx.x / row.cl, lane = row.lane;
+    const int n = guess_count(a.n_guess, i, L);
+    const bool writer = row.rank == 0;
+    pdl_wait();  // the kept rows come from keep_kernel
+    const KeptRow *rows = a.rows + (int64_t)i * (2 * L + 1);
+    if (row.warp == 0) {
+        if (writer && lane == 0 && a.n_guess && n != a.n_guess[i])
+            set_status(a.status, DDT_DEV_BAD_TREE);
+        bool keep = false, bad = false;
+        if (lane <= n)
+            bad = rows[L + lane].flags & KR_BAD;
+        if (lane < n) {
+            const KeptRow q = rows[lane], p = rows[L + lane];
+            bad |= (q.flags & KR_BAD) != 0;
+            const int x = a.tokens[(int64_t)i * L + lane];
+            const bool in = x >= 0 && x < V;
+            if (!in && writer)
+                set_status(a.status, DDT_DEV_BAD_TREE);
+            // (q(x) = 0 counts as a ratio of 1)
+            double ratio = 1.0;
+            if (q.guess > 0)
+                ratio = fmin(1.0, p.mass > 0 ? ((double)p.guess * (double)q.mass) / ((double)p.mass * (double)q.guess) : 0.0);
+            keep = in && (double)a.u[(int64_t)i * L + lane] < ratio;
+        }
+        bad = __any_sync(0xFFFFFFFFu, bad);
+        const uint32_t kept_ = __ballot_sync(0xFFFFFFFFu, keep && !bad);
+        const int first = __ffs(~kept_) - 1;  // (lanes from n on keep nothing)
+        if (lane == 0) {
+            s_first = first;
+            s_bad = bad;
+            if (first < n && !bad) {
+                const uint64_t mp = rows[L + first].mass, mq = rows[first].mass;
+                if (mp > 0 && mq > 0)
+                    s_ratio = make_ratio(mp, mq);
+            }
+        }
+        if (writer) {
+            if (lane == 0)
+                a.acc_len[i] = first + 1;
+            if (bad && lane == 0)
+                set_status(a.status, DDT_DEV_BAD_SETTING);
+            for (int t = lane; t <= L; t += 32)
+                if (t != first)
+                    a.acc_tokens[(int64_t)i * (L + 1) + t] = t < first ? a.tokens[(int64_t)i * L + t] : -1;
+        }
+    }
+    __syncthreads();
+    const int first = s_first;
+    int32_t *to = a.acc_tokens + (int64_t)i * (L + 1) + first;
+    const KeptRow kp = rows[L + first];
+    Leftover<TD, TT> f;
+    f.two = first < n && rows[first].mass > 0;
+    if (s_bad || kp.mass == 0) {
+        if (writer && row.tid == 0)
+            *to = -1;
+        return;
+    }
+    uint64_t *sub = reinterpret_cast<uint64_t *>(sr_smem + a.subs * SR_SUB);
+    unsigned char *smem_q = reinterpret_cast<unsigned char *>(sub + a.subs + (a.subs & 1));
+    row.load(sr_smem, a.target + ((int64_t)i * (L + 1) + first) * V, V);
+    f.p = make_scale(kp.zmax, load_settings(a.ft, i).T);
+    f.bp = kp.b;
+    f.inf_p = kp.flags & KR_INF;
+    f.tab = sh.tab;
+    if (f.two) {
+        const KeptRow kq = rows[first];
+        f.q = make_scale(kq.zmax, load_settings(a.fd, i).T);
+        f.bq = kq.b;
+        f.inf_q = kq.flags & KR_INF;
+        f.ratio = s_ratio;
+        const int lo = max(0, row.sl.index0(0, 0)), hi = min(V, row.sl.index0(row.sl.ns, 0));
+        f.zq = fetch_range(smem_q, a.draft + ((int64_t)i * L + first) * V, V, lo, hi, row.tid);
+    }
+    row.loaded();
+    const uint64_t(*all)[4];
+    const uint64_t mass = row.total(f, sub, &all);
+    if (mass == 0) {
+        if (writer && row.tid == 0)
+            *to = -1;
+        return;
+    }
+    const int token = row.locate(sub, all, draw_target(__ldg(a.r + i), mass), f);
+    if (token >= 0)
+        *to = token;
+}
+
+// ------------------------------------------------------------------ host side
+constexpr int SR_SMEM_MAX = 227 * 1024 - (int)sizeof(RowShared) - 256;
+
+// Bytes of shared memory of a CTA that holds a slice of a row of V: the slice, its sub-
+// chunks' sums, and (bytes_q > 0) as many elements of another row of that element size.
+template <typename T>
+int slice_bytes(int V, int cl, int bytes_q)
+{
+    const int subs = slice_subs<T>(V, cl);
+    const int q = bytes_q ? (subs * (SR_SUB / (int)sizeof(T)) * bytes_q + 32) : 0;
+    return subs * SR_SUB + (subs + (subs & 1)) * 8 + (q + 15) / 16 * 16;
+}
+
+// CTAs of a row's cluster
+template <typename T>
+int pick_cluster(int V, int64_t rows, int num_sms, int bytes_q)
+{
+    const int subs = row_subs<T>(V);
+    int cl = 1;
+    // as many as leave two sub-chunks a warp
+    while (cl < 8 && subs >= 2 * cl * 2 * SR_WARPS)
+        cl *= 2;
+    while (cl < SR_MAX_CL && slice_bytes<T>(V, cl, bytes_q) > SR_SMEM_MAX)
+        cl *= 2;
+    return cl;
+}
+
+template <typename Args>
+cudaError_t launch_rows(void (*kernel)(Args), DeviceFlags &ready, int dev, int64_t rows, int cl, int smem, bool dependent,
+                        const Args &args, cudaStream_t s)
+{
+    if (rows * cl > 0x7FFFFFFF)
+        return cudaErrorInvalidConfiguration;
+    if (!ready.test(dev)) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SR_SMEM_MAX);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess)
+            return e;
+        ready.set(dev);
+    }
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = cl;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3((unsigned)(rows * cl));
+    lc.blockDim = dim3(SR_THREADS);
+    lc.dynamicSmemBytes = smem;
+    lc.stream = s;
+    lc.attrs = at;
+    lc.numAttrs = dependent ? 2 : 1;
+    return cudaLaunchKernelEx(&lc, kernel, args);
+}
+
+template <typename T>
+cudaError_t sample_rows(const ddt_ctx *c, const void *logits, int N, const ddt_filter &f, const float *u, int32_t *tokens,
+                        float *logprobs, cudaStream_t s)
+{
+    static DeviceFlags ready;
+    const int V = c->cfg.V, cl = pick_cluster<T>(V, N, c->num_sms, 0);
+    const SampleArgs<T> a = {(const T *)logits, f, u, tokens, logprobs, c->status, V, slice_subs<T>(V, cl)};
+    return launch_rows(sample_kernel<T>, ready, c->device, N, cl, slice_bytes<T>(V, cl, 0), false, a, s);
+}
+
+template <typename T>
+cudaError_t keep_rows(const ddt_ctx *c, const void *draft, const void *target, const ddt_filter &fd, const ddt_filter &ft,
+                      const int32_t *tokens, const int32_t *n_guess, int R, bool dependent, cudaStream_t s)
+{
+    static DeviceFlags ready;
+    const int V = c->cfg.V, L = c->cfg.L;
+    const int64_t rows = (int64_t)R * ((draft ? L : 0) + (target ? L + 1 : 0));
+    const int cl = pick_cluster<T>(V, rows, c->num_sms, 0);
+    const KeepArgs<T> a = {(const T *)draft, (const T *)target, fd, ft, tokens, n_guess, (KeptRow *)c->sm_rows,
+                           c->status, L, V, slice_subs<T>(V, cl)};
+    return launch_rows(keep_kernel<T>, ready, c->device, rows, cl, slice_bytes<T>(V, cl, 0), dependent, a, s);
+}
+
+template <typename TD, typename TT>
+cudaError_t chains(const ddt_ctx *c, const void *draft, const void *target, const ddt_filter &fd, const ddt_filter &ft,
+                   const int32_t *tokens, const float *u, const float *r, int R, const int32_t *n_guess, int32_t *acc_len,
+                   int32_t *acc_tokens, cudaStream_t s)
+{
+    static DeviceFlags ready;
+    cudaError_t e;
+    if constexpr (sizeof(TD) == sizeof(TT)) {
+        e = keep_rows<TT>(c, draft, target, fd, ft, tokens, n_guess, R, false, s);
+    } else {
+        e = keep_rows<TD>(c, draft, nullptr, fd, ft, tokens, n_guess, R, false, s);
+        if (e == cudaSuccess)
+            e = keep_rows<TT>(c, nullptr, target, fd, ft, tokens, n_guess, R, true, s);
+    }
+    if (e != cudaSuccess)
+        return e;
+    const int V = c->cfg.V, cl = pick_cluster<TT>(V, R, c->num_sms, sizeof(TD));
+    const ChainArgs<TD, TT> a = {(const TD *)draft, (const TT *)target, fd, ft, tokens, n_guess, u, r,
+                                 (const KeptRow *)c->sm_rows, acc_len, acc_tokens, c->status, c->cfg.L, V,
+                                 slice_subs<TT>(V, cl)};
+    return launch_rows(chain_kernel<TD, TT>, ready, c->device, R, cl, slice_bytes<TT>(V, cl, sizeof(TD)), true, a, s);
+}
+
+}  // namespace
+
+size_t sample_row_bytes() { return sizeof(KeptRow); }
+
+cudaError_t launch_sample(const ddt_ctx *c, const void *logits, int dtype, int N, const ddt_filter &f, const float *u,
+                          int32_t *tokens, float *logprobs, cudaStream_t s)
+{
+    return dtype == DDT_BF16 ? sample_rows<uint16_t>(c, logits, N, f, u, tokens, logprobs, s)
+                             : sample_rows<float>(c, logits, N, f, u, tokens, logprobs, s);
+}
+
+cudaError_t launch_accept_sampled(const ddt_ctx *c, const void *draft, const void *target, const ddt_filter &fd,
+                                  const ddt_filter &ft, const int32_t *tokens, const float *u, const float *r, int R,
+                                  const int32_t *n_guess, int32_t *acc_len, int32_t *acc_tokens, cudaStream_t s)
+{
+    const bool bd = c->cfg.draft_dtype == DDT_BF16, bt = c->cfg.target_dtype == DDT_BF16;
+    if (bd && bt)
+        return chains<uint16_t, uint16_t>(c, draft, target, fd, ft, tokens, u, r, R, n_guess, acc_len, acc_tokens, s);
+    if (bd)
+        return chains<uint16_t, float>(c, draft, target, fd, ft, tokens, u, r, R, n_guess, acc_len, acc_tokens, s);
+    if (bt)
+        return chains<float, uint16_t>(c, draft, target, fd, ft, tokens, u, r, R, n_guess, acc_len, acc_tokens, s);
+    return chains<float, float>(c, draft, target, fd, ft, tokens, u, r, R, n_guess, acc_len, acc_tokens, s);
+}

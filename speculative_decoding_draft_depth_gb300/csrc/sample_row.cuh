@@ -1,0 +1,1159 @@
+// sample_row.cuh -- one row of logits held by a thread-block cluster: the tokens that
+// temperature, top-k, top-p and min-p keep, their weights, and the draw of one.
+//
+// With z_max the row's largest logit and T the temperature, token i's weight is
+//   w_i = exp((z_i - z_max) / T).
+// All three filters keep a front part of the order (z descending, index ascending):
+// min-p the tokens with w_i >= min_p, top-k the first k of those, top-p the shortest
+// front part of these whose weights reach p times their sum. So the kept set is one
+// border (value, index): z above the value, or equal to it and an index up to the
+// border's. The draw takes the kept tokens in index order: the first whose running sum
+// exceeds u times the sum.
+//
+// The border and the draw are decisions: an error in a sum decides wrongly whenever a
+// border lies within it, and a vocabulary has 10^5 of them. So weights are made to about
+// 2^-40 of themselves, from pairs of fp32 numbers (one fma more for each rounding that
+// is kept), and added up as 64-bit integers in units of 2^-44, whose sums do not depend
+// on an order. What is below 2^-64 of the largest weight counts as zero.
+//
+// A row is read from HBM once: the CTAs of its cluster hold it in shared memory (sub-
+// chunks of 512 bytes: 16 bytes a lane), and every further look at it reads that. What
+// the CTAs have to tell one another goes through distributed shared memory, one cluster
+// barrier an exchange, and each CTA then comes to the same decision by itself.
+#pragma once
+
+#include <stdint.h>
+
+#include "ddt_device.cuh"
+#include "ddt_internal.h"
+
+namespace {
+
+constexpr int SR_THREADS = 256, SR_WARPS = SR_THREADS / 32;
+constexpr int SR_SUB = 512;       // bytes of a sub-chunk
+constexpr int SR_MAX_CL = 16;     // CTAs of a cluster
+constexpr int SR_CAP = 512;       // candidates that are sorted in one place
+constexpr int SR_PROBE = 256;     // how many the first collection asks for, and the largest k that it serves
+constexpr int SR_BINS = 512;      // (two a thread)
+constexpr int SR_ONE = 44;        // a weight of 1 is 2^44
+constexpr float SR_MAX_FLOAT = 3.402823466e38f;
+constexpr float SR_TINY = 8.077935669e-28f;  // 2^-90: differences of logits stay far above what 1 / x can take
+
+// ---------------------------------------------------------------- cluster
+DDT_DEVINL uint32_t cl_rank()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+DDT_DEVINL uint32_t cl_size()
+{
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+DDT_DEVINL void cl_sync()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+DDT_DEVINL uint32_t cl_map(const void *p, uint32_t rank)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+    return r;
+}
+DDT_DEVINL void cl_st64(uint32_t at, uint64_t v)
+{
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(v) : "memory");
+}
+DDT_DEVINL uint32_t cl_ld32(uint32_t at)
+{
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+DDT_DEVINL uint32_t cl_add32(uint32_t at, uint32_t v)
+{
+    uint32_t r;
+    asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(r) : "r"(at), "r"(v) : "memory");
+    return r;
+}
+DDT_DEVINL void cp16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+DDT_DEVINL void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+DDT_DEVINL uint64_t f2mul(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+DDT_DEVINL uint64_t f2both(float x) { return f2pack(x, x); }
+
+// order-preserving map of floats to unsigned integers
+DDT_DEVINL uint32_t order_key(float z)
+{
+    const uint32_t b = __float_as_uint(z == 0.f ? 0.f : z);  // (-0 and 0 are equal)
+    return b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+DDT_DEVINL float key_value(uint32_t k)
+{
+    return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+
+// ---------------------------------------------------------------- weights
+struct Scale {
+    float zmax, ch, cl;  // log2(e) / T = ch + cl
+    float zfloor;        // smaller values have no weight (finite)
+};
+
+// (fp32 throughout: the fp64 units take 16 cycles a warp's instruction)
+DDT_DEVINL Scale make_scale(float zmax, float T)
+{
+    Scale s;
+    s.zmax = zmax;
+    const float LH = 1.44269502162933349609375f, LL = 1.92596299112661746887e-8f;  // log2(e)
+    s.ch = LH / T;
+    s.cl = (fmaf(-s.ch, T, LH) + LL) / T;
+    // 2^-64 is 44.36 T below; rounded up, so that no exponent is below -64. A difference of
+    // two values stays finite.
+    s.zfloor = fmaxf(__fsub_ru(zmax, 44.3614195f * T), fmaxf(-SR_MAX_FLOAT, zmax - SR_MAX_FLOAT));
+    return s;
+}
+
+// 2^(j / 32) as a pair of floats, j = 0 .. 31
+__device__ const float2 SR_TABLE[32] = {
+    {1.f, 0.f}, {1.0218972f, -4.81155986e-08f}, {1.04427373f, 4.83347016e-08f},
+    {1.06714046f, -5.93375198e-08f}, {1.09050775f, -1.30775399e-08f}, {1.1143868f, -5.43554002e-08f},
+    {1.13878858f, 5.38622231e-08f}, {1.1637249f, -4.05144149e-08f}, {1.18920708f, 3.79763527e-08f},
+    {1.21524739f, -3.26739489e-08f}, {1.24185777f, 4.4968381e-08f}, {1.26905096f, 1.41933332e-09f},
+    {1.29683959f, -4.01899953e-08f}, {1.32523668f, -3.49637332e-08f}, {1.35425556f, -1.01233493e-08f},
+    {1.38390994f, -5.87557736e-08f}, {1.41421354f, 2.4203235e-08f}, {1.44518077f, 3.32419994e-08f},
+    {1.47682619f, -4.50089885e-08f}, {1.50916445f, -2.49593732e-08f}, {1.54221082f, 8.07090483e-09f},
+    {1.5759809f, -5.66102543e-08f}, {1.61049032f, 9.83621717e-09f}, {1.64575553f, -5.12497209e-08f},
+    {1.68179286f, -2.47553267e-08f}, {1.71861935f, -4.8496176e-08f}, {1.75625217f, -9.23577037e-09f},
+    {1.79470909f, -1.14150449e-08f}, {1.8340081f, -1.1239278e-08f}, {1.87416768f, -4.66300563e-08f},
+    {1.91520655f, 9.84532811e-09f}, {1.95714414f, -1.70218044e-08f}};
+
+// Sums of weights. A weight of up to 1 is cut at 2^-18: the front parts add up without an
+// error (up to 16 of them), what is behind it in fp32 (2^-42 of 1 at most, each time).
+struct Sum2 {
+    uint64_t hi, lo;  // two lanes each
+};
+constexpr float SR_CUT = 48.0f;  // 1.5 * 2^5: fp32 numbers next to it are 2^-18 apart
+
+// weights of two logits; k0, k1: whether they count. EXACT: the error of z - z_max for any
+// floats (else the shorter form, which serves z of few bits, as bf16 numbers have)
+template <bool EXACT>
+DDT_DEVINL void add_weights(const Scale &sc, const float2 *tab, float x0, float x1, bool k0, bool k1, Sum2 &sum)
+{
+    const uint64_t m1 = f2both(-1.f);
+    const uint64_t z = f2pack(k0 ? x0 : sc.zmax, k1 ? x1 : sc.zmax), nz = f2both(-sc.zmax);
+    // d + dl = z - zmax
+    const uint64_t d = f2add(z, nz);
+    uint64_t dl;
+    if (EXACT) {
+        const uint64_t bb = f2fma(z, m1, d);                     // the part of -zmax that d took
+        dl = f2add(f2fma(f2fma(bb, m1, d), m1, z), f2fma(bb, m1, nz));
+    } else {
+        dl = f2fma(f2add(d, f2both(sc.zmax)), m1, z);
+    }
+    // y + yl = (d + dl) (ch + cl), the exponent
+    const uint64_t nch = f2both(-sc.ch);
+    const uint64_t y = f2mul(d, f2both(sc.ch));
+    uint64_t nyl = f2fma(d, nch, y);  // -yl
+    nyl = f2fma(d, f2both(-sc.cl), nyl);
+    nyl = f2fma(dl, nch, nyl);
+    // y = n / 32 + r; s + re = r + yl, |s| <= 2^-6
+    const float C5 = 393216.0f;  // 1.5 * 2^18: fp32 numbers next to it are 2^-5 apart
+    const uint64_t t = f2add(y, f2both(C5));
+    const uint64_t r = f2fma(f2add(t, f2both(-C5)), m1, y);
+    const uint64_t s = f2fma(nyl, m1, r);
+    const uint64_t nre = f2add(nyl, f2fma(r, m1, s));
+    // 2^(s + re) - 1 = h + he, h = s ln 2 in fp32 (ln 2 as a pair), the rest of the series
+    const float LH = 0.693147182464599609375f, LL = -1.90465429995776804525e-9f;
+    const uint64_t h = f2mul(s, f2both(LH));
+    uint64_t nhe = f2fma(s, f2both(-LH), h);
+    nhe = f2fma(s, f2both(-LL), nhe);
+    nhe = f2fma(nre, f2both(LH), nhe);
+    uint64_t g = f2fma(s, f2both(-9.6181291076e-3f), f2both(-5.5504108665e-2f));
+    g = f2fma(s, g, f2both(-0.24022650696f));
+    nhe = f2fma(f2mul(s, s), g, nhe);
+    float t0, t1;
+    f2unpack(t, t0, t1);
+    const int i0 = __float_as_int(t0), i1 = __float_as_int(t1);
+    const float2 a = tab[i0 & 31], b = tab[i1 & 31];
+    const uint64_t th = f2pack(a.x, b.x), tl = f2pack(a.y, b.y);
+    // (th + tl) (1 + h + he) = w + wl
+    const uint64_t w = f2fma(th, h, th);
+    uint64_t wl = f2fma(th, h, f2fma(w, m1, th));  // th + th h - w
+    wl = f2fma(th, f2mul(nhe, m1), wl);
+    wl = f2add(f2fma(tl, h, wl), tl);
+    // times 2^n
+    const float e0 = __int_as_float(((i0 << 18) & 0xFF800000) + 0x3F800000);
+    const float e1 = __int_as_float(((i1 << 18) & 0xFF800000) + 0x3F800000);
+    const uint64_t e = f2pack(k0 ? e0 : 0.f, k1 ? e1 : 0.f);
+    const uint64_t ws = f2mul(w, e);
+    const uint64_t front = f2add(f2add(ws, f2both(SR_CUT)), f2both(-SR_CUT));
+    sum.hi = f2add(sum.hi, front);
+    sum.lo = f2add(sum.lo, f2fma(wl, e, f2fma(front, m1, ws)));
+}
+
+DDT_DEVINL uint64_t to_fixed(float hi, float lo)
+{
+    const long long v = __float2ll_rn(hi * 17592186044416.0f) + __float2ll_rn(lo * 17592186044416.0f);  // 2^44
+    return v > 0 ? (uint64_t)v : 0;
+}
+DDT_DEVINL uint64_t to_fixed(const Sum2 &s)
+{
+    float a, b, c, d;
+    f2unpack(s.hi, a, b);
+    f2unpack(s.lo, c, d);
+    return to_fixed(a + b, c + d);
+}
+
+// one weight (z counts)
+template <bool EXACT>
+DDT_DEVINL uint64_t weight_of(const Scale &sc, const float2 *tab, float z)
+{
+    Sum2 s = {0, 0};
+    add_weights<EXACT>(sc, tab, z, z, z >= sc.zfloor, false, s);
+    return to_fixed(s);
+}
+
+// x m for 0 < x < 1, rounded down or up
+DDT_DEVINL uint64_t fraction_of(float x, uint64_t m, bool up)
+{
+    const uint32_t b = __float_as_uint(x);
+    const int sh = 126 - (int)(b >> 23);  // x = mantissa 2^-24 2^-sh (a subnormal x: 0)
+    if (sh > 125)
+        return up && x > 0.f ? 1 : 0;
+    const uint64_t a = (uint64_t)((b & 0x7FFFFFu) | 0x800000u) << 40;
+    const uint64_t hi = __umul64hi(a, m), lo = a * m;
+    if (sh >= 64)
+        return up ? 1 : 0;
+    const bool rest = lo != 0 || (hi & ((1ull << sh) - 1)) != 0;
+    return (hi >> sh) + (up && rest ? 1 : 0);
+}
+
+// ---------------------------------------------------------------- border
+struct Border {
+    float z;   // kept: above this value, or equal to it
+    int last;  //   with an index up to this
+};
+DDT_DEVINL bool kept(const Border &b, float z, int i) { return z > b.z || (z == b.z && i <= b.last); }
+
+// ---------------------------------------------------------------- a row in shared memory
+struct Xchg {
+    uint64_t w[2][SR_MAX_CL][4];  // what the CTAs tell one another, by turns
+};
+struct RowShared {
+    float2 tab[32];
+    Xchg x;
+    uint64_t warp[SR_WARPS][4];
+    uint64_t list[SR_CAP];   // candidates: (order_key << 32) | ~index
+    uint32_t hist[SR_BINS];
+    uint32_t count[4];       // candidates collected (the first CTA's; a place for each collection)
+    int found[4];
+    float2 off;              // T ln(min_p)
+};
+
+template <typename T> struct Vec;
+template <> struct Vec<uint16_t> {
+    static constexpr int E = 8;
+    static constexpr bool EXACT = false;
+    static constexpr uint32_t NONE = 0xFF80FF80u;
+    DDT_DEVINL static void get(const uint4 &v, float *z)
+    {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            z[2 * i] = bf16lo(w[i]);
+            z[2 * i + 1] = bf16hi(w[i]);
+        }
+    }
+};
+template <> struct Vec<float> {
+    static constexpr int E = 4;
+    static constexpr bool EXACT = true;
+    static constexpr uint32_t NONE = 0xFF800000u;
+    DDT_DEVINL static void get(const uint4 &v, float *z)
+    {
+        z[0] = __uint_as_float(v.x);
+        z[1] = __uint_as_float(v.y);
+        z[2] = __uint_as_float(v.z);
+        z[3] = __uint_as_float(v.w);
+    }
+};
+
+// a logit as the row in shared memory holds it (Row::top, Row::only_infinite)
+DDT_DEVINL float held_value(float z, bool infinite)
+{
+    if (infinite)
+        return z == -DDT_NEG_INF ? 0.f : DDT_NEG_INF;
+    return z != z ? DDT_NEG_INF : fabsf(z) < SR_TINY ? 0.f : z;
+}
+DDT_DEVINL float logit_value(const uint16_t *p, int64_t i) { return bf16_to_f32(__ldg(p + i)); }
+DDT_DEVINL float logit_value(const float *p, int64_t i) { return __ldg(p + i); }
+
+// sub-chunks of a row of V logits that begins anywhere (the row's first 16 bytes may hold
+// up to E - 1 of the row before), and how many of them one of cl CTAs holds at most
+template <typename T>
+__host__ __device__ constexpr int row_subs(int V) { return (int)(((int64_t)V + Vec<T>::E - 1) * sizeof(T) + SR_SUB - 1) / SR_SUB; }
+template <typename T>
+__host__ __device__ constexpr int slice_subs(int V, int cl) { return (row_subs<T>(V) + cl - 1) / cl; }
+
+// The slice of a row that a CTA holds. Element (sub-chunk s, lane, e) has index
+// index0(s, lane) + e.
+template <typename T>
+struct Slice {
+    static constexpr int E = Vec<T>::E, SE = SR_SUB / (int)sizeof(T);
+    unsigned char *at;  // ns sub-chunks
+    int s0, ns, off, V;
+
+    DDT_DEVINL void place(unsigned char *smem, const T *row, int V_, uint32_t rank, uint32_t cl)
+    {
+        at = smem;
+        V = V_;
+        off = (int)(((uintptr_t)row & 15) / sizeof(T));
+        const int subs = (int)(((int64_t)off + V + SE - 1) / SE);
+        s0 = (int)((int64_t)subs * rank / cl);
+        ns = (int)((int64_t)subs * (rank + 1) / cl) - s0;
+    }
+    // start this thread's copies. Whole 16-byte vectors of the row; what is before the
+    // row's first element comes from the row before it (the tensor begins on 16 bytes)
+    DDT_DEVINL void fetch(const T *row, int tid) const
+    {
+        const T *base = row - off;
+        const uint32_t dst = (uint32_t)__cvta_generic_to_shared(at);
+        const int64_t end = (int64_t)off + V;
+        for (int v = tid; v < ns * 32; v += SR_THREADS) {
+            const int64_t j = ((int64_t)s0 * 32 + v) * E;  // the vector's first element, from base
+            if (j + E <= end) {
+                cp16(dst + v * 16, base + j);
+            } else {
+                T *d = reinterpret_cast<T *>(at + v * 16);
+                for (int e = 0; e < E; ++e)
+                    d[e] = j + e < end ? base[j + e] : (T)none();
+            }
+        }
+    }
+    DDT_DEVINL static T none()
+    {
+        if constexpr (sizeof(T) == 2)
+            return (T)0xFF80u;
+        else
+            return DDT_NEG_INF;
+    }
+    // after the copies and a barrier: elements before the row's first
+    DDT_DEVINL void mend(int tid) const
+    {
+        if (s0 == 0 && ns > 0 && tid < off)
+            reinterpret_cast<T *>(at)[tid] = none();
+    }
+    DDT_DEVINL uint4 raw(int s, int lane) const { return *reinterpret_cast<const uint4 *>(at + s * SR_SUB + lane * 16); }
+    DDT_DEVINL int index0(int s, int lane) const { return (s0 + s) * SE + lane * E - off; }
+};
+
+// totals over a warp
+DDT_DEVINL uint64_t warp_sum64(uint64_t v)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
+    return v;
+}
+DDT_DEVINL uint64_t warp_incl64(uint64_t v, int lane)
+{
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint64_t y = __shfl_up_sync(0xFFFFFFFFu, v, o);
+        if (lane >= o)
+            v += y;
+    }
+    return v;
+}
+
+// One row of a cluster: what its threads share in doing it.
+template <typename T>
+struct Row {
+    static constexpr int E = Vec<T>::E;
+    static constexpr bool EXACT = Vec<T>::EXACT;
+    RowShared *sh;
+    Slice<T> sl;
+    int tid, lane, warp;
+    uint32_t rank, cl, turn, nth;
+
+    DDT_DEVINL void begin(RowShared *s)
+    {
+        sh = s;
+        tid = threadIdx.x;
+        lane = tid & 31;
+        warp = tid >> 5;
+        rank = cl_rank();
+        cl = cl_size();
+        turn = nth = 0;
+        if (tid < 4)
+            sh->count[tid] = 0;  // (a cluster barrier comes before the first collection)
+    }
+
+    // Every CTA tells the others up to four words (held by every thread). A place is
+    // written again only two exchanges later, behind a barrier that its readers reach
+    // after they have read. Returns the words of all CTAs.
+    DDT_DEVINL const uint64_t (*exchange(uint64_t a, uint64_t b, uint64_t c, uint64_t d))[4]
+    {
+        const uint32_t p = turn++ & 1;
+        if (tid < (int)cl * 4) {
+            const int q = tid & 3;
+            cl_st64(cl_map(&sh->x.w[p][rank][q], tid >> 2), q == 0 ? a : q == 1 ? b : q == 2 ? c : d);
+        }
+        cl_sync();
+        return sh->x.w[p];
+    }
+
+    // hold a row: copies started, and waited for
+    DDT_DEVINL void load(unsigned char *smem, const T *row, int V)
+    {
+        sl.place(smem, row, V, rank, cl);
+        sl.fetch(row, tid);
+        if (tid < 32)
+            sh->tab[tid] = SR_TABLE[tid];
+    }
+    DDT_DEVINL void loaded()
+    {
+        cp_wait_all();
+        __syncthreads();
+        sl.mend(tid);
+        __syncthreads();
+    }
+
+    // ---- the row's largest value, each thread's own, the least of the threads' finite ones
+    struct Top {
+        float zmax, own, least;
+        bool nan;
+    };
+    DDT_DEVINL Top top()
+    {
+        float m = DDT_NEG_INF;
+        bool nan = false;
+        for (int s = warp; s < sl.ns; s += SR_WARPS) {
+            const uint4 v = sl.raw(s, lane);
+            float z[E];
+            Vec<T>::get(v, z);
+            bool bad = false;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const bool odd = !(fabsf(z[e]) >= SR_TINY) && z[e] != 0.f;
+                bad |= odd;
+                m = fmaxf(m, odd ? (z[e] != z[e] ? m : 0.f) : z[e]);
+            }
+            if (bad) {  // from here on a NaN is -infinity, and what is next to 0 is 0
+                T *d = reinterpret_cast<T *>(sl.at + s * SR_SUB + lane * 16);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if (z[e] != z[e]) {
+                        nan = true;
+                        d[e] = Slice<T>::none();
+                    } else if (fabsf(z[e]) < SR_TINY) {
+                        d[e] = (T)0;
+                    }
+            }
+        }
+        Top r;
+        r.own = m;
+        float hi = m, lo = m == DDT_NEG_INF ? SR_MAX_FLOAT : m;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+            lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
+        }
+        nan = __any_sync(0xFFFFFFFFu, nan);
+        if (lane == 0)
+            sh->warp[warp][0] = ((uint64_t)__float_as_uint(hi) << 32) | __float_as_uint(lo), sh->warp[warp][1] = nan;
+        __syncthreads();
+        nan = false;
+#pragma unroll
+        for (int w = 0; w < SR_WARPS; ++w) {
+            const uint64_t x = sh->warp[w][0];
+            hi = fmaxf(hi, __uint_as_float((uint32_t)(x >> 32)));
+            lo = fminf(lo, __uint_as_float((uint32_t)x));
+            nan |= sh->warp[w][1] != 0;
+        }
+        const uint64_t(*all)[4] = exchange(((uint64_t)__float_as_uint(hi) << 32) | __float_as_uint(lo), nan, 0, 0);
+        for (uint32_t c = 0; c < cl; ++c) {
+            const uint64_t x = all[c][0];
+            hi = fmaxf(hi, __uint_as_float((uint32_t)(x >> 32)));
+            lo = fminf(lo, __uint_as_float((uint32_t)x));
+            nan |= all[c][1] != 0;
+        }
+        r.zmax = hi;
+        r.least = lo;
+        r.nan = nan;
+        return r;
+    }
+    // a row with +infinity: those tokens have equal weights, the others none
+    DDT_DEVINL void only_infinite(Top &t)
+    {
+        for (int s = warp; s < sl.ns; s += SR_WARPS) {
+            T *d = reinterpret_cast<T *>(sl.at + s * SR_SUB + lane * 16);
+            float z[E];
+            Vec<T>::get(sl.raw(s, lane), z);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                d[e] = z[e] == t.zmax ? (T)0 : Slice<T>::none();
+        }
+        __syncthreads();
+        t.own = t.own == t.zmax ? 0.f : DDT_NEG_INF;
+        t.zmax = t.least = 0.f;
+    }
+
+    // an element of this CTA's slice
+    DDT_DEVINL float value(int i) const
+    {
+        const T x = reinterpret_cast<const T *>(sl.at)[i + sl.off - sl.s0 * Slice<T>::SE];
+        if constexpr (sizeof(T) == 2)
+            return bf16_to_f32(x);
+        else
+            return x;
+    }
+
+    // block-wide sum of one word a thread, known to all
+    DDT_DEVINL uint64_t block_sum(uint64_t v)
+    {
+        v = warp_sum64(v);
+        __syncthreads();  // (the words before have been read)
+        if (lane == 0)
+            sh->warp[warp][0] = v;
+        __syncthreads();
+        uint64_t t = 0;
+#pragma unroll
+        for (int w = 0; w < SR_WARPS; ++w)
+            t += sh->warp[w][0];
+        return t;
+    }
+
+    // ---- sum of the weights of the kept tokens, over the row. sub: each sub-chunk's
+    // (or null). all: every CTA's total
+    DDT_DEVINL uint64_t mass(const Scale &sc, const Border &b, uint64_t *sub, const uint64_t (**all)[4])
+    {
+        uint64_t own = 0;
+        for (int s = warp; s < sl.ns; s += SR_WARPS) {
+            float z[E];
+            Vec<T>::get(sl.raw(s, lane), z);
+            const int i0 = sl.index0(s, lane);
+            bool k[E], some = false;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                some |= k[e] = kept(b, z[e], i0 + e);
+            uint64_t q = 0;
+            if (__any_sync(0xFFFFFFFFu, some)) {
+                Sum2 sum = {0, 0};
+#pragma unroll
+                for (int e = 0; e < E; e += 2)
+                    add_weights<EXACT>(sc, sh->tab, z[e], z[e + 1], k[e], k[e + 1], sum);
+                q = to_fixed(sum);
+                if (sub)
+                    q = warp_sum64(q);
+            }
+            if (sub) {
+                if (lane == 0)
+                    sub[s] = q;
+                else
+                    q = 0;
+            }
+            own += q;
+        }
+        const uint64_t mine = block_sum(own);
+        const uint64_t(*a)[4] = exchange(mine, 0, 0, 0);
+        uint64_t t = 0;
+        for (uint32_t c = 0; c < cl; ++c)
+            t += a[c][0];
+        if (all)
+            *all = a;
+        return t;
+    }
+
+    // ---- histogram of values from vhi down, and the first bin at which the tokens so far
+    // reach `want` (-1: never). Bins are even in value: (vhi - z) * scale, cut off.
+    DDT_DEVINL static int bin_of(float vhi, float scale, float z) { return min(SR_BINS - 1, (int)((vhi - z) * scale)); }
+    DDT_DEVINL static float bin_scale(float vhi, float vlo)
+    {
+        const float r = vhi - vlo;  // (finite: both within the floats' half range, or the difference is cut)
+        return r > 0.f ? (SR_BINS - 1) / fminf(r, SR_MAX_FLOAT) : 0.f;
+    }
+    DDT_DEVINL void clear_hist()
+    {
+        sh->hist[tid] = sh->hist[tid + SR_THREADS] = 0;
+        __syncthreads();
+    }
+    // after a cluster barrier: this thread's two bins over the whole row
+    DDT_DEVINL void row_bins(uint32_t &n0, uint32_t &n1)
+    {
+        n0 = n1 = 0;
+        for (uint32_t c = 0; c < cl; ++c) {
+            const uint32_t at = cl_map(&sh->hist[2 * tid], c);
+            n0 += cl_ld32(at);
+            n1 += cl_ld32(at + 4);
+        }
+    }
+    // inclusive running sum over the threads of one word each
+    DDT_DEVINL uint64_t block_incl(uint64_t v)
+    {
+        v = warp_incl64(v, lane);
+        __syncthreads();
+        if (lane == 31)
+            sh->warp[warp][0] = v;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w)
+            v += sh->warp[w][0];
+        return v;
+    }
+    // the smallest of the threads' candidates (none: 0x7fffffff), known to all
+    DDT_DEVINL int block_least(int v)
+    {
+        v = __reduce_min_sync(0xFFFFFFFFu, v);
+        __syncthreads();
+        if (lane == 0)
+            sh->warp[warp][0] = (uint64_t)(uint32_t)v;
+        __syncthreads();
+        int r = 0x7FFFFFFF;
+#pragma unroll
+        for (int w = 0; w < SR_WARPS; ++w)
+            r = min(r, (int)(uint32_t)sh->warp[w][0]);
+        return r;
+    }
+
+    // ---- collect the tokens that `in` names in the first CTA (in any order); returns how
+    // many there are, which may be more than the list holds. At most four a row.
+    template <typename In>
+    DDT_DEVINL uint32_t collect(In in)
+    {
+        const uint32_t cnt = cl_map(&sh->count[nth], 0), list = cl_map(&sh->list[0], 0);
+        nth = (nth + 1) & 3;
+        for (int s = warp; s < sl.ns; s += SR_WARPS) {
+            float z[E];
+            Vec<T>::get(sl.raw(s, lane), z);
+            const int i0 = sl.index0(s, lane);
+            bool k[E];
+            uint32_t n = 0;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                n += k[e] = in(z[e], i0 + e);
+            if (n > 0) {
+                uint32_t p = cl_add32(cnt, n);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if (k[e]) {
+                        if (p < SR_CAP)
+                            cl_st64(list + p * 8, ((uint64_t)order_key(z[e]) << 32) | (uint32_t)~(i0 + e));
+                        ++p;
+                    }
+            }
+        }
+        cl_sync();
+        return cl_ld32(cnt);
+    }
+
+    // the first CTA: its list's n candidates in descending order (value, then lower index)
+    DDT_DEVINL void sort_list(int n)
+    {
+        int p2 = 32;
+        while (p2 < n)
+            p2 <<= 1;
+        for (int i = n + tid; i < p2; i += SR_THREADS)
+            sh->list[i] = 0;
+        __syncthreads();
+        for (int k = 2; k <= p2; k <<= 1)
+            for (int j = k >> 1; j > 0; j >>= 1) {
+                for (int i = tid; i < p2 / 2; i += SR_THREADS) {
+                    const int lo = 2 * j * (i / j) + i % j, hi = lo + j;
+                    const uint64_t a = sh->list[lo], b = sh->list[hi];
+                    if ((a < b) == ((lo & k) == 0)) {
+                        sh->list[lo] = b;
+                        sh->list[hi] = a;
+                    }
+                }
+                __syncthreads();
+            }
+    }
+
+    // ---- the border among sorted candidates. They follow tokens of weight `above` in the
+    // order; at most n2 of the n count. want: what the sum has to reach (0: none asked for,
+    // the n2-th is the last). Known to all CTAs afterwards.
+    struct Cut {
+        Border b;
+        uint64_t mass;  // of all that is kept
+        bool ok;        // the candidates reach `want`
+    };
+    DDT_DEVINL Cut tell(float z, int last, uint64_t mass, bool ok)
+    {
+        const uint64_t(*a)[4] = exchange(((uint64_t)__float_as_uint(z) << 32) | (uint32_t)last, mass, ok, 0);
+        Cut c;
+        c.b.z = __uint_as_float((uint32_t)(a[0][0] >> 32));
+        c.b.last = (int)(uint32_t)a[0][0];
+        c.mass = a[0][1];
+        c.ok = a[0][2] != 0;
+        return c;
+    }
+    // limit: the tokens among the candidates that may be kept (k, or what the k-border left);
+    // p < 1: of `base` (0: of the limited candidates' own sum); whole: the candidates are all
+    // that could be kept, so rounding in `base` does not make them too few
+    DDT_DEVINL Cut cut_list(const Scale &sc, int n, int limit, float p, uint64_t base, uint64_t above, uint64_t want,
+                            bool whole)
+    {
+        float z = 0.f;
+        int last = 0;
+        uint64_t mass = 0;
+        bool ok = true;
+        if (rank == 0) {
+            sort_list(n);
+            const int n2 = min(n, limit), r0 = 2 * tid;
+            uint64_t w0 = 0, w1 = 0;
+            if (r0 < n2)
+                w0 = weight_of<EXACT>(sc, sh->tab, key_value((uint32_t)(sh->list[r0] >> 32)));
+            if (r0 + 1 < n2)
+                w1 = weight_of<EXACT>(sc, sh->tab, key_value((uint32_t)(sh->list[r0 + 1] >> 32)));
+            const uint64_t incl = above + block_incl(w0 + w1);
+            uint64_t total = above;
+            {
+                __syncthreads();
+                if (tid == SR_THREADS - 1)
+                    sh->warp[0][1] = incl;
+                __syncthreads();
+                total = sh->warp[0][1];
+            }
+            int first = n2 - 1;
+            if (p < 1.f) {
+                if (want == 0)
+                    want = share_of(p, base ? base : total);
+                const int c = r0 < n2 && incl - w1 >= want ? r0 : r0 + 1 < n2 && incl >= want ? r0 + 1 : 0x7FFFFFFF;
+                first = block_least(c);
+                if (first == 0x7FFFFFFF) {
+                    ok = whole;
+                    first = n2 - 1;
+                }
+            }
+            const uint64_t key = sh->list[first];
+            z = key_value((uint32_t)(key >> 32));
+            last = (int)~(uint32_t)key;
+            if (tid == (first >> 1))
+                sh->warp[0][2] = first & 1 ? incl : incl - w1;
+            __syncthreads();
+            mass = sh->warp[0][2];
+        }
+        return tell(z, last, mass, ok);
+    }
+    DDT_DEVINL static uint64_t share_of(float p, uint64_t mass) { return fraction_of(p, mass, true); }
+
+    // ---- a value that at least `need` tokens reach (lo, if fewer than that many reach lo),
+    // and not many more: from the threads' largest ones (each a different token), or, where
+    // these are too few, from all tokens
+    DDT_DEVINL float probe(const Top &t, float lo, uint32_t need)
+    {
+        const float vlo = fmaxf(t.least, lo), scale = bin_scale(t.zmax, vlo);
+        clear_hist();
+        if ((int64_t)sl.V >= (int64_t)4 * need * E && cl * SR_THREADS >= 4 * need) {
+            if (t.own >= vlo)
+                atomicAdd(&sh->hist[bin_of(t.zmax, scale, t.own)], 1u);
+        } else {
+            for (int s = warp; s < sl.ns; s += SR_WARPS) {
+                float z[E];
+                Vec<T>::get(sl.raw(s, lane), z);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if (z[e] >= vlo)
+                        atomicAdd(&sh->hist[bin_of(t.zmax, scale, z[e])], 1u);
+            }
+        }
+        cl_sync();
+        uint32_t n0, n1;
+        row_bins(n0, n1);
+        const uint64_t incl = block_incl(n0 + n1);
+        const int b = block_least(incl - n1 >= need ? 2 * tid : incl >= need ? 2 * tid + 1 : 0x7FFFFFFF);
+        if (b == 0x7FFFFFFF)
+            return lo;
+        // (a hundredth of a bin covers the rounding of bin_of: 511 * 2^-23 of one)
+        return scale > 0.f ? fmaxf(lo, t.zmax - (b + 1.01f) / scale) : t.zmax;
+    }
+
+    // members of an interval of values: how many, the least and the greatest, and the weight
+    // of the tokens that come before them
+    struct Members {
+        uint32_t n;
+        float lo, hi;
+        uint64_t before;
+    };
+    template <typename Before, typename In>
+    DDT_DEVINL Members members(const Scale &sc, Before before, In in)
+    {
+        uint64_t w = 0;
+        uint32_t n = 0;
+        float lo = SR_MAX_FLOAT, hi = -SR_MAX_FLOAT;
+        for (int s = warp; s < sl.ns; s += SR_WARPS) {
+            float z[E];
+            Vec<T>::get(sl.raw(s, lane), z);
+            const int i0 = sl.index0(s, lane);
+            bool k[E], some = false;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                some |= k[e] = before(z[e], i0 + e);
+                if (in(z[e], i0 + e)) {
+                    ++n;
+                    lo = fminf(lo, z[e]);
+                    hi = fmaxf(hi, z[e]);
+                }
+            }
+            if (some) {
+                Sum2 sum = {0, 0};
+#pragma unroll
+                for (int e = 0; e < E; e += 2)
+                    add_weights<EXACT>(sc, sh->tab, z[e], z[e + 1], k[e], k[e + 1], sum);
+                w += to_fixed(sum);
+            }
+        }
+        w = warp_sum64(w);
+        n = __reduce_add_sync(0xFFFFFFFFu, n);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
+            hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+        }
+        __syncthreads();
+        if (lane == 0) {
+            sh->warp[warp][0] = w;
+            sh->warp[warp][1] = n;
+            sh->warp[warp][2] = ((uint64_t)__float_as_uint(hi) << 32) | __float_as_uint(lo);
+        }
+        __syncthreads();
+        auto sum = [&](const uint64_t(*a)[4], uint32_t count) {
+            Members m = {0, SR_MAX_FLOAT, -SR_MAX_FLOAT, 0};
+            for (uint32_t c = 0; c < count; ++c) {
+                m.before += a[c][0];
+                m.n += (uint32_t)a[c][1];
+                m.lo = fminf(m.lo, __uint_as_float((uint32_t)a[c][2]));
+                m.hi = fmaxf(m.hi, __uint_as_float((uint32_t)(a[c][2] >> 32)));
+            }
+            return m;
+        };
+        const Members m = sum(sh->warp, SR_WARPS);
+        return sum(exchange(m.before, m.n, ((uint64_t)__float_as_uint(m.hi) << 32) | __float_as_uint(m.lo), 0), cl);
+    }
+
+    // ---- the CTA whose part holds `target` (the running sum first exceeds it there) finds
+    // the token. sub: the sub-chunks' sums; all: the CTAs'. F gives a lane's sum and the sum
+    // up to an element. Returns the index in one thread of one CTA, -1 elsewhere.
+    template <typename F>
+    DDT_DEVINL int locate(const uint64_t *sub, const uint64_t (*all)[4], uint64_t target, F f)
+    {
+        uint64_t before = 0;
+        for (uint32_t c = 0; c < rank; ++c)
+            before += all[c][0];
+        if (!(before <= target && target < before + all[rank][0]))
+            return -1;
+        const int per = (sl.ns + SR_THREADS - 1) / SR_THREADS, a = min(sl.ns, tid * per), b = min(sl.ns, a + per);
+        uint64_t own = 0;
+        for (int s = a; s < b; ++s)
+            own += sub[s];
+        uint64_t at = before + block_incl(own) - own;
+        if (at <= target && target < at + own) {
+            int s = a;
+            while (target >= at + sub[s])
+                at += sub[s++];
+            sh->found[0] = s;
+            sh->warp[0][3] = at;
+        }
+        __syncthreads();
+        if (warp > 0)
+            return -1;
+        const int s = sh->found[0];
+        at = sh->warp[0][3];
+        uint4 raw = sl.raw(s, lane);
+        float z[E];
+        Vec<T>::get(raw, z);
+        const uint64_t sum = f.lane_sum(z, sl.index0(s, lane));
+        uint64_t to = at + warp_incl64(sum, lane);
+        const uint32_t hit = __ballot_sync(0xFFFFFFFFu, target < to);
+        const int who = __ffs(hit) - 1;  // (the sub-chunk's sum is the lanes': one is hit)
+        at = __shfl_sync(0xFFFFFFFFu, to - sum, who);
+        raw.x = __shfl_sync(0xFFFFFFFFu, raw.x, who);
+        raw.y = __shfl_sync(0xFFFFFFFFu, raw.y, who);
+        raw.z = __shfl_sync(0xFFFFFFFFu, raw.z, who);
+        raw.w = __shfl_sync(0xFFFFFFFFu, raw.w, who);
+        Vec<T>::get(raw, z);
+        const int i0 = sl.index0(s, who), e = lane & (E - 1);
+        const uint32_t over = __ballot_sync(0xFFFFFFFFu, target < at + f.sum_to(z, i0, e));
+        const int pick = __ffs(over) - 1;
+        return lane == pick ? i0 + pick : -1;
+    }
+
+    // ---- the same sum for any weights: F gives a lane's, over a sub-chunk's 16 bytes
+    template <typename F>
+    DDT_DEVINL uint64_t total(const F &f, uint64_t *sub, const uint64_t (**all)[4])
+    {
+        uint64_t own = 0;
+        for (int s = warp; s < sl.ns; s += SR_WARPS) {
+            float z[E];
+            Vec<T>::get(sl.raw(s, lane), z);
+            const uint64_t q = warp_sum64(f.lane_sum(z, sl.index0(s, lane)));
+            if (lane == 0) {
+                sub[s] = q;
+                own += q;
+            }
+        }
+        const uint64_t(*a)[4] = exchange(block_sum(own), 0, 0, 0);
+        uint64_t t = 0;
+        for (uint32_t c = 0; c < cl; ++c)
+            t += a[c][0];
+        *all = a;
+        return t;
+    }
+
+    struct Equal {  // counts the tokens of one value that a border keeps
+        Border b;
+        float v;
+        DDT_DEVINL uint64_t sum_to(const float *z, int i0, int last) const
+        {
+            uint64_t n = 0;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                n += e <= last && z[e] == v && kept(b, z[e], i0 + e);
+            return n;
+        }
+        DDT_DEVINL uint64_t lane_sum(const float *z, int i0) const { return sum_to(z, i0, E - 1); }
+    };
+    // the index of the m-th token (1, 2, ...) of value v that b keeps; known to all
+    DDT_DEVINL int nth_equal(const Border &b, float v, uint64_t m, uint64_t *sub)
+    {
+        const Equal eq = {b, v};
+        const uint64_t(*all)[4];
+        total(eq, sub, &all);
+        const int i = locate(sub, all, m - 1, eq);
+        __syncthreads();
+        if (tid == 0)
+            sh->found[1] = -1;
+        __syncthreads();
+        if (i >= 0)
+            sh->found[1] = i;
+        __syncthreads();
+        const uint64_t(*who)[4] = exchange((uint64_t)(int64_t)sh->found[1], 0, 0, 0);
+        int r = -1;
+        for (uint32_t c = 0; c < cl; ++c)
+            r = max(r, (int)(int64_t)who[c][0]);
+        return r;
+    }
+
+    // ---- the border of the first k tokens at or above lo, by counts: histograms of ever
+    // smaller intervals, until their tokens fit the list or have one value
+    DDT_DEVINL Border count_border(const Top &t, const Scale &sc, float lo, int64_t k, uint64_t *sub)
+    {
+        float vhi = t.zmax, vlo = lo;
+        uint64_t before = 0;
+        for (int it = 0; it < 64; ++it) {
+            const float scale = bin_scale(vhi, vlo);
+            clear_hist();
+            for (int s = warp; s < sl.ns; s += SR_WARPS) {
+                float z[E];
+                Vec<T>::get(sl.raw(s, lane), z);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if (z[e] >= vlo && z[e] <= vhi)
+                        atomicAdd(&sh->hist[bin_of(vhi, scale, z[e])], 1u);
+            }
+            cl_sync();
+            uint32_t n0, n1;
+            row_bins(n0, n1);
+            const uint64_t incl = before + block_incl(n0 + n1);
+            const uint64_t want = (uint64_t)k;
+            const int b = block_least(incl - n1 >= want ? 2 * tid : incl >= want ? 2 * tid + 1 : 0x7FFFFFFF);
+            if (b == 0x7FFFFFFF)
+                break;  // fewer than k
+            if (tid == (b >> 1)) {
+                sh->warp[0][1] = b & 1 ? incl - n1 : incl - n1 - n0;
+                sh->warp[0][2] = b & 1 ? n1 : n0;
+            }
+            __syncthreads();
+            before = sh->warp[0][1];
+            const uint64_t n = sh->warp[0][2];
+            auto in = [=](float z, int) { return z >= vlo && z <= vhi && bin_of(vhi, scale, z) == b; };
+            if (n <= SR_CAP) {
+                collect(in);
+                return cut_list(sc, (int)n, (int)(want - before), 1.f, 0, 0, 0, true).b;
+            }
+            const Members m = members(sc, [](float, int) { return false; }, in);
+            if (m.lo == m.hi) {
+                Border r = {m.lo, 0x7FFFFFFF};
+                if (want - before < n)
+                    r.last = nth_equal(r, m.lo, want - before, sub);
+                return r;
+            }
+            vlo = m.lo;
+            vhi = m.hi;
+        }
+        return Border{lo, 0x7FFFFFFF};
+    }
+
+    // ---- the border of the front part of what b keeps whose weights first reach `want`, by
+    // bounds of the bins' weights (tokens times the bin's ends)
+    DDT_DEVINL Cut mass_border(const Top &t, const Scale &sc, const Border &b, uint64_t want, uint64_t *sub)
+    {
+        float vhi = t.zmax, vlo = b.z;
+        uint64_t above = 0;
+        for (int it = 0; it < 64; ++it) {
+            const float scale = bin_scale(vhi, vlo);
+            clear_hist();
+            for (int s = warp; s < sl.ns; s += SR_WARPS) {
+                float z[E];
+                Vec<T>::get(sl.raw(s, lane), z);
+                const int i0 = sl.index0(s, lane);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if (z[e] >= vlo && z[e] <= vhi && kept(b, z[e], i0 + e))
+                        atomicAdd(&sh->hist[bin_of(vhi, scale, z[e])], 1u);
+            }
+            cl_sync();
+            uint32_t n[2];
+            row_bins(n[0], n[1]);
+            uint64_t up[2], low[2];
+            const float inv = scale > 0.f ? 1.f / scale : 0.f;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int bin = 2 * tid + x;
+                // (a hundredth of a bin and 2^-16 of the weight cover what fp32 rounds here)
+                const float hi = fminf(0.f, (vhi - sc.zmax) - (bin - 0.01f) * inv), lo = (vhi - sc.zmax) - (bin + 1.01f) * inv;
+                up[x] = __float2ull_ru((float)n[x] * fminf(1.f, ex2(hi * sc.ch) * 1.0000153f) * 17592186044416.0f);
+                low[x] = __float2ull_rd((float)n[x] * (ex2(lo * sc.ch) * 0.9999847f) * 17592186044416.0f);
+            }
+            const uint64_t iu = above + block_incl(up[0] + up[1]);
+            int first = block_least(iu - up[1] >= want ? 2 * tid : iu >= want ? 2 * tid + 1 : 0x7FFFFFFF);
+            const uint64_t il = above + block_incl(low[0] + low[1]);
+            int final_ = block_least(il - low[1] >= want ? 2 * tid : il >= want ? 2 * tid + 1 : 0x7FFFFFFF);
+            first = min(first, SR_BINS - 1);
+            final_ = min(final_, SR_BINS - 1);
+            auto front = [=](float z, int i) { return z >= vlo && z <= vhi && bin_of(vhi, scale, z) < first && kept(b, z, i); };
+            auto in = [=](float z, int i) {
+                if (!(z >= vlo && z <= vhi && kept(b, z, i)))
+                    return false;
+                const int x = bin_of(vhi, scale, z);
+                return x >= first && x <= final_;
+            };
+            const Members m = members(sc, front, in);
+            above += m.before;
+            if (m.n == 0)  // (rounding: nothing beyond the tokens before is needed)
+                return Cut{{m.hi, 0x7FFFFFFF}, above, false};
+            if (m.n <= SR_CAP) {
+                collect(in);
+                return cut_list(sc, (int)m.n, (int)m.n, 0.5f, 0, above, max(want, (uint64_t)1), true);
+            }
+            if (m.lo == m.hi) {
+                const uint64_t w = weight_of<EXACT>(sc, sh->tab, m.lo);
+                uint64_t c = want > above && w > 0 ? (want - above + w - 1) / w : 1;
+                c = min(c, (uint64_t)m.n);
+                Border r = {m.lo, m.lo == b.z ? b.last : 0x7FFFFFFF};
+                if (c < m.n)
+                    r.last = nth_equal(r, m.lo, c, sub);
+                return Cut{r, above + c * w, true};
+            }
+            vlo = m.lo;
+            vhi = m.hi;
+        }
+        return Cut{b, 0, false};
+    }
+
+    // ---- the border of everything that the settings keep. mass: the kept tokens' weights
+    // (0 if they have not been added up yet). k: 0 or at least V means off; p >= 1 off
+    DDT_DEVINL Cut border(const Top &t, const Scale &sc, int k, float p, float min_z, uint64_t *sub)
+    {
+        const float lo = fmaxf(min_z, sc.zfloor);
+        const Border all = {lo, 0x7FFFFFFF};
+        if (k <= 0 || k >= sl.V)
+            k = 0;
+        if (k == 0 && !(p < 1.f))
+            return Cut{all, 0, true};
+        if (k > 0 && k <= SR_PROBE) {
+            const float tau = probe(t, lo, k);
+            const uint32_t n = collect([=](float z, int) { return z >= tau; });
+            if (n <= SR_CAP)
+                return cut_list(sc, (int)n, k, p, 0, 0, 0, true);
+        }
+        const Border b = k > 0 ? count_border(t, sc, lo, k, sub) : all;
+        if (!(p < 1.f))
+            return Cut{b, 0, true};
+        const uint64_t base = mass(sc, b, nullptr, nullptr);
+        if (k == 0 || k > SR_PROBE) {
+            const float tau = probe(t, b.z, SR_PROBE);
+            const uint32_t n = collect([=](float z, int i) { return z >= tau && kept(b, z, i); });
+            if (n <= SR_CAP) {
+                const Cut c = cut_list(sc, (int)n, (int)n, p, base, 0, 0, tau <= b.z);
+                if (c.ok)
+                    return c;
+            }
+        }
+        return mass_border(t, sc, b, share_of(p, base), sub);
+    }
+
+    struct Weight {  // adds up the kept tokens' weights
+        Scale sc;
+        Border b;
+        const float2 *tab;
+        DDT_DEVINL uint64_t sum_to(const float *z, int i0, int last) const
+        {
+            Sum2 sum = {0, 0};
+#pragma unroll
+            for (int e = 0; e < E; e += 2)
+                add_weights<EXACT>(sc, tab, z[e], z[e + 1], e <= last && kept(b, z[e], i0 + e),
+                                   e + 1 <= last && kept(b, z[e + 1], i0 + e + 1), sum);
+            return to_fixed(sum);
+        }
+        DDT_DEVINL uint64_t lane_sum(const float *z, int i0) const { return sum_to(z, i0, E - 1); }
+    };
+};
+
+// floor(u mass), within the running sums: the draw's token is the first whose sum exceeds it
+DDT_DEVINL uint64_t draw_target(float u, uint64_t mass)
+{
+    return u < 1.f ? min(u > 0.f ? fraction_of(u, mass, false) : 0, mass - 1) : u == u ? mass - 1 : 0;
+}
+
+// the settings of a row. k = 1 and T = 1 stand for T = 0 (the largest logit, the lowest
+// index of it)
+struct Settings {
+    float T, p, m;
+    int k;
+    bool good;
+};
+DDT_DEVINL Settings load_settings(const ddt_filter &f, int i)
+{
+    Settings s;
+    s.T = f.temperature ? __ldg(f.temperature + i) : 1.f;
+    s.k = f.top_k ? __ldg(f.top_k + i) : 0;
+    s.p = f.top_p ? __ldg(f.top_p + i) : 1.f;
+    s.m = f.min_p ? __ldg(f.min_p + i) : 0.f;
+    s.good = s.T >= 0.f && s.T <= SR_MAX_FLOAT && s.p >= 0.f && s.p <= 1.f && s.m >= 0.f && s.m <= 1.f;
+    if (s.T == 0.f) {
+        s.T = 1.f;
+        s.k = 1;
+    }
+    s.T = fmaxf(s.T, SR_TINY);
+    return s;
+}
+// T ln m as a pair of floats (one thread: fp64)
+DDT_DEVINL float2 min_offset(const Settings &s)
+{
+    const double v = (double)s.T * log((double)s.m);
+    const float h = (float)v;
+    return make_float2(h, (float)(v - (double)h));
+}
+// the smallest float at or above zmax + T ln m: exp((z - zmax) / T) >= m from there on
+DDT_DEVINL float min_value(float zmax, float2 off)
+{
+    float s = zmax + off.x, bb = s - zmax;
+    float e = ((zmax - (s - bb)) + (off.x - bb)) + off.y;
+    const float s2 = s + e;
+    bb = s2 - s;
+    e = (s - (s2 - bb)) + (e - bb);
+    return e > 0.f ? nextafterf(s2, SR_MAX_FLOAT) : s2;
+}
+
+}  // namespace

@@ -18,12 +18,13 @@ LIB_PATH = os.path.join(_HERE, "_build", "libddt.so")
 OK, EINVAL, EUNSUPPORTED, ECUDA, ENOMEM = 0, 1, 2, 3, 4
 BF16, F32 = 0, 1
 DEV_NAN_LOGITS, DEV_BAD_PAGE, DEV_BAD_TREE, DEV_TIMEOUT, DEV_BAD_LENGTH = 0x1, 0x2, 0x4, 0x8, 0x10
+DEV_BAD_SETTING = 0x20
 
 EXPORTS = ("ddt_create", "ddt_destroy", "ddt_workspace_bytes", "ddt_topk_logprobs",
            "ddt_build_tree", "ddt_build_tree_conditioned", "ddt_build_mask", "ddt_tree_attention", "ddt_target_argmax",
            "ddt_walk", "ddt_compact", "ddt_accept", "ddt_round", "ddt_round_conditioned",
            "ddt_markov_table", "ddt_build_tree_markov", "ddt_round_markov",
-           "ddt_accept_stochastic", "ddt_schedule_prefix", "ddt_append_kv", "ddt_append_kvq",
+           "ddt_accept_stochastic", "ddt_sample", "ddt_accept_sampled", "ddt_schedule_prefix", "ddt_append_kv", "ddt_append_kvq",
            "ddt_prompt_attention", "ddt_prompt_attention_kvq", "ddt_device_status", "ddt_strerror",
            "ddt_last_cuda_error", "ddt_debug_arm_attention_timeout", "ddt_debug_arm_prompt_timeout")
 
@@ -73,6 +74,25 @@ class Kv4(ctypes.Structure):
                 ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
 
 
+class FilterArgs(ctypes.Structure):
+    _fields_ = [(n, _P) for n in ("temperature", "top_k", "top_p", "min_p")]
+
+
+class Filter:
+    """Sampling settings of n rows or requests (ddt_filter in include/ddt.h):
+    CUDA tensors [n], f32 (top_k i32), each may be None (off). temperature 0
+    is greedy; top_k 0, top_p 1 and min_p 0 are off."""
+
+    def __init__(self, temperature=None, top_k=None, top_p=None, min_p=None):
+        self.temperature, self.top_k, self.top_p, self.min_p = temperature, top_k, top_p, min_p
+
+    def check(self, n):
+        for name, types in (("temperature", _F32), ("top_k", _I32), ("top_p", _F32), ("min_p", _F32)):
+            t = getattr(self, name)
+            if t is not None:
+                _shaped(t, name, types, (n,))
+
+
 class Rotary:
     """The position rotation of an append: a [max_pos, dim] f32 CUDA table of
     dim / 2 cosines and dim / 2 sines per position (rotary_table makes one);
@@ -118,8 +138,12 @@ class Kv4Cache:
 # what the packed-sequence calls look at, as plain values (a ctypes field is slow to read)
 Dims = collections.namedtuple("Dims", "R_max Hq Hkv d page_size max_pages_per_req num_pages")
 
+# and the sampling calls
+Sizes = collections.namedtuple("Sizes", "R_max L V draft_dtype target_dtype")
+
 _BF16 = (torch.bfloat16, torch.int16, torch.uint16)
 _I32 = (torch.int32,)
+_F32 = (torch.float32,)
 _U8 = (torch.uint8,)
 
 
@@ -180,6 +204,40 @@ def check_prompt(cfg, q, q_start, ctx_lens, block_table, R, out):
     return qs
 
 
+def check_sample(cfg, logits, u, tokens, filter, logprobs):
+    """Types and shapes of a sampling call's tensors; the logits' dtype code."""
+    N = logits.shape[0]
+    f32 = logits.dtype == torch.float32
+    _shaped(logits, "logits", _F32 if f32 else _BF16, (N, cfg.V))
+    _shaped(u, "u", _F32, (N,))
+    _shaped(tokens, "tokens", _I32, (N,))
+    if logprobs is not None:
+        _shaped(logprobs, "logprobs", _F32, (N,))
+    if filter is not None:
+        filter.check(N)
+    return F32 if f32 else BF16
+
+
+def check_accept_sampled(cfg, draft_logits, target_logits, draft_tokens, u, r, R, acc_len, acc_tokens,
+                         draft_filter, target_filter, n_guess):
+    """Types and shapes of a sampled chain verification's tensors."""
+    if not 0 <= R <= cfg.R_max:
+        raise ValueError("R: expected 0..%d" % cfg.R_max)
+    L, V = cfg.L, cfg.V
+    kinds = {BF16: _BF16, F32: _F32}
+    _shaped(draft_logits, "draft_logits", kinds[cfg.draft_dtype], (R, L, V))
+    _shaped(target_logits, "target_logits", kinds[cfg.target_dtype], (R, L + 1, V))
+    for t, name, types, shape in ((draft_tokens, "draft_tokens", _I32, (R, L)), (u, "u", _F32, (R, L)),
+                                  (r, "r", _F32, (R,)), (acc_len, "acc_len", _I32, (R,)),
+                                  (acc_tokens, "acc_tokens", _I32, (R, L + 1))):
+        _shaped(t, name, types, shape)
+    if n_guess is not None:
+        _shaped(n_guess, "n_guess", _I32, (R,))
+    for f in (draft_filter, target_filter):
+        if f is not None:
+            f.check(R)
+
+
 def _cache_shapes(cfg, k_cache, v_cache):
     for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
         _shaped(t, n, _BF16, (cfg.num_pages, cfg.page_size, cfg.Hkv, cfg.d))
@@ -218,6 +276,9 @@ def load(path=LIB_PATH):
         "ddt_build_tree_markov": ([_P, _P, _P, i32, _P, _P, _P, _P, _P, _P], i32),
         "ddt_round_markov": ([_P, ctypes.POINTER(RoundArgs), _P, _P, _P, _P], i32),
         "ddt_accept_stochastic": ([_P, _P, _P, _P, _P, _P, i32, _P, _P, _P, _P], i32),
+        "ddt_sample": ([_P, _P, i32, i32, ctypes.POINTER(FilterArgs), _P, _P, _P, _P], i32),
+        "ddt_accept_sampled": ([_P, _P, _P, _P, _P, _P, i32, ctypes.POINTER(FilterArgs),
+                                ctypes.POINTER(FilterArgs), _P, _P, _P, _P], i32),
         "ddt_schedule_prefix": ([_P, _P, i32, _P, _P, _P, _P, _P], i32),
         "ddt_append_kv": ([_P, ctypes.POINTER(AppendArgs), _P, _P, _P], i32),
         "ddt_append_kvq": ([_P, ctypes.POINTER(AppendArgs), ctypes.POINTER(Kv4), _P, _P, _P], i32),
@@ -281,6 +342,7 @@ class Context:
         self.device = torch.cuda.current_device()
         self.dims = Dims(cfg.R_max, cfg.Hq, cfg.Hkv, cfg.d, cfg.page_size, cfg.max_pages_per_req,
                          cfg.num_pages)
+        self.sizes = Sizes(cfg.R_max, cfg.L, cfg.V, cfg.draft_dtype, cfg.target_dtype)
         self.K = cfg.K if cfg.K else min(cfg.B, cfg.V)
         self.P = cfg.B + 1
         self.W = (self.P + 31) // 32
@@ -359,6 +421,35 @@ class Context:
                                           _ptr(draft_tokens), _ptr(u), _ptr(r), R, _ptr(acc_len),
                                           _ptr(acc_tokens), _ptr(n_guess), _stream(stream)),
                "ddt_accept_stochastic")
+
+    def _filter(self, f):
+        at = self._at
+        return None if f is None else ctypes.byref(FilterArgs(at(f.temperature), at(f.top_k),
+                                                              at(f.top_p), at(f.min_p)))
+
+    def ddt_sample(self, logits, u, tokens, filter=None, logprobs=None, stream=None):
+        """A token of each row of logits [N, V] (bf16 or f32) under the rows'
+        `filter` (a Filter of [N] tensors, or None), drawn by u [N] f32 into
+        tokens [N] i32; logprobs [N] f32 (optional): the tokens' log-probabilities
+        among what the filter keeps."""
+        dtype = check_sample(self.sizes, logits, u, tokens, filter, logprobs)
+        at = self._at
+        _check(_lib.ddt_sample(self._h, at(logits), dtype, logits.shape[0], self._filter(filter), at(u),
+                               at(tokens), at(logprobs), self._own_stream(stream)), "ddt_sample")
+
+    def ddt_accept_sampled(self, draft_logits, target_logits, draft_tokens, u, r, R, acc_len,
+                           acc_tokens, draft_filter=None, target_filter=None, n_guess=None,
+                           stream=None):
+        """ddt_accept_stochastic where the drafter's guesses were drawn under
+        draft_filter and the target samples under target_filter (Filters of [R]
+        tensors, or None)."""
+        check_accept_sampled(self.sizes, draft_logits, target_logits, draft_tokens, u, r, R, acc_len,
+                             acc_tokens, draft_filter, target_filter, n_guess)
+        at = self._at
+        _check(_lib.ddt_accept_sampled(self._h, at(draft_logits), at(target_logits), at(draft_tokens),
+                                       at(u), at(r), R, self._filter(draft_filter),
+                                       self._filter(target_filter), at(acc_len), at(acc_tokens),
+                                       at(n_guess), self._own_stream(stream)), "ddt_accept_sampled")
 
     def ddt_schedule_prefix(self, conf, R, cost_ms, n_keep, n_total=None, stats=None,
                             stream=None):
