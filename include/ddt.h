@@ -36,6 +36,8 @@
  *   ddt_prompt_attention / ddt_prompt_attention_kvq
  *       causal attention of packed sequences over that cache: prompts, chunks
  *       of prompts, drafted chains, single tokens
+ *   ddt_prefix_attention / ddt_prefix_attention_kvq
+ *       the same where requests share prefixes: each is read once for all of them
  *   ddt_topk_logprobs_noalloc
  *       a1 without a context
  *
@@ -134,6 +136,9 @@ typedef struct ddt_config {
      * not used. C: tokens kept per depth by the prefilter, 1..128 and <= V;
      * needs markov_dim > 0 and bf16 draft logits. */
     int32_t prefilter;
+    /* ddt_prefix_attention, ddt_prefix_attention_kvq: the most packed tokens of a call (0: not
+     * used, at most 2^20); the workspace holds two fp32 rows of Hq * d for each */
+    int32_t prefix_tokens;
 } ddt_config;
 
 typedef struct ddt_ctx ddt_ctx; /* opaque */
@@ -475,7 +480,7 @@ ddt_status ddt_accept_sampled(ddt_ctx *ctx, const void *draft_logits, const void
 ddt_status ddt_schedule_prefix(ddt_ctx *ctx, const float *conf, int32_t R, const float *cost_ms,
                                int32_t *n_keep, int32_t *n_total, double *stats, void *stream);
 
-/* Packed sequences (the four calls below). T new tokens of R requests lie one
+/* Packed sequences (the calls below). T new tokens of R requests lie one
  * behind the other: request r's are rows q_start[r] .. q_start[r+1] - 1 of q,
  * k and v (q_start [R+1] i32 on the device, ascending, within [0, T]; a request
  * may have none). The i-th of them has position ctx_lens[r] + i, which is also
@@ -586,6 +591,35 @@ ddt_status ddt_prompt_attention(ddt_ctx *ctx, const uint16_t *q, int64_t q_strid
 ddt_status ddt_prompt_attention_kvq(ddt_ctx *ctx, const uint16_t *q, int64_t q_stride,
                                     const int32_t *q_start, const int32_t *ctx_lens, int32_t R,
                                     int32_t T, const ddt_kv4 *cache, const int32_t *block_table,
+                                    uint16_t *out, void *stream);
+
+/* ddt_prompt_attention where requests share prefixes: several continuations of one
+ * prompt, or prompts behind one system prompt. Requests group_start[g] ..
+ * group_start[g+1] - 1 form group g (group_start [G+1] i32 on the device, ascending,
+ * within [0, R]; requests of no group are their own). The first prefix_lens[g] slots of
+ * a group's requests (prefix_lens [G] i32 on the device) have to hold the same keys and
+ * values: block tables that name the same pages, or copies. Each group's keys are then
+ * read once, through its first request's table, for all its rows: whole tiles of 128
+ * slots of the prefix (what it has beyond them is read by each request). The result is
+ * ddt_prompt_attention's up to the order of its sums.
+ * A request with ctx_lens[r] < prefix_lens[g], or whose rows lie outside its group's
+ * (q_start[group_start[g]] .. q_start[group_start[g+1]]), is skipped like one with bad
+ * lengths; so are all requests of a group whose group_start or prefix_lens are out of
+ * range (below 0, above R, more than max_pages_per_req * page_size).
+ * T is at most the config's prefix_tokens (else DDT_EUNSUPPORTED), G at most R_max. All
+ * else as for ddt_prompt_attention: arguments, slots past a request's last token, the
+ * workspace and its rule on calls that overlap, waits that give up. */
+ddt_status ddt_prefix_attention(ddt_ctx *ctx, const uint16_t *q, int64_t q_stride,
+                                const int32_t *q_start, const int32_t *ctx_lens, int32_t R,
+                                int32_t T, const uint16_t *k_cache, const uint16_t *v_cache,
+                                const int32_t *block_table, const int32_t *group_start,
+                                const int32_t *prefix_lens, int32_t G, uint16_t *out, void *stream);
+
+/* The same over a cache held in 4 bits. */
+ddt_status ddt_prefix_attention_kvq(ddt_ctx *ctx, const uint16_t *q, int64_t q_stride,
+                                    const int32_t *q_start, const int32_t *ctx_lens, int32_t R,
+                                    int32_t T, const ddt_kv4 *cache, const int32_t *block_table,
+                                    const int32_t *group_start, const int32_t *prefix_lens, int32_t G,
                                     uint16_t *out, void *stream);
 
 /* Wait for the context's device to finish all enqueued work, copy the

@@ -22,6 +22,9 @@ ddt_status cuda_fail(cudaError_t e)
 
 inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
+// tokens that a call with shared prefixes may carry (beyond some thousands its keys are read by full tiles anyway)
+const int32_t MAX_PREFIX_TOKENS = 1 << 20;
+
 // resolve K and check every field; fills *out with the resolved config
 ddt_status check_config(const ddt_config *in, ddt_config *out)
 {
@@ -55,8 +58,10 @@ ddt_status check_config(const ddt_config *in, ddt_config *out)
     // the pool's token rows are TMA row coordinates (signed 32-bit) in a4
     if (c.num_pages > (int64_t)0x7FFFFFFF / c.page_size)
         return DDT_EUNSUPPORTED;
-    if (c.markov_dim < 0 || c.frontier < 0 || c.prefilter < 0)
+    if (c.markov_dim < 0 || c.frontier < 0 || c.prefilter < 0 || c.prefix_tokens < 0)
         return DDT_EINVAL;
+    if (c.prefix_tokens > MAX_PREFIX_TOKENS)
+        return DDT_EUNSUPPORTED;
     if ((c.frontier > 0 || c.prefilter > 0) && c.markov_dim == 0)
         return DDT_EINVAL;
     if (c.markov_dim > 0 && c.frontier == 0 && c.prefilter == 0)
@@ -74,7 +79,7 @@ ddt_status check_config(const ddt_config *in, ddt_config *out)
 struct Layout {
     size_t status, tk_gkey, tk_wtop, tk_ms, am_val, am_idx, att_part_o, att_part_ml, cg_part_ms, cg_part_top, cg_fr_tok, cg_fr_cand,
         cg_fr_n, cg_fr_S, cg_c_S, cg_c_meta, cg_thr, cg_seed_lp, cg_seed_ids, mk_cand, mk_tab,
-        sv_part_d, sv_part_t, sv_cnt, sv_part_w, sm_rows, ps_rk, ps_rid, ps_arrive, total;
+        sv_part_d, sv_part_t, sv_cnt, sv_part_w, sm_rows, px_o, px_ml, ps_rk, ps_rid, ps_arrive, total;
     int tk_nch, am_nch, max_items, sv_nch_d, sv_nch_t, sv_nch_w;
 };
 
@@ -138,6 +143,10 @@ Layout layout_for(const ddt_config &c)
     L.sv_part_w = take((size_t)c.R_max * L.sv_nch_w * sizeof(float));
     // sampled chain verification: 32 bytes a row
     L.sm_rows = take((size_t)c.R_max * (2 * c.L + 1) * sample_row_bytes());
+    // shared prefixes: O and (m, l) of prefix_tokens rows of Hq heads, twice
+    const size_t px_rows = (size_t)2 * c.prefix_tokens * c.Hq;
+    L.px_o = take(px_rows * c.d * sizeof(float));
+    L.px_ml = take(px_rows * sizeof(float2));
     // prefix scheduler: the ranking of up to DDT_SCHED_MAX_SLOTS slots
     L.ps_rk = take((size_t)DDT_SCHED_MAX_SLOTS * sizeof(uint64_t));
     L.ps_rid = take((size_t)DDT_SCHED_MAX_SLOTS * sizeof(int32_t));
@@ -446,6 +455,8 @@ ddt_status ddt_create(const ddt_config *cfg, ddt_ctx **out)
     ctx->sv_cnt = (unsigned *)(w + L.sv_cnt);
     ctx->sv_part_w = (float *)(w + L.sv_part_w);
     ctx->sm_rows = w + L.sm_rows;
+    ctx->px_store_o = (float *)(w + L.px_o);
+    ctx->px_store_ml = (float2 *)(w + L.px_ml);
     ctx->ps_rk = (uint64_t *)(w + L.ps_rk);
     ctx->ps_rid = (int32_t *)(w + L.ps_rid);
     ctx->ps_arrive = (unsigned *)(w + L.ps_arrive);
@@ -745,7 +756,7 @@ ddt_status ddt_sample(ddt_ctx *ctx, const void *logits, int32_t dtype, int32_t N
     DDT_CHECK(filter_bytes(f, N, r + 2));
     const PsBytes w[2] = {{tokens, n}, {logprobs, n}};
     DDT_CHECK(ps_apart(w, 2, r, 6));
-    DDT_ON_DEVICE(ctx);
+    DDT_ON_DEVICE(ctx)
     DDT_TRY(launch_sample(ctx, logits, dtype, N, f, u, tokens, logprobs, (cudaStream_t)stream));
     return DDT_OK;
 }
@@ -777,7 +788,7 @@ ddt_status ddt_accept_sampled(ddt_ctx *ctx, const void *draft_logits, const void
     DDT_CHECK(filter_bytes(fd, R, rd + 6) && filter_bytes(ft, R, rd + 10));
     const PsBytes w[2] = {{acc_len, n}, {acc_tokens, n * (L + 1)}};
     DDT_CHECK(ps_apart(w, 2, rd, 14));
-    DDT_ON_DEVICE(ctx);
+    DDT_ON_DEVICE(ctx)
     DDT_TRY(launch_accept_sampled(ctx, draft_logits, target_logits, fd, ft, draft_tokens, u, r, R,
                                   n_guess, acc_len, acc_tokens, (cudaStream_t)stream));
     return DDT_OK;
@@ -1068,6 +1079,61 @@ ddt_status ddt_prompt_attention_kvq(ddt_ctx *ctx, const uint16_t *q, int64_t q_s
     DDT_TRY(launch_prompt_attention(ctx, q, q_stride, q_start, ctx_lens, R, T, nullptr, nullptr,
                                     cache, block_table, out, (cudaStream_t)stream));
     return DDT_OK;
+}
+
+// what both caches' calls share; *pools: what the cache is made of
+static ddt_status prefix_attention(ddt_ctx *ctx, const uint16_t *q, int64_t q_stride,
+                                   const int32_t *q_start, const int32_t *ctx_lens, int32_t R,
+                                   int32_t T, const uint16_t *k_cache, const uint16_t *v_cache,
+                                   const ddt_kv4 *cache, const PsBytes *pools, int npools,
+                                   const int32_t *block_table, const int32_t *group_start,
+                                   const int32_t *prefix_lens, int32_t G, uint16_t *out, void *stream)
+{
+    DDT_CHECK(G >= 0 && G <= ctx->cfg.R_max);
+    DDT_CHECK(G == 0 || (group_start && prefix_lens && aligned4(group_start) && aligned4(prefix_lens)));
+    DDT_CHECK(prompt_apart(ctx, q, q_stride, q_start, ctx_lens, R, T, block_table, pools, npools, out));
+    const int64_t nq = (int64_t)ctx->cfg.Hq * ctx->cfg.d;
+    const PsBytes w = {out, span_bytes(T, nq, nq)};
+    const PsBytes groups[2] = {{group_start, G > 0 ? 4 * ((int64_t)G + 1) : 0}, {prefix_lens, 4 * (int64_t)G}};
+    DDT_CHECK(ps_apart(&w, 1, groups, 2));
+    if (T > ctx->cfg.prefix_tokens)
+        return DDT_EUNSUPPORTED;
+    DDT_ON_DEVICE(ctx)
+    DDT_TRY(launch_prefix_attention(ctx, q, q_stride, q_start, ctx_lens, R, T, k_cache, v_cache, cache,
+                                    block_table, group_start, prefix_lens, G, out, (cudaStream_t)stream));
+    return DDT_OK;
+}
+
+ddt_status ddt_prefix_attention(ddt_ctx *ctx, const uint16_t *q, int64_t q_stride,
+                                const int32_t *q_start, const int32_t *ctx_lens, int32_t R,
+                                int32_t T, const uint16_t *k_cache, const uint16_t *v_cache,
+                                const int32_t *block_table, const int32_t *group_start,
+                                const int32_t *prefix_lens, int32_t G, uint16_t *out, void *stream)
+{
+    const ddt_status st = chk_prompt(ctx, q, &q_stride, q_start, ctx_lens, R, T, block_table, out);
+    if (st != DDT_OK || R == 0 || T == 0)
+        return st;
+    DDT_CHECK(k_cache && v_cache && aligned16(k_cache) && aligned16(v_cache));
+    const PsBytes pools[2] = {{k_cache, pool_bytes(ctx)}, {v_cache, pool_bytes(ctx)}};
+    return prefix_attention(ctx, q, q_stride, q_start, ctx_lens, R, T, k_cache, v_cache, nullptr, pools,
+                            2, block_table, group_start, prefix_lens, G, out, stream);
+}
+
+ddt_status ddt_prefix_attention_kvq(ddt_ctx *ctx, const uint16_t *q, int64_t q_stride,
+                                    const int32_t *q_start, const int32_t *ctx_lens, int32_t R,
+                                    int32_t T, const ddt_kv4 *cache, const int32_t *block_table,
+                                    const int32_t *group_start, const int32_t *prefix_lens, int32_t G,
+                                    uint16_t *out, void *stream)
+{
+    ddt_status st = chk_prompt(ctx, q, &q_stride, q_start, ctx_lens, R, T, block_table, out);
+    if (st != DDT_OK || (st = chk_kv4(cache)) != DDT_OK || R == 0 || T == 0)
+        return st;
+    const PsBytes pools[4] = {{cache->k_codes, code_bytes(ctx)},
+                              {cache->v_codes, code_bytes(ctx)},
+                              {cache->k_scales, code_bytes(ctx) / 8},
+                              {cache->v_scales, code_bytes(ctx) / 8}};
+    return prefix_attention(ctx, q, q_stride, q_start, ctx_lens, R, T, nullptr, nullptr, cache, pools, 4,
+                            block_table, group_start, prefix_lens, G, out, stream);
 }
 
 ddt_status ddt_device_status(ddt_ctx *ctx, int32_t *host_out)

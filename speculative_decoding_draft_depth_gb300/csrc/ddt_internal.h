@@ -87,6 +87,9 @@ struct ddt_ctx {
     float *sv_part_w;        // [R_max, sv_nch_w] chunk totals of the draw's weights
     // sampled chain verification
     void *sm_rows;           // [R_max, 2 L + 1] what the settings keep of each row
+    // attention with shared prefixes (prefix_tokens > 0): parts by rows, of prefixes and of own keys
+    float *px_store_o;       // [2, d / 4, prefix_tokens * Hq, 4] (less rows when a call has fewer tokens)
+    float2 *px_store_ml;     // [2, prefix_tokens * Hq]
     // prefix scheduler (rank-counting grid)
     uint64_t *ps_rk;         // [DDT_SCHED_MAX_SLOTS] survival bits in ranking order
     int32_t *ps_rid;         // [DDT_SCHED_MAX_SLOTS] their tie ids
@@ -173,6 +176,13 @@ cudaError_t launch_prompt_attention(ddt_ctx *c, const uint16_t *q, int64_t q_str
                                     const int32_t *q_start, const int32_t *ctx_lens, int R, int T,
                                     const uint16_t *k_cache, const uint16_t *v_cache,
                                     const ddt_kv4 *kv4, const int32_t *block_table, uint16_t *out,
+                                    cudaStream_t s);
+
+// the same where requests share prefixes (prefix.cu)
+cudaError_t launch_prefix_attention(ddt_ctx *c, const uint16_t *q, int64_t q_stride, const int32_t *q_start,
+                                    const int32_t *ctx_lens, int R, int T, const uint16_t *k_cache,
+                                    const uint16_t *v_cache, const ddt_kv4 *kv4, const int32_t *block_table,
+                                    const int32_t *group_start, const int32_t *prefix_lens, int ngroups, uint16_t *out,
                                     cudaStream_t s);
 
 // a1 with caller-supplied scratch (used by the allocation-free entry point)

@@ -23,6 +23,13 @@ struct PtArgs {
     int R, T, Hq, Hkv, g_shift, page_shift, max_pages, cap;
     int64_t num_pages;
     float scale_log2, out_scale;
+    // shared prefixes (ddt_prefix_attention): groups of consecutive requests, and for rows
+    // (KV head, token, head of the KV head) what a whole item leaves of them: O in columns
+    // of four channels, the rows side by side, and (m, l); [0] of prefixes, [1] of own keys
+    const int32_t *group_start, *prefix_lens;
+    int ngroups;
+    float4 *store_o[2];
+    float2 *store_ml[2];
     long long debug_wait;  // > 0 (tests only): each CTA starts with a wait that runs out after this many cycles
 };
 
@@ -43,10 +50,14 @@ constexpr float PBIAS = 7.0f;
 
 // a segment of an item: ring words
 //   0: request (-1: end of the share)   1: head | split << 8 | whole << 9 | slot << 10
+//   (bit 28: of a shared prefix, 29: of a request that has one)
 //   2: first packed row  3: tokens  4: position of the first  5, 6: key tiles [t0, t1)
 struct Seg {
     int r, h, row0, ntok, pos0, t0, t1, slot;
     bool split, whole;
+    bool flat, part;  // a shared prefix: every row's last key is pos0; the item is one part of its rows' keys
+    DDT_DEVINL int end() const { return flat ? pos0 + 1 : pos0 + ntok; }
+    DDT_DEVINL int last_key(int tok) const { return flat ? pos0 : pos0 + min(tok, ntok - 1); }  // (rows without a token: the last one's)
     DDT_DEVINL int steps(int g) const  // key tiles of group g
     {
         const int n = t1 - t0;
@@ -55,13 +66,16 @@ struct Seg {
     DDT_DEVINL int tile(int g, int j) const { return t0 + (split ? 2 * j + g : j); }
 };
 
+template <bool GROUPS>
 DDT_DEVINL void seg_decode(const int *w, Seg &s)
 {
     s.r = w[0];
     s.h = w[1] & 0xFF;
     s.split = (w[1] >> 8) & 1;
     s.whole = (w[1] >> 9) & 1;
-    s.slot = w[1] >> 10;
+    s.slot = (w[1] >> 10) & 0x3FFFF;
+    s.flat = GROUPS && ((w[1] >> 28) & 1);
+    s.part = GROUPS && ((w[1] >> 29) & 1);
     s.row0 = w[2];
     s.ntok = w[3];
     s.pos0 = w[4];
@@ -73,13 +87,79 @@ DDT_DEVINL void seg_decode(const int *w, Seg &s)
 // an infinity would make a score of zero NaN.
 DDT_DEVINL float row_scale(const PtArgs &a, float power) { return fminf(a.scale_log2 * power, 3.402823466e38f); }
 
-DDT_DEVINL PpReq load_req(const PtArgs &a, int r)
+// the group that holds request r (-1: none)
+DDT_DEVINL int group_of(const PtArgs &a, int r)
 {
+    int lo = -1, hi = a.ngroups - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (__ldg(&a.group_start[mid]) <= r)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    return lo >= 0 && r < __ldg(&a.group_start[lo + 1]) ? lo : -1;
+}
+// whether group g is sound: its requests, its prefix
+DDT_DEVINL bool group_ok(const PtArgs &a, int g)
+{
+    const int g0 = __ldg(&a.group_start[g]), g1 = __ldg(&a.group_start[g + 1]), p = __ldg(&a.prefix_lens[g]);
+    return g0 >= 0 && g1 >= g0 && g1 <= a.R && p >= 0 && p <= a.cap;
+}
+// a group: its rows, and the tiles of its prefix that its members read together (flat; 0:
+// none). len 0: not sound.
+DDT_DEVINL PpReq load_group(const PtArgs &a, int g)
+{
+    PpReq q = {0, 0, 0, 0, 0};
+    if (!group_ok(a, g))
+        return q;
+    const int g0 = __ldg(&a.group_start[g]), g1 = __ldg(&a.group_start[g + 1]);
+    const int s0 = __ldg(&a.q_start[g0]), s1 = __ldg(&a.q_start[g1]);
+    if (s0 < 0 || s1 < s0 || s1 > a.T)
+        return q;
+    q.q0 = s0;
+    q.len = s1 - s0;
+    q.flat = g1 - g0 >= 2 ? __ldg(&a.prefix_lens[g]) / PP_TILE : 0;
+    q.ctx = q.flat * PP_TILE;
+    return q;
+}
+
+// unit of work `r`: a request; with GROUPS the groups' prefixes, then the requests
+template <bool GROUPS>
+DDT_DEVINL int num_reqs(const PtArgs &a) { return GROUPS ? a.ngroups + a.R : a.R; }
+
+// sound: whether its lengths are (a unit that is not has no tokens)
+template <bool GROUPS = false>
+DDT_DEVINL PpReq load_req(const PtArgs &a, int r, bool *sound = nullptr)
+{
+    PpReq q = {0, 0, 0, 0, 0};
+    int g0 = 0, g1 = a.T, least = 0;  // GROUPS: where a member's rows lie, and what is cached at least
+    if (GROUPS) {
+        if (r < a.ngroups) {
+            q = load_group(a, r);
+            if (sound)
+                *sound = group_ok(a, r);
+            if (q.flat == 0)
+                q.len = 0;
+            return q;
+        }
+        r -= a.ngroups;
+        const int g = group_of(a, r);
+        if (g >= 0) {
+            const PpReq pre = load_group(a, g);
+            least = group_ok(a, g) ? __ldg(&a.prefix_lens[g]) : 0x7FFFFFFF;
+            q.off = pre.flat;
+            if (pre.flat > 0)
+                g0 = pre.q0, g1 = pre.q0 + pre.len;
+        }
+    }
     const int s0 = __ldg(&a.q_start[r]), s1 = __ldg(&a.q_start[r + 1]), c = __ldg(&a.ctx_lens[r]);
-    PpReq q;
+    const bool ok = packed_ok(s0, s1, a.T, c, a.cap) && (!GROUPS || (c >= least && s0 >= g0 && s1 <= g1));
+    if (sound)
+        *sound = ok;
     q.q0 = s0;
     q.ctx = c;
-    q.len = packed_ok(s0, s1, a.T, c, a.cap) ? s1 - s0 : 0;
+    q.len = ok ? s1 - s0 : 0;
     return q;
 }
 
@@ -88,7 +168,7 @@ constexpr int NO_PAGE = -0x7fffffff - 1;
 DDT_DEVINL int group_page(const PtArgs &a, const Seg &s, int j, int u)
 {
     const int t16 = j * PP_TILE + 16 * u;  // never straddles a page (page % 16 == 0)
-    return t16 >= s.pos0 + s.ntok ? NO_PAGE
+    return t16 >= s.end() ? NO_PAGE
                                   : __ldg(&a.block_table[(int64_t)s.r * a.max_pages + (t16 >> a.page_shift)]);
 }
 // whether the group has rows to read; a page out of range is reported
@@ -103,14 +183,15 @@ DDT_DEVINL bool page_ok(const PtArgs &a, int pg)
 // this CTA's share: the totals by a scan over the requests (whole block), then
 // the request that holds the share's first unit. found: [0] request, [1..2] its
 // first unit, [3..4] total
+template <bool GROUPS = false>
 DDT_DEVINL void find_share(const PtArgs &a, int tq, int grid, int cta, long long *sums,
                            volatile long long *found, int tid, int nthreads)
 {
-    const int per = (a.R + nthreads - 1) / nthreads;
-    const int r0 = min(tid * per, a.R), r1 = min(r0 + per, a.R);
+    const int count = num_reqs<GROUPS>(a), per = (count + nthreads - 1) / nthreads;
+    const int r0 = min(tid * per, count), r1 = min(r0 + per, count);
     long long mine = 0;
     for (int r = r0; r < r1; ++r)
-        mine += pp_units(load_req(a, r), tq, a.Hkv);
+        mine += pp_units(load_req<GROUPS>(a, r), tq, a.Hkv);
     long long incl = mine;
     const int lane = tid & 31, warp = tid >> 5;
 #pragma unroll
@@ -139,7 +220,7 @@ DDT_DEVINL void find_share(const PtArgs &a, int tq, int grid, int cta, long long
         if (cta < nc && excl <= lo && lo < excl + mine) {
             long long acc = excl;
             for (int r = r0; r < r1; ++r) {
-                const long long u = pp_units(load_req(a, r), tq, a.Hkv);
+                const long long u = pp_units(load_req<GROUPS>(a, r), tq, a.Hkv);
                 if (lo < acc + u) {
                     found[0] = r;
                     found[1] = acc;
@@ -154,6 +235,7 @@ DDT_DEVINL void find_share(const PtArgs &a, int tq, int grid, int cta, long long
 
 // the segments of a CTA's share, one behind the other (every thread that walks holds
 // the same state)
+template <bool GROUPS = false>
 struct ShareWalk {
     int r;
     long long base, cur, hi;  // the request's first unit; the walk's place and end
@@ -172,7 +254,7 @@ struct ShareWalk {
             const int nc = pp_ctas(total, grid, MIN_UNITS);
             cur = pp_share(total, c, nc);
             hi = pp_share(total, c + 1, nc);
-            rq = load_req(a, r);
+            rq = load_req<GROUPS>(a, r);
             it = pp_find(rq, cur - base, tq, a.Hkv);
         }
     }
@@ -188,13 +270,15 @@ struct ShareWalk {
             s.h = it.h;
             s.row0 = rq.q0 + it.qt * tq;
             s.ntok = min(tq, rq.len - it.qt * tq);
-            s.pos0 = rq.ctx + it.qt * tq;
-            s.t0 = t0;
-            s.t1 = t1;
+            s.flat = GROUPS && rq.flat > 0;
+            s.part = GROUPS && (rq.flat > 0 || rq.off > 0);
+            s.pos0 = s.flat ? rq.ctx - 1 : rq.ctx + it.qt * tq;
+            s.t0 = t0 + (GROUPS ? rq.off : 0);
+            s.t1 = t1 + (GROUPS ? rq.off : 0);
             s.whole = t0 == 0 && t1 == it.n;
             s.split = (s.ntok << a.g_shift) <= split_rows;
             s.slot = 2 * cta + (t0 > 0 ? 0 : 1);
-            const int sr = r;
+            const int sr = !GROUPS ? r : r < a.ngroups ? __ldg(&a.group_start[r]) : r - a.ngroups;
             cur = min(hi, i1);
             if (cur < hi) {  // the item behind it
                 it.start += it.n + PP_ITEM;
@@ -205,11 +289,11 @@ struct ShareWalk {
                         it.start = 0;
                         it.qt = 0;
                         do {  // (units remain, so a request with tokens follows)
-                            if (++r >= a.R) {
+                            if (++r >= num_reqs<GROUPS>(a)) {
                                 cur = hi;  // (not so: lengths that changed under the call)
                                 break;
                             }
-                            rq = load_req(a, r);
+                            rq = load_req<GROUPS>(a, r);
                         } while (rq.len == 0);
                     }
                     it.n = pp_tiles(rq, it.qt, tq);

@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(FT, NR == 1 ? 2 : 1) prompt_few_kernel(const F
     find_share(a, tq, gridDim.x, blockIdx.x, s_sums, s_found, tid, FT);
     Copier<D> copier;
     copier.begin(a, lane);
-    ShareWalk walk;
+    ShareWalk<> walk;
     walk.begin(a, s_found, tq, gridDim.x, blockIdx.x);
     // this warp's blocks of a segment: the next one, their end, the page of the one FS
     // turns ahead; their copies begin while the segment before is merged

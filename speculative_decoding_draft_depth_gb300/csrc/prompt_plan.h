@@ -10,6 +10,10 @@
 // at about the same time). An item counts n + PP_ITEM units: its tiles, behind
 // PP_ITEM units for what it costs once. CTA c of nc takes units
 // [total c / nc, total (c + 1) / nc).
+//
+// Where requests share prefixes, a group's prefix is one more request ahead of the others:
+// the group's tokens against `flat` tiles, the same for every query tile; and its members'
+// items leave out their first `off` tiles.
 #pragma once
 
 #include <stdint.h>
@@ -22,13 +26,16 @@ constexpr int PP_ITEM = 3;     // units of an item besides its tiles
 
 struct PpReq {   // one request, and where its units begin
     int q0, len, ctx;  // first packed row, tokens (0: none, or skipped), cached tokens
+    int off, flat;     // key tiles left out; tiles of a shared prefix (0: not one)
 };
 
 PS_FN int pp_tiles(const PpReq &q, int qt, int tq)
 {
+    if (q.flat)
+        return q.flat;
     const int64_t last = (int64_t)(qt + 1) * tq;
     const int end = q.ctx + (last < q.len ? (int)last : q.len);
-    return (end + PP_TILE - 1) / PP_TILE;
+    return (end + PP_TILE - 1) / PP_TILE - q.off;
 }
 
 PS_FN int pp_qtiles(const PpReq &q, int tq) { return (q.len + tq - 1) / tq; }
@@ -43,13 +50,16 @@ PS_FN int64_t pp_floor_sum(int64_t x, int w)
 // tiles of query tiles 0 .. m - 1, all of them full (m TQ <= len)
 PS_FN int64_t pp_tiles_before(const PpReq &q, int m, int tq)
 {
+    if (q.flat)
+        return (int64_t)m * q.flat;
+    const int64_t out = (int64_t)m * q.off;
     if (tq >= PP_TILE) {
         const int64_t c = (q.ctx + PP_TILE - 1) / PP_TILE, k = tq / PP_TILE;
-        return m * c + k * ((int64_t)m * (m + 1) / 2);
+        return m * c + k * ((int64_t)m * (m + 1) / 2) - out;
     }
     const int w = PP_TILE / tq;
     const int64_t b = (q.ctx + PP_TILE - 1) / tq;
-    return pp_floor_sum(b + m, w) - pp_floor_sum(b, w);
+    return pp_floor_sum(b + m, w) - pp_floor_sum(b, w) - out;
 }
 
 // units of one head's items of query tiles 0 .. m - 1 (m <= pp_qtiles)

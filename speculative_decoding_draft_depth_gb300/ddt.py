@@ -25,7 +25,8 @@ EXPORTS = ("ddt_create", "ddt_destroy", "ddt_workspace_bytes", "ddt_topk_logprob
            "ddt_walk", "ddt_compact", "ddt_accept", "ddt_round", "ddt_round_conditioned",
            "ddt_markov_table", "ddt_build_tree_markov", "ddt_round_markov",
            "ddt_accept_stochastic", "ddt_sample", "ddt_accept_sampled", "ddt_schedule_prefix", "ddt_append_kv", "ddt_append_kvq",
-           "ddt_prompt_attention", "ddt_prompt_attention_kvq", "ddt_device_status", "ddt_strerror",
+           "ddt_prompt_attention", "ddt_prompt_attention_kvq", "ddt_prefix_attention",
+           "ddt_prefix_attention_kvq", "ddt_device_status", "ddt_strerror",
            "ddt_last_cuda_error", "ddt_debug_arm_attention_timeout", "ddt_debug_arm_prompt_timeout")
 
 
@@ -46,7 +47,7 @@ class Config(ctypes.Structure):
                 ("max_pages_per_req", ctypes.c_int32), ("num_pages", ctypes.c_int64),
                 ("draft_dtype", ctypes.c_int32), ("target_dtype", ctypes.c_int32),
                 ("markov_dim", ctypes.c_int32), ("frontier", ctypes.c_int32),
-                ("prefilter", ctypes.c_int32)]
+                ("prefilter", ctypes.c_int32), ("prefix_tokens", ctypes.c_int32)]
 
 
 _P = ctypes.c_void_p
@@ -204,6 +205,16 @@ def check_prompt(cfg, q, q_start, ctx_lens, block_table, R, out):
     return qs
 
 
+def check_groups(cfg, group_start, prefix_lens):
+    """Types and shapes of shared prefixes; the number of groups."""
+    G = prefix_lens.shape[0]
+    if G > cfg.R_max:
+        raise ValueError("prefix_lens: expected at most %d groups" % cfg.R_max)
+    _shaped(prefix_lens, "prefix_lens", _I32, (G,))
+    _shaped(group_start, "group_start", _I32, (G + 1,))
+    return G
+
+
 def check_sample(cfg, logits, u, tokens, filter, logprobs):
     """Types and shapes of a sampling call's tensors; the logits' dtype code."""
     N = logits.shape[0]
@@ -285,6 +296,9 @@ def load(path=LIB_PATH):
         "ddt_prompt_attention": ([_P, _P, i64, _P, _P, i32, i32, _P, _P, _P, _P, _P], i32),
         "ddt_prompt_attention_kvq": ([_P, _P, i64, _P, _P, i32, i32, ctypes.POINTER(Kv4), _P, _P,
                                       _P], i32),
+        "ddt_prefix_attention": ([_P, _P, i64, _P, _P, i32, i32, _P, _P, _P, _P, _P, i32, _P, _P], i32),
+        "ddt_prefix_attention_kvq": ([_P, _P, i64, _P, _P, i32, i32, ctypes.POINTER(Kv4), _P, _P, _P,
+                                      i32, _P, _P], i32),
         "ddt_device_status": ([_P, ctypes.POINTER(i32)], i32),
         "ddt_debug_arm_attention_timeout": ([_P, i64], i32),
         "ddt_debug_arm_prompt_timeout": ([_P, i64], i32),
@@ -321,9 +335,10 @@ def _check(status, where):
 
 
 def make_config(R_max, L, V, B, Hq, Hkv, d, page_size, max_pages_per_req, num_pages, K=0,
-                draft_dtype=BF16, target_dtype=BF16, markov_dim=0, frontier=0, prefilter=0):
+                draft_dtype=BF16, target_dtype=BF16, markov_dim=0, frontier=0, prefilter=0,
+                prefix_tokens=0):
     return Config(R_max, L, V, B, K, Hq, Hkv, d, page_size, max_pages_per_req, num_pages,
-                  draft_dtype, target_dtype, markov_dim, frontier, prefilter)
+                  draft_dtype, target_dtype, markov_dim, frontier, prefilter, prefix_tokens)
 
 
 def workspace_bytes(cfg):
@@ -541,6 +556,33 @@ class Context:
         _check(_lib.ddt_prompt_attention_kvq(self._h, at(q, False), qs, at(q_start), at(ctx_lens), R,
                                              q.shape[0], ctypes.byref(c), at(block_table), at(out),
                                              self._own_stream(stream)), "ddt_prompt_attention_kvq")
+
+    def ddt_prefix_attention(self, q, q_start, ctx_lens, block_table, R, group_start, prefix_lens,
+                             k_cache, v_cache, out, stream=None):
+        """ddt_prompt_attention where requests share prefixes: requests
+        group_start[g] .. group_start[g + 1] - 1 (i32 [G + 1]) hold the same keys
+        and values in their first prefix_lens[g] slots (i32 [G]), which are read
+        once for the group. q has at most the config's prefix_tokens rows."""
+        qs = check_prompt(self.dims, q, q_start, ctx_lens, block_table, R, out)
+        G = check_groups(self.dims, group_start, prefix_lens)
+        _cache_shapes(self.dims, k_cache, v_cache)
+        at = self._at
+        _check(_lib.ddt_prefix_attention(self._h, at(q, False), qs, at(q_start), at(ctx_lens), R, q.shape[0],
+                                         at(k_cache), at(v_cache), at(block_table), at(group_start),
+                                         at(prefix_lens), G, at(out), self._own_stream(stream)),
+               "ddt_prefix_attention")
+
+    def ddt_prefix_attention_kvq(self, q, q_start, ctx_lens, block_table, R, group_start, prefix_lens,
+                                 cache, out, stream=None):
+        """The same over a Kv4Cache."""
+        qs = check_prompt(self.dims, q, q_start, ctx_lens, block_table, R, out)
+        G = check_groups(self.dims, group_start, prefix_lens)
+        c = self._kv4(cache)
+        at = self._at
+        _check(_lib.ddt_prefix_attention_kvq(self._h, at(q, False), qs, at(q_start), at(ctx_lens), R,
+                                             q.shape[0], ctypes.byref(c), at(block_table), at(group_start),
+                                             at(prefix_lens), G, at(out), self._own_stream(stream)),
+               "ddt_prefix_attention_kvq")
 
     def alloc_kv4(self, k_scale=1.0, v_scale=1.0, device="cuda"):
         """An empty (all zero) Kv4Cache of this context's page pool."""
