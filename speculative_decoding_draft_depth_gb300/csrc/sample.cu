@@ -18,6 +18,7 @@
 #include <algorithm>
 
 #include "device_flags.h"
+#include "sample_bins.cuh"
 #include "sample_row.cuh"
 
 namespace {
@@ -37,11 +38,11 @@ extern __shared__ __align__(16) unsigned char sr_smem[];
 
 // the row's top value and scale, and the border under the row's settings (a row in place
 // in shared memory). false: no token has a weight
-template <typename T>
-DDT_DEVINL bool row_border(Row<T> &row, const Settings &set, uint64_t *sub, int32_t *status, Scale &sc,
-                           typename Row<T>::Cut &cut, bool &infinite)
+template <typename T, bool SMEM>
+DDT_DEVINL bool row_border(Row<T, SMEM> &row, const Settings &set, uint64_t *sub, int32_t *status, Scale &sc,
+                           typename Row<T, SMEM>::Cut &cut, bool &infinite)
 {
-    typename Row<T>::Top t = row.top();
+    typename Row<T, SMEM>::Top t = row.top();
     if (t.nan && row.rank == 0 && row.tid == 0)
         set_status(status, DDT_DEV_NAN_LOGITS);
     if (t.zmax == DDT_NEG_INF)
@@ -56,49 +57,106 @@ DDT_DEVINL bool row_border(Row<T> &row, const Settings &set, uint64_t *sub, int3
 }
 
 template <typename T>
-__global__ void __launch_bounds__(SR_THREADS) sample_kernel(const SampleArgs<T> a)
+DDT_DEVINL void store_token(const SampleArgs<T> &a, int64_t n, int token, float logprob)
 {
-    __shared__ RowShared sh;
-    Row<T> row;
-    row.begin(&sh);
-    const int64_t n = blockIdx.x / row.cl;
-    const Settings set = load_settings(a.f, (int)n);
-    if (!set.good) {
-        if (row.rank == 0 && row.tid == 0) {
-            a.tokens[n] = -1;
-            if (a.logprobs)
-                a.logprobs[n] = DDT_NEG_INF;
-            set_status(a.status, DDT_DEV_BAD_SETTING);
-        }
-        return;
-    }
-    uint64_t *sub = reinterpret_cast<uint64_t *>(sr_smem + a.subs * SR_SUB);
-    row.load(sr_smem, a.logits + n * a.V, a.V);
-    if (row.tid == 0 && set.m > 0.f)
-        sh.off = min_offset(set);
-    row.loaded();
+    a.tokens[n] = token;
+    if (a.logprobs)
+        a.logprobs[n] = logprob;
+}
+// log of a token's weight over all that is kept (the largest weight is 2^44, so the sum is
+// at least that)
+DDT_DEVINL float log_share(float z, const Scale &sc, float T, uint64_t mass)
+{
+    return (z - sc.zmax) / T - log1pf((float)(mass - (1ull << SR_ONE)) * 5.684341886e-14f);
+}
+
+// a row from its border on: the kept weights' sums, and the draw
+template <typename T, bool SMEM>
+DDT_DEVINL void draw_row(Row<T, SMEM> &row, const SampleArgs<T> &a, int64_t n, const Settings &set, uint64_t *sub)
+{
     Scale sc;
-    typename Row<T>::Cut cut;
+    typename Row<T, SMEM>::Cut cut;
     bool infinite;
     if (!row_border(row, set, sub, a.status, sc, cut, infinite)) {
-        if (row.rank == 0 && row.tid == 0) {
-            a.tokens[n] = -1;
-            if (a.logprobs)
-                a.logprobs[n] = DDT_NEG_INF;
-        }
+        if (row.rank == 0 && row.tid == 0)
+            store_token(a, n, -1, DDT_NEG_INF);
         return;
     }
     const uint64_t(*all)[4];
     const uint64_t mass = row.mass(sc, cut.b, sub, &all);
-    const typename Row<T>::Weight w = {sc, cut.b, sh.tab};
+    const typename Row<T, SMEM>::Weight w = {sc, cut.b, row.sh->tab};
     const int i = row.locate(sub, all, draw_target(__ldg(a.u + n), mass), w);
-    if (i >= 0) {
-        a.tokens[n] = i;
-        if (a.logprobs) {
-            // (the largest weight is 2^44, so the sum is at least that)
-            a.logprobs[n] = (row.value(i) - sc.zmax) / set.T - log1pf((float)(mass - (1ull << SR_ONE)) * 5.684341886e-14f);
+    if (i >= 0)
+        store_token(a, n, i, log_share(row.value(i), sc, set.T, mass));
+}
+
+template <typename T>
+__global__ void __launch_bounds__(SR_THREADS) sample_kernel(const SampleArgs<T> a)
+{
+    __shared__ RowShared sh;
+    const int64_t n = blockIdx.x / cl_size();
+    const Settings set = load_settings(a.f, (int)n);
+    if (!set.good) {
+        if (cl_rank() == 0 && threadIdx.x == 0) {
+            store_token(a, n, -1, DDT_NEG_INF);
+            set_status(a.status, DDT_DEV_BAD_SETTING);
         }
+        return;
     }
+    Row<T, true> row;
+    row.begin(&sh);
+    row.load(sr_smem, a.logits + n * a.V, a.V);
+    if (row.tid == 0 && set.m > 0.f)
+        sh.off = min_offset(set);
+    row.loaded();
+    draw_row(row, a, n, set, reinterpret_cast<uint64_t *>(sr_smem + a.subs * SR_SUB));
+}
+
+// (rows that are not counted: apart, for the registers of those that are)
+__device__ __noinline__ void draw_general(Row<uint16_t, false> row, const SampleArgs<uint16_t> &a, int64_t n,
+                                          const Settings &set)
+{
+    draw_row(row, a, n, set, reinterpret_cast<uint64_t *>(sr_smem));
+}
+
+// the same by counts (bf16)
+template <int CL>
+__global__ void __launch_bounds__(SR_THREADS, 5) sample_bins_kernel(const SampleArgs<uint16_t> a)
+{
+    __shared__ RowShared sh;
+    __shared__ BinShared<CL> bs;
+    const int64_t n = blockIdx.x / cl_size();
+    const Settings set = load_settings(a.f, (int)n);
+    if (!set.good) {
+        if (cl_rank() == 0 && threadIdx.x == 0) {
+            store_token(a, n, -1, DDT_NEG_INF);
+            set_status(a.status, DDT_DEV_BAD_SETTING);
+        }
+        return;
+    }
+    Row<uint16_t, false> row;
+    row.begin(&sh);
+    const uint16_t *z = a.logits + n * a.V;
+    row.load(nullptr, z, a.V);
+    if (row.tid == 0 && set.m > 0.f)
+        sh.off = min_offset(set);
+    BinRow<CL> bins(row, &bs, sr_smem, z, a.V);
+    Scale sc;
+    typename BinRow<CL>::Kept k;
+    const int way = bins.run(set, sc, k, a.status);
+    if (way == BinRow<CL>::GENERAL) {
+        draw_general(row, a, n, set);
+        return;
+    }
+    if (way == BinRow<CL>::NONE) {
+        if (row.rank == 0 && row.tid == 0)
+            store_token(a, n, -1, DDT_NEG_INF);
+        return;
+    }
+    Border b;
+    const int i = bins.draw(sc, k, __ldg(a.u + n), b);
+    if (i >= 0)
+        store_token(a, n, i, log_share(held_value(logit_value(z, i), false), sc, set.T, k.mass));
 }
 
 // what keep_kernel leaves of a row
@@ -125,54 +183,121 @@ DDT_DEVINL int guess_count(const int32_t *n_guess, int i, int L)
     return n_guess ? max(0, min(L, __ldg(n_guess + i))) : L;
 }
 
+// which row a cluster has; false: one that is not verified
+template <typename T>
+struct KeepRow {
+    const T *z;
+    KeptRow *to;
+    Settings set;
+    int x;  // the guess, -1: none
+
+    DDT_DEVINL bool find(const KeepArgs<T> &a, int64_t n)
+    {
+        const int L = a.L, per = (a.draft ? L : 0) + (a.target ? L + 1 : 0);
+        const int i = (int)(n / per), j = (int)(n % per);
+        const bool isd = a.draft && j < L;
+        const int k = isd || !a.draft ? j : j - L;
+        const int guesses = guess_count(a.n_guess, i, L);
+        if (isd ? k >= guesses : k > guesses)
+            return false;
+        to = a.rows + (int64_t)i * (2 * L + 1) + (isd ? k : L + k);
+        z = isd ? a.draft + ((int64_t)i * L + k) * a.V : a.target + ((int64_t)i * (L + 1) + k) * a.V;
+        set = load_settings(isd ? a.fd : a.ft, i);
+        x = k < guesses ? __ldg(a.tokens + (int64_t)i * L + k) : -1;
+        if (x >= a.V)
+            x = -1;
+        if (!set.good && cl_rank() == 0 && threadIdx.x == 0)
+            *to = KeptRow{0.f, {0.f, 0}, KR_BAD, 0, 0};
+        return set.good;
+    }
+};
+
+// what is kept of a row, by its border
+template <typename T, bool SMEM>
+DDT_DEVINL void keep_row(Row<T, SMEM> &row, const KeepRow<T> &kr, int32_t *status, uint64_t *sub)
+{
+    KeptRow r = {0.f, {0.f, 0}, 0, 0, 0};
+    Scale sc;
+    typename Row<T, SMEM>::Cut cut;
+    bool infinite;
+    if (row_border(row, kr.set, sub, status, sc, cut, infinite)) {
+        r.zmax = sc.zmax;
+        r.b = cut.b;
+        r.flags = infinite ? KR_INF : 0;
+        r.mass = cut.mass ? cut.mass : row.mass(sc, cut.b, nullptr, nullptr);
+        if (row.rank == 0 && row.tid == 0 && kr.x >= 0) {
+            const float v = held_value(logit_value(kr.z, kr.x), infinite);
+            if (kept(r.b, v, kr.x))
+                r.guess = weight_of<Row<T, SMEM>::EXACT>(sc, row.sh->tab, v);
+        }
+    }
+    if (row.rank == 0 && row.tid == 0)
+        *kr.to = r;
+}
+
 template <typename T>
 __global__ void __launch_bounds__(SR_THREADS) keep_kernel(const KeepArgs<T> a)
 {
     __shared__ RowShared sh;
-    Row<T> row;
-    row.begin(&sh);
     pdl_trigger();
-    const int L = a.L, per = (a.draft ? L : 0) + (a.target ? L + 1 : 0);
-    const int64_t n = blockIdx.x / row.cl;
-    const int i = (int)(n / per), j = (int)(n % per);
-    const bool isd = a.draft && j < L;
-    const int k = isd || !a.draft ? j : j - L;
-    const int guesses = guess_count(a.n_guess, i, L);
-    if (isd ? k >= guesses : k > guesses) {
-        pdl_wait();
-        return;
-    }
-    KeptRow *to = a.rows + (int64_t)i * (2 * L + 1) + (isd ? k : L + k);
-    const T *z = isd ? a.draft + ((int64_t)i * L + k) * a.V : a.target + ((int64_t)i * (L + 1) + k) * a.V;
-    const Settings set = load_settings(isd ? a.fd : a.ft, i);
-    KeptRow r = {0.f, {0.f, 0}, 0, 0, 0};
-    if (!set.good) {
-        r.flags = KR_BAD;
-    } else {
-        uint64_t *sub = reinterpret_cast<uint64_t *>(sr_smem + a.subs * SR_SUB);
-        row.load(sr_smem, z, a.V);
-        if (row.tid == 0 && set.m > 0.f)
-            sh.off = min_offset(set);
+    KeepRow<T> kr;
+    if (kr.find(a, blockIdx.x / cl_size())) {
+        Row<T, true> row;
+        row.begin(&sh);
+        row.load(sr_smem, kr.z, a.V);
+        if (row.tid == 0 && kr.set.m > 0.f)
+            sh.off = min_offset(kr.set);
         row.loaded();
+        keep_row(row, kr, a.status, reinterpret_cast<uint64_t *>(sr_smem + a.subs * SR_SUB));
+    }
+    pdl_wait();  // (rows of the other type may be done by the launch before; what follows waits for both)
+}
+
+__device__ __noinline__ void keep_general(Row<uint16_t, false> row, const KeepRow<uint16_t> &kr, int32_t *status)
+{
+    keep_row(row, kr, status, reinterpret_cast<uint64_t *>(sr_smem));
+}
+
+// the same by counts (bf16)
+template <int CL>
+__global__ void __launch_bounds__(SR_THREADS, 5) keep_bins_kernel(const KeepArgs<uint16_t> a)
+{
+    __shared__ RowShared sh;
+    __shared__ BinShared<CL> bs;
+    pdl_trigger();
+    KeepRow<uint16_t> kr;
+    if (kr.find(a, blockIdx.x / cl_size())) {
+        Row<uint16_t, false> row;
+        row.begin(&sh);
+        row.load(nullptr, kr.z, a.V);
+        if (row.tid == 0 && kr.set.m > 0.f)
+            sh.off = min_offset(kr.set);
+        BinRow<CL> bins(row, &bs, sr_smem, kr.z, a.V);
         Scale sc;
-        typename Row<T>::Cut cut;
-        bool infinite;
-        if (row_border(row, set, sub, a.status, sc, cut, infinite)) {
-            r.zmax = sc.zmax;
-            r.b = cut.b;
-            r.flags = infinite ? KR_INF : 0;
-            r.mass = cut.mass ? cut.mass : row.mass(sc, cut.b, nullptr, nullptr);
-            const int x = k < L ? __ldg(a.tokens + (int64_t)i * L + k) : -1;
-            if (row.rank == 0 && row.tid == 0 && x >= 0 && x < a.V) {
-                const float v = held_value(logit_value(z, x), infinite);
-                if (kept(r.b, v, x))
-                    r.guess = weight_of<Row<T>::EXACT>(sc, sh.tab, v);
+        typename BinRow<CL>::Kept k;
+        const int way = bins.run(kr.set, sc, k, a.status);
+        if (way == BinRow<CL>::GENERAL) {
+            keep_general(row, kr, a.status);
+        } else if (way == BinRow<CL>::NONE) {
+            if (row.rank == 0 && row.tid == 0)
+                *kr.to = KeptRow{0.f, {0.f, 0}, 0, 0, 0};
+        } else {
+            // the thread that knows the border writes: the last kept index's, or the first
+            const bool cut = k.d != SB_VALUES && k.count != k.of;
+            const int last = bins.last_kept(k);
+            if (cut ? last >= 0 : row.rank == 0 && row.tid == 0) {
+                KeptRow r = {sc.zmax, {k.d == SB_VALUES ? bins.least : sb_value(k.d), cut ? last : 0x7FFFFFFF}, 0, k.mass, 0};
+                if (kr.x >= 0) {
+                    const float v = held_value(logit_value(kr.z, kr.x), false);
+                    if (kept(r.b, v, kr.x))
+                        r.guess = weight_of<false>(sc, sh.tab, v);
+                }
+                *kr.to = r;
             }
+            cl_sync();  // (the counts have been read by other CTAs)
         }
     }
-    if (row.rank == 0 && row.tid == 0)
-        *to = r;
-    pdl_wait();  // (rows of the other type may be done by the launch before; what follows waits for both)
+    pdl_wait();
 }
 
 template <typename TD, typename TT>
@@ -224,20 +349,6 @@ DDT_DEVINL Ratio make_ratio(uint64_t num, uint64_t den)
     r.m = q;
     r.e += big ? 1 : 0;
     return r;
-}
-
-// two weights in fixed point
-template <bool EXACT>
-DDT_DEVINL void fixed_pair(const Scale &sc, const float2 *tab, float x0, float x1, bool k0, bool k1, uint64_t &w0,
-                           uint64_t &w1)
-{
-    Sum2 s = {0, 0};
-    add_weights<EXACT>(sc, tab, x0, x1, k0, k1, s);
-    float h0, h1, l0, l1;
-    f2unpack(s.hi, h0, h1);
-    f2unpack(s.lo, l0, l1);
-    w0 = to_fixed(h0, l0);
-    w1 = to_fixed(h1, l1);
 }
 
 // weights of the draw: p's, less p's share of q's where there is a q
@@ -316,7 +427,7 @@ __global__ void __launch_bounds__(SR_THREADS) chain_kernel(const ChainArgs<TD, T
     __shared__ RowShared sh;
     __shared__ Ratio s_ratio;
     __shared__ int s_first, s_bad;
-    Row<TT> row;
+    Row<TT, true> row;
     row.begin(&sh);
     const int L = a.L, V = a.V, i = blockIdx.x / row.cl, lane = row.lane;
     const int n = guess_count(a.n_guess, i, L);
@@ -371,6 +482,7 @@ __global__ void __launch_bounds__(SR_THREADS) chain_kernel(const ChainArgs<TD, T
     Leftover<TD, TT> f;
     f.two = first < n && rows[first].mass > 0;
     if (s_bad || kp.mass == 0) {
+        row.started();
         if (writer && row.tid == 0)
             *to = -1;
         return;
@@ -405,7 +517,7 @@ __global__ void __launch_bounds__(SR_THREADS) chain_kernel(const ChainArgs<TD, T
 }
 
 // ------------------------------------------------------------------ host side
-constexpr int SR_SMEM_MAX = 227 * 1024 - (int)sizeof(RowShared) - 256;
+constexpr int SR_SMEM_MAX = 227 * 1024 - (int)sizeof(RowShared) - (int)sizeof(BinShared<SR_MAX_CL>) - 256;
 
 // Bytes of shared memory of a CTA that holds a slice of a row of V: the slice, its sub-
 // chunks' sums, and (bytes_q > 0) as many elements of another row of that element size.
@@ -430,6 +542,18 @@ int pick_cluster(int V, int64_t rows, int num_sms, int bytes_q)
         cl *= 2;
     return cl;
 }
+
+// Rows of bf16 logits are counted by their values from this many on: 
+constexpr int SB_LEAST = 8192;
+// CTAs of such a row's cluster: a slice's counts are 16 bits
+int bins_cluster(int V)
+{
+    int cl = 8;
+    while (cl < SR_MAX_CL && (V + 14) / 8 / cl * 8 + 8 > 65535)
+        cl *= 2;
+    return (V + 14) / 8 / cl * 8 + 8 > 65535 ? 0 : cl;
+}
+int bins_bytes(int V, int cl) { return std::max(sb_bytes(cl), slice_subs<uint16_t>(V, cl) * 8); }
 
 template <typename Args>
 cudaError_t launch_rows(void (*kernel)(Args), DeviceFlags &ready, int dev, int64_t rows, int cl, int smem, bool dependent,
@@ -466,7 +590,17 @@ cudaError_t sample_rows(const ddt_ctx *c, const void *logits, int N, const ddt_f
                         float *logprobs, cudaStream_t s)
 {
     static DeviceFlags ready;
-    const int V = c->cfg.V, cl = pick_cluster<T>(V, N, c->num_sms, 0);
+    const int V = c->cfg.V;
+    if constexpr (sizeof(T) == 2) {
+        static DeviceFlags ready_bins[2];
+        const int cl = V >= SB_LEAST ? bins_cluster(V) : 0;
+        if (cl > 0) {
+            const SampleArgs<T> a = {(const T *)logits, f, u, tokens, logprobs, c->status, V, 0};
+            return launch_rows(cl == 8 ? sample_bins_kernel<8> : sample_bins_kernel<16>, ready_bins[cl == 8], c->device, N,
+                               cl, bins_bytes(V, cl), false, a, s);
+        }
+    }
+    const int cl = pick_cluster<T>(V, N, c->num_sms, 0);
     const SampleArgs<T> a = {(const T *)logits, f, u, tokens, logprobs, c->status, V, slice_subs<T>(V, cl)};
     return launch_rows(sample_kernel<T>, ready, c->device, N, cl, slice_bytes<T>(V, cl, 0), false, a, s);
 }
@@ -478,6 +612,16 @@ cudaError_t keep_rows(const ddt_ctx *c, const void *draft, const void *target, c
     static DeviceFlags ready;
     const int V = c->cfg.V, L = c->cfg.L;
     const int64_t rows = (int64_t)R * ((draft ? L : 0) + (target ? L + 1 : 0));
+    if constexpr (sizeof(T) == 2) {
+        static DeviceFlags ready_bins[2];
+        const int cl = V >= SB_LEAST ? bins_cluster(V) : 0;
+        if (cl > 0) {
+            const KeepArgs<T> a = {(const T *)draft, (const T *)target, fd, ft, tokens, n_guess, (KeptRow *)c->sm_rows,
+                                   c->status, L, V, 0};
+            return launch_rows(cl == 8 ? keep_bins_kernel<8> : keep_bins_kernel<16>, ready_bins[cl == 8], c->device, rows,
+                               cl, bins_bytes(V, cl), dependent, a, s);
+        }
+    }
     const int cl = pick_cluster<T>(V, rows, c->num_sms, 0);
     const KeepArgs<T> a = {(const T *)draft, (const T *)target, fd, ft, tokens, n_guess, (KeptRow *)c->sm_rows,
                            c->status, L, V, slice_subs<T>(V, cl)};

@@ -52,9 +52,12 @@ DDT_DEVINL uint32_t cl_size()
     asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
 }
+DDT_DEVINL void cl_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+DDT_DEVINL void cl_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 DDT_DEVINL void cl_sync()
 {
-    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cl_arrive();
+    cl_wait();
 }
 DDT_DEVINL uint32_t cl_map(const void *p, uint32_t rank)
 {
@@ -69,7 +72,7 @@ DDT_DEVINL void cl_st64(uint32_t at, uint64_t v)
 DDT_DEVINL uint32_t cl_ld32(uint32_t at)
 {
     uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at));  // (stays between the barriers around it)
     return v;
 }
 DDT_DEVINL uint32_t cl_add32(uint32_t at, uint32_t v)
@@ -214,6 +217,20 @@ DDT_DEVINL uint64_t to_fixed(const Sum2 &s)
     return to_fixed(a + b, c + d);
 }
 
+// two weights in fixed point
+template <bool EXACT>
+DDT_DEVINL void fixed_pair(const Scale &sc, const float2 *tab, float x0, float x1, bool k0, bool k1, uint64_t &w0,
+                           uint64_t &w1)
+{
+    Sum2 s = {0, 0};
+    add_weights<EXACT>(sc, tab, x0, x1, k0, k1, s);
+    float h0, h1, l0, l1;
+    f2unpack(s.hi, h0, h1);
+    f2unpack(s.lo, l0, l1);
+    w0 = to_fixed(h0, l0);
+    w1 = to_fixed(h1, l1);
+}
+
 // one weight (z counts)
 template <bool EXACT>
 DDT_DEVINL uint64_t weight_of(const Scale &sc, const float2 *tab, float z)
@@ -307,15 +324,19 @@ __host__ __device__ constexpr int slice_subs(int V, int cl) { return (row_subs<T
 
 // The slice of a row that a CTA holds. Element (sub-chunk s, lane, e) has index
 // index0(s, lane) + e.
-template <typename T>
+template <typename T, bool SMEM>
 struct Slice {
     static constexpr int E = Vec<T>::E, SE = SR_SUB / (int)sizeof(T);
-    unsigned char *at;  // ns sub-chunks
+    unsigned char *at;  // SMEM: ns sub-chunks
+    const T *base;      // else: 16 bytes that hold the row's first element
     int s0, ns, off, V;
+    bool infinite;      // else: (see held_value)
 
     DDT_DEVINL void place(unsigned char *smem, const T *row, int V_, uint32_t rank, uint32_t cl)
     {
         at = smem;
+        base = row - (int)(((uintptr_t)row & 15) / sizeof(T));
+        infinite = false;
         V = V_;
         off = (int)(((uintptr_t)row & 15) / sizeof(T));
         const int subs = (int)(((int64_t)off + V + SE - 1) / SE);
@@ -324,9 +345,8 @@ struct Slice {
     }
     // start this thread's copies. Whole 16-byte vectors of the row; what is before the
     // row's first element comes from the row before it (the tensor begins on 16 bytes)
-    DDT_DEVINL void fetch(const T *row, int tid) const
+    DDT_DEVINL void fetch(int tid) const
     {
-        const T *base = row - off;
         const uint32_t dst = (uint32_t)__cvta_generic_to_shared(at);
         const int64_t end = (int64_t)off + V;
         for (int v = tid; v < ns * 32; v += SR_THREADS) {
@@ -355,6 +375,25 @@ struct Slice {
     }
     DDT_DEVINL uint4 raw(int s, int lane) const { return *reinterpret_cast<const uint4 *>(at + s * SR_SUB + lane * 16); }
     DDT_DEVINL int index0(int s, int lane) const { return (s0 + s) * SE + lane * E - off; }
+    // the E logits of a lane
+    DDT_DEVINL void get(int s, int lane, float *z) const
+    {
+        if constexpr (SMEM) {
+            Vec<T>::get(raw(s, lane), z);
+        } else {
+            const int i0 = index0(s, lane);
+            if (i0 >= 0 && i0 + E <= V) {
+                Vec<T>::get(__ldg(reinterpret_cast<const uint4 *>(base + off + i0)), z);
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    z[e] = i0 + e >= 0 && i0 + e < V ? logit_value(base + off, i0 + e) : DDT_NEG_INF;
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                z[e] = held_value(z[e], infinite);
+        }
+    }
 };
 
 // totals over a warp
@@ -377,12 +416,12 @@ DDT_DEVINL uint64_t warp_incl64(uint64_t v, int lane)
 }
 
 // One row of a cluster: what its threads share in doing it.
-template <typename T>
+template <typename T, bool SMEM>
 struct Row {
     static constexpr int E = Vec<T>::E;
     static constexpr bool EXACT = Vec<T>::EXACT;
     RowShared *sh;
-    Slice<T> sl;
+    Slice<T, SMEM> sl;
     int tid, lane, warp;
     uint32_t rank, cl, turn, nth;
 
@@ -397,7 +436,10 @@ struct Row {
         turn = nth = 0;
         if (tid < 4)
             sh->count[tid] = 0;  // (a cluster barrier comes before the first collection)
+        cl_arrive();  // (ended by started(): a CTA's shared memory is there once it runs)
     }
+    // before the first access to another CTA's shared memory
+    DDT_DEVINL void started() { cl_wait(); }
 
     // Every CTA tells the others up to four words (held by every thread). A place is
     // written again only two exchanges later, behind a barrier that its readers reach
@@ -417,16 +459,20 @@ struct Row {
     DDT_DEVINL void load(unsigned char *smem, const T *row, int V)
     {
         sl.place(smem, row, V, rank, cl);
-        sl.fetch(row, tid);
+        if (SMEM)
+            sl.fetch(tid);
         if (tid < 32)
             sh->tab[tid] = SR_TABLE[tid];
     }
     DDT_DEVINL void loaded()
     {
-        cp_wait_all();
+        if (SMEM) {
+            cp_wait_all();
+            __syncthreads();
+            sl.mend(tid);
+        }
         __syncthreads();
-        sl.mend(tid);
-        __syncthreads();
+        started();
     }
 
     // ---- the row's largest value, each thread's own, the least of the threads' finite ones
@@ -439,9 +485,8 @@ struct Row {
         float m = DDT_NEG_INF;
         bool nan = false;
         for (int s = warp; s < sl.ns; s += SR_WARPS) {
-            const uint4 v = sl.raw(s, lane);
             float z[E];
-            Vec<T>::get(v, z);
+            sl.get(s, lane, z);
             bool bad = false;
 #pragma unroll
             for (int e = 0; e < E; ++e) {
@@ -449,13 +494,13 @@ struct Row {
                 bad |= odd;
                 m = fmaxf(m, odd ? (z[e] != z[e] ? m : 0.f) : z[e]);
             }
-            if (bad) {  // from here on a NaN is -infinity, and what is next to 0 is 0
+            if (SMEM && bad) {  // from here on a NaN is -infinity, and what is next to 0 is 0
                 T *d = reinterpret_cast<T *>(sl.at + s * SR_SUB + lane * 16);
 #pragma unroll
                 for (int e = 0; e < E; ++e)
                     if (z[e] != z[e]) {
                         nan = true;
-                        d[e] = Slice<T>::none();
+                        d[e] = Slice<T, SMEM>::none();
                     } else if (fabsf(z[e]) < SR_TINY) {
                         d[e] = (T)0;
                     }
@@ -496,13 +541,14 @@ struct Row {
     // a row with +infinity: those tokens have equal weights, the others none
     DDT_DEVINL void only_infinite(Top &t)
     {
-        for (int s = warp; s < sl.ns; s += SR_WARPS) {
+        sl.infinite = true;
+        for (int s = warp; SMEM && s < sl.ns; s += SR_WARPS) {
             T *d = reinterpret_cast<T *>(sl.at + s * SR_SUB + lane * 16);
             float z[E];
-            Vec<T>::get(sl.raw(s, lane), z);
+            sl.get(s, lane, z);
 #pragma unroll
             for (int e = 0; e < E; ++e)
-                d[e] = z[e] == t.zmax ? (T)0 : Slice<T>::none();
+                d[e] = z[e] == t.zmax ? (T)0 : Slice<T, SMEM>::none();
         }
         __syncthreads();
         t.own = t.own == t.zmax ? 0.f : DDT_NEG_INF;
@@ -512,7 +558,9 @@ struct Row {
     // an element of this CTA's slice
     DDT_DEVINL float value(int i) const
     {
-        const T x = reinterpret_cast<const T *>(sl.at)[i + sl.off - sl.s0 * Slice<T>::SE];
+        if (!SMEM)
+            return held_value(logit_value(sl.base + sl.off, i), sl.infinite);
+        const T x = reinterpret_cast<const T *>(sl.at)[i + sl.off - sl.s0 * Slice<T, SMEM>::SE];
         if constexpr (sizeof(T) == 2)
             return bf16_to_f32(x);
         else
@@ -539,14 +587,19 @@ struct Row {
     DDT_DEVINL uint64_t mass(const Scale &sc, const Border &b, uint64_t *sub, const uint64_t (**all)[4])
     {
         uint64_t own = 0;
+        const bool cut = b.last < sl.V - 1;
         for (int s = warp; s < sl.ns; s += SR_WARPS) {
             float z[E];
-            Vec<T>::get(sl.raw(s, lane), z);
+            sl.get(s, lane, z);
             const int i0 = sl.index0(s, lane);
             bool k[E], some = false;
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                some |= k[e] = kept(b, z[e], i0 + e);
+            for (int e = 0; e < E; ++e) {
+                k[e] = z[e] >= b.z;
+                if (cut && z[e] == b.z)
+                    k[e] = i0 + e <= b.last;
+                some |= k[e];
+            }
             uint64_t q = 0;
             if (__any_sync(0xFFFFFFFFu, some)) {
                 Sum2 sum = {0, 0};
@@ -634,7 +687,7 @@ struct Row {
         nth = (nth + 1) & 3;
         for (int s = warp; s < sl.ns; s += SR_WARPS) {
             float z[E];
-            Vec<T>::get(sl.raw(s, lane), z);
+            sl.get(s, lane, z);
             const int i0 = sl.index0(s, lane);
             bool k[E];
             uint32_t n = 0;
@@ -760,7 +813,7 @@ struct Row {
         } else {
             for (int s = warp; s < sl.ns; s += SR_WARPS) {
                 float z[E];
-                Vec<T>::get(sl.raw(s, lane), z);
+                sl.get(s, lane, z);
 #pragma unroll
                 for (int e = 0; e < E; ++e)
                     if (z[e] >= vlo)
@@ -793,7 +846,7 @@ struct Row {
         float lo = SR_MAX_FLOAT, hi = -SR_MAX_FLOAT;
         for (int s = warp; s < sl.ns; s += SR_WARPS) {
             float z[E];
-            Vec<T>::get(sl.raw(s, lane), z);
+            sl.get(s, lane, z);
             const int i0 = sl.index0(s, lane);
             bool k[E], some = false;
 #pragma unroll
@@ -869,19 +922,16 @@ struct Row {
             return -1;
         const int s = sh->found[0];
         at = sh->warp[0][3];
-        uint4 raw = sl.raw(s, lane);
         float z[E];
-        Vec<T>::get(raw, z);
+        sl.get(s, lane, z);
         const uint64_t sum = f.lane_sum(z, sl.index0(s, lane));
         uint64_t to = at + warp_incl64(sum, lane);
         const uint32_t hit = __ballot_sync(0xFFFFFFFFu, target < to);
         const int who = __ffs(hit) - 1;  // (the sub-chunk's sum is the lanes': one is hit)
         at = __shfl_sync(0xFFFFFFFFu, to - sum, who);
-        raw.x = __shfl_sync(0xFFFFFFFFu, raw.x, who);
-        raw.y = __shfl_sync(0xFFFFFFFFu, raw.y, who);
-        raw.z = __shfl_sync(0xFFFFFFFFu, raw.z, who);
-        raw.w = __shfl_sync(0xFFFFFFFFu, raw.w, who);
-        Vec<T>::get(raw, z);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            z[e] = __shfl_sync(0xFFFFFFFFu, z[e], who);
         const int i0 = sl.index0(s, who), e = lane & (E - 1);
         const uint32_t over = __ballot_sync(0xFFFFFFFFu, target < at + f.sum_to(z, i0, e));
         const int pick = __ffs(over) - 1;
@@ -895,7 +945,7 @@ struct Row {
         uint64_t own = 0;
         for (int s = warp; s < sl.ns; s += SR_WARPS) {
             float z[E];
-            Vec<T>::get(sl.raw(s, lane), z);
+            sl.get(s, lane, z);
             const uint64_t q = warp_sum64(f.lane_sum(z, sl.index0(s, lane)));
             if (lane == 0) {
                 sub[s] = q;
@@ -955,7 +1005,7 @@ struct Row {
             clear_hist();
             for (int s = warp; s < sl.ns; s += SR_WARPS) {
                 float z[E];
-                Vec<T>::get(sl.raw(s, lane), z);
+                sl.get(s, lane, z);
 #pragma unroll
                 for (int e = 0; e < E; ++e)
                     if (z[e] >= vlo && z[e] <= vhi)
@@ -1005,7 +1055,7 @@ struct Row {
             clear_hist();
             for (int s = warp; s < sl.ns; s += SR_WARPS) {
                 float z[E];
-                Vec<T>::get(sl.raw(s, lane), z);
+                sl.get(s, lane, z);
                 const int i0 = sl.index0(s, lane);
 #pragma unroll
                 for (int e = 0; e < E; ++e)
