@@ -425,7 +425,7 @@ typedef struct ddt_filter {
  *             weights exceeds u times the kept weights' sum
  *   tokens    [N] i32
  *   logprobs  [N] f32 or NULL: log of the token's probability in the row's
- *             distribution
+ *             distribution, to 2^-20 (where top-k or top-p apply: to its rounding)
  * A row without weights (every logit -infinity or NaN) and a row with a bad setting
  * get token -1 and log-probability -infinity. One kernel is enqueued; it uses no
  * workspace, so calls on several streams may overlap. tokens and logprobs may not

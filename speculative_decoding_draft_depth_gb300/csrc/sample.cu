@@ -36,26 +36,6 @@ struct SampleArgs {
 
 extern __shared__ __align__(16) unsigned char sr_smem[];
 
-// the row's top value and scale, and the border under the row's settings (a row in place
-// in shared memory). false: no token has a weight
-template <typename T, bool SMEM>
-DDT_DEVINL bool row_border(Row<T, SMEM> &row, const Settings &set, uint64_t *sub, int32_t *status, Scale &sc,
-                           typename Row<T, SMEM>::Cut &cut, bool &infinite)
-{
-    typename Row<T, SMEM>::Top t = row.top();
-    if (t.nan && row.rank == 0 && row.tid == 0)
-        set_status(status, DDT_DEV_NAN_LOGITS);
-    if (t.zmax == DDT_NEG_INF)
-        return false;
-    infinite = t.zmax == -DDT_NEG_INF;
-    if (infinite)
-        row.only_infinite(t);
-    sc = make_scale(t.zmax, set.T);
-    const float min_z = set.m > 0.f ? min_value(t.zmax, row.sh->off) : DDT_NEG_INF;
-    cut = row.border(t, sc, set.k, set.p, min_z, sub);
-    return true;
-}
-
 template <typename T>
 DDT_DEVINL void store_token(const SampleArgs<T> &a, int64_t n, int token, float logprob)
 {
@@ -63,100 +43,116 @@ DDT_DEVINL void store_token(const SampleArgs<T> &a, int64_t n, int token, float 
     if (a.logprobs)
         a.logprobs[n] = logprob;
 }
-// log of a token's weight over all that is kept (the largest weight is 2^44, so the sum is
-// at least that)
-DDT_DEVINL float log_share(float z, const Scale &sc, float T, uint64_t mass)
-{
-    return (z - sc.zmax) / T - log1pf((float)(mass - (1ull << SR_ONE)) * 5.684341886e-14f);
-}
 
-// a row from its border on: the kept weights' sums, and the draw
-template <typename T, bool SMEM>
-DDT_DEVINL void draw_row(Row<T, SMEM> &row, const SampleArgs<T> &a, int64_t n, const Settings &set, uint64_t *sub)
-{
+// what became of a row in shared memory
+struct Solved {
     Scale sc;
-    typename Row<T, SMEM>::Cut cut;
-    bool infinite;
-    if (!row_border(row, set, sub, a.status, sc, cut, infinite)) {
-        if (row.rank == 0 && row.tid == 0)
-            store_token(a, n, -1, DDT_NEG_INF);
-        return;
-    }
-    const uint64_t(*all)[4];
-    const uint64_t mass = row.mass(sc, cut.b, sub, &all);
-    const typename Row<T, SMEM>::Weight w = {sc, cut.b, row.sh->tab};
-    const int i = row.locate(sub, all, draw_target(__ldg(a.u + n), mass), w);
-    if (i >= 0)
-        store_token(a, n, i, log_share(row.value(i), sc, set.T, mass));
-}
-
-template <typename T>
-__global__ void __launch_bounds__(SR_THREADS) sample_kernel(const SampleArgs<T> a)
-{
-    __shared__ RowShared sh;
-    const int64_t n = blockIdx.x / cl_size();
-    const Settings set = load_settings(a.f, (int)n);
-    if (!set.good) {
-        if (cl_rank() == 0 && threadIdx.x == 0) {
-            store_token(a, n, -1, DDT_NEG_INF);
-            set_status(a.status, DDT_DEV_BAD_SETTING);
-        }
-        return;
-    }
-    Row<T, true> row;
-    row.begin(&sh);
-    row.load(sr_smem, a.logits + n * a.V, a.V);
-    if (row.tid == 0 && set.m > 0.f)
-        sh.off = min_offset(set);
-    row.loaded();
-    draw_row(row, a, n, set, reinterpret_cast<uint64_t *>(sr_smem + a.subs * SR_SUB));
-}
-
-// (rows that are not counted: apart, for the registers of those that are)
-__device__ __noinline__ void draw_general(Row<uint16_t, false> row, const SampleArgs<uint16_t> &a, int64_t n,
-                                          const Settings &set)
-{
-    draw_row(row, a, n, set, reinterpret_cast<uint64_t *>(sr_smem));
-}
-
-// the same by counts (bf16)
-template <int CL>
-__global__ void __launch_bounds__(SR_THREADS, 5) sample_bins_kernel(const SampleArgs<uint16_t> a)
-{
-    __shared__ RowShared sh;
-    __shared__ BinShared<CL> bs;
-    const int64_t n = blockIdx.x / cl_size();
-    const Settings set = load_settings(a.f, (int)n);
-    if (!set.good) {
-        if (cl_rank() == 0 && threadIdx.x == 0) {
-            store_token(a, n, -1, DDT_NEG_INF);
-            set_status(a.status, DDT_DEV_BAD_SETTING);
-        }
-        return;
-    }
-    Row<uint16_t, false> row;
-    row.begin(&sh);
-    const uint16_t *z = a.logits + n * a.V;
-    row.load(nullptr, z, a.V);
-    if (row.tid == 0 && set.m > 0.f)
-        sh.off = min_offset(set);
-    BinRow<CL> bins(row, &bs, sr_smem, z, a.V);
-    Scale sc;
-    typename BinRow<CL>::Kept k;
-    const int way = bins.run(set, sc, k, a.status);
-    if (way == BinRow<CL>::GENERAL) {
-        draw_general(row, a, n, set);
-        return;
-    }
-    if (way == BinRow<CL>::NONE) {
-        if (row.rank == 0 && row.tid == 0)
-            store_token(a, n, -1, DDT_NEG_INF);
-        return;
-    }
     Border b;
-    const int i = bins.draw(sc, k, __ldg(a.u + n), b);
-    if (i >= 0)
-        store_token(a, n, i, log_share(held_value(logit_value(z, i), false), sc, set.T, k.mass));
+    uint64_t mass;
+    int token;
+    bool infinite, none;  // none: no token has a weight
+};
+
+// a row in place in shared memory (see Row::solve). false: to be counted
+template <bool COUNTS, typename T>
+DDT_DEVINL bool solve_row(Row<T> &row, const Settings &set, float u, uint64_t *sub, int32_t *status, Solved &r)
+{
+    typename Row<T>::Top t = row.top();
+    if (t.nan && row.rank == 0 && row.tid == 0)
+        set_status(status, DDT_DEV_NAN_LOGITS);
+    r.none = t.zmax == DDT_NEG_INF;
+    r.token = -1;
+    if (r.none)
+        return true;
+    r.infinite = t.zmax == -DDT_NEG_INF;
+    if (r.infinite)
+        row.only_infinite(t);
+    r.sc = make_scale(t.zmax, set.T);
+    typename Row<T>::Found f;
+    if (!row.template solve<COUNTS>(t, r.sc, set, set.m > 0.f ? min_value(t.zmax, row.sh->off) : DDT_NEG_INF, u, sub, f))
+        return false;
+    r.b = f.b;
+    r.mass = f.mass;
+    r.token = f.token;
+    return true;
+}
+// the same for a row that cannot be counted after all (apart, for the registers of the rest)
+__device__ __noinline__ void solve_general(Row<uint16_t> row, const uint16_t *z, int V, const Settings &set, float u,
+                                           uint64_t *sub, int32_t *status, Solved &r)
+{
+    __syncthreads();
+    row.load(sr_smem, z, V);
+    row.loaded();
+    solve_row<false>(row, set, u, sub, status, r);
+}
+
+// A row from its logits on. CL > 0: the cluster's size, of rows that may be counted. In
+// r.token >= 0 the drawn token, in one thread; for u < 0 the border and the mass, in `here`.
+template <int CL, typename T>
+DDT_DEVINL void whole_row(Row<T> &row, RowShared *sh, BinShared<(CL > 0 ? CL : 1)> *bs, const T *z, int V, int subs,
+                          const Settings &set, float u, int32_t *status, Solved &r, bool &here)
+{
+    uint64_t *sub = reinterpret_cast<uint64_t *>(sr_smem + subs * SR_SUB);
+    row.begin(sh);
+    row.load(sr_smem, z, V);
+    if (row.tid == 0 && set.m > 0.f)
+        sh->off = min_offset(set);
+    row.loaded();
+    row.started();
+    here = row.rank == 0 && row.tid == 0;
+    if constexpr (CL == 0) {
+        solve_row<false>(row, set, u, sub, status, r);
+    } else if (!solve_row<true>(row, set, u, sub, status, r)) {
+        BinRow<CL> bins(row, bs, sr_smem, z, V);
+        typename BinRow<CL>::Kept k;
+        if (!bins.run(set, r.sc, k)) {
+            Solved g;
+            solve_general(row, z, V, set, u, sub, status, g);
+            r = g;
+            return;
+        }
+        r.mass = k.mass;
+        if (u >= 0.f) {
+            r.token = bins.draw(r.sc, k, u, r.b);
+            return;
+        }
+        // the thread that knows the border answers: the last kept index's, or the first
+        const bool cut = k.d != SB_VALUES && k.count != k.of;
+        const int last = bins.last_kept(k);
+        r.b = {k.d == SB_VALUES ? bins.least : sb_value(k.d), cut ? last : 0x7FFFFFFF};
+        here = cut ? last >= 0 : here;
+        cl_sync();  // (the counts have been read by other CTAs)
+    }
+}
+
+template <typename T, int CL>
+__global__ void __launch_bounds__(SR_THREADS, 4) sample_kernel(const SampleArgs<T> a)
+{
+    __shared__ RowShared sh;
+    __shared__ BinShared<(CL > 0 ? CL : 1)> bs;
+    const int64_t n = blockIdx.x / cl_size();
+    const Settings set = load_settings(a.f, (int)n);
+    Solved r;
+    r.none = !set.good;
+    r.token = -1;
+    if (set.good) {
+        Row<T> row;
+        bool here;
+        const float u = __ldg(a.u + n);
+        const T *z = a.logits + n * a.V;
+        whole_row<CL>(row, &sh, &bs, z, a.V, a.subs, set, u > 0.f ? u : 0.f, a.status, r, here);
+        // log of the token's weight over all that is kept (the largest weight is 2^44, so
+        // the sum is about that at least)
+        if (r.token >= 0) {
+            const float over = (float)(int64_t)(r.mass - (1ull << SR_ONE)) * 5.684341886e-14f;
+            store_token(a, n, r.token, (held_value(logit_value(z, r.token), r.infinite) - r.sc.zmax) / set.T - log1pf(over));
+        }
+    }
+    if (r.none && cl_rank() == 0 && threadIdx.x == 0) {
+        store_token(a, n, -1, DDT_NEG_INF);
+        if (!set.good)
+            set_status(a.status, DDT_DEV_BAD_SETTING);
+    }
 }
 
 // what keep_kernel leaves of a row
@@ -212,92 +208,31 @@ struct KeepRow {
     }
 };
 
-// what is kept of a row, by its border
-template <typename T, bool SMEM>
-DDT_DEVINL void keep_row(Row<T, SMEM> &row, const KeepRow<T> &kr, int32_t *status, uint64_t *sub)
-{
-    KeptRow r = {0.f, {0.f, 0}, 0, 0, 0};
-    Scale sc;
-    typename Row<T, SMEM>::Cut cut;
-    bool infinite;
-    if (row_border(row, kr.set, sub, status, sc, cut, infinite)) {
-        r.zmax = sc.zmax;
-        r.b = cut.b;
-        r.flags = infinite ? KR_INF : 0;
-        r.mass = cut.mass ? cut.mass : row.mass(sc, cut.b, nullptr, nullptr);
-        if (row.rank == 0 && row.tid == 0 && kr.x >= 0) {
-            const float v = held_value(logit_value(kr.z, kr.x), infinite);
-            if (kept(r.b, v, kr.x))
-                r.guess = weight_of<Row<T, SMEM>::EXACT>(sc, row.sh->tab, v);
-        }
-    }
-    if (row.rank == 0 && row.tid == 0)
-        *kr.to = r;
-}
-
-template <typename T>
-__global__ void __launch_bounds__(SR_THREADS) keep_kernel(const KeepArgs<T> a)
+template <typename T, int CL>
+__global__ void __launch_bounds__(SR_THREADS, 4) keep_kernel(const KeepArgs<T> a)
 {
     __shared__ RowShared sh;
     pdl_trigger();
     KeepRow<T> kr;
     if (kr.find(a, blockIdx.x / cl_size())) {
-        Row<T, true> row;
-        row.begin(&sh);
-        row.load(sr_smem, kr.z, a.V);
-        if (row.tid == 0 && kr.set.m > 0.f)
-            sh.off = min_offset(kr.set);
-        row.loaded();
-        keep_row(row, kr, a.status, reinterpret_cast<uint64_t *>(sr_smem + a.subs * SR_SUB));
-    }
-    pdl_wait();  // (rows of the other type may be done by the launch before; what follows waits for both)
-}
-
-__device__ __noinline__ void keep_general(Row<uint16_t, false> row, const KeepRow<uint16_t> &kr, int32_t *status)
-{
-    keep_row(row, kr, status, reinterpret_cast<uint64_t *>(sr_smem));
-}
-
-// the same by counts (bf16)
-template <int CL>
-__global__ void __launch_bounds__(SR_THREADS, 5) keep_bins_kernel(const KeepArgs<uint16_t> a)
-{
-    __shared__ RowShared sh;
-    __shared__ BinShared<CL> bs;
-    pdl_trigger();
-    KeepRow<uint16_t> kr;
-    if (kr.find(a, blockIdx.x / cl_size())) {
-        Row<uint16_t, false> row;
-        row.begin(&sh);
-        row.load(nullptr, kr.z, a.V);
-        if (row.tid == 0 && kr.set.m > 0.f)
-            sh.off = min_offset(kr.set);
-        BinRow<CL> bins(row, &bs, sr_smem, kr.z, a.V);
-        Scale sc;
-        typename BinRow<CL>::Kept k;
-        const int way = bins.run(kr.set, sc, k, a.status);
-        if (way == BinRow<CL>::GENERAL) {
-            keep_general(row, kr, a.status);
-        } else if (way == BinRow<CL>::NONE) {
-            if (row.rank == 0 && row.tid == 0)
-                *kr.to = KeptRow{0.f, {0.f, 0}, 0, 0, 0};
-        } else {
-            // the thread that knows the border writes: the last kept index's, or the first
-            const bool cut = k.d != SB_VALUES && k.count != k.of;
-            const int last = bins.last_kept(k);
-            if (cut ? last >= 0 : row.rank == 0 && row.tid == 0) {
-                KeptRow r = {sc.zmax, {k.d == SB_VALUES ? bins.least : sb_value(k.d), cut ? last : 0x7FFFFFFF}, 0, k.mass, 0};
+        Row<T> row;
+        Solved r;
+        bool here;
+        whole_row<CL>(row, &sh, (BinShared<(CL > 0 ? CL : 1)> *)nullptr, kr.z, a.V, a.subs, kr.set, -1.f, a.status, r, here);
+        if (here) {
+            KeptRow k = {0.f, {0.f, 0}, 0, 0, 0};
+            if (!r.none) {
+                k = {r.sc.zmax, r.b, r.infinite ? KR_INF : 0, r.mass, 0};
                 if (kr.x >= 0) {
-                    const float v = held_value(logit_value(kr.z, kr.x), false);
+                    const float v = held_value(logit_value(kr.z, kr.x), r.infinite);
                     if (kept(r.b, v, kr.x))
-                        r.guess = weight_of<false>(sc, sh.tab, v);
+                        k.guess = weight_of<Row<T>::EXACT>(r.sc, sh.tab, v);
                 }
-                *kr.to = r;
             }
-            cl_sync();  // (the counts have been read by other CTAs)
+            *kr.to = k;
         }
     }
-    pdl_wait();
+    pdl_wait();  // (rows of the other type may be done by the launch before; what follows waits for both)
 }
 
 template <typename TD, typename TT>
@@ -427,7 +362,7 @@ __global__ void __launch_bounds__(SR_THREADS) chain_kernel(const ChainArgs<TD, T
     __shared__ RowShared sh;
     __shared__ Ratio s_ratio;
     __shared__ int s_first, s_bad;
-    Row<TT, true> row;
+    Row<TT> row;
     row.begin(&sh);
     const int L = a.L, V = a.V, i = blockIdx.x / row.cl, lane = row.lane;
     const int n = guess_count(a.n_guess, i, L);
@@ -504,6 +439,7 @@ __global__ void __launch_bounds__(SR_THREADS) chain_kernel(const ChainArgs<TD, T
         f.zq = fetch_range(smem_q, a.draft + ((int64_t)i * L + first) * V, V, lo, hi, row.tid);
     }
     row.loaded();
+    row.started();
     const uint64_t(*all)[4];
     const uint64_t mass = row.total(f, sub, &all);
     if (mass == 0) {
@@ -543,17 +479,18 @@ int pick_cluster(int V, int64_t rows, int num_sms, int bytes_q)
     return cl;
 }
 
-// Rows of bf16 logits are counted by their values from this many on: 
+// Rows of bf16 logits from this length on may be counted by their values: their cluster has
+// eight CTAs, sixteen where a slice's counts would pass 16 bits (0: not even then).
 constexpr int SB_LEAST = 8192;
-// CTAs of such a row's cluster: a slice's counts are 16 bits
 int bins_cluster(int V)
 {
-    int cl = 8;
-    while (cl < SR_MAX_CL && (V + 14) / 8 / cl * 8 + 8 > 65535)
-        cl *= 2;
-    return (V + 14) / 8 / cl * 8 + 8 > 65535 ? 0 : cl;
+    if (V < SB_LEAST)
+        return 0;
+    for (int cl = 8; cl <= SR_MAX_CL; cl *= 2)
+        if ((V + 14) / 8 / cl * 8 + 8 <= 65535 && slice_bytes<uint16_t>(V, cl, 0) <= SR_SMEM_MAX)
+            return cl;
+    return 0;
 }
-int bins_bytes(int V, int cl) { return std::max(sb_bytes(cl), slice_subs<uint16_t>(V, cl) * 8); }
 
 template <typename Args>
 cudaError_t launch_rows(void (*kernel)(Args), DeviceFlags &ready, int dev, int64_t rows, int cl, int smem, bool dependent,
@@ -585,47 +522,52 @@ cudaError_t launch_rows(void (*kernel)(Args), DeviceFlags &ready, int dev, int64
     return cudaLaunchKernelEx(&lc, kernel, args);
 }
 
+template <typename T, int CL>
+cudaError_t sample_rows_cl(const ddt_ctx *c, const SampleArgs<T> &a, int N, int cl, int smem, cudaStream_t s)
+{
+    static DeviceFlags ready;
+    return launch_rows(sample_kernel<T, CL>, ready, c->device, N, cl, smem, false, a, s);
+}
 template <typename T>
 cudaError_t sample_rows(const ddt_ctx *c, const void *logits, int N, const ddt_filter &f, const float *u, int32_t *tokens,
                         float *logprobs, cudaStream_t s)
 {
-    static DeviceFlags ready;
-    const int V = c->cfg.V;
-    if constexpr (sizeof(T) == 2) {
-        static DeviceFlags ready_bins[2];
-        const int cl = V >= SB_LEAST ? bins_cluster(V) : 0;
-        if (cl > 0) {
-            const SampleArgs<T> a = {(const T *)logits, f, u, tokens, logprobs, c->status, V, 0};
-            return launch_rows(cl == 8 ? sample_bins_kernel<8> : sample_bins_kernel<16>, ready_bins[cl == 8], c->device, N,
-                               cl, bins_bytes(V, cl), false, a, s);
-        }
-    }
-    const int cl = pick_cluster<T>(V, N, c->num_sms, 0);
+    const int V = c->cfg.V, bins = sizeof(T) == 2 ? bins_cluster(V) : 0;
+    const int cl = bins > 0 ? bins : pick_cluster<T>(V, N, c->num_sms, 0);
     const SampleArgs<T> a = {(const T *)logits, f, u, tokens, logprobs, c->status, V, slice_subs<T>(V, cl)};
-    return launch_rows(sample_kernel<T>, ready, c->device, N, cl, slice_bytes<T>(V, cl, 0), false, a, s);
+    const int smem = std::max(slice_bytes<T>(V, cl, 0), bins > 0 ? sb_bytes(cl) : 0);
+    if constexpr (sizeof(T) == 2) {
+        if (bins == 8)
+            return sample_rows_cl<T, 8>(c, a, N, cl, smem, s);
+        if (bins == 16)
+            return sample_rows_cl<T, 16>(c, a, N, cl, smem, s);
+    }
+    return sample_rows_cl<T, 0>(c, a, N, cl, smem, s);
 }
 
+template <typename T, int CL>
+cudaError_t keep_rows_cl(const ddt_ctx *c, const KeepArgs<T> &a, int64_t rows, int cl, int smem, bool dependent, cudaStream_t s)
+{
+    static DeviceFlags ready;
+    return launch_rows(keep_kernel<T, CL>, ready, c->device, rows, cl, smem, dependent, a, s);
+}
 template <typename T>
 cudaError_t keep_rows(const ddt_ctx *c, const void *draft, const void *target, const ddt_filter &fd, const ddt_filter &ft,
                       const int32_t *tokens, const int32_t *n_guess, int R, bool dependent, cudaStream_t s)
 {
-    static DeviceFlags ready;
-    const int V = c->cfg.V, L = c->cfg.L;
+    const int V = c->cfg.V, L = c->cfg.L, bins = sizeof(T) == 2 ? bins_cluster(V) : 0;
     const int64_t rows = (int64_t)R * ((draft ? L : 0) + (target ? L + 1 : 0));
-    if constexpr (sizeof(T) == 2) {
-        static DeviceFlags ready_bins[2];
-        const int cl = V >= SB_LEAST ? bins_cluster(V) : 0;
-        if (cl > 0) {
-            const KeepArgs<T> a = {(const T *)draft, (const T *)target, fd, ft, tokens, n_guess, (KeptRow *)c->sm_rows,
-                                   c->status, L, V, 0};
-            return launch_rows(cl == 8 ? keep_bins_kernel<8> : keep_bins_kernel<16>, ready_bins[cl == 8], c->device, rows,
-                               cl, bins_bytes(V, cl), dependent, a, s);
-        }
-    }
-    const int cl = pick_cluster<T>(V, rows, c->num_sms, 0);
+    const int cl = bins > 0 ? bins : pick_cluster<T>(V, rows, c->num_sms, 0);
     const KeepArgs<T> a = {(const T *)draft, (const T *)target, fd, ft, tokens, n_guess, (KeptRow *)c->sm_rows,
                            c->status, L, V, slice_subs<T>(V, cl)};
-    return launch_rows(keep_kernel<T>, ready, c->device, rows, cl, slice_bytes<T>(V, cl, 0), dependent, a, s);
+    const int smem = std::max(slice_bytes<T>(V, cl, 0), bins > 0 ? sb_bytes(cl) : 0);
+    if constexpr (sizeof(T) == 2) {
+        if (bins == 8)
+            return keep_rows_cl<T, 8>(c, a, rows, cl, smem, dependent, s);
+        if (bins == 16)
+            return keep_rows_cl<T, 16>(c, a, rows, cl, smem, dependent, s);
+    }
+    return keep_rows_cl<T, 0>(c, a, rows, cl, smem, dependent, s);
 }
 
 template <typename TD, typename TT>

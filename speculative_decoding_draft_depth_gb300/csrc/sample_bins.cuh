@@ -17,7 +17,6 @@
 // there) is left to the general way of sample_row.cuh: run() says so.
 #pragma once
 
-#include "logit_vec.cuh"
 #include "sample_row.cuh"
 
 namespace {
@@ -57,7 +56,7 @@ struct BinShared {
 
 template <int CL>
 struct BinRow {
-    using Base = Row<uint16_t, false>;
+    using Base = Row<uint16_t>;
     Base &row;  // its exchanges and block sums
     BinShared<CL> *bs;
     uint32_t *hist;
@@ -97,33 +96,24 @@ struct BinRow {
         if (b < 0x8000u + SB_LOW + SB_MAGS)  // (not the negative ones beyond)
             atomicAdd(&hist[word], b & 0x8000u ? 0x10000u : 1u);
     }
-    struct Seen {
-        uint32_t hi, lo, mag;  // pairs of: the largest, the smallest (numbers), the largest magnitude's bits
-    };
-    DDT_DEVINL static void see(uint32_t x, Seen &s)
+    DDT_DEVINL void add2(uint32_t x, uint32_t &least2) const
     {
-        s.hi = bf16x2_max(s.hi, x);
-        asm("min.bf16x2 %0, %0, %1;" : "+r"(s.lo) : "r"(x));
-        s.mag = __vmaxu2(s.mag, x & 0x7FFF7FFFu);
-    }
-    DDT_DEVINL void add2(uint32_t x, Seen &s) const
-    {
-        see(x, s);
+        asm("min.bf16x2 %0, %0, %1;" : "+r"(least2) : "r"(x));
         add(x & 0xFFFFu);
         add(x >> 16);
     }
-    DDT_DEVINL void add8(const uint4 &x, Seen &s) const
+    DDT_DEVINL void add8(const uint4 &x, uint32_t &least2) const
     {
-        add2(x.x, s);
-        add2(x.y, s);
-        add2(x.z, s);
-        add2(x.w, s);
+        add2(x.x, least2);
+        add2(x.y, least2);
+        add2(x.z, least2);
+        add2(x.w, least2);
     }
-    DDT_DEVINL void edge(int v, Seen &s) const  // a vector that is partly the row's
+    DDT_DEVINL void edge(int v, uint32_t &least2) const  // a vector that is partly the row's
     {
         for (int i = max(0, v * 8 - off); i < min(V, v * 8 + 8 - off); ++i) {
             const uint32_t b = __ldg(z + i);
-            see(b * 0x10001u, s);
+            asm("min.bf16x2 %0, %0, %1;" : "+r"(least2) : "r"(b * 0x10001u));
             add(b);
         }
     }
@@ -135,10 +125,8 @@ struct BinRow {
         uint64_t of;     //   out of so many
         uint64_t mass;
     };
-    enum { NONE, GENERAL, DONE };
-
-    // counts, weights, borders. GENERAL: this row is not one for counting
-    DDT_DEVINL int run(const Settings &set, Scale &sc, Kept &k, int32_t *status)
+    // counts, weights, borders. false: this row is not one for counting
+    DDT_DEVINL bool run(const Settings &set, const Scale &sc, Kept &k)
     {
         const int tid = row.tid;
         for (int i = tid; i < SB_WORDS; i += SR_THREADS)
@@ -146,68 +134,40 @@ struct BinRow {
         if (tid == 0)
             row.sh->list[0] = 0;  // (see hold)
         __syncthreads();
-        Seen s = {0xFF80FF80u, 0x7F807F80u, 0};
-        int v = v0 + tid;
+        uint32_t least2 = 0x7F807F80u;  // pairs of the least (numbers)
         const uint4 *at = reinterpret_cast<const uint4 *>(z - off);
+        int v = v0 + tid;
         for (; v + (SB_UNROLL - 1) * SR_THREADS < v1; v += SB_UNROLL * SR_THREADS) {
             uint4 x[SB_UNROLL];
 #pragma unroll
             for (int u = 0; u < SB_UNROLL; ++u) {
                 const int vu = v + u * SR_THREADS;
-                x[u] = inner(vu) ? ldg_stream(at + vu) : make_uint4(0, 0, 0, 0);
+                x[u] = inner(vu) ? __ldg(at + vu) : make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
             for (int u = 0; u < SB_UNROLL; ++u) {
                 if (inner(v + u * SR_THREADS))
-                    add8(x[u], s);
+                    add8(x[u], least2);
                 else
-                    edge(v + u * SR_THREADS, s);
+                    edge(v + u * SR_THREADS, least2);
             }
         }
         for (; v < v1; v += SR_THREADS) {
             if (inner(v))
-                add8(ldg_stream(at + v), s);
+                add8(__ldg(at + v), least2);
             else
-                edge(v, s);
+                edge(v, least2);
         }
-        float hi = fmaxf(bf16lo(s.hi), bf16hi(s.hi)), lo = fminf(bf16lo(s.lo), bf16hi(s.lo));
-        uint32_t mag = max(s.mag & 0xFFFFu, s.mag >> 16);
-        mag = __reduce_max_sync(0xFFFFFFFFu, mag);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
-            lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
-        }
-        if (row.lane == 0) {
-            row.sh->warp[row.warp][0] = ((uint64_t)__float_as_uint(hi) << 32) | __float_as_uint(lo);
-            row.sh->warp[row.warp][1] = mag;
-        }
-        __syncthreads();
-        for (int q = 0; q < SR_WARPS; ++q) {
-            const uint64_t x = row.sh->warp[q][0];
-            hi = fmaxf(hi, __uint_as_float((uint32_t)(x >> 32)));
-            lo = fminf(lo, __uint_as_float((uint32_t)x));
-            mag = max(mag, (uint32_t)row.sh->warp[q][1]);
-        }
+        bool low = fminf(bf16lo(least2), bf16hi(least2)) <= -128.f;
+        low = __syncthreads_or(low);
         const bool odd = hist[1] != 0 || (hist[SB_WORDS - 1] & 0xFFFFu) != 0;
-        row.started();
-        const uint64_t(*all)[4] = row.exchange(((uint64_t)__float_as_uint(hi) << 32) | __float_as_uint(lo), mag, odd, 0);
-        bool general = false;
-        for (int c = 0; c < CL; ++c) {
-            const uint64_t x = all[c][0];
-            hi = fmaxf(hi, __uint_as_float((uint32_t)(x >> 32)));
-            lo = fminf(lo, __uint_as_float((uint32_t)x));
-            mag = max(mag, (uint32_t)all[c][1]);
-            general |= all[c][2] != 0;
-        }
-        if (mag > 0x7F80u && row.rank == 0 && tid == 0)
-            set_status(status, DDT_DEV_NAN_LOGITS);
-        if (hi == DDT_NEG_INF)
-            return NONE;
-        sc = make_scale(hi, set.T);
-        if (general || hi <= -128.f || (lo <= -128.f && sc.zfloor < -128.f))
-            return GENERAL;
-        least = fmaxf(sc.zfloor, set.m > 0.f ? min_value(hi, row.sh->off) : DDT_NEG_INF);
+        const uint64_t(*all)[4] = row.exchange(odd || (low && sc.zfloor < -128.f), 0, 0, 0);
+        bool general = sc.zmax <= -128.f;
+        for (int c = 0; c < CL; ++c)
+            general |= all[c][0] != 0;
+        if (general)
+            return false;
+        least = fmaxf(sc.zfloor, set.m > 0.f ? min_value(sc.zmax, row.sh->off) : DDT_NEG_INF);
 
         // ---- this CTA's values, over all slices
         for (int i = tid; i < d1 - d0; i += SR_THREADS) {
@@ -271,7 +231,7 @@ struct BinRow {
             }
             k = told();
         }
-        return DONE;
+        return true;
     }
 
     // one thread of the cluster has the answer; all know it afterwards (told() also makes

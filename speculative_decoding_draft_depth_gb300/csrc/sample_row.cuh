@@ -35,6 +35,7 @@ constexpr int SR_MAX_CL = 16;     // CTAs of a cluster
 constexpr int SR_CAP = 512;       // candidates that are sorted in one place
 constexpr int SR_PROBE = 256;     // how many the first collection asks for, and the largest k that it serves
 constexpr int SR_BINS = 512;      // (two a thread)
+constexpr int SR_SMALL = 256;     // candidates of which each has a thread
 constexpr int SR_ONE = 44;        // a weight of 1 is 2^44
 constexpr float SR_MAX_FLOAT = 3.402823466e38f;
 constexpr float SR_TINY = 8.077935669e-28f;  // 2^-90: differences of logits stay far above what 1 / x can take
@@ -240,6 +241,33 @@ DDT_DEVINL uint64_t weight_of(const Scale &sc, const float2 *tab, float z)
     return to_fixed(s);
 }
 
+// The weights of two logits by the hardware's 2^x, the exponent's rounding carried: off by at
+// most 2^-22 of themselves (ex2), and 2^-24 each for the product's rounding, what is left of
+// the exponent's and (bf16) z - z_max where it has more than 24 bits.
+template <bool EXACT>
+DDT_DEVINL uint64_t quick_weights(const Scale &sc, float x0, float x1, bool k0, bool k1)
+{
+    const uint64_t z = f2pack(k0 ? x0 : sc.zmax, k1 ? x1 : sc.zmax), nz = f2both(-sc.zmax);
+    const uint64_t d = f2add(z, nz);
+    const uint64_t y = f2mul(d, f2both(sc.ch));
+    uint64_t nyl = f2fma(d, f2both(-sc.ch), y);  // -(what y lacks)
+    nyl = f2fma(d, f2both(-sc.cl), nyl);
+    if (EXACT) {
+        const uint64_t m1 = f2both(-1.f), bb = f2fma(z, m1, d);
+        nyl = f2fma(f2add(f2fma(f2fma(bb, m1, d), m1, z), f2fma(bb, m1, nz)), f2both(-sc.ch), nyl);
+    }
+    float a, b, la, lb;
+    f2unpack(y, a, b);
+    f2unpack(nyl, la, lb);
+    const float LN2 = 0.693147182464599609375f;
+    a = ex2(a);
+    b = ex2(b);
+    return f2pack(k0 ? fmaf(-a * LN2, la, a) : 0.f, k1 ? fmaf(-b * LN2, lb, b) : 0.f);
+}
+// What a sum of such weights may be off by: 2^-22 + 3 * 2^-24 of itself for the weights, and
+// 4 * 2^-24 for sums of up to eight in fp32 (then they are integers): below 2^-20.
+DDT_DEVINL uint64_t quick_slack(uint64_t mass) { return mass >> 20; }
+
 // x m for 0 < x < 1, rounded down or up
 DDT_DEVINL uint64_t fraction_of(float x, uint64_t m, bool up)
 {
@@ -255,6 +283,34 @@ DDT_DEVINL uint64_t fraction_of(float x, uint64_t m, bool up)
     return (hi >> sh) + (up && rest ? 1 : 0);
 }
 
+// floor(u mass), within the running sums: the draw's token is the first whose sum exceeds it
+DDT_DEVINL uint64_t draw_target(float u, uint64_t mass)
+{
+    return u < 1.f ? min(u > 0.f ? fraction_of(u, mass, false) : 0, mass - 1) : u == u ? mass - 1 : 0;
+}
+
+// the settings of a row. k = 1 and T = 1 stand for T = 0 (the largest logit, the lowest
+// index of it)
+struct Settings {
+    float T, p, m;
+    int k;
+    bool good;
+};
+DDT_DEVINL Settings load_settings(const ddt_filter &f, int i)
+{
+    Settings s;
+    s.T = f.temperature ? __ldg(f.temperature + i) : 1.f;
+    s.k = f.top_k ? __ldg(f.top_k + i) : 0;
+    s.p = f.top_p ? __ldg(f.top_p + i) : 1.f;
+    s.m = f.min_p ? __ldg(f.min_p + i) : 0.f;
+    s.good = s.T >= 0.f && s.T <= SR_MAX_FLOAT && s.p >= 0.f && s.p <= 1.f && s.m >= 0.f && s.m <= 1.f;
+    if (s.T == 0.f) {
+        s.T = 1.f;
+        s.k = 1;
+    }
+    s.T = fmaxf(s.T, SR_TINY);
+    return s;
+}
 // ---------------------------------------------------------------- border
 struct Border {
     float z;   // kept: above this value, or equal to it
@@ -275,6 +331,7 @@ struct RowShared {
     uint32_t count[4];       // candidates collected (the first CTA's; a place for each collection)
     int found[4];
     float2 off;              // T ln(min_p)
+    uint64_t kept[SR_SMALL]; // the candidates' weights
 };
 
 template <typename T> struct Vec;
@@ -324,19 +381,15 @@ __host__ __device__ constexpr int slice_subs(int V, int cl) { return (row_subs<T
 
 // The slice of a row that a CTA holds. Element (sub-chunk s, lane, e) has index
 // index0(s, lane) + e.
-template <typename T, bool SMEM>
+template <typename T>
 struct Slice {
     static constexpr int E = Vec<T>::E, SE = SR_SUB / (int)sizeof(T);
-    unsigned char *at;  // SMEM: ns sub-chunks
-    const T *base;      // else: 16 bytes that hold the row's first element
+    unsigned char *at;  // ns sub-chunks
     int s0, ns, off, V;
-    bool infinite;      // else: (see held_value)
 
     DDT_DEVINL void place(unsigned char *smem, const T *row, int V_, uint32_t rank, uint32_t cl)
     {
         at = smem;
-        base = row - (int)(((uintptr_t)row & 15) / sizeof(T));
-        infinite = false;
         V = V_;
         off = (int)(((uintptr_t)row & 15) / sizeof(T));
         const int subs = (int)(((int64_t)off + V + SE - 1) / SE);
@@ -345,8 +398,9 @@ struct Slice {
     }
     // start this thread's copies. Whole 16-byte vectors of the row; what is before the
     // row's first element comes from the row before it (the tensor begins on 16 bytes)
-    DDT_DEVINL void fetch(int tid) const
+    DDT_DEVINL void fetch(const T *row, int tid) const
     {
+        const T *base = row - off;
         const uint32_t dst = (uint32_t)__cvta_generic_to_shared(at);
         const int64_t end = (int64_t)off + V;
         for (int v = tid; v < ns * 32; v += SR_THREADS) {
@@ -374,26 +428,8 @@ struct Slice {
             reinterpret_cast<T *>(at)[tid] = none();
     }
     DDT_DEVINL uint4 raw(int s, int lane) const { return *reinterpret_cast<const uint4 *>(at + s * SR_SUB + lane * 16); }
+    DDT_DEVINL void get(int s, int lane, float *z) const { Vec<T>::get(raw(s, lane), z); }
     DDT_DEVINL int index0(int s, int lane) const { return (s0 + s) * SE + lane * E - off; }
-    // the E logits of a lane
-    DDT_DEVINL void get(int s, int lane, float *z) const
-    {
-        if constexpr (SMEM) {
-            Vec<T>::get(raw(s, lane), z);
-        } else {
-            const int i0 = index0(s, lane);
-            if (i0 >= 0 && i0 + E <= V) {
-                Vec<T>::get(__ldg(reinterpret_cast<const uint4 *>(base + off + i0)), z);
-            } else {
-#pragma unroll
-                for (int e = 0; e < E; ++e)
-                    z[e] = i0 + e >= 0 && i0 + e < V ? logit_value(base + off, i0 + e) : DDT_NEG_INF;
-            }
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                z[e] = held_value(z[e], infinite);
-        }
-    }
 };
 
 // totals over a warp
@@ -416,12 +452,12 @@ DDT_DEVINL uint64_t warp_incl64(uint64_t v, int lane)
 }
 
 // One row of a cluster: what its threads share in doing it.
-template <typename T, bool SMEM>
+template <typename T>
 struct Row {
     static constexpr int E = Vec<T>::E;
     static constexpr bool EXACT = Vec<T>::EXACT;
     RowShared *sh;
-    Slice<T, SMEM> sl;
+    Slice<T> sl;
     int tid, lane, warp;
     uint32_t rank, cl, turn, nth;
 
@@ -459,30 +495,26 @@ struct Row {
     DDT_DEVINL void load(unsigned char *smem, const T *row, int V)
     {
         sl.place(smem, row, V, rank, cl);
-        if (SMEM)
-            sl.fetch(tid);
+        sl.fetch(row, tid);
         if (tid < 32)
             sh->tab[tid] = SR_TABLE[tid];
     }
     DDT_DEVINL void loaded()
     {
-        if (SMEM) {
-            cp_wait_all();
-            __syncthreads();
-            sl.mend(tid);
-        }
+        cp_wait_all();
         __syncthreads();
-        started();
+        sl.mend(tid);
+        __syncthreads();
     }
 
-    // ---- the row's largest value, each thread's own, the least of the threads' finite ones
+    // ---- the row's largest and least (finite) value, the largest of each thread's
     struct Top {
-        float zmax, own, least;
+        float zmax, own, low;
         bool nan;
     };
     DDT_DEVINL Top top()
     {
-        float m = DDT_NEG_INF;
+        float m = DDT_NEG_INF, lo = SR_MAX_FLOAT;
         bool nan = false;
         for (int s = warp; s < sl.ns; s += SR_WARPS) {
             float z[E];
@@ -490,77 +522,76 @@ struct Row {
             bool bad = false;
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const bool odd = !(fabsf(z[e]) >= SR_TINY) && z[e] != 0.f;
-                bad |= odd;
-                m = fmaxf(m, odd ? (z[e] != z[e] ? m : 0.f) : z[e]);
+                bad |= !(fabsf(z[e]) >= SR_TINY) && z[e] != 0.f;
+                m = fmaxf(m, z[e]);  // (of a NaN and a number: the number)
+                lo = fminf(lo, z[e] == DDT_NEG_INF ? SR_MAX_FLOAT : z[e]);
             }
-            if (SMEM && bad) {  // from here on a NaN is -infinity, and what is next to 0 is 0
+            if (bad) {  // from here on a NaN is -infinity, and what is next to 0 is 0
                 T *d = reinterpret_cast<T *>(sl.at + s * SR_SUB + lane * 16);
 #pragma unroll
                 for (int e = 0; e < E; ++e)
                     if (z[e] != z[e]) {
                         nan = true;
-                        d[e] = Slice<T, SMEM>::none();
+                        d[e] = Slice<T>::none();
                     } else if (fabsf(z[e]) < SR_TINY) {
                         d[e] = (T)0;
                     }
             }
         }
+        // (what lies next to 0 counts as 0, here too)
+        m = fabsf(m) < SR_TINY ? 0.f : m;
+        lo = fabsf(lo) < SR_TINY ? 0.f : lo;
         Top r;
         r.own = m;
-        float hi = m, lo = m == DDT_NEG_INF ? SR_MAX_FLOAT : m;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
-            hi = fmaxf(hi, __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+            m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
             lo = fminf(lo, __shfl_xor_sync(0xFFFFFFFFu, lo, o));
         }
         nan = __any_sync(0xFFFFFFFFu, nan);
         if (lane == 0)
-            sh->warp[warp][0] = ((uint64_t)__float_as_uint(hi) << 32) | __float_as_uint(lo), sh->warp[warp][1] = nan;
+            sh->warp[warp][0] = ((uint64_t)__float_as_uint(m) << 32) | __float_as_uint(lo), sh->warp[warp][1] = nan;
         __syncthreads();
         nan = false;
 #pragma unroll
         for (int w = 0; w < SR_WARPS; ++w) {
             const uint64_t x = sh->warp[w][0];
-            hi = fmaxf(hi, __uint_as_float((uint32_t)(x >> 32)));
+            m = fmaxf(m, __uint_as_float((uint32_t)(x >> 32)));
             lo = fminf(lo, __uint_as_float((uint32_t)x));
             nan |= sh->warp[w][1] != 0;
         }
-        const uint64_t(*all)[4] = exchange(((uint64_t)__float_as_uint(hi) << 32) | __float_as_uint(lo), nan, 0, 0);
+        const uint64_t(*all)[4] = exchange(((uint64_t)__float_as_uint(m) << 32) | __float_as_uint(lo), nan, 0, 0);
         for (uint32_t c = 0; c < cl; ++c) {
             const uint64_t x = all[c][0];
-            hi = fmaxf(hi, __uint_as_float((uint32_t)(x >> 32)));
+            m = fmaxf(m, __uint_as_float((uint32_t)(x >> 32)));
             lo = fminf(lo, __uint_as_float((uint32_t)x));
             nan |= all[c][1] != 0;
         }
-        r.zmax = hi;
-        r.least = lo;
+        r.zmax = m;
+        r.low = lo;
         r.nan = nan;
         return r;
     }
     // a row with +infinity: those tokens have equal weights, the others none
     DDT_DEVINL void only_infinite(Top &t)
     {
-        sl.infinite = true;
-        for (int s = warp; SMEM && s < sl.ns; s += SR_WARPS) {
+        for (int s = warp; s < sl.ns; s += SR_WARPS) {
             T *d = reinterpret_cast<T *>(sl.at + s * SR_SUB + lane * 16);
             float z[E];
             sl.get(s, lane, z);
 #pragma unroll
             for (int e = 0; e < E; ++e)
-                d[e] = z[e] == t.zmax ? (T)0 : Slice<T, SMEM>::none();
+                d[e] = z[e] == t.zmax ? (T)0 : Slice<T>::none();
         }
         __syncthreads();
         t.own = t.own == t.zmax ? 0.f : DDT_NEG_INF;
-        t.zmax = t.least = 0.f;
+        t.zmax = t.low = 0.f;
     }
 
     // an element of this CTA's slice
     DDT_DEVINL float value(int i) const
     {
-        if (!SMEM)
-            return held_value(logit_value(sl.base + sl.off, i), sl.infinite);
-        const T x = reinterpret_cast<const T *>(sl.at)[i + sl.off - sl.s0 * Slice<T, SMEM>::SE];
+        const T x = reinterpret_cast<const T *>(sl.at)[i + sl.off - sl.s0 * Slice<T>::SE];
         if constexpr (sizeof(T) == 2)
             return bf16_to_f32(x);
         else
@@ -628,6 +659,48 @@ struct Row {
         return t;
     }
 
+    // ---- the same in plain fp32 (see quick_slack), of the tokens from lo up
+    DDT_DEVINL uint64_t quick_mass(const Scale &sc, float lo, uint64_t *sub, const uint64_t (**all)[4])
+    {
+        uint64_t own = 0;
+        for (int s = warp; s < sl.ns; s += SR_WARPS) {
+            float z[E];
+            sl.get(s, lane, z);
+            uint64_t q = quick_fixed(sc, lo, z, E - 1);
+            if (sub) {
+                q = warp_sum64(q);
+                if (lane == 0)
+                    sub[s] = q;
+                else
+                    q = 0;
+            }
+            own += q;
+        }
+        const uint64_t(*a)[4] = exchange(block_sum(own), 0, 0, 0);
+        uint64_t t = 0;
+        for (uint32_t c = 0; c < cl; ++c)
+            t += a[c][0];
+        if (all)
+            *all = a;
+        return t;
+    }
+    DDT_DEVINL static uint64_t quick_fixed(const Scale &sc, float lo, const float *z, int last)
+    {
+        uint64_t w = 0;
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+            w = f2add(w, quick_weights<EXACT>(sc, z[e], z[e + 1], e <= last && z[e] >= lo, e + 1 <= last && z[e + 1] >= lo));
+        float a, b;
+        f2unpack(w, a, b);
+        return __float2ull_rn((a + b) * 17592186044416.0f);
+    }
+    struct QuickWeight {  // adds these up
+        Scale sc;
+        float lo;
+        DDT_DEVINL uint64_t sum_to(const float *z, int, int last) const { return quick_fixed(sc, lo, z, last); }
+        DDT_DEVINL uint64_t lane_sum(const float *z, int) const { return quick_fixed(sc, lo, z, E - 1); }
+    };
+
     // ---- histogram of values from vhi down, and the first bin at which the tokens so far
     // reach `want` (-1: never). Bins are even in value: (vhi - z) * scale, cut off.
     DDT_DEVINL static int bin_of(float vhi, float scale, float z) { return min(SR_BINS - 1, (int)((vhi - z) * scale)); }
@@ -679,12 +752,14 @@ struct Row {
     }
 
     // ---- collect the tokens that `in` names in the first CTA (in any order); returns how
-    // many there are, which may be more than the list holds. At most four a row.
+    // many there are, which may be more than the list holds. At most four a row. (The number
+    // comes by an exchange: the first CTA may be done, and gone, right after it.)
     template <typename In>
     DDT_DEVINL uint32_t collect(In in)
     {
         const uint32_t cnt = cl_map(&sh->count[nth], 0), list = cl_map(&sh->list[0], 0);
         nth = (nth + 1) & 3;
+        uint32_t own = 0;
         for (int s = warp; s < sl.ns; s += SR_WARPS) {
             float z[E];
             sl.get(s, lane, z);
@@ -695,6 +770,7 @@ struct Row {
             for (int e = 0; e < E; ++e)
                 n += k[e] = in(z[e], i0 + e);
             if (n > 0) {
+                own += n;
                 uint32_t p = cl_add32(cnt, n);
 #pragma unroll
                 for (int e = 0; e < E; ++e)
@@ -705,8 +781,11 @@ struct Row {
                     }
             }
         }
-        cl_sync();
-        return cl_ld32(cnt);
+        const uint64_t(*all)[4] = exchange(block_sum(own), 0, 0, 0);
+        uint32_t n = 0;
+        for (uint32_t c = 0; c < cl; ++c)
+            n += (uint32_t)all[c][0];
+        return n;
     }
 
     // the first CTA: its list's n candidates in descending order (value, then lower index)
@@ -732,34 +811,76 @@ struct Row {
             }
     }
 
-    // ---- the border among sorted candidates. They follow tokens of weight `above` in the
-    // order; at most n2 of the n count. want: what the sum has to reach (0: none asked for,
-    // the n2-th is the last). Known to all CTAs afterwards.
+    // ---- the border among the collected candidates (the first CTA), and the draw. They are
+    // all tokens from some value up. At most `limit` of them count; p < 1: the fewest that
+    // reach p of `base` (0: of the sum of those that count), within `slack` of which no
+    // border may lie.
     struct Cut {
         Border b;
         uint64_t mass;  // of all that is kept
-        bool ok;        // the candidates reach `want`
+        bool ok;        // the border was found
     };
-    DDT_DEVINL Cut tell(float z, int last, uint64_t mass, bool ok)
+    // up to SR_SMALL of them, a thread each: its place in the order and what comes before it
+    // by looking at all. u >= 0: the token drawn, in one thread (-1 elsewhere)
+    DDT_DEVINL Cut small_list(const Scale &sc, int n, int limit, float p, uint64_t base, uint64_t slack, float u, int &token)
     {
-        const uint64_t(*a)[4] = exchange(((uint64_t)__float_as_uint(z) << 32) | (uint32_t)last, mass, ok, 0);
+        token = -1;
+        const uint64_t key = tid < n ? sh->list[tid] : 0;
+        const float z = key_value((uint32_t)(key >> 32));
+        const uint64_t w = tid < n ? weight_of<EXACT>(sc, sh->tab, z) : 0;
+        sh->kept[tid] = w;
+        if (tid == 0)
+            sh->found[0] = 0;
+        __syncthreads();
+        int place = 0;
+        uint64_t before = 0;
+        for (int j = 0; j < n; ++j) {
+            const bool b = sh->list[j] > key;
+            place += b;
+            before += b ? sh->kept[j] : 0;
+        }
+        bool in = tid < n && place < limit;
+        bool ok = true;
+        if (p < 1.f) {
+            const uint64_t own = block_sum(in ? w : 0), want = max(share_of(p, base ? base : own), (uint64_t)1);
+            const uint64_t gap = base ? slack : 0;
+            // reached, and by no doubtful step
+            ok = !base || own >= want + gap;
+            const bool doubt = in && gap > 0 && ((before < want + gap && want < before + gap) ||
+                                                 (before + w < want + gap && want < before + w + gap));
+            ok = ok && !__syncthreads_or(doubt);
+            in = in && before < want;
+        }
+        const int m = __syncthreads_count(in);
+        if (in && place == m - 1) {
+            sh->found[0] = tid;
+            sh->warp[0][3] = before + w;
+        }
+        sh->kept[tid] = in ? w : 0;
+        __syncthreads();
         Cut c;
-        c.b.z = __uint_as_float((uint32_t)(a[0][0] >> 32));
-        c.b.last = (int)(uint32_t)a[0][0];
-        c.mass = a[0][1];
-        c.ok = a[0][2] != 0;
+        const uint64_t last = sh->list[sh->found[0]];
+        c.b.z = key_value((uint32_t)(last >> 32));
+        c.b.last = (int)~(uint32_t)last;
+        c.mass = sh->warp[0][3];
+        c.ok = ok;
+        if (u >= 0.f && ok) {
+            const uint64_t target = draw_target(u, c.mass);
+            uint64_t sum = 0;  // of the kept tokens of lower index
+            for (int j = 0; j < n; ++j)
+                sum += (uint32_t)sh->list[j] > (uint32_t)key ? sh->kept[j] : 0;
+            if (in && sum <= target && target < sum + w)
+                token = (int)~(uint32_t)key;
+        }
         return c;
     }
-    // limit: the tokens among the candidates that may be kept (k, or what the k-border left);
-    // p < 1: of `base` (0: of the limited candidates' own sum); whole: the candidates are all
-    // that could be kept, so rounding in `base` does not make them too few
-    DDT_DEVINL Cut cut_list(const Scale &sc, int n, int limit, float p, uint64_t base, uint64_t above, uint64_t want,
-                            bool whole)
+    // any number that the list holds, sorted; what is above them weighs `above`, the sum has
+    // to reach `want` (0: `limit` is the border). Known to all CTAs afterwards
+    DDT_DEVINL Cut cut_list(const Scale &sc, int n, int limit, uint64_t above, uint64_t want)
     {
         float z = 0.f;
         int last = 0;
         uint64_t mass = 0;
-        bool ok = true;
         if (rank == 0) {
             sort_list(n);
             const int n2 = min(n, limit), r0 = 2 * tid;
@@ -769,34 +890,28 @@ struct Row {
             if (r0 + 1 < n2)
                 w1 = weight_of<EXACT>(sc, sh->tab, key_value((uint32_t)(sh->list[r0 + 1] >> 32)));
             const uint64_t incl = above + block_incl(w0 + w1);
-            uint64_t total = above;
-            {
-                __syncthreads();
-                if (tid == SR_THREADS - 1)
-                    sh->warp[0][1] = incl;
-                __syncthreads();
-                total = sh->warp[0][1];
-            }
             int first = n2 - 1;
-            if (p < 1.f) {
-                if (want == 0)
-                    want = share_of(p, base ? base : total);
-                const int c = r0 < n2 && incl - w1 >= want ? r0 : r0 + 1 < n2 && incl >= want ? r0 + 1 : 0x7FFFFFFF;
-                first = block_least(c);
-                if (first == 0x7FFFFFFF) {
-                    ok = whole;
+            if (want > 0) {
+                first = block_least(r0 < n2 && incl - w1 >= want ? r0 : r0 + 1 < n2 && incl >= want ? r0 + 1 : 0x7FFFFFFF);
+                if (first == 0x7FFFFFFF)  // (rounding in `want`)
                     first = n2 - 1;
-                }
             }
             const uint64_t key = sh->list[first];
             z = key_value((uint32_t)(key >> 32));
             last = (int)~(uint32_t)key;
+            __syncthreads();
             if (tid == (first >> 1))
                 sh->warp[0][2] = first & 1 ? incl : incl - w1;
             __syncthreads();
             mass = sh->warp[0][2];
         }
-        return tell(z, last, mass, ok);
+        const uint64_t(*a)[4] = exchange(((uint64_t)__float_as_uint(z) << 32) | (uint32_t)last, mass, 0, 0);
+        Cut c;
+        c.b.z = __uint_as_float((uint32_t)(a[0][0] >> 32));
+        c.b.last = (int)(uint32_t)a[0][0];
+        c.mass = a[0][1];
+        c.ok = true;
+        return c;
     }
     DDT_DEVINL static uint64_t share_of(float p, uint64_t mass) { return fraction_of(p, mass, true); }
 
@@ -805,7 +920,7 @@ struct Row {
     // these are too few, from all tokens
     DDT_DEVINL float probe(const Top &t, float lo, uint32_t need)
     {
-        const float vlo = fmaxf(t.least, lo), scale = bin_scale(t.zmax, vlo);
+        const float vlo = fmaxf(t.low, lo), scale = bin_scale(t.zmax, vlo);
         clear_hist();
         if ((int64_t)sl.V >= (int64_t)4 * need * E && cl * SR_THREADS >= 4 * need) {
             if (t.own >= vlo)
@@ -832,16 +947,16 @@ struct Row {
     }
 
     // members of an interval of values: how many, the least and the greatest, and the weight
-    // of the tokens that come before them
+    // of the tokens that come before them (and, ALL, of all that a border keeps)
     struct Members {
         uint32_t n;
         float lo, hi;
-        uint64_t before;
+        uint64_t before, all;
     };
-    template <typename Before, typename In>
-    DDT_DEVINL Members members(const Scale &sc, Before before, In in)
+    template <bool ALL, typename Before, typename In>
+    DDT_DEVINL Members members(const Scale &sc, const Border &keep, Before before, In in)
     {
-        uint64_t w = 0;
+        uint64_t w = 0, all = 0;
         uint32_t n = 0;
         float lo = SR_MAX_FLOAT, hi = -SR_MAX_FLOAT;
         for (int s = warp; s < sl.ns; s += SR_WARPS) {
@@ -858,15 +973,24 @@ struct Row {
                     hi = fmaxf(hi, z[e]);
                 }
             }
-            if (some) {
+            if (__any_sync(0xFFFFFFFFu, some)) {
                 Sum2 sum = {0, 0};
 #pragma unroll
                 for (int e = 0; e < E; e += 2)
                     add_weights<EXACT>(sc, sh->tab, z[e], z[e + 1], k[e], k[e + 1], sum);
                 w += to_fixed(sum);
             }
+            if (ALL) {
+                Sum2 sum = {0, 0};
+#pragma unroll
+                for (int e = 0; e < E; e += 2)
+                    add_weights<EXACT>(sc, sh->tab, z[e], z[e + 1], !k[e] && kept(keep, z[e], i0 + e),
+                                       !k[e + 1] && kept(keep, z[e + 1], i0 + e + 1), sum);
+                all += to_fixed(sum);
+            }
         }
         w = warp_sum64(w);
+        all = warp_sum64(all) + w;
         n = __reduce_add_sync(0xFFFFFFFFu, n);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
@@ -878,27 +1002,30 @@ struct Row {
             sh->warp[warp][0] = w;
             sh->warp[warp][1] = n;
             sh->warp[warp][2] = ((uint64_t)__float_as_uint(hi) << 32) | __float_as_uint(lo);
+            sh->warp[warp][3] = all;
         }
         __syncthreads();
         auto sum = [&](const uint64_t(*a)[4], uint32_t count) {
-            Members m = {0, SR_MAX_FLOAT, -SR_MAX_FLOAT, 0};
+            Members m = {0, SR_MAX_FLOAT, -SR_MAX_FLOAT, 0, 0};
             for (uint32_t c = 0; c < count; ++c) {
                 m.before += a[c][0];
                 m.n += (uint32_t)a[c][1];
                 m.lo = fminf(m.lo, __uint_as_float((uint32_t)a[c][2]));
                 m.hi = fmaxf(m.hi, __uint_as_float((uint32_t)(a[c][2] >> 32)));
+                m.all += a[c][3];
             }
             return m;
         };
         const Members m = sum(sh->warp, SR_WARPS);
-        return sum(exchange(m.before, m.n, ((uint64_t)__float_as_uint(m.hi) << 32) | __float_as_uint(m.lo), 0), cl);
+        return sum(exchange(m.before, m.n, ((uint64_t)__float_as_uint(m.hi) << 32) | __float_as_uint(m.lo), m.all), cl);
     }
 
     // ---- the CTA whose part holds `target` (the running sum first exceeds it there) finds
     // the token. sub: the sub-chunks' sums; all: the CTAs'. F gives a lane's sum and the sum
     // up to an element. Returns the index in one thread of one CTA, -1 elsewhere.
     template <typename F>
-    DDT_DEVINL int locate(const uint64_t *sub, const uint64_t (*all)[4], uint64_t target, F f)
+    DDT_DEVINL int locate(const uint64_t *sub, const uint64_t (*all)[4], uint64_t target, F f, uint64_t *from = nullptr,
+                          uint64_t *to_ = nullptr)
     {
         uint64_t before = 0;
         for (uint32_t c = 0; c < rank; ++c)
@@ -933,8 +1060,14 @@ struct Row {
         for (int e = 0; e < E; ++e)
             z[e] = __shfl_sync(0xFFFFFFFFu, z[e], who);
         const int i0 = sl.index0(s, who), e = lane & (E - 1);
-        const uint32_t over = __ballot_sync(0xFFFFFFFFu, target < at + f.sum_to(z, i0, e));
+        const uint64_t sum_e = at + f.sum_to(z, i0, e);
+        const uint32_t over = __ballot_sync(0xFFFFFFFFu, target < sum_e);
         const int pick = __ffs(over) - 1;
+        if (from) {  // the running sum ahead of the token and with it
+            const uint64_t ahead = __shfl_up_sync(0xFFFFFFFFu, sum_e, 1);
+            *from = lane > 0 ? ahead : at;
+            *to_ = sum_e;
+        }
         return lane == pick ? i0 + pick : -1;
     }
 
@@ -998,7 +1131,7 @@ struct Row {
     // smaller intervals, until their tokens fit the list or have one value
     DDT_DEVINL Border count_border(const Top &t, const Scale &sc, float lo, int64_t k, uint64_t *sub)
     {
-        float vhi = t.zmax, vlo = lo;
+        float vhi = t.zmax, vlo = fmaxf(lo, t.low);
         uint64_t before = 0;
         for (int it = 0; it < 64; ++it) {
             const float scale = bin_scale(vhi, vlo);
@@ -1029,9 +1162,9 @@ struct Row {
             auto in = [=](float z, int) { return z >= vlo && z <= vhi && bin_of(vhi, scale, z) == b; };
             if (n <= SR_CAP) {
                 collect(in);
-                return cut_list(sc, (int)n, (int)(want - before), 1.f, 0, 0, 0, true).b;
+                return cut_list(sc, (int)n, (int)(want - before), 0, 0).b;
             }
-            const Members m = members(sc, [](float, int) { return false; }, in);
+            const Members m = members<false>(sc, Border{0.f, 0}, [](float, int) { return false; }, in);
             if (m.lo == m.hi) {
                 Border r = {m.lo, 0x7FFFFFFF};
                 if (want - before < n)
@@ -1044,12 +1177,13 @@ struct Row {
         return Border{lo, 0x7FFFFFFF};
     }
 
-    // ---- the border of the front part of what b keeps whose weights first reach `want`, by
-    // bounds of the bins' weights (tokens times the bin's ends)
-    DDT_DEVINL Cut mass_border(const Top &t, const Scale &sc, const Border &b, uint64_t want, uint64_t *sub)
+    // ---- the border of the front part of what b keeps whose weights first reach p of their
+    // sum, by bounds of the bins' weights (tokens times the bin's ends). about: that sum by
+    // quick weights; the first look at all tokens' weights makes it exact
+    DDT_DEVINL Cut mass_border(const Top &t, const Scale &sc, const Border &b, float p, uint64_t about, uint64_t *sub)
     {
-        float vhi = t.zmax, vlo = b.z;
-        uint64_t above = 0;
+        float vhi = t.zmax, vlo = fmaxf(b.z, t.low);
+        uint64_t above = 0, least = share_of(p, about - quick_slack(about)), most = share_of(p, about + quick_slack(about));
         for (int it = 0; it < 64; ++it) {
             const float scale = bin_scale(vhi, vlo);
             clear_hist();
@@ -1076,9 +1210,9 @@ struct Row {
                 low[x] = __float2ull_rd((float)n[x] * (ex2(lo * sc.ch) * 0.9999847f) * 17592186044416.0f);
             }
             const uint64_t iu = above + block_incl(up[0] + up[1]);
-            int first = block_least(iu - up[1] >= want ? 2 * tid : iu >= want ? 2 * tid + 1 : 0x7FFFFFFF);
+            int first = block_least(iu - up[1] >= least ? 2 * tid : iu >= least ? 2 * tid + 1 : 0x7FFFFFFF);
             const uint64_t il = above + block_incl(low[0] + low[1]);
-            int final_ = block_least(il - low[1] >= want ? 2 * tid : il >= want ? 2 * tid + 1 : 0x7FFFFFFF);
+            int final_ = block_least(il - low[1] >= most ? 2 * tid : il >= most ? 2 * tid + 1 : 0x7FFFFFFF);
             first = min(first, SR_BINS - 1);
             final_ = min(final_, SR_BINS - 1);
             auto front = [=](float z, int i) { return z >= vlo && z <= vhi && bin_of(vhi, scale, z) < first && kept(b, z, i); };
@@ -1088,17 +1222,23 @@ struct Row {
                 const int x = bin_of(vhi, scale, z);
                 return x >= first && x <= final_;
             };
-            const Members m = members(sc, front, in);
+            Members m;
+            if (it == 0) {
+                m = members<true>(sc, b, front, in);
+                least = most = max(share_of(p, m.all), (uint64_t)1);
+            } else {
+                m = members<false>(sc, b, front, in);
+            }
             above += m.before;
-            if (m.n == 0)  // (rounding: nothing beyond the tokens before is needed)
-                return Cut{{m.hi, 0x7FFFFFFF}, above, false};
+            if (m.n == 0)  // (not so: the bounds hold)
+                break;
             if (m.n <= SR_CAP) {
                 collect(in);
-                return cut_list(sc, (int)m.n, (int)m.n, 0.5f, 0, above, max(want, (uint64_t)1), true);
+                return cut_list(sc, (int)m.n, (int)m.n, above, least);
             }
             if (m.lo == m.hi) {
                 const uint64_t w = weight_of<EXACT>(sc, sh->tab, m.lo);
-                uint64_t c = want > above && w > 0 ? (want - above + w - 1) / w : 1;
+                uint64_t c = least > above && w > 0 ? (least - above + w - 1) / w : 1;
                 c = min(c, (uint64_t)m.n);
                 Border r = {m.lo, m.lo == b.z ? b.last : 0x7FFFFFFF};
                 if (c < m.n)
@@ -1111,36 +1251,103 @@ struct Row {
         return Cut{b, 0, false};
     }
 
-    // ---- the border of everything that the settings keep. mass: the kept tokens' weights
-    // (0 if they have not been added up yet). k: 0 or at least V means off; p >= 1 off
-    DDT_DEVINL Cut border(const Top &t, const Scale &sc, int k, float p, float min_z, uint64_t *sub)
+    // ---- What the settings keep, and (u >= 0) the token drawn: in one thread of the cluster
+    // token >= 0, and that thread's mass. u < 0: the border and the mass, in the first CTA.
+    // COUNTS: false is returned where counting values serves better (nothing has been found,
+    // and this CTA's part of the row may be overwritten).
+    struct Found {
+        Border b;
+        uint64_t mass;
+        int token;
+    };
+    template <bool COUNTS>
+    DDT_DEVINL bool solve(const Top &t, const Scale &sc, const Settings &set, float min_z, float u, uint64_t *sub, Found &r)
     {
-        const float lo = fmaxf(min_z, sc.zfloor);
-        const Border all = {lo, 0x7FFFFFFF};
-        if (k <= 0 || k >= sl.V)
-            k = 0;
-        if (k == 0 && !(p < 1.f))
-            return Cut{all, 0, true};
+        const float lo = fmaxf(min_z, sc.zfloor), p = set.p;
+        const int k = set.k <= 0 || set.k >= sl.V ? 0 : set.k;
+        Border b = {lo, 0x7FFFFFFF};
+        r.token = -1;
+        r.mass = 0;
         if (k > 0 && k <= SR_PROBE) {
             const float tau = probe(t, lo, k);
             const uint32_t n = collect([=](float z, int) { return z >= tau; });
-            if (n <= SR_CAP)
-                return cut_list(sc, (int)n, k, p, 0, 0, 0, true);
-        }
-        const Border b = k > 0 ? count_border(t, sc, lo, k, sub) : all;
-        if (!(p < 1.f))
-            return Cut{b, 0, true};
-        const uint64_t base = mass(sc, b, nullptr, nullptr);
-        if (k == 0 || k > SR_PROBE) {
-            const float tau = probe(t, b.z, SR_PROBE);
-            const uint32_t n = collect([=](float z, int i) { return z >= tau && kept(b, z, i); });
-            if (n <= SR_CAP) {
-                const Cut c = cut_list(sc, (int)n, (int)n, p, base, 0, 0, tau <= b.z);
-                if (c.ok)
-                    return c;
+            if (n <= SR_SMALL) {
+                if (rank == 0) {
+                    const Cut c = small_list(sc, (int)n, k, p, 0, 0, u, r.token);
+                    r.b = c.b;
+                    r.mass = c.mass;
+                }
+                return true;
             }
+            if (n <= SR_CAP && !(p < 1.f)) {
+                const Cut c = cut_list(sc, (int)n, k, 0, 0);
+                b = c.b;
+                r.mass = c.mass;
+            } else {
+                if (COUNTS)
+                    return false;
+                b = count_border(t, sc, lo, k, sub);
+            }
+        } else if (k > 0) {
+            if (COUNTS)
+                return false;
+            b = count_border(t, sc, lo, k, sub);
         }
-        return mass_border(t, sc, b, share_of(p, base), sub);
+        if (p < 1.f) {
+            const bool whole = b.last == 0x7FFFFFFF && b.z == lo;
+            const uint64_t about = whole ? quick_mass(sc, lo, nullptr, nullptr) : mass(sc, b, nullptr, nullptr);
+            const float tau = probe(t, b.z, SR_PROBE / 2);
+            const uint32_t n = collect([=](float z, int i) { return z >= tau && kept(b, z, i); });
+            if (n <= SR_SMALL) {
+                // (all that is kept: its own sum is exact)
+                Cut c = {};
+                if (rank == 0) {
+                    c = small_list(sc, (int)n, (int)n, p, tau <= b.z ? 0 : about, whole ? quick_slack(about) : 0, u, r.token);
+                    r.b = c.b;
+                    r.mass = c.mass;
+                }
+                if (exchange(c.ok, 0, 0, 0)[0][0])
+                    return true;
+                r.token = -1;
+            }
+            if (COUNTS)
+                return false;
+            const Cut c = mass_border(t, sc, b, p, about, sub);
+            b = c.b;
+            r.mass = c.mass;
+        }
+        r.b = b;
+        if (u < 0.f) {
+            if (r.mass == 0)
+                r.mass = mass(sc, b, nullptr, nullptr);
+            return true;
+        }
+        const uint64_t(*all)[4];
+        if (b.last == 0x7FFFFFFF && !(p < 1.f)) {
+            // by quick weights; they stand unless the token's ends lie within their error
+            const QuickWeight f = {sc, b.z};
+            r.mass = quick_mass(sc, b.z, sub, &all);
+            const uint64_t target = draw_target(u, r.mass), slack = 2 * quick_slack(r.mass);
+            uint64_t from = 0, to = 0;
+            r.token = locate(sub, all, target, f, &from, &to);
+            __syncthreads();
+            if (tid == 0)
+                sh->found[1] = 0;
+            __syncthreads();
+            if (r.token >= 0)
+                sh->found[1] = (from == 0 || target - from >= slack) && (to == r.mass || to - target > slack);
+            __syncthreads();
+            const uint64_t(*sure)[4] = exchange(sh->found[1], 0, 0, 0);
+            uint64_t any = 0;
+            for (uint32_t c = 0; c < cl; ++c)
+                any |= sure[c][0];
+            if (any)
+                return true;
+        }
+        r.mass = mass(sc, b, sub, &all);
+        const Weight w = {sc, b, sh->tab};
+        r.token = locate(sub, all, draw_target(u, r.mass), w);
+        return true;
     }
 
     struct Weight {  // adds up the kept tokens' weights
@@ -1160,34 +1367,6 @@ struct Row {
     };
 };
 
-// floor(u mass), within the running sums: the draw's token is the first whose sum exceeds it
-DDT_DEVINL uint64_t draw_target(float u, uint64_t mass)
-{
-    return u < 1.f ? min(u > 0.f ? fraction_of(u, mass, false) : 0, mass - 1) : u == u ? mass - 1 : 0;
-}
-
-// the settings of a row. k = 1 and T = 1 stand for T = 0 (the largest logit, the lowest
-// index of it)
-struct Settings {
-    float T, p, m;
-    int k;
-    bool good;
-};
-DDT_DEVINL Settings load_settings(const ddt_filter &f, int i)
-{
-    Settings s;
-    s.T = f.temperature ? __ldg(f.temperature + i) : 1.f;
-    s.k = f.top_k ? __ldg(f.top_k + i) : 0;
-    s.p = f.top_p ? __ldg(f.top_p + i) : 1.f;
-    s.m = f.min_p ? __ldg(f.min_p + i) : 0.f;
-    s.good = s.T >= 0.f && s.T <= SR_MAX_FLOAT && s.p >= 0.f && s.p <= 1.f && s.m >= 0.f && s.m <= 1.f;
-    if (s.T == 0.f) {
-        s.T = 1.f;
-        s.k = 1;
-    }
-    s.T = fmaxf(s.T, SR_TINY);
-    return s;
-}
 // T ln m as a pair of floats (one thread: fp64)
 DDT_DEVINL float2 min_offset(const Settings &s)
 {

@@ -9,7 +9,10 @@ log-probability is a difference of two fp32 numbers, each rounded a few times:
 of two roundings, and the difference's own: together below 8 * 2^-24 of the
 larger of the two. Beside that the sum itself, which is 1 or more, is off by 2^-40 of
 itself and by 2^-44 for each 16 bytes of a row (a rounding to units of 2^-44), and so its
-logarithm by as much: of a sum next to 1, whose logarithm is next to 0, this is what counts."""
+logarithm by as much: of a sum next to 1, whose logarithm is next to 0, this is what counts.
+Where no top-k and no top-p apply, the sum may be one of the hardware's 2^x, off by 2^-20 of
+itself: 2^-22 for a weight, 2^-24 each for three roundings of it and 4 * 2^-24 for a sum of
+eight, in all 13 * 2^-24 (the draw is made anew with exact sums where that could decide it)."""
 import numpy as np
 import pytest
 import torch
@@ -76,7 +79,8 @@ def check(logits, u, s=None, status=0, **kw):
             assert lp[i] == wlp[i] or abs(lp[i] - wlp[i]) <= 8 * 2.0 ** -24 * abs(wlp[i]) + 2.0 ** -40
             continue
         big = abs((np.nanmax(z[i]) - z[i][t]) / T[i])
-        of_sum = 2.0 ** -40 + len(z[i]) / 4 * 2.0 ** -44
+        quick = s is None or (not 0 < s[1][i] < len(z[i]) and s[2][i] >= 1)
+        of_sum = 2.0 ** -40 + len(z[i]) / 4 * 2.0 ** -44 + quick * 2.0 ** -20
         assert abs(lp[i] - wlp[i]) <= 8 * 2.0 ** -24 * max(big, abs(wlp[i]) + big) + of_sum
     return tok
 
