@@ -35,6 +35,7 @@ constexpr int SR_MAX_CL = 16;     // CTAs of a cluster
 constexpr int SR_CAP = 512;       // candidates that are sorted in one place
 constexpr int SR_PROBE = 256;     // how many the first collection asks for, and the largest k that it serves
 constexpr int SR_BINS = 512;      // (two a thread)
+constexpr int SR_FLAT = 8;        // rows that weigh more than so many of their largest tokens are flat
 constexpr int SR_SMALL = 256;     // candidates of which each has a thread
 constexpr int SR_ONE = 44;        // a weight of 1 is 2^44
 constexpr float SR_MAX_FLOAT = 3.402823466e38f;
@@ -76,11 +77,11 @@ DDT_DEVINL uint32_t cl_ld32(uint32_t at)
     asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at));  // (stays between the barriers around it)
     return v;
 }
-DDT_DEVINL uint32_t cl_add32(uint32_t at, uint32_t v)
+DDT_DEVINL uint64_t cl_ld64(uint32_t at)
 {
-    uint32_t r;
-    asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(r) : "r"(at), "r"(v) : "memory");
-    return r;
+    uint64_t v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(at));
+    return v;
 }
 DDT_DEVINL void cp16(uint32_t dst, const void *src)
 {
@@ -327,18 +328,46 @@ struct RowShared {
     Xchg x;
     uint64_t warp[SR_WARPS][4];
     uint64_t list[SR_CAP];   // candidates: (order_key << 32) | ~index
+    uint64_t mine[SR_CAP];   //   of this CTA's slice
     uint32_t hist[SR_BINS];
-    uint32_t count[4];       // candidates collected (the first CTA's; a place for each collection)
+    uint32_t count;          //   how many
     int found[4];
     float2 off;              // T ln(min_p)
     uint64_t kept[SR_SMALL]; // the candidates' weights
 };
 
+// 16 bytes of logits. Range: their largest, and their least but for -infinity; look() says
+// whether there are odd ones among them: NaN, or not 0 and next to 0 (SR_TINY)
 template <typename T> struct Vec;
 template <> struct Vec<uint16_t> {
     static constexpr int E = 8;
     static constexpr bool EXACT = false;
     static constexpr uint32_t NONE = 0xFF80FF80u;
+    struct Range {
+        uint32_t hi, lo;
+    };
+    DDT_DEVINL static void begin(Range &r) { r = {NONE, 0x7F7F7F7Fu}; }
+    DDT_DEVINL static bool look(Range &r, const uint4 &v)
+    {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            asm("max.bf16x2 %0, %0, %1;" : "+r"(r.hi) : "r"(w[i]));
+            uint32_t x;  // (x 0 + x: an infinity becomes NaN, which the least is not)
+            asm("fma.rn.bf16x2 %0, %1, %2, %1;" : "=r"(x) : "r"(w[i]), "r"(0u));
+            asm("min.bf16x2 %0, %0, %1;" : "+r"(r.lo) : "r"(x));
+            const uint32_t a = w[i] & 0x7FFFu, b = (w[i] >> 16) & 0x7FFFu;
+            // bits of an odd value: 1 .. 2^-90's less 1, or above infinity's
+            bad |= a - 1 < (37u << 7) - 1 || a > 0x7F80u || b - 1 < (37u << 7) - 1 || b > 0x7F80u;
+        }
+        return bad;
+    }
+    DDT_DEVINL static void end(const Range &r, float &hi, float &lo)
+    {
+        hi = fmaxf(bf16lo(r.hi), bf16hi(r.hi));
+        lo = fminf(bf16lo(r.lo), bf16hi(r.lo));
+    }
     DDT_DEVINL static void get(const uint4 &v, float *z)
     {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
@@ -353,6 +382,28 @@ template <> struct Vec<float> {
     static constexpr int E = 4;
     static constexpr bool EXACT = true;
     static constexpr uint32_t NONE = 0xFF800000u;
+    struct Range {
+        float hi, lo;
+    };
+    DDT_DEVINL static void begin(Range &r) { r = {DDT_NEG_INF, SR_MAX_FLOAT}; }
+    DDT_DEVINL static bool look(Range &r, const uint4 &v)
+    {
+        float z[E];
+        get(v, z);
+        bool bad = false;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            r.hi = fmaxf(r.hi, z[e]);
+            r.lo = fminf(r.lo, fmaf(z[e], 0.f, z[e]));  // (an infinity becomes NaN, which the least is not)
+            bad |= !(fabsf(z[e]) >= SR_TINY) && z[e] != 0.f;
+        }
+        return bad;
+    }
+    DDT_DEVINL static void end(const Range &r, float &hi, float &lo)
+    {
+        hi = r.hi;
+        lo = r.lo;
+    }
     DDT_DEVINL static void get(const uint4 &v, float *z)
     {
         z[0] = __uint_as_float(v.x);
@@ -459,7 +510,7 @@ struct Row {
     RowShared *sh;
     Slice<T> sl;
     int tid, lane, warp;
-    uint32_t rank, cl, turn, nth;
+    uint32_t rank, cl, turn;
 
     DDT_DEVINL void begin(RowShared *s)
     {
@@ -469,9 +520,7 @@ struct Row {
         warp = tid >> 5;
         rank = cl_rank();
         cl = cl_size();
-        turn = nth = 0;
-        if (tid < 4)
-            sh->count[tid] = 0;  // (a cluster barrier comes before the first collection)
+        turn = 0;
         cl_arrive();  // (ended by started(): a CTA's shared memory is there once it runs)
     }
     // before the first access to another CTA's shared memory
@@ -514,30 +563,22 @@ struct Row {
     };
     DDT_DEVINL Top top()
     {
-        float m = DDT_NEG_INF, lo = SR_MAX_FLOAT;
+        float m, lo;
         bool nan = false;
-        for (int s = warp; s < sl.ns; s += SR_WARPS) {
-            float z[E];
-            sl.get(s, lane, z);
-            bool bad = false;
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                bad |= !(fabsf(z[e]) >= SR_TINY) && z[e] != 0.f;
-                m = fmaxf(m, z[e]);  // (of a NaN and a number: the number)
-                lo = fminf(lo, z[e] == DDT_NEG_INF ? SR_MAX_FLOAT : z[e]);
-            }
+        typename Vec<T>::Range range;
+        Vec<T>::begin(range);
+        for (int s = warp; s < sl.ns; s += 2 * SR_WARPS) {
+            const bool two = s + SR_WARPS < sl.ns;
+            const uint4 x = sl.raw(s, lane), y = sl.raw(two ? s + SR_WARPS : s, lane);
+            bool bad = Vec<T>::look(range, x);
+            bad |= Vec<T>::look(range, y);
             if (bad) {  // from here on a NaN is -infinity, and what is next to 0 is 0
-                T *d = reinterpret_cast<T *>(sl.at + s * SR_SUB + lane * 16);
-#pragma unroll
-                for (int e = 0; e < E; ++e)
-                    if (z[e] != z[e]) {
-                        nan = true;
-                        d[e] = Slice<T>::none();
-                    } else if (fabsf(z[e]) < SR_TINY) {
-                        d[e] = (T)0;
-                    }
+                nan |= mend_vector(s);
+                if (two)
+                    nan |= mend_vector(s + SR_WARPS);
             }
         }
+        Vec<T>::end(range, m, lo);
         // (what lies next to 0 counts as 0, here too)
         m = fabsf(m) < SR_TINY ? 0.f : m;
         lo = fabsf(lo) < SR_TINY ? 0.f : lo;
@@ -571,6 +612,23 @@ struct Row {
         r.low = lo;
         r.nan = nan;
         return r;
+    }
+    // a lane's vector with odd values; whether it has a NaN
+    DDT_DEVINL bool mend_vector(int s)
+    {
+        T *d = reinterpret_cast<T *>(sl.at + s * SR_SUB + lane * 16);
+        float z[E];
+        sl.get(s, lane, z);
+        bool nan = false;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (z[e] != z[e]) {
+                nan = true;
+                d[e] = Slice<T>::none();
+            } else if (fabsf(z[e]) < SR_TINY) {
+                d[e] = (T)0;
+            }
+        return nan;
     }
     // a row with +infinity: those tokens have equal weights, the others none
     DDT_DEVINL void only_infinite(Top &t)
@@ -718,10 +776,18 @@ struct Row {
     DDT_DEVINL void row_bins(uint32_t &n0, uint32_t &n1)
     {
         n0 = n1 = 0;
-        for (uint32_t c = 0; c < cl; ++c) {
-            const uint32_t at = cl_map(&sh->hist[2 * tid], c);
-            n0 += cl_ld32(at);
-            n1 += cl_ld32(at + 4);
+        for (uint32_t b = 0; b < cl; b += 4) {  // (four at a time: the loads overlap)
+            uint32_t x[4], y[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const uint32_t at = cl_map(&sh->hist[2 * tid], min(b + c, cl - 1));
+                x[c] = cl_ld32(at);
+                y[c] = cl_ld32(at + 4);
+            }
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                if (b + c < cl)
+                    n0 += x[c], n1 += y[c];
         }
     }
     // inclusive running sum over the threads of one word each
@@ -752,14 +818,14 @@ struct Row {
     }
 
     // ---- collect the tokens that `in` names in the first CTA (in any order); returns how
-    // many there are, which may be more than the list holds. At most four a row. (The number
-    // comes by an exchange: the first CTA may be done, and gone, right after it.)
+    // many there are, which may be more than the list holds (then it holds none). Each CTA
+    // lists its own; the first one fetches them: the others may not leave before fetched().
     template <typename In>
     DDT_DEVINL uint32_t collect(In in)
     {
-        const uint32_t cnt = cl_map(&sh->count[nth], 0), list = cl_map(&sh->list[0], 0);
-        nth = (nth + 1) & 3;
-        uint32_t own = 0;
+        if (tid == 0)
+            sh->count = 0;
+        __syncthreads();
         for (int s = warp; s < sl.ns; s += SR_WARPS) {
             float z[E];
             sl.get(s, lane, z);
@@ -770,23 +836,37 @@ struct Row {
             for (int e = 0; e < E; ++e)
                 n += k[e] = in(z[e], i0 + e);
             if (n > 0) {
-                own += n;
-                uint32_t p = cl_add32(cnt, n);
+                uint32_t p = atomicAdd(&sh->count, n);
 #pragma unroll
                 for (int e = 0; e < E; ++e)
                     if (k[e]) {
                         if (p < SR_CAP)
-                            cl_st64(list + p * 8, ((uint64_t)order_key(z[e]) << 32) | (uint32_t)~(i0 + e));
+                            sh->mine[p] = ((uint64_t)order_key(z[e]) << 32) | (uint32_t)~(i0 + e);
                         ++p;
                     }
             }
         }
-        const uint64_t(*all)[4] = exchange(block_sum(own), 0, 0, 0);
+        __syncthreads();
+        const uint64_t(*all)[4] = exchange(sh->count, 0, 0, 0);
         uint32_t n = 0;
         for (uint32_t c = 0; c < cl; ++c)
             n += (uint32_t)all[c][0];
+        if (n <= SR_CAP) {
+            if (rank == 0) {
+                for (uint32_t i = tid; i < n; i += SR_THREADS) {
+                    uint32_t c = 0, j = i;
+                    while (j >= (uint32_t)all[c][0])
+                        j -= (uint32_t)all[c++][0];
+                    sh->list[i] = cl_ld64(cl_map(&sh->mine[j], c));
+                }
+                __syncthreads();
+            }
+            cl_arrive();
+        }
         return n;
     }
+    // (after a collection that the list holds, before anything else between CTAs)
+    DDT_DEVINL void fetched() { cl_wait(); }
 
     // the first CTA: its list's n candidates in descending order (value, then lower index)
     DDT_DEVINL void sort_list(int n)
@@ -1162,6 +1242,7 @@ struct Row {
             auto in = [=](float z, int) { return z >= vlo && z <= vhi && bin_of(vhi, scale, z) == b; };
             if (n <= SR_CAP) {
                 collect(in);
+                fetched();
                 return cut_list(sc, (int)n, (int)(want - before), 0, 0).b;
             }
             const Members m = members<false>(sc, Border{0.f, 0}, [](float, int) { return false; }, in);
@@ -1234,6 +1315,7 @@ struct Row {
                 break;
             if (m.n <= SR_CAP) {
                 collect(in);
+                fetched();
                 return cut_list(sc, (int)m.n, (int)m.n, above, least);
             }
             if (m.lo == m.hi) {
@@ -1277,8 +1359,11 @@ struct Row {
                     r.b = c.b;
                     r.mass = c.mass;
                 }
+                fetched();
                 return true;
             }
+            if (n <= SR_CAP)
+                fetched();
             if (n <= SR_CAP && !(p < 1.f)) {
                 const Cut c = cut_list(sc, (int)n, k, 0, 0);
                 b = c.b;
@@ -1296,8 +1381,14 @@ struct Row {
         if (p < 1.f) {
             const bool whole = b.last == 0x7FFFFFFF && b.z == lo;
             const uint64_t about = whole ? quick_mass(sc, lo, nullptr, nullptr) : mass(sc, b, nullptr, nullptr);
-            const float tau = probe(t, b.z, SR_PROBE / 2);
-            const uint32_t n = collect([=](float z, int i) { return z >= tau && kept(b, z, i); });
+            // (a share of which more tokens are needed than the list takes, as no token weighs
+            // more than 1, or very likely so, is not looked for there)
+            uint32_t n = SR_CAP + 1;
+            float tau = b.z;
+            if (about < (uint64_t)SR_FLAT << SR_ONE) {
+                tau = probe(t, b.z, SR_PROBE / 2);
+                n = collect([=](float z, int i) { return z >= tau && kept(b, z, i); });
+            }
             if (n <= SR_SMALL) {
                 // (all that is kept: its own sum is exact)
                 Cut c = {};
@@ -1306,9 +1397,12 @@ struct Row {
                     r.b = c.b;
                     r.mass = c.mass;
                 }
+                fetched();
                 if (exchange(c.ok, 0, 0, 0)[0][0])
                     return true;
                 r.token = -1;
+            } else if (n <= SR_CAP) {
+                fetched();
             }
             if (COUNTS)
                 return false;
