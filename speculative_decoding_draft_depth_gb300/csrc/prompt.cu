@@ -8,7 +8,7 @@ template <int D, bool KV4>
 cudaError_t launch_d(int dev, int grid, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const PtArgs &a,
                      cudaStream_t s)
 {
-    const cudaError_t e = launch_main<D, KV4, false>(dev, grid, tq, tk, tv, a, s);
+    const cudaError_t e = launch_main<D, KV4, PLAIN>(dev, grid, tq, tk, tv, a, s);
     return e != cudaSuccess || grid == 1 ? e : launch_merge<D>(a, grid, PP_ROWS, s);
 }
 

@@ -30,6 +30,8 @@ struct PtArgs {
     int ngroups;
     float4 *store_o[2];
     float2 *store_ml[2];
+    float *few_o;          // slots of own keys' cut items where a kernel of few rows has them
+    float2 *few_ml;
     long long debug_wait;  // > 0 (tests only): each CTA starts with a wait that runs out after this many cycles
 };
 
@@ -37,6 +39,13 @@ struct PtArgs {
 // rows, or 16
 cudaError_t launch_prompt_few(ddt_ctx *c, const PtArgs &a, const uint16_t *q, int64_t q_stride, int rows,
                               cudaStream_t s);
+// the own keys of few rows of each request, where prefixes are shared, as a programmatic
+// dependent of the prefixes' kernel: 4 bits (prompt_few.cu) and bf16 (prefix_few.cu).
+// *ctas: the CTAs that share the work
+cudaError_t launch_own_few_kvq(ddt_ctx *c, const PtArgs &a, const uint16_t *q, int64_t q_stride, int rows, int *ctas,
+                               cudaStream_t s);
+cudaError_t launch_own_few(ddt_ctx *c, const PtArgs &a, const uint16_t *q, int64_t q_stride, const uint16_t *k_cache,
+                           int rows, int *ctas, cudaStream_t s);
 
 namespace {
 
@@ -124,18 +133,20 @@ DDT_DEVINL PpReq load_group(const PtArgs &a, int g)
     return q;
 }
 
-// unit of work `r`: a request; with GROUPS the groups' prefixes, then the requests
-template <bool GROUPS>
-DDT_DEVINL int num_reqs(const PtArgs &a) { return GROUPS ? a.ngroups + a.R : a.R; }
+// What a launch works on, units r = 0 ..: requests; where prefixes are shared the groups'
+// prefixes, then the requests' own keys; or one of the two.
+enum Units { PLAIN, BOTH, PREFIXES, OWN };
+template <Units U>
+DDT_DEVINL int num_units(const PtArgs &a) { return U == BOTH ? a.ngroups + a.R : U == PREFIXES ? a.ngroups : a.R; }
 
 // sound: whether its lengths are (a unit that is not has no tokens)
-template <bool GROUPS = false>
+template <Units U = PLAIN>
 DDT_DEVINL PpReq load_req(const PtArgs &a, int r, bool *sound = nullptr)
 {
     PpReq q = {0, 0, 0, 0, 0};
-    int g0 = 0, g1 = a.T, least = 0;  // GROUPS: where a member's rows lie, and what is cached at least
-    if (GROUPS) {
-        if (r < a.ngroups) {
+    int g0 = 0, g1 = a.T, least = 0;  // where a group's member's rows lie, and what is cached at least
+    if (U != PLAIN) {
+        if (U == PREFIXES || (U == BOTH && r < a.ngroups)) {
             q = load_group(a, r);
             if (sound)
                 *sound = group_ok(a, r);
@@ -143,7 +154,8 @@ DDT_DEVINL PpReq load_req(const PtArgs &a, int r, bool *sound = nullptr)
                 q.len = 0;
             return q;
         }
-        r -= a.ngroups;
+        if (U == BOTH)
+            r -= a.ngroups;
         const int g = group_of(a, r);
         if (g >= 0) {
             const PpReq pre = load_group(a, g);
@@ -154,7 +166,7 @@ DDT_DEVINL PpReq load_req(const PtArgs &a, int r, bool *sound = nullptr)
         }
     }
     const int s0 = __ldg(&a.q_start[r]), s1 = __ldg(&a.q_start[r + 1]), c = __ldg(&a.ctx_lens[r]);
-    const bool ok = packed_ok(s0, s1, a.T, c, a.cap) && (!GROUPS || (c >= least && s0 >= g0 && s1 <= g1));
+    const bool ok = packed_ok(s0, s1, a.T, c, a.cap) && (U == PLAIN || (c >= least && s0 >= g0 && s1 <= g1));
     if (sound)
         *sound = ok;
     q.q0 = s0;
@@ -183,15 +195,15 @@ DDT_DEVINL bool page_ok(const PtArgs &a, int pg)
 // this CTA's share: the totals by a scan over the requests (whole block), then
 // the request that holds the share's first unit. found: [0] request, [1..2] its
 // first unit, [3..4] total
-template <bool GROUPS = false>
+template <Units U = PLAIN>
 DDT_DEVINL void find_share(const PtArgs &a, int tq, int grid, int cta, long long *sums,
                            volatile long long *found, int tid, int nthreads)
 {
-    const int count = num_reqs<GROUPS>(a), per = (count + nthreads - 1) / nthreads;
+    const int count = num_units<U>(a), per = (count + nthreads - 1) / nthreads;
     const int r0 = min(tid * per, count), r1 = min(r0 + per, count);
     long long mine = 0;
     for (int r = r0; r < r1; ++r)
-        mine += pp_units(load_req<GROUPS>(a, r), tq, a.Hkv);
+        mine += pp_units(load_req<U>(a, r), tq, a.Hkv);
     long long incl = mine;
     const int lane = tid & 31, warp = tid >> 5;
 #pragma unroll
@@ -220,7 +232,7 @@ DDT_DEVINL void find_share(const PtArgs &a, int tq, int grid, int cta, long long
         if (cta < nc && excl <= lo && lo < excl + mine) {
             long long acc = excl;
             for (int r = r0; r < r1; ++r) {
-                const long long u = pp_units(load_req<GROUPS>(a, r), tq, a.Hkv);
+                const long long u = pp_units(load_req<U>(a, r), tq, a.Hkv);
                 if (lo < acc + u) {
                     found[0] = r;
                     found[1] = acc;
@@ -235,7 +247,7 @@ DDT_DEVINL void find_share(const PtArgs &a, int tq, int grid, int cta, long long
 
 // the segments of a CTA's share, one behind the other (every thread that walks holds
 // the same state)
-template <bool GROUPS = false>
+template <Units U = PLAIN>
 struct ShareWalk {
     int r;
     long long base, cur, hi;  // the request's first unit; the walk's place and end
@@ -254,7 +266,7 @@ struct ShareWalk {
             const int nc = pp_ctas(total, grid, MIN_UNITS);
             cur = pp_share(total, c, nc);
             hi = pp_share(total, c + 1, nc);
-            rq = load_req<GROUPS>(a, r);
+            rq = load_req<U>(a, r);
             it = pp_find(rq, cur - base, tq, a.Hkv);
         }
     }
@@ -270,15 +282,15 @@ struct ShareWalk {
             s.h = it.h;
             s.row0 = rq.q0 + it.qt * tq;
             s.ntok = min(tq, rq.len - it.qt * tq);
-            s.flat = GROUPS && rq.flat > 0;
-            s.part = GROUPS && (rq.flat > 0 || rq.off > 0);
+            s.flat = U != PLAIN && rq.flat > 0;
+            s.part = U != PLAIN && (rq.flat > 0 || rq.off > 0);
             s.pos0 = s.flat ? rq.ctx - 1 : rq.ctx + it.qt * tq;
-            s.t0 = t0 + (GROUPS ? rq.off : 0);
-            s.t1 = t1 + (GROUPS ? rq.off : 0);
+            s.t0 = t0 + (U != PLAIN ? rq.off : 0);
+            s.t1 = t1 + (U != PLAIN ? rq.off : 0);
             s.whole = t0 == 0 && t1 == it.n;
             s.split = (s.ntok << a.g_shift) <= split_rows;
             s.slot = 2 * cta + (t0 > 0 ? 0 : 1);
-            const int sr = !GROUPS ? r : r < a.ngroups ? __ldg(&a.group_start[r]) : r - a.ngroups;
+            const int sr = U == PREFIXES || (U == BOTH && r < a.ngroups) ? __ldg(&a.group_start[r]) : U == BOTH ? r - a.ngroups : r;
             cur = min(hi, i1);
             if (cur < hi) {  // the item behind it
                 it.start += it.n + PP_ITEM;
@@ -289,11 +301,11 @@ struct ShareWalk {
                         it.start = 0;
                         it.qt = 0;
                         do {  // (units remain, so a request with tokens follows)
-                            if (++r >= num_reqs<GROUPS>(a)) {
+                            if (++r >= num_units<U>(a)) {
                                 cur = hi;  // (not so: lengths that changed under the call)
                                 break;
                             }
-                            rq = load_req<GROUPS>(a, r);
+                            rq = load_req<U>(a, r);
                         } while (rq.len == 0);
                     }
                     it.n = pp_tiles(rq, it.qt, tq);

@@ -172,7 +172,7 @@ DDT_DEVINL void read_block(const unsigned char *raw, Block<D> &b, int lane)
     }
 }
 
-template <int D, int NR>
+template <int D, int NR, Units U>
 __global__ void __launch_bounds__(FT, NR == 1 ? 2 : 1) prompt_few_kernel(const FewArgs f)
 {
     constexpr int ROWS = 8 * NR, KW = Block<D>::KW, KS = D / 16, CH = D / 8;  // CH: channels of a lane's V
@@ -187,15 +187,16 @@ __global__ void __launch_bounds__(FT, NR == 1 ? 2 : 1) prompt_few_kernel(const F
     const int tq = ROWS >> a.g_shift, G = 1 << a.g_shift;
     if (blockIdx.x == 0)
         for (int r = tid; r < a.R; r += FT) {
-            const int s0 = __ldg(&a.q_start[r]), s1 = __ldg(&a.q_start[r + 1]);
-            if (!packed_ok(s0, s1, a.T, __ldg(&a.ctx_lens[r]), a.cap))
+            bool sound;
+            load_req<U>(a, r, &sound);
+            if (!sound)
                 set_status(a.status, DDT_DEV_BAD_LENGTH);
         }
     pdl_trigger();  // (the merge stages itself; it waits for this grid before it reads)
-    find_share(a, tq, gridDim.x, blockIdx.x, s_sums, s_found, tid, FT);
+    find_share<U>(a, tq, gridDim.x, blockIdx.x, s_sums, s_found, tid, FT);
     Copier<D> copier;
     copier.begin(a, lane);
-    ShareWalk<> walk;
+    ShareWalk<U> walk;
     walk.begin(a, s_found, tq, gridDim.x, blockIdx.x);
     // this warp's blocks of a segment: the next one, their end, the page of the one FS
     // turns ahead; their copies begin while the segment before is merged
@@ -441,38 +442,60 @@ __global__ void __launch_bounds__(FT, NR == 1 ? 2 : 1) prompt_few_kernel(const F
                 r.z += v.z * k;
                 r.w += v.w * k;
             }
-            if (was.whole) {
+            if (was.whole && !was.part) {
                 const float inv = L > 0.f || L != L ? a.out_scale / L : 0.f;
                 uint32_t *dst = reinterpret_cast<uint32_t *>(
                     a.out + ((int64_t)(was.row0 + (row >> a.g_shift)) * a.Hq + (was.h << a.g_shift) + (row & (G - 1))) * D) + 2 * c4;
                 *reinterpret_cast<uint2 *>(dst) =
                     make_uint2(pack_bf16x2(r.x * inv, r.y * inv), pack_bf16x2(r.z * inv, r.w * inv));
-            } else {
-                reinterpret_cast<float4 *>(a.part_o + (int64_t)was.slot * ROWS * D)[c4 * ROWS + row] = r;
+            } else if (was.whole) {
+                const int64_t at = (((int64_t)was.h * a.T + was.row0) << a.g_shift) + row;
+                a.store_o[1][(int64_t)c4 * a.T * a.Hq + at] = r;
                 if (c4 == 0)
-                    a.part_ml[(int64_t)was.slot * ROWS + row] = make_float2(M, L);
+                    a.store_ml[1][at] = make_float2(M, L);
+            } else {
+                const int64_t slot = (int64_t)was.slot * ROWS;
+                reinterpret_cast<float4 *>((U == PLAIN ? a.part_o : a.few_o) + slot * D)[c4 * ROWS + row] = r;
+                if (c4 == 0)
+                    (U == PLAIN ? a.part_ml : a.few_ml)[slot + row] = make_float2(M, L);
             }
         }
         __syncthreads();
     }
     cp_async_wait_all();
+    if (U != PLAIN)
+        pdl_wait();  // (the prefixes' kernel is before this one; the merge waits for this one only)
 }
 
-template <int D, int NR>
-cudaError_t launch_few(const FewArgs &f, int dev, int num_sms, cudaStream_t s)
+template <int D, int NR, Units U>
+cudaError_t launch_few(const FewArgs &f, int dev, int num_sms, int *ctas, cudaStream_t s)
 {
     constexpr int ROWS = 8 * NR, BYTES = FW * (ROWS * (D * 4 + 8) + FS * RAW_BYTES<D>);
     static_assert(ROWS * 2 * 2 * PR_MAX_CTAS <= 2 * PR_MAX_CTAS * PR_ROWS, "partial slots");
     static DeviceFlags ready;
     cudaError_t e = cudaSuccess;
     if (!ready.test(dev)) {
-        e = cudaFuncSetAttribute(prompt_few_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
+        e = cudaFuncSetAttribute(prompt_few_kernel<D, NR, U>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
         if (e != cudaSuccess)
             return e;
         ready.set(dev);
     }
     const int grid = (num_sms < PR_MAX_CTAS ? num_sms : PR_MAX_CTAS) * (NR == 1 ? 2 : 1);
-    prompt_few_kernel<D, NR><<<grid, FT, BYTES, s>>>(f);
+    if (U != PLAIN) {  // (beside the prefixes' kernel, which reads and writes elsewhere)
+        *ctas = grid;
+        cudaLaunchConfig_t lc = {};
+        lc.gridDim = dim3(grid);
+        lc.blockDim = dim3(FT);
+        lc.dynamicSmemBytes = BYTES;
+        lc.stream = s;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[0].val.programmaticStreamSerializationAllowed = 1;
+        lc.attrs = at;
+        lc.numAttrs = 1;
+        return cudaLaunchKernelEx(&lc, prompt_few_kernel<D, NR, U>, f);
+    }
+    prompt_few_kernel<D, NR, U><<<grid, FT, BYTES, s>>>(f);
     e = cudaGetLastError();
     if (e != cudaSuccess || grid == 1)
         return e;
@@ -488,6 +511,22 @@ cudaError_t launch_prompt_few(ddt_ctx *c, const PtArgs &a, const uint16_t *q, in
     f.q = q;
     f.q_stride = q_stride;
     if (c->cfg.d == 128)
-        return rows <= 8 ? launch_few<128, 1>(f, c->device, c->num_sms, s) : launch_few<128, 2>(f, c->device, c->num_sms, s);
-    return rows <= 8 ? launch_few<64, 1>(f, c->device, c->num_sms, s) : launch_few<64, 2>(f, c->device, c->num_sms, s);
+        return rows <= 8 ? launch_few<128, 1, PLAIN>(f, c->device, c->num_sms, nullptr, s)
+                         : launch_few<128, 2, PLAIN>(f, c->device, c->num_sms, nullptr, s);
+    return rows <= 8 ? launch_few<64, 1, PLAIN>(f, c->device, c->num_sms, nullptr, s)
+                     : launch_few<64, 2, PLAIN>(f, c->device, c->num_sms, nullptr, s);
+}
+
+cudaError_t launch_own_few_kvq(ddt_ctx *c, const PtArgs &a, const uint16_t *q, int64_t q_stride, int rows, int *ctas,
+                               cudaStream_t s)
+{
+    FewArgs f;
+    f.a = a;
+    f.q = q;
+    f.q_stride = q_stride;
+    if (c->cfg.d == 128)
+        return rows <= 8 ? launch_few<128, 1, OWN>(f, c->device, c->num_sms, ctas, s)
+                         : launch_few<128, 2, OWN>(f, c->device, c->num_sms, ctas, s);
+    return rows <= 8 ? launch_few<64, 1, OWN>(f, c->device, c->num_sms, ctas, s)
+                     : launch_few<64, 2, OWN>(f, c->device, c->num_sms, ctas, s);
 }

@@ -356,11 +356,12 @@ DDT_DEVINL float halve_row(unsigned char *q, int row)
     return __uint_as_float((uint32_t)(127 + e) << 23);
 }
 
-template <int D, bool KV4, bool GROUPS>
+template <int D, bool KV4, Units U>
 __global__ void __launch_bounds__(NT<KV4>, 1)
 prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const PtArgs a)
 {
+    constexpr bool GROUPS = U != PLAIN;
     extern __shared__ unsigned char smem_raw[];
     const uint32_t raw = (uint32_t)__cvta_generic_to_shared(smem_raw);
     const uint32_t sb = (raw + 1023u) & ~1023u;
@@ -415,7 +416,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     }
     volatile long long *found = reinterpret_cast<volatile long long *>(sgen + SM_BAR<KV4> + B_FOUND);
     pdl_trigger();  // (the merge stages itself; it waits for this grid before it reads)
-    find_share<GROUPS>(a, tq, gridDim.x, blockIdx.x, reinterpret_cast<long long *>(sgen + SM_BAR<KV4> + B_ML), found, tid, NT<KV4>);
+    find_share<U>(a, tq, gridDim.x, blockIdx.x, reinterpret_cast<long long *>(sgen + SM_BAR<KV4> + B_ML), found, tid, NT<KV4>);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -444,13 +445,13 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     if (warp == W_WALK) {
         // ============================================================ share walk, Q and K loads
         if (blockIdx.x == 0)
-            for (int r = lane; r < num_reqs<GROUPS>(a); r += 32) {
+            for (int r = lane; r < num_units<U>(a); r += 32) {
                 bool sound;
-                load_req<GROUPS>(a, r, &sound);
+                load_req<U>(a, r, &sound);
                 if (!sound)
                     atomicOr(a.status, DDT_DEV_BAD_LENGTH);
             }
-        ShareWalk<GROUPS> walk;
+        ShareWalk<U> walk;
         walk.begin(a, found, tq, gridDim.x, blockIdx.x);
         int k = 0, kn = 0;
         bool ok = true;
@@ -1052,26 +1053,26 @@ bool make_map(CUtensorMap *m, const void *base, int d, int heads, int64_t rows, 
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, bool KV4, bool GROUPS>
+template <int D, bool KV4, Units U>
 cudaError_t launch_main(int dev, int grid, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const PtArgs &a,
                         cudaStream_t s)
 {
     static DeviceFlags ready;
     cudaError_t e = cudaSuccess;
     if (!ready.test(dev)) {
-        e = cudaFuncSetAttribute(prompt_tc_kernel<D, KV4, GROUPS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        e = cudaFuncSetAttribute(prompt_tc_kernel<D, KV4, U>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)SM_ALLOC<KV4>);
         // a block launched with fewer registers would wait forever for its split
         cudaFuncAttributes fa;
         if (e == cudaSuccess)
-            e = cudaFuncGetAttributes(&fa, prompt_tc_kernel<D, KV4, GROUPS>);
+            e = cudaFuncGetAttributes(&fa, prompt_tc_kernel<D, KV4, U>);
         if (e != cudaSuccess)
             return e;
         if (fa.numRegs < REGS_LAUNCH<KV4>)
             return cudaErrorLaunchOutOfResources;
         ready.set(dev);
     }
-    prompt_tc_kernel<D, KV4, GROUPS><<<grid, NT<KV4>, SM_ALLOC<KV4>, s>>>(tq, tk, tv, a);
+    prompt_tc_kernel<D, KV4, U><<<grid, NT<KV4>, SM_ALLOC<KV4>, s>>>(tq, tk, tv, a);
     return cudaGetLastError();
 }
 
