@@ -606,6 +606,7 @@ ddt_status ddt_prompt_attention_kvq(ddt_ctx *ctx, const uint16_t *q, int64_t q_s
  * (q_start[group_start[g]] .. q_start[group_start[g+1]]), is skipped like one with bad
  * lengths; so are all requests of a group whose group_start or prefix_lens are out of
  * range (below 0, above R, more than max_pages_per_req * page_size).
+ * Rows that two requests name (q_start fell between them) hold no result.
  * T is at most the config's prefix_tokens (else DDT_EUNSUPPORTED), G at most R_max. All
  * else as for ddt_prompt_attention: arguments, slots past a request's last token, the
  * workspace and its rule on calls that overlap, waits that give up. */

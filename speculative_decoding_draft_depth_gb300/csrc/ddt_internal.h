@@ -90,6 +90,7 @@ struct ddt_ctx {
     // attention with shared prefixes (prefix_tokens > 0): parts by rows, of prefixes and of own keys
     float *px_store_o;       // [2, d / 4, prefix_tokens * Hq, 4] (less rows when a call has fewer tokens)
     float2 *px_store_ml;     // [2, prefix_tokens * Hq]
+    int2 *px_item_ctas;      // [2, Hkv * prefix_tokens]
     float *px_few_o;         // [4 * PR_MAX_CTAS, 16, d] slots of a kernel of few rows
     float2 *px_few_ml;       // [4 * PR_MAX_CTAS, 16]
     // prefix scheduler (rank-counting grid)

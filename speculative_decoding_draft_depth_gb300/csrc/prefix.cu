@@ -16,20 +16,18 @@
 namespace {
 
 constexpr int PM_THREADS = 256;
+constexpr int PM_WARPS = PM_THREADS / 32;
+constexpr int PM_AHEAD = 4;  // parts of a row whose loads are in flight
 
-// what one item left of a row: whole (c0 == c1), in the store, or in the slots of CTAs c0..c1
-struct RowPart {
-    int c0, c1, row;  // row: of the item's tile
-};
-
+// a row's sum so far: of columns of four channels
 struct Acc {
     float M, L;
     float4 o;
-    DDT_DEVINL void add(float2 ml, const float4 &v)
+    DDT_DEVINL void add(float m, float l, const float4 &v)
     {
-        const float n = fmaxf(M, ml.x);
-        const float f = M == DDT_NEG_INF ? 0.f : ex2(M - n), w = ml.x == DDT_NEG_INF ? 0.f : ex2(ml.x - n);
-        L = L * f + ml.y * w;
+        const float n = fmaxf(M, m);
+        const float f = M == DDT_NEG_INF ? 0.f : ex2(M - n), w = m == DDT_NEG_INF ? 0.f : ex2(m - n);
+        L = L * f + l * w;
         o.x = o.x * f + v.x * w;
         o.y = o.y * f + v.y * w;
         o.z = o.z * f + v.z * w;
@@ -38,153 +36,118 @@ struct Acc {
     }
 };
 
-// what was cut: slots of `rows` rows
-struct Slots {
-    const float *o;
-    const float2 *ml;
-    int rows;
-};
+// add what an item left of a row, of its parts every `by`-th from `from` on. The parts lie in
+// slots of `rows` rows, of CTA c0 the second one, of those up to c1 the first ones.
 template <int D>
-DDT_DEVINL void add_part(const PtArgs &a, const RowPart &p, const Slots &sl, int store, int64_t srow, int c4, Acc &acc)
+DDT_DEVINL void add_parts(const float *so, const float2 *sml, int rows, int c0, int c1, int row, int c4, int from, int by, Acc &acc)
 {
-    if (p.c0 == p.c1) {
-        acc.add(__ldcg(a.store_ml[store] + srow), __ldcg(a.store_o[store] + (int64_t)c4 * a.T * a.Hq + srow));
-        return;
-    }
-#pragma unroll 4
-    for (int c = p.c0; c <= p.c1; ++c) {
-        const int64_t slot = 2 * (int64_t)c + (c == p.c0 ? 1 : 0);
-        acc.add(__ldcg(&sl.ml[slot * sl.rows + p.row]),
-                __ldcg(reinterpret_cast<const float4 *>(sl.o + slot * sl.rows * D) + c4 * sl.rows + p.row));
-    }
-}
-
-// the units' places in the shares: their first units, and (returned) all units
-template <Units U>
-DDT_DEVINL long long unit_places(const PtArgs &a, int tq, long long *base, long long *sums)
-{
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int count = num_units<U>(a), per = (count + PM_THREADS - 1) / PM_THREADS;
-    const int u0 = min(tid * per, count), u1 = min(u0 + per, count);
-    long long mine = 0;
-    for (int u = u0; u < u1; ++u) {
-        base[u] = mine;
-        mine += pp_units(load_req<U>(a, u), tq, a.Hkv);
-    }
-    long long incl = mine;
+    const int64_t slot = (int64_t)rows * D;
+    const float *o = so + (int64_t)c4 * rows * 4 + row * 4;
+    for (int c = c0 + from; c <= c1; c += PM_AHEAD * by) {
+        float2 ml[PM_AHEAD];
+        float4 v[PM_AHEAD];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-        if (lane >= o)
-            incl += y;
+        for (int y = 0; y < PM_AHEAD; ++y) {
+            const int x = min(c + y * by, c1), at = 2 * x + (x == c0 ? 1 : 0);
+            ml[y] = __ldcg(sml + (int64_t)at * rows + row);
+            v[y] = __ldcg(reinterpret_cast<const float4 *>(o + at * slot));
+        }
+#pragma unroll
+        for (int y = 0; y < PM_AHEAD; ++y)
+            if (c + y * by <= c1)
+                acc.add(ml[y].x, ml[y].y, v[y]);
     }
-    __syncthreads();
-    if (lane == 31)
-        sums[warp] = incl;
-    __syncthreads();
-    long long before = incl - mine, total = 0;
-    for (int w = 0; w < PM_THREADS / 32; ++w) {
-        before += w < warp ? sums[w] : 0;
-        total += sums[w];
-    }
-    for (int u = u0; u < u1; ++u)
-        base[u] += before;
-    return total;
 }
 
 // A CTA: items (request, KV head) by turns. rows: of an item of own keys (PP_ROWS: the same
-// launch did both, with `grid` CTAs; else a launch of its own with `own_grid`).
+// launch did both, else a launch of its own). What counts is the parts' way from L2: where an
+// item has few rows, several warps share a row's parts.
 template <int D>
-__global__ void __launch_bounds__(PM_THREADS) prefix_merge_kernel(const PtArgs a, int grid, int rows, int own_grid)
+__global__ void __launch_bounds__(PM_THREADS) prefix_merge_kernel(const PtArgs a, int rows)
 {
-    extern __shared__ long long s_base[];  // each unit's first share unit: prefixes, then requests
-    __shared__ long long s_sums[PM_THREADS / 32];
-    __shared__ RowPart s_part[PP_ROWS];    // of each token of an item: the prefix's
+    __shared__ Acc s_acc[PM_WARPS][32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int tp = PP_ROWS >> a.g_shift, tq = rows >> a.g_shift, G = 1 << a.g_shift;
     const bool both = rows == PP_ROWS;
-    long long total, own_total;
-    if (both) {
-        total = own_total = unit_places<BOTH>(a, tp, s_base, s_sums);
-    } else {
-        total = unit_places<PREFIXES>(a, tp, s_base, s_sums);
-        own_total = unit_places<OWN>(a, tq, s_base + a.ngroups, s_sums);
-    }
-    __syncthreads();
-    pdl_wait();  // (every CTA: what comes next in the stream must find the main kernel done)
-    if (own_total == 0)
-        return;
-    const int nc = total > 0 ? pp_ctas(total, grid, MIN_UNITS) : 1;
-    const int own_nc = both ? nc : pp_ctas(own_total, own_grid, MIN_UNITS);
-    const Slots ps = {a.part_o, a.part_ml, PP_ROWS}, os = {both ? a.part_o : a.few_o, both ? a.part_ml : a.few_ml, rows};
-    auto part_of = [&](const PpReq &q, int unit, int t, long long all, int ctas, int qt, int h, int row) {
-        const int n = pp_tiles(q, qt, t);
-        const long long i0 = s_base[unit] + a.Hkv * pp_units_before(q, qt, t) + (long long)h * (n + PP_ITEM) + PP_ITEM;
-        return RowPart{pp_cta_of(i0, all, ctas), pp_cta_of(i0 + n - 1, all, ctas), row};
-    };
+    bool waited = false;
     for (int x = blockIdx.x; x < a.R * a.Hkv; x += gridDim.x) {
         const int r = x / a.Hkv, h = x - r * a.Hkv;
         const PpReq q = load_req<OWN>(a, r);
-        if (q.len == 0)
-            continue;
-        const int g = q.off > 0 ? group_of(a, r) : 0;
         PpReq pre = {0, 0, 0, 0, 0};
         if (q.off > 0)
-            pre = load_group(a, g);
+            pre = load_group(a, group_of(a, r));
+        if (!waited)  // (every CTA: what comes next in the stream must find the kernels before done)
+            pdl_wait();
+        waited = true;
         for (int qt = 0; qt * tq < q.len; ++qt) {
-            const int ntok = min(tq, q.len - qt * tq), nrows = ntok << a.g_shift;
-            const RowPart own = part_of(q, a.ngroups + r, tq, own_total, own_nc, qt, h, 0);
-            if (q.off == 0 && own.c0 == own.c1)
+            const int ntok = min(tq, q.len - qt * tq), nrows = ntok << a.g_shift, row0 = q.q0 + qt * tq;
+            const int2 oc = __ldcg(a.item_ctas[1] + (int64_t)h * a.T + row0);
+            if (q.off == 0 && oc.x == oc.y)
                 continue;  // (the kernel before wrote the result)
-            if (q.off > 0) {
-                __syncthreads();
-                for (int t = tid; t < ntok; t += PM_THREADS) {
-                    const int i = q.q0 + qt * tq + t - pre.q0;
-                    s_part[t] = part_of(pre, g, tp, total, nc, i / tp, h, (i % tp) << a.g_shift);
-                }
-                __syncthreads();
-            }
             // a warp: up to eight rows (side by side in the parts), the rest of its lanes
             // columns of four channels (side by side in the output)
             constexpr int least = D == 128 ? 0 : 1;  // (a row of 64 channels has 16 such columns)
             const int rw = nrows > 1 ? max(least, min(3, 32 - __clz(nrows - 1))) : least, cw = 5 - rw;
-            const int blocks = (nrows + (1 << rw) - 1) >> rw, cols = (D / 4) >> cw;
-            for (int e = warp; e < blocks * cols; e += PM_THREADS / 32) {
+            const int cols = (D / 4) >> cw, tasks = ((nrows + (1 << rw) - 1) >> rw) * cols;
+            const int by = tasks > PM_WARPS / 2 ? 1 : tasks > PM_WARPS / 4 ? 2 : 4;  // warps to a task
+            for (int e0 = 0; e0 < tasks; e0 += PM_WARPS / by) {
+                const int e = e0 + warp / by, from = warp % by;
                 const int row = ((e / cols) << rw) + (lane & ((1 << rw) - 1)), c4 = ((e % cols) << cw) + (lane >> rw);
-                if (row >= nrows)
-                    continue;
                 const int tok = row >> a.g_shift, hl = row & (G - 1);
-                const int64_t t = q.q0 + qt * tq + tok;
-                const int64_t srow = (((int64_t)h * a.T + t) << a.g_shift) + hl;
+                const int64_t t = row0 + tok, srow = (((int64_t)h * a.T + t) << a.g_shift) + hl;
                 Acc acc = {DDT_NEG_INF, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-                if (q.off > 0) {
-                    RowPart p = s_part[tok];
-                    p.row += hl;
-                    add_part<D>(a, p, ps, 0, srow, c4, acc);
+                if (e < tasks && row < nrows) {
+                    auto stored = [&](int i) {
+                        const float2 ml = __ldcg(a.store_ml[i] + srow);
+                        acc.add(ml.x, ml.y, __ldcg(a.store_o[i] + (int64_t)c4 * a.T * a.Hq + srow));
+                    };
+                    if (q.off > 0) {
+                        const int in = (int)(t - pre.q0) % tp;
+                        const int2 pc = __ldcg(a.item_ctas[0] + (int64_t)h * a.T + t - in);
+                        if (pc.x != pc.y)
+                            add_parts<D>(a.part_o, a.part_ml, PP_ROWS, pc.x, pc.y, (in << a.g_shift) + hl, c4, from, by, acc);
+                        else if (from == 0)
+                            stored(0);
+                    }
+                    if (oc.x != oc.y)
+                        add_parts<D>(both ? a.part_o : a.few_o, both ? a.part_ml : a.few_ml, rows, oc.x, oc.y, row, c4, from, by, acc);
+                    else if (from == by - 1)
+                        stored(1);
                 }
-                add_part<D>(a, RowPart{own.c0, own.c1, row}, os, 1, srow, c4, acc);
-                const float inv = acc.L > 0.f || acc.L != acc.L ? a.out_scale / acc.L : 0.f;
-                *reinterpret_cast<uint2 *>(a.out + (t * a.Hq + (h << a.g_shift) + hl) * D + 4 * c4) =
-                    make_uint2(pack_bf16x2(acc.o.x * inv, acc.o.y * inv), pack_bf16x2(acc.o.z * inv, acc.o.w * inv));
+                if (by > 1) {
+                    __syncthreads();  // (of the round before: read)
+                    s_acc[warp][lane] = acc;
+                    __syncthreads();
+                    if (from > 0)
+                        continue;
+                    for (int w = 1; w < by; ++w)
+                        acc.add(s_acc[warp + w][lane].M, s_acc[warp + w][lane].L, s_acc[warp + w][lane].o);
+                }
+                if (e < tasks && row < nrows) {
+                    const float inv = acc.L > 0.f || acc.L != acc.L ? a.out_scale / acc.L : 0.f;
+                    *reinterpret_cast<uint2 *>(a.out + (t * a.Hq + (h << a.g_shift) + hl) * D + 4 * c4) =
+                        make_uint2(pack_bf16x2(acc.o.x * inv, acc.o.y * inv), pack_bf16x2(acc.o.z * inv, acc.o.w * inv));
+                }
             }
         }
     }
+    if (!waited)
+        pdl_wait();
 }
 
 template <int D>
-cudaError_t launch_merge_rows(const ddt_ctx *c, const PtArgs &a, int grid, int rows, int own_grid, cudaStream_t s)
+cudaError_t launch_merge_rows(const ddt_ctx *c, const PtArgs &a, int rows, cudaStream_t s)
 {
     cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3((unsigned)std::min((int64_t)a.R * a.Hkv, (int64_t)c->num_sms * 6));
     lc.blockDim = dim3(PM_THREADS);
-    lc.dynamicSmemBytes = (size_t)(a.R + a.ngroups) * sizeof(long long);
     lc.stream = s;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     lc.attrs = at;
     lc.numAttrs = 1;
-    return cudaLaunchKernelEx(&lc, prefix_merge_kernel<D>, a, grid, rows, own_grid);
+    return cudaLaunchKernelEx(&lc, prefix_merge_kernel<D>, a, rows);
 }
 
 // few: own keys by a kernel of few rows, this many an item (0: everything in one launch)
@@ -193,16 +156,15 @@ cudaError_t launch_d(ddt_ctx *c, int grid, const CUtensorMap &tq, const CUtensor
                      const PtArgs &a, const uint16_t *q, int64_t q_stride, const uint16_t *k_cache, int few, cudaStream_t s)
 {
     cudaError_t e;
-    int own_grid = grid;
     if (few > 0) {
         e = launch_main<D, KV4, PREFIXES>(c->device, grid, tq, tk, tv, a, s);
         if (e == cudaSuccess)
-            e = KV4 ? launch_own_few_kvq(c, a, q, q_stride, few, &own_grid, s)
-                    : launch_own_few(c, a, q, q_stride, k_cache, few, &own_grid, s);
+            e = KV4 ? launch_own_few_kvq(c, a, q, q_stride, few, s)
+                    : launch_own_few(c, a, q, q_stride, k_cache, few, s);
     } else {
         e = launch_main<D, KV4, BOTH>(c->device, grid, tq, tk, tv, a, s);
     }
-    return e != cudaSuccess ? e : launch_merge_rows<D>(c, a, grid, few > 0 ? few : PP_ROWS, own_grid, s);
+    return e != cudaSuccess ? e : launch_merge_rows<D>(c, a, few > 0 ? few : PP_ROWS, s);
 }
 
 }  // namespace
@@ -228,6 +190,8 @@ cudaError_t launch_prefix_attention(ddt_ctx *c, const uint16_t *q, int64_t q_str
     const int grid = c->num_sms < PR_MAX_CTAS ? c->num_sms : PR_MAX_CTAS;
     a.debug_wait = c->debug_pr_wait;  // one-shot test setting
     c->debug_pr_wait = 0;
+    for (int i = 0; i < 2; ++i)
+        a.item_ctas[i] = c->px_item_ctas + (int64_t)i * cfg.Hkv * cfg.prefix_tokens;
     a.few_o = c->px_few_o;
     a.few_ml = c->px_few_ml;
     const int G = cfg.Hq / cfg.Hkv;

@@ -245,6 +245,8 @@ __global__ void __launch_bounds__(OT, 1) own_few_kernel(const OwnArgs f)
             slot = slot + 1 == S ? 0 : slot + 1;
         }
         const Seg was = s;
+        if (tid == 0)
+            note_ctas(a, was, blockIdx.x);
         start();
         // ---- the warps' parts to shared memory: O row by row, (m, l)
 #pragma unroll
@@ -308,7 +310,7 @@ __global__ void __launch_bounds__(OT, 1) own_few_kernel(const OwnArgs f)
 }
 
 template <int D, int NR>
-cudaError_t launch_own(const OwnArgs &f, int dev, int num_sms, int *ctas, cudaStream_t s)
+cudaError_t launch_own(const OwnArgs &f, int dev, int num_sms, cudaStream_t s)
 {
     constexpr int ROWS = 8 * NR, BYTES = OW * (ROWS * (D * 4 + 8) + OS<NR> * (int)OWN_BLOCK<D>);
     static_assert(BYTES <= 226 * 1024, "shared memory of one CTA");
@@ -319,9 +321,8 @@ cudaError_t launch_own(const OwnArgs &f, int dev, int num_sms, int *ctas, cudaSt
             return e;
         ready.set(dev);
     }
-    *ctas = num_sms < PR_MAX_CTAS ? num_sms : PR_MAX_CTAS;
     cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3(*ctas);
+    lc.gridDim = dim3(num_sms < PR_MAX_CTAS ? num_sms : PR_MAX_CTAS);
     lc.blockDim = dim3(OT);
     lc.dynamicSmemBytes = BYTES;
     lc.stream = s;
@@ -336,7 +337,7 @@ cudaError_t launch_own(const OwnArgs &f, int dev, int num_sms, int *ctas, cudaSt
 }  // namespace
 
 cudaError_t launch_own_few(ddt_ctx *c, const PtArgs &a, const uint16_t *q, int64_t q_stride, const uint16_t *k_cache,
-                           int rows, int *ctas, cudaStream_t s)
+                           int rows, cudaStream_t s)
 {
     OwnArgs f;
     f.a = a;
@@ -344,8 +345,8 @@ cudaError_t launch_own_few(ddt_ctx *c, const PtArgs &a, const uint16_t *q, int64
     f.q_stride = q_stride;
     f.k_cache = k_cache;
     if (c->cfg.d == 128)
-        return rows <= 8 ? launch_own<128, 1>(f, c->device, c->num_sms, ctas, s)
-                         : launch_own<128, 2>(f, c->device, c->num_sms, ctas, s);
-    return rows <= 8 ? launch_own<64, 1>(f, c->device, c->num_sms, ctas, s)
-                     : launch_own<64, 2>(f, c->device, c->num_sms, ctas, s);
+        return rows <= 8 ? launch_own<128, 1>(f, c->device, c->num_sms, s)
+                         : launch_own<128, 2>(f, c->device, c->num_sms, s);
+    return rows <= 8 ? launch_own<64, 1>(f, c->device, c->num_sms, s)
+                     : launch_own<64, 2>(f, c->device, c->num_sms, s);
 }

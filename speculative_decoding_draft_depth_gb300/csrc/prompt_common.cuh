@@ -30,6 +30,7 @@ struct PtArgs {
     int ngroups;
     float4 *store_o[2];
     float2 *store_ml[2];
+    int2 *item_ctas[2];    // by KV head and an item's first row: the first and last CTA that had of its tiles
     float *few_o;          // slots of own keys' cut items where a kernel of few rows has them
     float2 *few_ml;
     long long debug_wait;  // > 0 (tests only): each CTA starts with a wait that runs out after this many cycles
@@ -41,11 +42,10 @@ cudaError_t launch_prompt_few(ddt_ctx *c, const PtArgs &a, const uint16_t *q, in
                               cudaStream_t s);
 // the own keys of few rows of each request, where prefixes are shared, as a programmatic
 // dependent of the prefixes' kernel: 4 bits (prompt_few.cu) and bf16 (prefix_few.cu).
-// *ctas: the CTAs that share the work
-cudaError_t launch_own_few_kvq(ddt_ctx *c, const PtArgs &a, const uint16_t *q, int64_t q_stride, int rows, int *ctas,
+cudaError_t launch_own_few_kvq(ddt_ctx *c, const PtArgs &a, const uint16_t *q, int64_t q_stride, int rows,
                                cudaStream_t s);
 cudaError_t launch_own_few(ddt_ctx *c, const PtArgs &a, const uint16_t *q, int64_t q_stride, const uint16_t *k_cache,
-                           int rows, int *ctas, cudaStream_t s);
+                           int rows, cudaStream_t s);
 
 namespace {
 
@@ -59,11 +59,13 @@ constexpr float PBIAS = 7.0f;
 
 // a segment of an item: ring words
 //   0: request (-1: end of the share)   1: head | split << 8 | whole << 9 | slot << 10
-//   (bit 28: of a shared prefix, 29: of a request that has one)
+//   (bit 28: of a shared prefix, 29: of a request that has one, 30, 31: the item's first and
+//   last tile are in it)
 //   2: first packed row  3: tokens  4: position of the first  5, 6: key tiles [t0, t1)
 struct Seg {
     int r, h, row0, ntok, pos0, t0, t1, slot;
     bool split, whole;
+    bool first, last; // the segment has the item's first tile, its last
     bool flat, part;  // a shared prefix: every row's last key is pos0; the item is one part of its rows' keys
     DDT_DEVINL int end() const { return flat ? pos0 + 1 : pos0 + ntok; }
     DDT_DEVINL int last_key(int tok) const { return flat ? pos0 : pos0 + min(tok, ntok - 1); }  // (rows without a token: the last one's)
@@ -85,6 +87,8 @@ DDT_DEVINL void seg_decode(const int *w, Seg &s)
     s.slot = (w[1] >> 10) & 0x3FFFF;
     s.flat = GROUPS && ((w[1] >> 28) & 1);
     s.part = GROUPS && ((w[1] >> 29) & 1);
+    s.first = GROUPS && ((w[1] >> 30) & 1);
+    s.last = GROUPS && w[1] < 0;
     s.row0 = w[2];
     s.ntok = w[3];
     s.pos0 = w[4];
@@ -173,6 +177,16 @@ DDT_DEVINL PpReq load_req(const PtArgs &a, int r, bool *sound = nullptr)
     q.ctx = c;
     q.len = ok ? s1 - s0 : 0;
     return q;
+}
+
+// one thread of a segment's: who had the item's ends (prefixes', or own keys')
+DDT_DEVINL void note_ctas(const PtArgs &a, const Seg &s, int cta)
+{
+    int *at = &a.item_ctas[s.flat ? 0 : 1][(int64_t)s.h * a.T + s.row0].x;
+    if (s.first)
+        at[0] = cta;
+    if (s.last)
+        at[1] = cta;
 }
 
 // the page of 16-token group u of key tile j (NO_PAGE: past the item's last key)
@@ -288,6 +302,8 @@ struct ShareWalk {
             s.t0 = t0 + (U != PLAIN ? rq.off : 0);
             s.t1 = t1 + (U != PLAIN ? rq.off : 0);
             s.whole = t0 == 0 && t1 == it.n;
+            s.first = U != PLAIN && t0 == 0;
+            s.last = U != PLAIN && t1 == it.n;
             s.split = (s.ntok << a.g_shift) <= split_rows;
             s.slot = 2 * cta + (t0 > 0 ? 0 : 1);
             const int sr = U == PREFIXES || (U == BOTH && r < a.ngroups) ? __ldg(&a.group_start[r]) : U == BOTH ? r - a.ngroups : r;

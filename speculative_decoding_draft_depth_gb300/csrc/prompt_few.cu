@@ -401,6 +401,8 @@ __global__ void __launch_bounds__(FT, NR == 1 ? 2 : 1) prompt_few_kernel(const F
             }
         }
         const Seg was = s;
+        if (U != PLAIN && tid == 0)
+            note_ctas(a, was, blockIdx.x);
         start();
         // ---- the warps' parts to shared memory: O row by row, (m, l)
 #pragma unroll
@@ -468,7 +470,7 @@ __global__ void __launch_bounds__(FT, NR == 1 ? 2 : 1) prompt_few_kernel(const F
 }
 
 template <int D, int NR, Units U>
-cudaError_t launch_few(const FewArgs &f, int dev, int num_sms, int *ctas, cudaStream_t s)
+cudaError_t launch_few(const FewArgs &f, int dev, int num_sms, cudaStream_t s)
 {
     constexpr int ROWS = 8 * NR, BYTES = FW * (ROWS * (D * 4 + 8) + FS * RAW_BYTES<D>);
     static_assert(ROWS * 2 * 2 * PR_MAX_CTAS <= 2 * PR_MAX_CTAS * PR_ROWS, "partial slots");
@@ -482,7 +484,6 @@ cudaError_t launch_few(const FewArgs &f, int dev, int num_sms, int *ctas, cudaSt
     }
     const int grid = (num_sms < PR_MAX_CTAS ? num_sms : PR_MAX_CTAS) * (NR == 1 ? 2 : 1);
     if (U != PLAIN) {  // (beside the prefixes' kernel, which reads and writes elsewhere)
-        *ctas = grid;
         cudaLaunchConfig_t lc = {};
         lc.gridDim = dim3(grid);
         lc.blockDim = dim3(FT);
@@ -511,13 +512,13 @@ cudaError_t launch_prompt_few(ddt_ctx *c, const PtArgs &a, const uint16_t *q, in
     f.q = q;
     f.q_stride = q_stride;
     if (c->cfg.d == 128)
-        return rows <= 8 ? launch_few<128, 1, PLAIN>(f, c->device, c->num_sms, nullptr, s)
-                         : launch_few<128, 2, PLAIN>(f, c->device, c->num_sms, nullptr, s);
-    return rows <= 8 ? launch_few<64, 1, PLAIN>(f, c->device, c->num_sms, nullptr, s)
-                     : launch_few<64, 2, PLAIN>(f, c->device, c->num_sms, nullptr, s);
+        return rows <= 8 ? launch_few<128, 1, PLAIN>(f, c->device, c->num_sms, s)
+                         : launch_few<128, 2, PLAIN>(f, c->device, c->num_sms, s);
+    return rows <= 8 ? launch_few<64, 1, PLAIN>(f, c->device, c->num_sms, s)
+                     : launch_few<64, 2, PLAIN>(f, c->device, c->num_sms, s);
 }
 
-cudaError_t launch_own_few_kvq(ddt_ctx *c, const PtArgs &a, const uint16_t *q, int64_t q_stride, int rows, int *ctas,
+cudaError_t launch_own_few_kvq(ddt_ctx *c, const PtArgs &a, const uint16_t *q, int64_t q_stride, int rows,
                                cudaStream_t s)
 {
     FewArgs f;
@@ -525,8 +526,8 @@ cudaError_t launch_own_few_kvq(ddt_ctx *c, const PtArgs &a, const uint16_t *q, i
     f.q = q;
     f.q_stride = q_stride;
     if (c->cfg.d == 128)
-        return rows <= 8 ? launch_few<128, 1, OWN>(f, c->device, c->num_sms, ctas, s)
-                         : launch_few<128, 2, OWN>(f, c->device, c->num_sms, ctas, s);
-    return rows <= 8 ? launch_few<64, 1, OWN>(f, c->device, c->num_sms, ctas, s)
-                     : launch_few<64, 2, OWN>(f, c->device, c->num_sms, ctas, s);
+        return rows <= 8 ? launch_few<128, 1, OWN>(f, c->device, c->num_sms, s)
+                         : launch_few<128, 2, OWN>(f, c->device, c->num_sms, s);
+    return rows <= 8 ? launch_few<64, 1, OWN>(f, c->device, c->num_sms, s)
+                     : launch_few<64, 2, OWN>(f, c->device, c->num_sms, s);
 }

@@ -468,7 +468,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                 w[0] = s.r;
                 if (s.r >= 0) {
                     w[1] = s.h | (s.split ? 256 : 0) | (s.whole ? 512 : 0) | (s.slot << 10) |
-                           (s.flat ? 1 << 28 : 0) | (s.part ? 1 << 29 : 0);
+                           (s.flat ? 1 << 28 : 0) | (s.part ? 1 << 29 : 0) | (s.first ? 1 << 30 : 0) | (s.last ? 1 << 31 : 0);
                     w[2] = s.row0;
                     w[3] = s.ntok;
                     w[4] = s.pos0;
@@ -941,6 +941,8 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     m_used = M;
                 }
             }
+            if (GROUPS && g == 0 && row == 0)
+                note_ctas(a, s, blockIdx.x);
             const bool row_ok = tok < s.ntok;
             const bool final_ = s.whole && !s.part;
             const float inv = final_ ? (l > 0.f || l != l ? a.out_scale / l : 0.f) : 1.f;
