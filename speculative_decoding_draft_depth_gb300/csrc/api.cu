@@ -6,6 +6,8 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <algorithm>
+
 #include "ddt_internal.h"
 #include "device_scope.h"
 #include "packed_seq.h"
@@ -79,7 +81,7 @@ ddt_status check_config(const ddt_config *in, ddt_config *out)
 struct Layout {
     size_t status, tk_gkey, tk_wtop, tk_ms, am_val, am_idx, att_part_o, att_part_ml, cg_part_ms, cg_part_top, cg_fr_tok, cg_fr_cand,
         cg_fr_n, cg_fr_S, cg_c_S, cg_c_meta, cg_thr, cg_seed_lp, cg_seed_ids, mk_cand, mk_tab,
-        sv_part_d, sv_part_t, sv_cnt, sv_part_w, sm_rows, px_o, px_ml, px_ctas, px_few_o, px_few_ml, ps_rk, ps_rid, ps_arrive, total;
+        sv_part_d, sv_part_t, sv_cnt, sv_part_w, sm_rows, px_o, px_ml, px_ctas, px_own_o, px_own_ml, ps_rk, ps_rid, ps_arrive, total;
     int tk_nch, am_nch, max_items, sv_nch_d, sv_nch_t, sv_nch_w;
 };
 
@@ -148,9 +150,10 @@ Layout layout_for(const ddt_config &c)
     L.px_o = take(px_rows * c.d * sizeof(float));
     L.px_ml = take(px_rows * sizeof(float2));
     L.px_ctas = take((size_t)2 * c.prefix_tokens * c.Hkv * sizeof(int2));
-    const size_t few_rows = c.prefix_tokens > 0 ? (size_t)4 * PR_MAX_CTAS * 16 : 0;
-    L.px_few_o = take(few_rows * c.d * sizeof(float));
-    L.px_few_ml = take(few_rows * sizeof(float2));
+    // (slots: two a CTA, of PR_ROWS rows, or of 16 where a kernel of few rows has more CTAs)
+    const size_t own_rows = c.prefix_tokens > 0 ? (size_t)2 * PR_MAX_CTAS * std::max(PR_ROWS, OWN_FEW_CTAS * 16) : 0;
+    L.px_own_o = take(own_rows * c.d * sizeof(float));
+    L.px_own_ml = take(own_rows * sizeof(float2));
     // prefix scheduler: the ranking of up to DDT_SCHED_MAX_SLOTS slots
     L.ps_rk = take((size_t)DDT_SCHED_MAX_SLOTS * sizeof(uint64_t));
     L.ps_rid = take((size_t)DDT_SCHED_MAX_SLOTS * sizeof(int32_t));
@@ -462,8 +465,8 @@ ddt_status ddt_create(const ddt_config *cfg, ddt_ctx **out)
     ctx->px_store_o = (float *)(w + L.px_o);
     ctx->px_store_ml = (float2 *)(w + L.px_ml);
     ctx->px_item_ctas = (int2 *)(w + L.px_ctas);
-    ctx->px_few_o = (float *)(w + L.px_few_o);
-    ctx->px_few_ml = (float2 *)(w + L.px_few_ml);
+    ctx->px_own_o = (float *)(w + L.px_own_o);
+    ctx->px_own_ml = (float2 *)(w + L.px_own_ml);
     ctx->ps_rk = (uint64_t *)(w + L.ps_rk);
     ctx->ps_rid = (int32_t *)(w + L.ps_rid);
     ctx->ps_arrive = (unsigned *)(w + L.ps_arrive);

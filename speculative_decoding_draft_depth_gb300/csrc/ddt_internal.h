@@ -35,6 +35,9 @@ constexpr int ATT_MAX_CTX = 262144;  // tokens of context per request
 // (two partial slots each; the partials share a4's memory)
 constexpr int PR_ROWS = 256;
 constexpr int PR_MAX_CTAS = 160;
+// CTAs, for each SM, of a launch that has the own keys of few rows where prefixes are
+// shared: small shares, as they begin when the prefixes' CTAs leave an SM (two slots each)
+constexpr int OWN_FEW_CTAS = 4;
 
 // parent-conditioned tree: most CTAs of its per-depth GEMM (partials per CTA)
 constexpr int CG_GRID_MAX = 256;
@@ -91,8 +94,8 @@ struct ddt_ctx {
     float *px_store_o;       // [2, d / 4, prefix_tokens * Hq, 4] (less rows when a call has fewer tokens)
     float2 *px_store_ml;     // [2, prefix_tokens * Hq]
     int2 *px_item_ctas;      // [2, Hkv * prefix_tokens]
-    float *px_few_o;         // [4 * PR_MAX_CTAS, 16, d] slots of a kernel of few rows
-    float2 *px_few_ml;       // [4 * PR_MAX_CTAS, 16]
+    float *px_own_o;         // slots of own keys' cut items, [px_own_rows, d]
+    float2 *px_own_ml;       // [px_own_rows]
     // prefix scheduler (rank-counting grid)
     uint64_t *ps_rk;         // [DDT_SCHED_MAX_SLOTS] survival bits in ranking order
     int32_t *ps_rid;         // [DDT_SCHED_MAX_SLOTS] their tie ids

@@ -7,9 +7,8 @@
 //   M = max m_i,  O = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.
 // The prefix is one more item of the tensor-core kernel (prompt_tc.cuh): the group's
 // tokens, packed one behind the other, fill its tiles of 256 rows, against keys without a
-// mask; its members' items begin behind it. One launch does both, in equal shares, or, where
-// requests have few rows, two launches: prefixes there, own keys in a kernel of few rows
-// (prefix_few.cu, prompt_few.cu). Items leave their parts in a store by rows, cut ones in the
+// mask. Own keys are a launch that begins beside that one, of the same kernel or, where
+// requests have few rows, of one for few rows (prefix_few.cu, prompt_few.cu). Items leave their parts in a store by rows, cut ones in the
 // CTAs' slots, and prefix_merge_kernel adds each row's up.
 #include "prompt_tc.cuh"
 
@@ -59,16 +58,14 @@ DDT_DEVINL void add_parts(const float *so, const float2 *sml, int rows, int c0, 
     }
 }
 
-// A CTA: items (request, KV head) by turns. rows: of an item of own keys (PP_ROWS: the same
-// launch did both, else a launch of its own). What counts is the parts' way from L2: where an
+// A CTA: items (request, KV head) by turns. What counts is the parts' way from L2: where an
 // item has few rows, several warps share a row's parts.
 template <int D>
-__global__ void __launch_bounds__(PM_THREADS) prefix_merge_kernel(const PtArgs a, int rows)
+__global__ void __launch_bounds__(PM_THREADS) prefix_merge_kernel(const PtArgs a)
 {
     __shared__ Acc s_acc[PM_WARPS][32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int tp = PP_ROWS >> a.g_shift, tq = rows >> a.g_shift, G = 1 << a.g_shift;
-    const bool both = rows == PP_ROWS;
+    const int tp = PP_ROWS >> a.g_shift, tq = a.own_rows >> a.g_shift, G = 1 << a.g_shift;
     bool waited = false;
     for (int x = blockIdx.x; x < a.R * a.Hkv; x += gridDim.x) {
         const int r = x / a.Hkv, h = x - r * a.Hkv;
@@ -110,7 +107,7 @@ __global__ void __launch_bounds__(PM_THREADS) prefix_merge_kernel(const PtArgs a
                             stored(0);
                     }
                     if (oc.x != oc.y)
-                        add_parts<D>(both ? a.part_o : a.few_o, both ? a.part_ml : a.few_ml, rows, oc.x, oc.y, row, c4, from, by, acc);
+                        add_parts<D>(a.own_o, a.own_ml, a.own_rows, oc.x, oc.y, row, c4, from, by, acc);
                     else if (from == by - 1)
                         stored(1);
                 }
@@ -136,7 +133,7 @@ __global__ void __launch_bounds__(PM_THREADS) prefix_merge_kernel(const PtArgs a
 }
 
 template <int D>
-cudaError_t launch_merge_rows(const ddt_ctx *c, const PtArgs &a, int rows, cudaStream_t s)
+cudaError_t launch_merge_rows(const ddt_ctx *c, const PtArgs &a, cudaStream_t s)
 {
     cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3((unsigned)std::min((int64_t)a.R * a.Hkv, (int64_t)c->num_sms * 6));
@@ -147,24 +144,26 @@ cudaError_t launch_merge_rows(const ddt_ctx *c, const PtArgs &a, int rows, cudaS
     at[0].val.programmaticStreamSerializationAllowed = 1;
     lc.attrs = at;
     lc.numAttrs = 1;
-    return cudaLaunchKernelEx(&lc, prefix_merge_kernel<D>, a, rows);
+    return cudaLaunchKernelEx(&lc, prefix_merge_kernel<D>, a);
 }
 
-// few: own keys by a kernel of few rows, this many an item (0: everything in one launch)
 template <int D, bool KV4>
 cudaError_t launch_d(ddt_ctx *c, int grid, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
-                     const PtArgs &a, const uint16_t *q, int64_t q_stride, const uint16_t *k_cache, int few, cudaStream_t s)
+                     const PtArgs &a, const uint16_t *q, int64_t q_stride, const uint16_t *k_cache, cudaStream_t s)
 {
-    cudaError_t e;
-    if (few > 0) {
-        e = launch_main<D, KV4, PREFIXES>(c->device, grid, tq, tk, tv, a, s);
-        if (e == cudaSuccess)
-            e = KV4 ? launch_own_few_kvq(c, a, q, q_stride, few, s)
-                    : launch_own_few(c, a, q, q_stride, k_cache, few, s);
+    cudaError_t e = launch_main<D, KV4, PREFIXES>(c->device, grid, tq, tk, tv, a, s);
+    if (e != cudaSuccess)
+        return e;
+    if (a.own_rows == PP_ROWS) {
+        PtArgs own = a;
+        own.part_o = a.own_o;
+        own.part_ml = a.own_ml;
+        own.debug_wait = 0;
+        e = launch_main<D, KV4, OWN>(c->device, grid, tq, tk, tv, own, s);
     } else {
-        e = launch_main<D, KV4, BOTH>(c->device, grid, tq, tk, tv, a, s);
+        e = KV4 ? launch_own_few_kvq(c, a, q, q_stride, a.own_rows, s) : launch_own_few(c, a, q, q_stride, k_cache, a.own_rows, s);
     }
-    return e != cudaSuccess ? e : launch_merge_rows<D>(c, a, few > 0 ? few : PP_ROWS, s);
+    return e != cudaSuccess ? e : launch_merge_rows<D>(c, a, s);
 }
 
 }  // namespace
@@ -192,14 +191,21 @@ cudaError_t launch_prefix_attention(ddt_ctx *c, const uint16_t *q, int64_t q_str
     c->debug_pr_wait = 0;
     for (int i = 0; i < 2; ++i)
         a.item_ctas[i] = c->px_item_ctas + (int64_t)i * cfg.Hkv * cfg.prefix_tokens;
-    a.few_o = c->px_few_o;
-    a.few_ml = c->px_few_ml;
+    a.own_o = c->px_own_o;
+    a.own_ml = c->px_own_ml;
     const int G = cfg.Hq / cfg.Hkv;
     // Few rows of a request on average (lengths are the device's) go to a kernel of their own.
-    const int few = (int64_t)T * G > (int64_t)R * 16 ? 0 : G <= 8 && (int64_t)T * G <= (int64_t)R * 8 ? 8 : 16;
+    a.own_rows = (int64_t)T * G > (int64_t)R * 16 ? PP_ROWS : G <= 8 && (int64_t)T * G <= (int64_t)R * 8 ? 8 : 16;
+    // Measured: a prefix's tile 2 us of an SM (4 bits as well), a unit of own keys 0.9 us, a
+    // CTA of the prefixes' 6 us besides.
+    if (a.own_rows < PP_ROWS) {
+        a.cost[0] = 20;
+        a.cost[1] = 9;
+        a.cost[2] = 60;
+    }
     if (kv4)
-        return cfg.d == 128 ? launch_d<128, true>(c, grid, tq, tk, tv, a, q, q_stride, nullptr, few, s)
-                            : launch_d<64, true>(c, grid, tq, tk, tv, a, q, q_stride, nullptr, few, s);
-    return cfg.d == 128 ? launch_d<128, false>(c, grid, tq, tk, tv, a, q, q_stride, k_cache, few, s)
-                        : launch_d<64, false>(c, grid, tq, tk, tv, a, q, q_stride, k_cache, few, s);
+        return cfg.d == 128 ? launch_d<128, true>(c, grid, tq, tk, tv, a, q, q_stride, nullptr, s)
+                            : launch_d<64, true>(c, grid, tq, tk, tv, a, q, q_stride, nullptr, s);
+    return cfg.d == 128 ? launch_d<128, false>(c, grid, tq, tk, tv, a, q, q_stride, k_cache, s)
+                        : launch_d<64, false>(c, grid, tq, tk, tv, a, q, q_stride, k_cache, s);
 }

@@ -8,7 +8,7 @@
 //   S^T (16 keys x 8 rows) = K Q^T, K's rows by ldmatrix, Q's in registers;
 //   O^T (16 channels x 8 rows) += V^T P^T, V by transposing ldmatrix, P^T transposed in the
 //   warp.
-// Eight warps of a CTA take the 16-key blocks of a segment in turn, each with its own running
+// Four warps of a CTA take the 16-key blocks of a segment in turn, each with its own running
 // maximum and sum; blocks come by cp.async into a ring of the warp's own, 16-byte vectors of
 // a key's row exchanged by the key's low bits (the ldmatrix rows then lie in all banks).
 // Shares of the work as in prompt_plan.h; the parts are added up by prefix_merge_kernel.
@@ -21,7 +21,7 @@
 
 namespace {
 
-constexpr int OW = 8;  // warps of a CTA
+constexpr int OW = 4;  // warps of a CTA (two CTAs an SM)
 constexpr int OT = OW * 32;
 template <int NR>
 constexpr int OS = NR == 1 ? 3 : 2;  // blocks that a warp has in flight
@@ -69,14 +69,14 @@ template <int D>
 DDT_DEVINL uint32_t own_place(int key, int x) { return key * OWN_ROW<D> + ((x ^ (key & 7)) << 4); }
 
 template <int D, int NR>
-__global__ void __launch_bounds__(OT, 1) own_few_kernel(const OwnArgs f)
+__global__ void __launch_bounds__(OT, 2) own_few_kernel(const OwnArgs f)
 {
     constexpr int ROWS = 8 * NR, KS = D / 16, S = OS<NR>;
     extern __shared__ float4 own_smem[];
     float *so = reinterpret_cast<float *>(own_smem);               // [OW][ROWS][D]
     float2 *sml = reinterpret_cast<float2 *>(so + OW * ROWS * D);  // [OW][ROWS]
     const uint32_t raws = (uint32_t)__cvta_generic_to_shared(sml + OW * ROWS) + (threadIdx.x >> 5) * S * OWN_BLOCK<D>;
-    __shared__ long long s_sums[OW], s_found[3];
+    __shared__ long long s_sums[OW], s_found[4];
     const PtArgs &a = f.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, i = lane >> 2, c = lane & 3;
     const int tq = ROWS >> a.g_shift, G = 1 << a.g_shift;
@@ -90,7 +90,7 @@ __global__ void __launch_bounds__(OT, 1) own_few_kernel(const OwnArgs f)
     pdl_trigger();  // (the merge stages itself; it waits for this grid before it reads)
     find_share<OWN>(a, tq, gridDim.x, blockIdx.x, s_sums, s_found, tid, OT);
     ShareWalk<OWN> walk;
-    walk.begin(a, s_found, tq, gridDim.x, blockIdx.x);
+    walk.begin(a, s_found, tq, blockIdx.x);
     int blk = 0, bend = 0, page = NO_PAGE;
     Seg s = {};
     auto page_of = [&](int b) {
@@ -298,22 +298,22 @@ __global__ void __launch_bounds__(OT, 1) own_few_kernel(const OwnArgs f)
                     a.store_ml[1][at] = make_float2(M, L);
             } else {
                 const int64_t sl = (int64_t)was.slot * ROWS;
-                reinterpret_cast<float4 *>(a.few_o + sl * D)[c4 * ROWS + row] = r;
+                reinterpret_cast<float4 *>(a.own_o + sl * D)[c4 * ROWS + row] = r;
                 if (c4 == 0)
-                    a.few_ml[sl + row] = make_float2(M, L);
+                    a.own_ml[sl + row] = make_float2(M, L);
             }
         }
         __syncthreads();
     }
     cp_async_wait_all();
-    pdl_wait();  // (the prefixes' kernel is before this one; the merge waits for this one only)
+    own_done();  // (the prefixes' kernel is before this one; the merge waits for this one only)
 }
 
 template <int D, int NR>
 cudaError_t launch_own(const OwnArgs &f, int dev, int num_sms, cudaStream_t s)
 {
     constexpr int ROWS = 8 * NR, BYTES = OW * (ROWS * (D * 4 + 8) + OS<NR> * (int)OWN_BLOCK<D>);
-    static_assert(BYTES <= 226 * 1024, "shared memory of one CTA");
+    static_assert(BYTES <= 115200, "shared memory of one CTA of two");
     static DeviceFlags ready;
     if (!ready.test(dev)) {
         const cudaError_t e = cudaFuncSetAttribute(own_few_kernel<D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
@@ -322,7 +322,7 @@ cudaError_t launch_own(const OwnArgs &f, int dev, int num_sms, cudaStream_t s)
         ready.set(dev);
     }
     cudaLaunchConfig_t lc = {};
-    lc.gridDim = dim3(num_sms < PR_MAX_CTAS ? num_sms : PR_MAX_CTAS);
+    lc.gridDim = dim3((num_sms < PR_MAX_CTAS ? num_sms : PR_MAX_CTAS) * OWN_FEW_CTAS);
     lc.blockDim = dim3(OT);
     lc.dynamicSmemBytes = BYTES;
     lc.stream = s;

@@ -31,8 +31,10 @@ struct PtArgs {
     float4 *store_o[2];
     float2 *store_ml[2];
     int2 *item_ctas[2];    // by KV head and an item's first row: the first and last CTA that had of its tiles
-    float *few_o;          // slots of own keys' cut items where a kernel of few rows has them
-    float2 *few_ml;
+    int own_rows;          // rows of an item of own keys in the launch beside the prefixes'
+    int cost[3];           // 0.1 us on an SM: a unit of a prefix, of own keys (0: prefixes have all SMs), a CTA besides
+    float *own_o;          // slots of own keys' cut items (rows: own_rows)
+    float2 *own_ml;
     long long debug_wait;  // > 0 (tests only): each CTA starts with a wait that runs out after this many cycles
 };
 
@@ -137,11 +139,11 @@ DDT_DEVINL PpReq load_group(const PtArgs &a, int g)
     return q;
 }
 
-// What a launch works on, units r = 0 ..: requests; where prefixes are shared the groups'
-// prefixes, then the requests' own keys; or one of the two.
-enum Units { PLAIN, BOTH, PREFIXES, OWN };
+// What a launch works on: requests; where prefixes are shared, the groups' prefixes or the
+// requests' own keys.
+enum Units { PLAIN, PREFIXES, OWN };
 template <Units U>
-DDT_DEVINL int num_units(const PtArgs &a) { return U == BOTH ? a.ngroups + a.R : U == PREFIXES ? a.ngroups : a.R; }
+DDT_DEVINL int num_units(const PtArgs &a) { return U == PREFIXES ? a.ngroups : a.R; }
 
 // sound: whether its lengths are (a unit that is not has no tokens)
 template <Units U = PLAIN>
@@ -150,7 +152,7 @@ DDT_DEVINL PpReq load_req(const PtArgs &a, int r, bool *sound = nullptr)
     PpReq q = {0, 0, 0, 0, 0};
     int g0 = 0, g1 = a.T, least = 0;  // where a group's member's rows lie, and what is cached at least
     if (U != PLAIN) {
-        if (U == PREFIXES || (U == BOTH && r < a.ngroups)) {
+        if (U == PREFIXES) {
             q = load_group(a, r);
             if (sound)
                 *sound = group_ok(a, r);
@@ -158,8 +160,6 @@ DDT_DEVINL PpReq load_req(const PtArgs &a, int r, bool *sound = nullptr)
                 q.len = 0;
             return q;
         }
-        if (U == BOTH)
-            r -= a.ngroups;
         const int g = group_of(a, r);
         if (g >= 0) {
             const PpReq pre = load_group(a, g);
@@ -177,6 +177,15 @@ DDT_DEVINL PpReq load_req(const PtArgs &a, int r, bool *sound = nullptr)
     q.ctx = c;
     q.len = ok ? s1 - s0 : 0;
     return q;
+}
+
+// The end of the launch of own keys, which begins while that of the prefixes still runs: it
+// may not end before that, since the merge waits for this one only. One CTA, the last to
+// begin, waits; the others would keep theirs from an SM.
+DDT_DEVINL void own_done()
+{
+    if (blockIdx.x == gridDim.x - 1)
+        pdl_wait();
 }
 
 // one thread of a segment's: who had the item's ends (prefixes', or own keys')
@@ -206,18 +215,10 @@ DDT_DEVINL bool page_ok(const PtArgs &a, int pg)
         atomicOr(a.status, DDT_DEV_BAD_PAGE);
     return false;
 }
-// this CTA's share: the totals by a scan over the requests (whole block), then
-// the request that holds the share's first unit. found: [0] request, [1..2] its
-// first unit, [3..4] total
-template <Units U = PLAIN>
-DDT_DEVINL void find_share(const PtArgs &a, int tq, int grid, int cta, long long *sums,
-                           volatile long long *found, int tid, int nthreads)
+// all units of a launch (every thread of the block gives its own sum, and learns the sums of
+// the warps)
+DDT_DEVINL long long block_units(long long mine, long long *sums, int tid, int nthreads, long long &excl)
 {
-    const int count = num_units<U>(a), per = (count + nthreads - 1) / nthreads;
-    const int r0 = min(tid * per, count), r1 = min(r0 + per, count);
-    long long mine = 0;
-    for (int r = r0; r < r1; ++r)
-        mine += pp_units(load_req<U>(a, r), tq, a.Hkv);
     long long incl = mine;
     const int lane = tid & 31, warp = tid >> 5;
 #pragma unroll
@@ -234,14 +235,43 @@ DDT_DEVINL void find_share(const PtArgs &a, int tq, int grid, int cta, long long
         before += w < warp ? sums[w] : 0;
         total += sums[w];
     }
-    const long long excl = before + incl - mine;
+    excl = before + incl - mine;
+    return total;
+}
+
+// this CTA's share: the totals by a scan over the requests (whole block), then
+// the request that holds the share's first unit. found: [0] request, [1] its first unit,
+// [2] total, [3] CTAs that share. Prefixes may take a part of the grid: what is left of it
+// ends at once, and the launch of the own keys has those SMs meanwhile.
+template <Units U = PLAIN>
+DDT_DEVINL void find_share(const PtArgs &a, int tq, int grid, int cta, long long *sums,
+                           volatile long long *found, int tid, int nthreads)
+{
+    const int count = num_units<U>(a), per = (count + nthreads - 1) / nthreads;
+    const int r0 = min(tid * per, count), r1 = min(r0 + per, count);
+    long long mine = 0, excl;
+    for (int r = r0; r < r1; ++r)
+        mine += pp_units(load_req<U>(a, r), tq, a.Hkv);
+    const long long total = block_units(mine, sums, tid, nthreads, excl);
+    int nc = total > 0 ? pp_ctas(total, grid, MIN_UNITS) : 1;
+    if (U == PREFIXES) {
+        __syncthreads();
+        long long own = 0, none;
+        for (int r = tid; r < a.R; r += nthreads)
+            own += pp_units(load_req<OWN>(a, r), a.own_rows >> a.g_shift, a.Hkv);
+        own = block_units(own, sums, tid, nthreads, none);
+        // as many as are done, beginning and end included, when the own keys are on the rest
+        const long long p = total * a.cost[0], all = (p + own * a.cost[1]) / grid;
+        if (a.cost[1] > 0)
+            nc = min(nc, (int)min((long long)grid, 1 + p / max(all - a.cost[2], 30LL)));
+    }
     if (tid == 0) {
         found[0] = -1;
         found[2] = total;
+        found[3] = nc;
     }
     __syncthreads();
     if (total > 0) {
-        const int nc = pp_ctas(total, grid, MIN_UNITS);
         const long long lo = pp_share(total, cta, nc);
         if (cta < nc && excl <= lo && lo < excl + mine) {
             long long acc = excl;
@@ -269,7 +299,7 @@ struct ShareWalk {
     PpItem it;
     int cta;
 
-    DDT_DEVINL void begin(const PtArgs &a, const volatile long long *found, int tq, int grid, int c)
+    DDT_DEVINL void begin(const PtArgs &a, const volatile long long *found, int tq, int c)
     {
         const long long total = found[2];
         r = (int)found[0];
@@ -277,7 +307,7 @@ struct ShareWalk {
         cta = c;
         cur = hi = 0;
         if (r >= 0) {
-            const int nc = pp_ctas(total, grid, MIN_UNITS);
+            const int nc = (int)found[3];
             cur = pp_share(total, c, nc);
             hi = pp_share(total, c + 1, nc);
             rq = load_req<U>(a, r);
@@ -306,7 +336,7 @@ struct ShareWalk {
             s.last = U != PLAIN && t1 == it.n;
             s.split = (s.ntok << a.g_shift) <= split_rows;
             s.slot = 2 * cta + (t0 > 0 ? 0 : 1);
-            const int sr = U == PREFIXES || (U == BOTH && r < a.ngroups) ? __ldg(&a.group_start[r]) : U == BOTH ? r - a.ngroups : r;
+            const int sr = U == PREFIXES ? __ldg(&a.group_start[r]) : r;
             cur = min(hi, i1);
             if (cur < hi) {  // the item behind it
                 it.start += it.n + PP_ITEM;
@@ -372,7 +402,7 @@ constexpr int MG_THREADS = 256, MG_SPLIT = 4;
 template <int D>
 __global__ void __launch_bounds__(MG_THREADS) prompt_merge_kernel(const PtArgs a, int grid, int rows)
 {
-    __shared__ long long s_sums[MG_THREADS / 32], s_found[3];
+    __shared__ long long s_sums[MG_THREADS / 32], s_found[4];
     const int tq = rows >> a.g_shift, tid = threadIdx.x, b = blockIdx.x + 1;
     find_share(a, tq, grid, b, s_sums, s_found, tid, MG_THREADS);
     const long long total = s_found[2], base = s_found[1];

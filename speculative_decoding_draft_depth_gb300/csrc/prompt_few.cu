@@ -181,7 +181,7 @@ __global__ void __launch_bounds__(FT, NR == 1 ? 2 : 1) prompt_few_kernel(const F
     float2 *sml = reinterpret_cast<float2 *>(so + FW * ROWS * D);  // [FW][ROWS]
     unsigned char *rawp = reinterpret_cast<unsigned char *>(sml + FW * ROWS) + (threadIdx.x >> 5) * FS * RAW_BYTES<D>;
     const uint32_t raws = (uint32_t)__cvta_generic_to_shared(rawp);
-    __shared__ long long s_sums[FW], s_found[3];
+    __shared__ long long s_sums[FW], s_found[4];
     const PtArgs &a = f.a;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, i = lane >> 2, c = lane & 3;
     const int tq = ROWS >> a.g_shift, G = 1 << a.g_shift;
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(FT, NR == 1 ? 2 : 1) prompt_few_kernel(const F
     Copier<D> copier;
     copier.begin(a, lane);
     ShareWalk<U> walk;
-    walk.begin(a, s_found, tq, gridDim.x, blockIdx.x);
+    walk.begin(a, s_found, tq, blockIdx.x);
     // this warp's blocks of a segment: the next one, their end, the page of the one FS
     // turns ahead; their copies begin while the segment before is merged
     int blk = 0, bend = 0, page = NO_PAGE;
@@ -457,16 +457,16 @@ __global__ void __launch_bounds__(FT, NR == 1 ? 2 : 1) prompt_few_kernel(const F
                     a.store_ml[1][at] = make_float2(M, L);
             } else {
                 const int64_t slot = (int64_t)was.slot * ROWS;
-                reinterpret_cast<float4 *>((U == PLAIN ? a.part_o : a.few_o) + slot * D)[c4 * ROWS + row] = r;
+                reinterpret_cast<float4 *>((U == PLAIN ? a.part_o : a.own_o) + slot * D)[c4 * ROWS + row] = r;
                 if (c4 == 0)
-                    (U == PLAIN ? a.part_ml : a.few_ml)[slot + row] = make_float2(M, L);
+                    (U == PLAIN ? a.part_ml : a.own_ml)[slot + row] = make_float2(M, L);
             }
         }
         __syncthreads();
     }
     cp_async_wait_all();
     if (U != PLAIN)
-        pdl_wait();  // (the prefixes' kernel is before this one; the merge waits for this one only)
+        own_done();  // (the prefixes' kernel is before this one; the merge waits for this one only)
 }
 
 template <int D, int NR, Units U>
@@ -485,7 +485,7 @@ cudaError_t launch_few(const FewArgs &f, int dev, int num_sms, cudaStream_t s)
     const int grid = (num_sms < PR_MAX_CTAS ? num_sms : PR_MAX_CTAS) * (NR == 1 ? 2 : 1);
     if (U != PLAIN) {  // (beside the prefixes' kernel, which reads and writes elsewhere)
         cudaLaunchConfig_t lc = {};
-        lc.gridDim = dim3(grid);
+        lc.gridDim = dim3((num_sms < PR_MAX_CTAS ? num_sms : PR_MAX_CTAS) * OWN_FEW_CTAS);
         lc.blockDim = dim3(FT);
         lc.dynamicSmemBytes = BYTES;
         lc.stream = s;

@@ -132,15 +132,15 @@ constexpr uint32_t B_QFULL = 0, B_QEMPTY = 8, B_KFULL = 16, B_KEMPTY = 32, B_VFU
                    B_RFULL = 240,     // [NRING]
                    B_REMPTY = 304,    // [NRING]
                    B_RING = 368,      // [NRING][8] ints
-                   B_FOUND = 624,     // three 64-bit words of the share search: apart from the ring, whose first
+                   B_FOUND = 624,     // four 64-bit words of the share search: apart from the ring, whose first
                                       // entry one lane of the walker writes while others may still read them
-                   B_ML = 648,        // [128] float2: B's (m, l); before the roles start, the scan's sums
-                   B_ROWSC = 1672;    // 4 bits: [2][256] floats: the row's factor, by item parity
+                   B_ML = 656,        // [128] float2: B's (m, l); before the roles start, the scan's sums
+                   B_ROWSC = 1680;    // 4 bits: [2][256] floats: the row's factor, by item parity
 template <bool KV4>
 constexpr uint32_t B_END = B_ROWSC + (KV4 ? 2048 : 0);
 template <bool KV4>
 constexpr uint32_t SM_ALLOC = SM_BAR<KV4> + B_END<KV4> + 1024;
-static_assert(B_FOUND >= B_RING + NRING * 8 * 4 && B_ML >= B_FOUND + 3 * 8, "the share search's words are their own");
+static_assert(B_FOUND >= B_RING + NRING * 8 * 4 && B_ML >= B_FOUND + 4 * 8, "the share search's words are their own");
 static_assert(B_ML % 8 == 0 && B_ROWSC >= B_ML + 128 * 8, "(m, l) pairs");
 static_assert(SM_ALLOC<false> <= 232448 && SM_ALLOC<true> <= 232448, "shared memory of one CTA");
 
@@ -452,7 +452,7 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
                     atomicOr(a.status, DDT_DEV_BAD_LENGTH);
             }
         ShareWalk<U> walk;
-        walk.begin(a, found, tq, gridDim.x, blockIdx.x);
+        walk.begin(a, found, tq, blockIdx.x);
         int k = 0, kn = 0;
         bool ok = true;
         if (a.debug_wait > 0)  // (armed by a test) nothing is announced: this wait runs out, and the other roles give up
@@ -1017,6 +1017,8 @@ prompt_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     tc_fence_after();
     if (warp == W_MMA)
         tmem_dealloc(tmem, TMEM_COLS);
+    if (U == OWN)
+        own_done();
 }
 
 // ------------------------------------------------------------------ host side
@@ -1074,8 +1076,17 @@ cudaError_t launch_main(int dev, int grid, const CUtensorMap &tq, const CUtensor
             return cudaErrorLaunchOutOfResources;
         ready.set(dev);
     }
-    prompt_tc_kernel<D, KV4, U><<<grid, NT<KV4>, SM_ALLOC<KV4>, s>>>(tq, tk, tv, a);
-    return cudaGetLastError();
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(grid);
+    lc.blockDim = dim3(NT<KV4>);
+    lc.dynamicSmemBytes = SM_ALLOC<KV4>;
+    lc.stream = s;
+    cudaLaunchAttribute at[1];  // (own keys beside the prefixes' kernel, which reads and writes elsewhere)
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = at;
+    lc.numAttrs = U == OWN ? 1 : 0;
+    return cudaLaunchKernelEx(&lc, prompt_tc_kernel<D, KV4, U>, tq, tk, tv, a);
 }
 
 // the maps of the queries and (bf16) of the cache
