@@ -48,6 +48,23 @@ DDT_DEVINL uint32_t sb_count(uint32_t word, int d)
 __host__ __device__ constexpr int sb_part(int cl) { return (SB_VALUES + cl - 1) / cl; }
 __host__ __device__ constexpr int sb_bytes(int cl) { return (SB_WORDS * 4 + 15) / 16 * 16 + sb_part(cl) * 12 + 16; }
 
+// where a logit's bits are counted (0: zeros, 1: what is smaller than 2^-30, SB_WORDS - 1: what
+// is larger), and whether they are
+DDT_DEVINL int sb_place(uint32_t b)
+{
+    const uint32_t mag = b & 0x7FFFu;
+    return min(max((int)mag - (SB_LOW - 2), min((int)mag, 1)), SB_WORDS - 1);
+}
+DDT_DEVINL bool sb_counts(uint32_t b) { return b < 0x8000u + SB_LOW + SB_MAGS; }  // (not the negative ones beyond)
+
+// what the settings keep, as a value of which so many count, and its sum
+struct Kept {
+    int d;           // SB_VALUES: everything
+    uint64_t count;  // of value d
+    uint64_t of;     //   out of so many
+    uint64_t mass;
+};
+
 template <int CL>
 struct BinShared {
     uint64_t mass[CL][CL];  // [of a part of the values][in a CTA's slice]
@@ -91,10 +108,8 @@ struct BinRow {
 
     DDT_DEVINL void add(uint32_t b) const  // one logit's bits
     {
-        const uint32_t mag = b & 0x7FFFu;
-        const int word = min(max((int)mag - (SB_LOW - 2), min((int)mag, 1)), SB_WORDS - 1);
-        if (b < 0x8000u + SB_LOW + SB_MAGS)  // (not the negative ones beyond)
-            atomicAdd(&hist[word], b & 0x8000u ? 0x10000u : 1u);
+        if (sb_counts(b))
+            atomicAdd(&hist[sb_place(b)], b & 0x8000u ? 0x10000u : 1u);
     }
     DDT_DEVINL void add2(uint32_t x, uint32_t &least2) const
     {
@@ -118,13 +133,6 @@ struct BinRow {
         }
     }
 
-    // the border of what the settings keep, as a value, how many of it, and all that is kept
-    struct Kept {
-        int d;           // SB_VALUES: everything
-        uint64_t count;  // of value d
-        uint64_t of;     //   out of so many
-        uint64_t mass;
-    };
     // counts, weights, borders. false: this row is not one for counting
     DDT_DEVINL bool run(const Settings &set, const Scale &sc, Kept &k)
     {
@@ -436,5 +444,212 @@ struct BinRow {
         return t;
     }
 };
+
+// The same for a row that one CTA reads from global memory: a 32-bit count each of a
+// magnitude's two signs; weights are made where they are needed (a thread has some twenty
+// values, few of which occur). Under top-p alone only the front of the row is counted, and
+// the tokens behind it are added up by quick weights: a sixteenth of the row tells from where
+// up the tokens hold more than p of the sum, and the border stands unless two tokens lie
+// within the error of that small rest.
+struct FarBins {
+    using Base = Row<uint16_t, true>;
+    static constexpr int T = Base::THREADS, SAMPLE = 16;
+    Base &row;
+    const Scale &sc;
+    uint32_t *hist;      // 2 SB_WORDS
+    float least;         // values from here up may count
+    float from;          //   and are counted from here up
+    int a, b;            // this thread's values
+    uint64_t cnt, mass;  //   their tokens and weights
+    uint64_t cnt0, mass0, cnt_all, mass_all;  // before them, and of all that are counted
+    uint64_t rest;       // weights of the others, quick ones
+
+    DDT_DEVINL uint32_t count(int d) const
+    {
+        const int w = 2 * sb_word(d);
+        return d < SB_MAGS ? hist[w] : d > SB_MAGS ? hist[w + 1] : hist[w] + hist[w + 1];
+    }
+    DDT_DEVINL uint64_t weight(int d) const { return weight_of<false>(sc, row.sh->tab, sb_value(d)); }
+
+    // a value from which up the tokens very likely weigh more than p of all
+    DDT_DEVINL float front(float p, float low)
+    {
+        const float vlo = fmaxf(low, least), scale = row.bin_scale(sc.zmax, vlo);
+        row.clear_hist();
+        const int ng = row.sl.groups(), n_look = min(ng, max(Base::WARPS, ng / SAMPLE));
+        for (int g = row.warp; g < n_look; g += Base::WARPS) {
+            uint4 x[SR_GROUP];
+            row.sl.raws((int)((int64_t)g * ng / n_look) * SR_GROUP, row.lane, x);
+#pragma unroll
+            for (int i = 0; i < SR_GROUP; ++i) {
+                float z[8];
+                row.sl.values(x[i], z);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (z[e] >= vlo)
+                        atomicAdd(&row.sh->hist[row.bin_of(sc.zmax, scale, z[e])], 1u);
+            }
+        }
+        __syncthreads();
+        uint32_t n[2];
+        row.row_bins(n[0], n[1]);
+        const float inv = scale > 0.f ? 1.f / scale : 0.f, share = (float)ng / n_look;
+        uint64_t w[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            w[x] = __float2ull_rn((float)n[x] * share * ex2(-(2 * row.tid + x) * inv * sc.ch) * 17592186044416.0f);
+        const uint64_t incl = row.block_incl(w[0] + w[1]);
+        __syncthreads();
+        if (row.tid == T - 1)
+            row.sh->warp[0][1] = incl;
+        __syncthreads();
+        const uint64_t all = row.sh->warp[0][1], tail = (uint64_t)((1.f - p) * 0.5f * (float)all);
+        // the first bin behind which no more than `tail` lies
+        const int bin = row.block_least(all - (incl - w[1]) <= tail ? 2 * row.tid : all - incl <= tail ? 2 * row.tid + 1 : 0x7FFFFFFF);
+        return bin >= SR_BINS - 1 || !(scale > 0.f) ? least : fmaxf(least, sc.zmax - (bin + 1) * inv);
+    }
+    // count the tokens from `from` up. false: not a row for this
+    DDT_DEVINL bool run()
+    {
+        const int tid = row.tid;
+        for (int i = tid; i < 2 * SB_WORDS; i += T)
+            hist[i] = 0;
+        __syncthreads();
+        uint32_t least2 = 0x7F807F80u;
+        const bool some = from > least, positive = some && from >= 9.313225746e-10f && sc.zmax < 128.f;  // (2^-30)
+        rest = 0;
+        row.each([&](int, const uint4 &v) {
+            if (some) {
+                float z[8];
+                Vec<uint16_t>::get(v, z);
+                uint64_t w = 0;
+#pragma unroll
+                for (int e = 0; e < 8; e += 2)
+                    w = f2add(w, quick_weights<false>(sc, z[e], z[e + 1], z[e] >= least && z[e] < from,
+                                                      z[e + 1] >= least && z[e + 1] < from));
+                float w0, w1;
+                f2unpack(w, w0, w1);
+                rest += __float2ull_rn((w0 + w1) * 17592186044416.0f);
+                if (!Vec<uint16_t>::reaches(v, from))
+                    return;
+            }
+            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+            if (positive) {  // (the same, in fewer instructions)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (bf16lo(x[i]) >= from)
+                        atomicAdd(&hist[2 * ((int)(x[i] & 0xFFFFu) - (SB_LOW - 2))], 1u);
+                    if (bf16hi(x[i]) >= from)
+                        atomicAdd(&hist[2 * ((int)(x[i] >> 16) - (SB_LOW - 2))], 1u);
+                }
+                return;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                asm("min.bf16x2 %0, %0, %1;" : "+r"(least2) : "r"(x[i]));
+                const uint32_t lo = x[i] & 0xFFFFu, hi = x[i] >> 16;
+                if (some ? bf16lo(x[i]) >= from : sb_counts(lo))
+                    atomicAdd(&hist[2 * sb_place(lo) + (lo >> 15)], 1u);
+                if (some ? bf16hi(x[i]) >= from : sb_counts(hi))
+                    atomicAdd(&hist[2 * sb_place(hi) + (hi >> 15)], 1u);
+            }
+        });
+        const bool low = __syncthreads_or(fminf(bf16lo(least2), bf16hi(least2)) <= -128.f);
+        if (hist[2] != 0 || hist[3] != 0 || hist[2 * SB_WORDS - 2] != 0 || sc.zmax <= -128.f || (low && fmaxf(from, sc.zfloor) < -128.f))
+            return false;
+        // (with the front alone, its values only: that of `from` rounded down, and above)
+        const int d_end = positive ? SB_MAGS + 2 - sb_place(__float_as_uint(from) >> 16) : SB_VALUES;
+        const int d_first = positive ? SB_MAGS + 1 - sb_place(__float_as_uint(sc.zmax) >> 16) : 0;
+        const int per = (d_end - d_first + T - 1) / T;
+        a = min(d_end, d_first + tid * per);
+        b = min(d_end, a + per);
+        cnt = mass = 0;
+        for (int d = a; d < b; ++d) {
+            const uint32_t n = count(d);
+            if (n > 0 && sb_value(d) >= least) {
+                cnt += n;
+                mass += n * weight(d);
+            }
+        }
+        cnt0 = row.block_incl(cnt) - cnt;
+        mass0 = row.block_incl(mass) - mass;
+        __syncthreads();
+        if (tid == T - 1) {
+            row.sh->warp[0][1] = cnt0 + cnt;
+            row.sh->warp[0][2] = mass0 + mass;
+        }
+        __syncthreads();
+        cnt_all = row.sh->warp[0][1];
+        mass_all = row.sh->warp[0][2];
+        if (some)
+            rest = row.block_sum(rest);
+        return true;
+    }
+    // the value at which the tokens (or their weights) reach `want`, which they do
+    DDT_DEVINL Kept find(bool tokens, uint64_t want)
+    {
+        const uint64_t before = tokens ? cnt0 : mass0, own = tokens ? cnt : mass;
+        uint64_t *to = row.sh->list;
+        __syncthreads();
+        if (before < want && want <= before + own) {
+            uint64_t q = cnt0, m = mass0;
+            for (int d = a; d < b; ++d) {
+                const uint32_t n = count(d);
+                if (n == 0 || !(sb_value(d) >= least))
+                    continue;
+                const uint64_t w = weight(d);
+                const uint64_t c = tokens ? want - q : w > 0 ? (want - m + w - 1) / w : n + 1ull;
+                if (c <= n) {
+                    to[0] = ((uint64_t)d << 32) | (uint32_t)c;
+                    to[1] = n;
+                    to[2] = m + c * w;
+                    break;
+                }
+                q += n;
+                m += n * w;
+            }
+        }
+        __syncthreads();
+        return {(int)(to[0] >> 32), (uint32_t)to[0], to[1], to[2]};
+    }
+    DDT_DEVINL bool solve(const Settings &set, float low, Kept &k)
+    {
+        least = fmaxf(sc.zfloor, set.m > 0.f ? min_value(sc.zmax, row.sh->off) : DDT_NEG_INF);
+        if (!(set.k > 0 && set.k < row.sl.V)) {
+            from = front(set.p, low);
+            if (!run())
+                return false;
+            const uint64_t slack = quick_slack(rest) + 1, most = Base::share_of(set.p, mass_all + rest + slack);
+            if (from > least && most <= mass_all) {
+                k = find(false, max(Base::share_of(set.p, mass_all + rest - min(rest, slack)), (uint64_t)1));
+                const Kept other = find(false, max(most, (uint64_t)1));
+                if (k.d == other.d && k.count == other.count)
+                    return true;
+            }
+            if (!(from > least)) {  // (all of it has been counted)
+                k = find(false, max(Base::share_of(set.p, mass_all), (uint64_t)1));
+                return true;
+            }
+        }
+        from = least;
+        if (!run())
+            return false;
+        k = {SB_VALUES, 0, 0, mass_all};
+        if (set.k > 0 && (uint64_t)set.k < cnt_all)
+            k = find(true, set.k);
+        if (set.p < 1.f)
+            k = find(false, max(Base::share_of(set.p, k.mass), (uint64_t)1));
+        return true;
+    }
+    // the border that this is
+    DDT_DEVINL Border border(const Kept &k, uint64_t *sub)
+    {
+        Border r = {k.d == SB_VALUES ? least : sb_value(k.d), 0x7FFFFFFF};
+        if (k.d != SB_VALUES && k.count != k.of)
+            r.last = row.nth_equal(r, r.z, k.count, sub);
+        return r;
+    }
+};
+constexpr int FB_BYTES = 2 * SB_WORDS * 4;
 
 }  // namespace

@@ -16,13 +16,14 @@
 // is kept), and added up as 64-bit integers in units of 2^-44, whose sums do not depend
 // on an order. What is below 2^-64 of the largest weight counts as zero.
 //
-// A row is read from HBM once: the CTAs of its cluster hold it in shared memory (sub-
-// chunks of 512 bytes: 16 bytes a lane), and every further look at it reads that. What
+// A row is read from HBM once (but see FAR below): the CTAs of its cluster hold it in shared
+// memory (sub-chunks of 512 bytes: 16 bytes a lane), and every further look at it reads that. What
 // the CTAs have to tell one another goes through distributed shared memory, one cluster
 // barrier an exchange, and each CTA then comes to the same decision by itself.
 #pragma once
 
 #include <stdint.h>
+#include <string.h>
 
 #include "ddt_device.cuh"
 #include "ddt_internal.h"
@@ -31,6 +32,9 @@ namespace {
 
 constexpr int SR_THREADS = 256, SR_WARPS = SR_THREADS / 32;
 constexpr int SR_SUB = 512;       // bytes of a sub-chunk
+constexpr int SR_FAR = 512;       // threads of a CTA that reads a row from global memory
+constexpr int SR_GROUP = 4;       // sub-chunks that a warp takes at once from global memory
+constexpr int SR_OWN = 8;         // parts of a thread's logits of which it knows the largest there
 constexpr int SR_MAX_CL = 16;     // CTAs of a cluster
 constexpr int SR_CAP = 512;       // candidates that are sorted in one place
 constexpr int SR_PROBE = 256;     // how many the first collection asks for, and the largest k that it serves
@@ -326,7 +330,7 @@ struct Xchg {
 struct RowShared {
     float2 tab[32];
     Xchg x;
-    uint64_t warp[SR_WARPS][4];
+    uint64_t warp[SR_FAR / 32][4];
     uint64_t list[SR_CAP];   // candidates: (order_key << 32) | ~index
     uint64_t mine[SR_CAP];   //   of this CTA's slice
     uint32_t hist[SR_BINS];
@@ -336,37 +340,52 @@ struct RowShared {
     uint64_t kept[SR_SMALL]; // the candidates' weights
 };
 
-// 16 bytes of logits. Range: their largest, and their least but for -infinity; look() says
-// whether there are odd ones among them: NaN, or not 0 and next to 0 (SR_TINY)
+// 16 bytes of logits. Range: the largest and the least that look() has seen; odd(): there may
+// be odd ones among them: NaN (which is then the largest), or not 0 and next to 0 (SR_TINY)
 template <typename T> struct Vec;
 template <> struct Vec<uint16_t> {
     static constexpr int E = 8;
     static constexpr bool EXACT = false;
     static constexpr uint32_t NONE = 0xFF80FF80u;
     struct Range {
-        uint32_t hi, lo;
+        uint32_t hi, lo, odd;  // odd: the least of (bits of the magnitude) - 1, of either half
     };
-    DDT_DEVINL static void begin(Range &r) { r = {NONE, 0x7F7F7F7Fu}; }
-    DDT_DEVINL static bool look(Range &r, const uint4 &v)
+    DDT_DEVINL static void begin(Range &r) { r = {NONE, 0x7F7F7F7Fu, 0xFFFFFFFFu}; }
+    DDT_DEVINL static void look(Range &r, const uint4 &v)
     {
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        bool bad = false;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            asm("max.bf16x2 %0, %0, %1;" : "+r"(r.hi) : "r"(w[i]));
-            uint32_t x;  // (x 0 + x: an infinity becomes NaN, which the least is not)
-            asm("fma.rn.bf16x2 %0, %1, %2, %1;" : "=r"(x) : "r"(w[i]), "r"(0u));
-            asm("min.bf16x2 %0, %0, %1;" : "+r"(r.lo) : "r"(x));
-            const uint32_t a = w[i] & 0x7FFFu, b = (w[i] >> 16) & 0x7FFFu;
-            // bits of an odd value: 1 .. 2^-90's less 1, or above infinity's
-            bad |= a - 1 < (37u << 7) - 1 || a > 0x7F80u || b - 1 < (37u << 7) - 1 || b > 0x7F80u;
+            asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(r.hi) : "r"(w[i]));
+            asm("min.bf16x2 %0, %0, %1;" : "+r"(r.lo) : "r"(w[i]));
+            // (a zero in the low half takes one more from the high half, which then counts as
+            // odd one bit pattern early)
+            asm("min.u16x2 %0, %0, %1;" : "+r"(r.odd) : "r"((w[i] & 0x7FFF7FFFu) - 0x00010001u));
         }
-        return bad;
+    }
+    DDT_DEVINL static bool odd(const Range &r)
+    {
+        const uint32_t a = r.odd & 0xFFFFu, b = r.odd >> 16;
+        const float x = bf16lo(r.hi), y = bf16hi(r.hi);
+        return a < (37u << 7) - 1 || b < (37u << 7) - 1 || x != x || y != y;
     }
     DDT_DEVINL static void end(const Range &r, float &hi, float &lo)
     {
         hi = fmaxf(bf16lo(r.hi), bf16hi(r.hi));
         lo = fminf(bf16lo(r.lo), bf16hi(r.lo));
+    }
+    DDT_DEVINL static uint4 put(const uint16_t *x)
+    {
+        return make_uint4(x[0] | (uint32_t)x[1] << 16, x[2] | (uint32_t)x[3] << 16, x[4] | (uint32_t)x[5] << 16,
+                          x[6] | (uint32_t)x[7] << 16);
+    }
+    // whether one of them reaches `from`
+    DDT_DEVINL static bool reaches(const uint4 &v, float from)
+    {
+        uint32_t m;
+        asm("{\n .reg .b32 a, b;\n max.bf16x2 a, %1, %2;\n max.bf16x2 b, %3, %4;\n max.bf16x2 %0, a, b;\n}\n"
+            : "=r"(m) : "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w));
+        return bf16lo(m) >= from || bf16hi(m) >= from;
     }
     DDT_DEVINL static void get(const uint4 &v, float *z)
     {
@@ -384,25 +403,34 @@ template <> struct Vec<float> {
     static constexpr uint32_t NONE = 0xFF800000u;
     struct Range {
         float hi, lo;
+        uint32_t odd;
     };
-    DDT_DEVINL static void begin(Range &r) { r = {DDT_NEG_INF, SR_MAX_FLOAT}; }
-    DDT_DEVINL static bool look(Range &r, const uint4 &v)
+    DDT_DEVINL static void begin(Range &r) { r = {DDT_NEG_INF, SR_MAX_FLOAT, 0xFFFFFFFFu}; }
+    DDT_DEVINL static void look(Range &r, const uint4 &v)
     {
-        float z[E];
-        get(v, z);
-        bool bad = false;
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            r.hi = fmaxf(r.hi, z[e]);
-            r.lo = fminf(r.lo, fmaf(z[e], 0.f, z[e]));  // (an infinity becomes NaN, which the least is not)
-            bad |= !(fabsf(z[e]) >= SR_TINY) && z[e] != 0.f;
+            asm("max.NaN.f32 %0, %0, %1;" : "+f"(r.hi) : "f"(__uint_as_float(w[e])));
+            r.lo = fminf(r.lo, __uint_as_float(w[e]));
+            r.odd = min(r.odd, (w[e] & 0x7FFFFFFFu) - 1u);
         }
-        return bad;
     }
+    DDT_DEVINL static bool odd(const Range &r) { return r.odd < (37u << 23) - 1 || r.hi != r.hi; }
     DDT_DEVINL static void end(const Range &r, float &hi, float &lo)
     {
         hi = r.hi;
         lo = r.lo;
+    }
+    DDT_DEVINL static uint4 put(const float *x)
+    {
+        return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
+    }
+    DDT_DEVINL static bool reaches(const uint4 &v, float from)
+    {
+        float z[E];
+        get(v, z);
+        return fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])) >= from;
     }
     DDT_DEVINL static void get(const uint4 &v, float *z)
     {
@@ -431,27 +459,32 @@ template <typename T>
 __host__ __device__ constexpr int slice_subs(int V, int cl) { return (row_subs<T>(V) + cl - 1) / cl; }
 
 // The slice of a row that a CTA holds. Element (sub-chunk s, lane, e) has index
-// index0(s, lane) + e.
-template <typename T>
+// index0(s, lane) + e. FAR: the whole row, where it is in global memory.
+template <typename T, bool FAR>
 struct Slice {
     static constexpr int E = Vec<T>::E, SE = SR_SUB / (int)sizeof(T);
+    static constexpr int G = FAR ? SR_GROUP : 1;  // sub-chunks of a group
     unsigned char *at;  // ns sub-chunks
+    const T *base;      // the tensor's 16-byte vector that the row begins in
     int s0, ns, off, V;
+    bool odd, infinite;  // FAR: the row has odd values; infinities
 
     DDT_DEVINL void place(unsigned char *smem, const T *row, int V_, uint32_t rank, uint32_t cl)
     {
         at = smem;
+        odd = infinite = false;
         V = V_;
         off = (int)(((uintptr_t)row & 15) / sizeof(T));
         const int subs = (int)(((int64_t)off + V + SE - 1) / SE);
         s0 = (int)((int64_t)subs * rank / cl);
         ns = (int)((int64_t)subs * (rank + 1) / cl) - s0;
+        base = row - off;
     }
+    DDT_DEVINL int groups() const { return (ns + G - 1) / G; }
     // start this thread's copies. Whole 16-byte vectors of the row; what is before the
     // row's first element comes from the row before it (the tensor begins on 16 bytes)
-    DDT_DEVINL void fetch(const T *row, int tid) const
+    DDT_DEVINL void fetch(int tid) const
     {
-        const T *base = row - off;
         const uint32_t dst = (uint32_t)__cvta_generic_to_shared(at);
         const int64_t end = (int64_t)off + V;
         for (int v = tid; v < ns * 32; v += SR_THREADS) {
@@ -478,8 +511,58 @@ struct Slice {
         if (s0 == 0 && ns > 0 && tid < off)
             reinterpret_cast<T *>(at)[tid] = none();
     }
-    DDT_DEVINL uint4 raw(int s, int lane) const { return *reinterpret_cast<const uint4 *>(at + s * SR_SUB + lane * 16); }
-    DDT_DEVINL void get(int s, int lane, float *z) const { Vec<T>::get(raw(s, lane), z); }
+    // a lane's vector of a sub-chunk (FAR: any sub-chunk; what is not the row's is -infinity)
+    DDT_DEVINL uint4 raw(int s, int lane) const
+    {
+        if (!FAR)
+            return *reinterpret_cast<const uint4 *>(at + s * SR_SUB + lane * 16);
+        const int j = s * SE + lane * E;  // its first element, from base (off + V stays below 2^31)
+        if (j >= off && j - off <= V - E)
+            return __ldg(reinterpret_cast<const uint4 *>(base + j));
+        T x[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            x[e] = j + e >= off && j + e - off < V ? __ldg(base + j + e) : none();
+        return Vec<T>::put(x);
+    }
+    // those of N sub-chunks (FAR: where all of it is the row's, loads with no branch between)
+    template <int N>
+    DDT_DEVINL void raws(int s, int lane, uint4 (&x)[N]) const
+    {
+        if (FAR && s * SE >= off && (s + N) * SE <= off + V) {
+            const uint4 *p = reinterpret_cast<const uint4 *>(base) + s * 32 + lane;
+#pragma unroll
+            for (int b = 0; b < N; ++b)
+                x[b] = __ldg(p + b * 32);
+        } else {
+#pragma unroll
+            for (int b = 0; b < N; ++b)
+                x[b] = raw(s + b, lane);
+        }
+    }
+    // a vector without odd values: a NaN is -infinity, what is next to 0 is 0
+    DDT_DEVINL static uint4 mended(const uint4 &v)
+    {
+        T x[E];
+        memcpy(x, &v, 16);
+        float z[E];
+        Vec<T>::get(v, z);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            x[e] = z[e] != z[e] ? none() : fabsf(z[e]) < SR_TINY ? (T)0 : x[e];
+        return Vec<T>::put(x);
+    }
+    // its logits, as the row holds them
+    DDT_DEVINL void values(const uint4 &v, float *z) const
+    {
+        Vec<T>::get(v, z);
+        if (FAR && odd) {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                z[e] = held_value(z[e], infinite);
+        }
+    }
+    DDT_DEVINL void get(int s, int lane, float *z) const { values(raw(s, lane), z); }
     DDT_DEVINL int index0(int s, int lane) const { return (s0 + s) * SE + lane * E - off; }
 };
 
@@ -502,13 +585,17 @@ DDT_DEVINL uint64_t warp_incl64(uint64_t v, int lane)
     return v;
 }
 
-// One row of a cluster: what its threads share in doing it.
-template <typename T>
+// One row of a cluster: what its threads share in doing it. FAR: of one CTA that reads it
+// from global memory each time.
+template <typename T, bool FAR = false>
 struct Row {
+    static constexpr int THREADS = FAR ? SR_FAR : SR_THREADS, WARPS = THREADS / 32;
+    static constexpr int OWN = FAR ? SR_OWN : 1;
     static constexpr int E = Vec<T>::E;
     static constexpr bool EXACT = Vec<T>::EXACT;
     RowShared *sh;
-    Slice<T> sl;
+    using Part = Slice<T, FAR>;
+    Part sl;
     int tid, lane, warp;
     uint32_t rank, cl, turn;
 
@@ -518,13 +605,45 @@ struct Row {
         tid = threadIdx.x;
         lane = tid & 31;
         warp = tid >> 5;
-        rank = cl_rank();
-        cl = cl_size();
+        rank = FAR ? 0 : cl_rank();
+        cl = FAR ? 1 : cl_size();
         turn = 0;
-        cl_arrive();  // (ended by started(): a CTA's shared memory is there once it runs)
+        if (!FAR)
+            cl_arrive();  // (ended by started(): a CTA's shared memory is there once it runs)
     }
     // before the first access to another CTA's shared memory
-    DDT_DEVINL void started() { cl_wait(); }
+    DDT_DEVINL void started()
+    {
+        if (!FAR)
+            cl_wait();
+    }
+    DDT_DEVINL void sync_row()
+    {
+        if (FAR)
+            __syncthreads();
+        else
+            cl_sync();
+    }
+    // f(sub-chunk, its raw 16 bytes) over this warp's part; end(group) after each group
+    template <typename F, typename End>
+    DDT_DEVINL void each(F f, End end) const
+    {
+        constexpr int G = Part::G;
+        const int n = sl.groups();
+        for (int g = warp; g < n; g += WARPS) {
+            uint4 x[G];
+            sl.raws(g * G, lane, x);
+#pragma unroll
+            for (int b = 0; b < G; ++b)
+                f(g * G + b, x[b]);
+            end(g);
+        }
+    }
+    template <typename F>
+    DDT_DEVINL void each(F f) const
+    {
+        each(f, [](int) {});
+    }
 
     // Every CTA tells the others up to four words (held by every thread). A place is
     // written again only two exchanges later, behind a barrier that its readers reach
@@ -532,6 +651,12 @@ struct Row {
     DDT_DEVINL const uint64_t (*exchange(uint64_t a, uint64_t b, uint64_t c, uint64_t d))[4]
     {
         const uint32_t p = turn++ & 1;
+        if (FAR) {
+            if (tid < 4)
+                sh->x.w[p][0][tid] = tid == 0 ? a : tid == 1 ? b : tid == 2 ? c : d;
+            __syncthreads();
+            return sh->x.w[p];
+        }
         if (tid < (int)cl * 4) {
             const int q = tid & 3;
             cl_st64(cl_map(&sh->x.w[p][rank][q], tid >> 2), q == 0 ? a : q == 1 ? b : q == 2 ? c : d);
@@ -544,46 +669,49 @@ struct Row {
     DDT_DEVINL void load(unsigned char *smem, const T *row, int V)
     {
         sl.place(smem, row, V, rank, cl);
-        sl.fetch(row, tid);
+        if (!FAR)
+            sl.fetch(tid);
         if (tid < 32)
             sh->tab[tid] = SR_TABLE[tid];
     }
     DDT_DEVINL void loaded()
     {
+        if (FAR) {
+            __syncthreads();
+            return;
+        }
         cp_wait_all();
         __syncthreads();
         sl.mend(tid);
         __syncthreads();
     }
 
-    // ---- the row's largest and least (finite) value, the largest of each thread's
+    // ---- the row's largest and least (finite) value, the largest of each thread's (FAR: of
+    // each of SR_OWN parts of them)
     struct Top {
-        float zmax, own, low;
+        float zmax, own[OWN], low;
         bool nan;
     };
     DDT_DEVINL Top top()
     {
-        float m, lo;
-        bool nan = false;
-        typename Vec<T>::Range range;
-        Vec<T>::begin(range);
-        for (int s = warp; s < sl.ns; s += 2 * SR_WARPS) {
-            const bool two = s + SR_WARPS < sl.ns;
-            const uint4 x = sl.raw(s, lane), y = sl.raw(two ? s + SR_WARPS : s, lane);
-            bool bad = Vec<T>::look(range, x);
-            bad |= Vec<T>::look(range, y);
-            if (bad) {  // from here on a NaN is -infinity, and what is next to 0 is 0
-                nan |= mend_vector(s);
-                if (two)
-                    nan |= mend_vector(s + SR_WARPS);
-            }
-        }
-        Vec<T>::end(range, m, lo);
-        // (what lies next to 0 counts as 0, here too)
-        m = fabsf(m) < SR_TINY ? 0.f : m;
-        lo = fabsf(lo) < SR_TINY ? 0.f : lo;
         Top r;
-        r.own = m;
+        bool nan = false;
+        float m, lo;
+        if (__syncthreads_or(look(r, m, lo))) {
+            // from here on a NaN is -infinity, and what is next to 0 is 0
+            sl.odd = FAR;
+            each([&](int s, const uint4 &v) {
+                float z[E];
+                Vec<T>::get(v, z);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    nan |= z[e] != z[e];
+                if (!FAR)
+                    mend_vector(s);
+            });
+            __syncthreads();
+            look(r, m, lo);
+        }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
@@ -595,7 +723,7 @@ struct Row {
         __syncthreads();
         nan = false;
 #pragma unroll
-        for (int w = 0; w < SR_WARPS; ++w) {
+        for (int w = 0; w < WARPS; ++w) {
             const uint64_t x = sh->warp[w][0];
             m = fmaxf(m, __uint_as_float((uint32_t)(x >> 32)));
             lo = fminf(lo, __uint_as_float((uint32_t)x));
@@ -613,47 +741,67 @@ struct Row {
         r.nan = nan;
         return r;
     }
-    // a lane's vector with odd values; whether it has a NaN
-    DDT_DEVINL bool mend_vector(int s)
+    // this thread's part of that; whether there are odd values
+    DDT_DEVINL bool look(Top &r, float &m, float &lo)
     {
-        T *d = reinterpret_cast<T *>(sl.at + s * SR_SUB + lane * 16);
-        float z[E];
-        sl.get(s, lane, z);
-        bool nan = false;
+        typename Vec<T>::Range range[OWN];
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (z[e] != z[e]) {
-                nan = true;
-                d[e] = Slice<T>::none();
-            } else if (fabsf(z[e]) < SR_TINY) {
-                d[e] = (T)0;
+        for (int o = 0; o < OWN; ++o)
+            Vec<T>::begin(range[o]);
+        // (sub-chunks at once; near ones may be looked at twice)
+        constexpr int N = FAR ? SR_OWN : 2;
+        for (int s = warp * (FAR ? N : 1); s < sl.ns; s += WARPS * N) {
+            uint4 x[N];
+            if (FAR) {
+                sl.raws(s, lane, x);
+                if (sl.odd) {
+#pragma unroll
+                    for (int o = 0; o < N; ++o)
+                        x[o] = sl.mended(x[o]);
+                }
+            } else {
+#pragma unroll
+                for (int o = 0; o < N; ++o)
+                    x[o] = sl.raw(s + o * WARPS < sl.ns ? s + o * WARPS : s, lane);
             }
-        return nan;
+#pragma unroll
+            for (int o = 0; o < N; ++o)
+                Vec<T>::look(range[FAR ? o : 0], x[o]);
+        }
+        bool odd = false;
+        m = DDT_NEG_INF;
+        lo = SR_MAX_FLOAT;
+#pragma unroll
+        for (int o = 0; o < OWN; ++o) {
+            float l;
+            odd |= Vec<T>::odd(range[o]);
+            Vec<T>::end(range[o], r.own[o], l);
+            m = fmaxf(m, r.own[o]);
+            lo = fminf(lo, l);
+        }
+        return odd;
     }
+    // a lane's vector with odd values
+    DDT_DEVINL void mend_vector(int s) { *reinterpret_cast<uint4 *>(sl.at + s * SR_SUB + lane * 16) = sl.mended(sl.raw(s, lane)); }
     // a row with +infinity: those tokens have equal weights, the others none
     DDT_DEVINL void only_infinite(Top &t)
     {
-        for (int s = warp; s < sl.ns; s += SR_WARPS) {
-            T *d = reinterpret_cast<T *>(sl.at + s * SR_SUB + lane * 16);
-            float z[E];
-            sl.get(s, lane, z);
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                d[e] = z[e] == t.zmax ? (T)0 : Slice<T>::none();
-        }
-        __syncthreads();
-        t.own = t.own == t.zmax ? 0.f : DDT_NEG_INF;
-        t.zmax = t.low = 0.f;
-    }
-
-    // an element of this CTA's slice
-    DDT_DEVINL float value(int i) const
-    {
-        const T x = reinterpret_cast<const T *>(sl.at)[i + sl.off - sl.s0 * Slice<T>::SE];
-        if constexpr (sizeof(T) == 2)
-            return bf16_to_f32(x);
+        if (FAR)
+            sl.odd = sl.infinite = true;
         else
-            return x;
+            for (int s = warp; s < sl.ns; s += WARPS) {
+                T *d = reinterpret_cast<T *>(sl.at + s * SR_SUB + lane * 16);
+                float z[E];
+                sl.get(s, lane, z);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    d[e] = z[e] == t.zmax ? (T)0 : Part::none();
+            }
+        __syncthreads();
+#pragma unroll
+        for (int o = 0; o < OWN; ++o)
+            t.own[o] = t.own[o] == t.zmax ? 0.f : DDT_NEG_INF;
+        t.zmax = t.low = 0.f;
     }
 
     // block-wide sum of one word a thread, known to all
@@ -666,7 +814,7 @@ struct Row {
         __syncthreads();
         uint64_t t = 0;
 #pragma unroll
-        for (int w = 0; w < SR_WARPS; ++w)
+        for (int w = 0; w < WARPS; ++w)
             t += sh->warp[w][0];
         return t;
     }
@@ -677,9 +825,10 @@ struct Row {
     {
         uint64_t own = 0;
         const bool cut = b.last < sl.V - 1;
-        for (int s = warp; s < sl.ns; s += SR_WARPS) {
+        uint64_t group = 0;
+        each([&](int s, const uint4 &v) {
             float z[E];
-            sl.get(s, lane, z);
+            sl.values(v, z);
             const int i0 = sl.index0(s, lane);
             bool k[E], some = false;
 #pragma unroll
@@ -689,24 +838,21 @@ struct Row {
                     k[e] = i0 + e <= b.last;
                 some |= k[e];
             }
-            uint64_t q = 0;
             if (__any_sync(0xFFFFFFFFu, some)) {
                 Sum2 sum = {0, 0};
 #pragma unroll
                 for (int e = 0; e < E; e += 2)
                     add_weights<EXACT>(sc, sh->tab, z[e], z[e + 1], k[e], k[e + 1], sum);
-                q = to_fixed(sum);
-                if (sub)
-                    q = warp_sum64(q);
+                group += to_fixed(sum);
             }
-            if (sub) {
-                if (lane == 0)
-                    sub[s] = q;
-                else
-                    q = 0;
-            }
-            own += q;
-        }
+        }, [&](int g) {
+            own += group;
+            if (sub && __any_sync(0xFFFFFFFFu, group != 0))
+                group = warp_sum64(group);
+            if (sub && lane == 0)
+                sub[g] = group;
+            group = 0;
+        });
         const uint64_t mine = block_sum(own);
         const uint64_t(*a)[4] = exchange(mine, 0, 0, 0);
         uint64_t t = 0;
@@ -717,23 +863,24 @@ struct Row {
         return t;
     }
 
-    // ---- the same in plain fp32 (see quick_slack), of the tokens from lo up
-    DDT_DEVINL uint64_t quick_mass(const Scale &sc, float lo, uint64_t *sub, const uint64_t (**all)[4])
+    // ---- the same in plain fp32 (see quick_slack)
+    DDT_DEVINL uint64_t quick_mass(const Scale &sc, const Border &b, uint64_t *sub, const uint64_t (**all)[4])
     {
-        uint64_t own = 0;
-        for (int s = warp; s < sl.ns; s += SR_WARPS) {
+        uint64_t own = 0, group = 0;
+        const bool cut = b.last < sl.V - 1;
+        each([&](int s, const uint4 &v) {
             float z[E];
-            sl.get(s, lane, z);
-            uint64_t q = quick_fixed(sc, lo, z, E - 1);
+            sl.values(v, z);
+            group += cut ? quick_fixed(sc, b, z, sl.index0(s, lane), E - 1) : quick_fixed(sc, {b.z, 0x7FFFFFFF}, z, 0, E - 1);
+        }, [&](int g) {
+            own += group;
             if (sub) {
-                q = warp_sum64(q);
+                group = warp_sum64(group);
                 if (lane == 0)
-                    sub[s] = q;
-                else
-                    q = 0;
+                    sub[g] = group;
             }
-            own += q;
-        }
+            group = 0;
+        });
         const uint64_t(*a)[4] = exchange(block_sum(own), 0, 0, 0);
         uint64_t t = 0;
         for (uint32_t c = 0; c < cl; ++c)
@@ -742,21 +889,22 @@ struct Row {
             *all = a;
         return t;
     }
-    DDT_DEVINL static uint64_t quick_fixed(const Scale &sc, float lo, const float *z, int last)
+    DDT_DEVINL static uint64_t quick_fixed(const Scale &sc, const Border &b, const float *z, int i0, int last)
     {
         uint64_t w = 0;
+        const auto in = [&](int e) { return e <= last && (b.last == 0x7FFFFFFF ? z[e] >= b.z : kept(b, z[e], i0 + e)); };
 #pragma unroll
         for (int e = 0; e < E; e += 2)
-            w = f2add(w, quick_weights<EXACT>(sc, z[e], z[e + 1], e <= last && z[e] >= lo, e + 1 <= last && z[e + 1] >= lo));
-        float a, b;
-        f2unpack(w, a, b);
-        return __float2ull_rn((a + b) * 17592186044416.0f);
+            w = f2add(w, quick_weights<EXACT>(sc, z[e], z[e + 1], in(e), in(e + 1)));
+        float w0, w1;
+        f2unpack(w, w0, w1);
+        return __float2ull_rn((w0 + w1) * 17592186044416.0f);
     }
     struct QuickWeight {  // adds these up
         Scale sc;
-        float lo;
-        DDT_DEVINL uint64_t sum_to(const float *z, int, int last) const { return quick_fixed(sc, lo, z, last); }
-        DDT_DEVINL uint64_t lane_sum(const float *z, int) const { return quick_fixed(sc, lo, z, E - 1); }
+        Border b;
+        DDT_DEVINL uint64_t sum_to(const float *z, int i0, int last) const { return quick_fixed(sc, b, z, i0, last); }
+        DDT_DEVINL uint64_t lane_sum(const float *z, int i0) const { return quick_fixed(sc, b, z, i0, E - 1); }
     };
 
     // ---- histogram of values from vhi down, and the first bin at which the tokens so far
@@ -769,13 +917,21 @@ struct Row {
     }
     DDT_DEVINL void clear_hist()
     {
-        sh->hist[tid] = sh->hist[tid + SR_THREADS] = 0;
+        for (int i = tid; i < SR_BINS; i += THREADS)
+            sh->hist[i] = 0;
         __syncthreads();
     }
     // after a cluster barrier: this thread's two bins over the whole row
     DDT_DEVINL void row_bins(uint32_t &n0, uint32_t &n1)
     {
         n0 = n1 = 0;
+        if (FAR) {
+            if (2 * tid < SR_BINS) {
+                n0 = sh->hist[2 * tid];
+                n1 = sh->hist[2 * tid + 1];
+            }
+            return;
+        }
         for (uint32_t b = 0; b < cl; b += 4) {  // (four at a time: the loads overlap)
             uint32_t x[4], y[4];
 #pragma unroll
@@ -812,23 +968,27 @@ struct Row {
         __syncthreads();
         int r = 0x7FFFFFFF;
 #pragma unroll
-        for (int w = 0; w < SR_WARPS; ++w)
+        for (int w = 0; w < WARPS; ++w)
             r = min(r, (int)(uint32_t)sh->warp[w][0]);
         return r;
     }
 
-    // ---- collect the tokens that `in` names in the first CTA (in any order); returns how
-    // many there are, which may be more than the list holds (then it holds none). Each CTA
-    // lists its own; the first one fetches them: the others may not leave before fetched().
+    // ---- collect the tokens that `in` names, all of them at or above `from`, in the first
+    // CTA (in any order); returns how many there are, which may be more than the list holds
+    // (then it holds none). Each CTA lists its own; the first one fetches them: the others
+    // may not leave before fetched().
     template <typename In>
-    DDT_DEVINL uint32_t collect(In in)
+    DDT_DEVINL uint32_t collect(float from, In in)
     {
         if (tid == 0)
             sh->count = 0;
         __syncthreads();
-        for (int s = warp; s < sl.ns; s += SR_WARPS) {
+        uint64_t *to = FAR ? sh->list : sh->mine;
+        each([&](int s, const uint4 &v) {
+            if (!(FAR && sl.odd) && !Vec<T>::reaches(v, from))
+                return;
             float z[E];
-            sl.get(s, lane, z);
+            sl.values(v, z);
             const int i0 = sl.index0(s, lane);
             bool k[E];
             uint32_t n = 0;
@@ -841,19 +1001,21 @@ struct Row {
                 for (int e = 0; e < E; ++e)
                     if (k[e]) {
                         if (p < SR_CAP)
-                            sh->mine[p] = ((uint64_t)order_key(z[e]) << 32) | (uint32_t)~(i0 + e);
+                            to[p] = ((uint64_t)order_key(z[e]) << 32) | (uint32_t)~(i0 + e);
                         ++p;
                     }
             }
-        }
+        });
         __syncthreads();
+        if (FAR)
+            return sh->count;
         const uint64_t(*all)[4] = exchange(sh->count, 0, 0, 0);
         uint32_t n = 0;
         for (uint32_t c = 0; c < cl; ++c)
             n += (uint32_t)all[c][0];
         if (n <= SR_CAP) {
             if (rank == 0) {
-                for (uint32_t i = tid; i < n; i += SR_THREADS) {
+                for (uint32_t i = tid; i < n; i += THREADS) {
                     uint32_t c = 0, j = i;
                     while (j >= (uint32_t)all[c][0])
                         j -= (uint32_t)all[c++][0];
@@ -866,7 +1028,13 @@ struct Row {
         return n;
     }
     // (after a collection that the list holds, before anything else between CTAs)
-    DDT_DEVINL void fetched() { cl_wait(); }
+    DDT_DEVINL void fetched()
+    {
+        if (FAR)
+            __syncthreads();
+        else
+            cl_wait();
+    }
 
     // the first CTA: its list's n candidates in descending order (value, then lower index)
     DDT_DEVINL void sort_list(int n)
@@ -874,12 +1042,12 @@ struct Row {
         int p2 = 32;
         while (p2 < n)
             p2 <<= 1;
-        for (int i = n + tid; i < p2; i += SR_THREADS)
+        for (int i = n + tid; i < p2; i += THREADS)
             sh->list[i] = 0;
         __syncthreads();
         for (int k = 2; k <= p2; k <<= 1)
             for (int j = k >> 1; j > 0; j >>= 1) {
-                for (int i = tid; i < p2 / 2; i += SR_THREADS) {
+                for (int i = tid; i < p2 / 2; i += THREADS) {
                     const int lo = 2 * j * (i / j) + i % j, hi = lo + j;
                     const uint64_t a = sh->list[lo], b = sh->list[hi];
                     if ((a < b) == ((lo & k) == 0)) {
@@ -908,7 +1076,8 @@ struct Row {
         const uint64_t key = tid < n ? sh->list[tid] : 0;
         const float z = key_value((uint32_t)(key >> 32));
         const uint64_t w = tid < n ? weight_of<EXACT>(sc, sh->tab, z) : 0;
-        sh->kept[tid] = w;
+        if (tid < SR_SMALL)
+            sh->kept[tid] = w;
         if (tid == 0)
             sh->found[0] = 0;
         __syncthreads();
@@ -936,7 +1105,8 @@ struct Row {
             sh->found[0] = tid;
             sh->warp[0][3] = before + w;
         }
-        sh->kept[tid] = in ? w : 0;
+        if (tid < SR_SMALL)
+            sh->kept[tid] = in ? w : 0;
         __syncthreads();
         Cut c;
         const uint64_t last = sh->list[sh->found[0]];
@@ -1002,20 +1172,22 @@ struct Row {
     {
         const float vlo = fmaxf(t.low, lo), scale = bin_scale(t.zmax, vlo);
         clear_hist();
-        if ((int64_t)sl.V >= (int64_t)4 * need * E && cl * SR_THREADS >= 4 * need) {
-            if (t.own >= vlo)
-                atomicAdd(&sh->hist[bin_of(t.zmax, scale, t.own)], 1u);
+        if ((int64_t)sl.V >= (int64_t)4 * need * E && cl * THREADS * OWN >= 4 * need) {
+#pragma unroll
+            for (int o = 0; o < OWN; ++o)
+                if (t.own[o] >= vlo)
+                    atomicAdd(&sh->hist[bin_of(t.zmax, scale, t.own[o])], 1u);
         } else {
-            for (int s = warp; s < sl.ns; s += SR_WARPS) {
+            each([&](int, const uint4 &v) {
                 float z[E];
-                sl.get(s, lane, z);
+                sl.values(v, z);
 #pragma unroll
                 for (int e = 0; e < E; ++e)
                     if (z[e] >= vlo)
                         atomicAdd(&sh->hist[bin_of(t.zmax, scale, z[e])], 1u);
-            }
+            });
         }
-        cl_sync();
+        sync_row();
         uint32_t n0, n1;
         row_bins(n0, n1);
         const uint64_t incl = block_incl(n0 + n1);
@@ -1039,9 +1211,9 @@ struct Row {
         uint64_t w = 0, all = 0;
         uint32_t n = 0;
         float lo = SR_MAX_FLOAT, hi = -SR_MAX_FLOAT;
-        for (int s = warp; s < sl.ns; s += SR_WARPS) {
+        each([&](int s, const uint4 &v) {
             float z[E];
-            sl.get(s, lane, z);
+            sl.values(v, z);
             const int i0 = sl.index0(s, lane);
             bool k[E], some = false;
 #pragma unroll
@@ -1068,7 +1240,7 @@ struct Row {
                                        !k[e + 1] && kept(keep, z[e + 1], i0 + e + 1), sum);
                 all += to_fixed(sum);
             }
-        }
+        });
         w = warp_sum64(w);
         all = warp_sum64(all) + w;
         n = __reduce_add_sync(0xFFFFFFFFu, n);
@@ -1096,7 +1268,7 @@ struct Row {
             }
             return m;
         };
-        const Members m = sum(sh->warp, SR_WARPS);
+        const Members m = sum(sh->warp, WARPS);
         return sum(exchange(m.before, m.n, ((uint64_t)__float_as_uint(m.hi) << 32) | __float_as_uint(m.lo), m.all), cl);
     }
 
@@ -1112,7 +1284,7 @@ struct Row {
             before += all[c][0];
         if (!(before <= target && target < before + all[rank][0]))
             return -1;
-        const int per = (sl.ns + SR_THREADS - 1) / SR_THREADS, a = min(sl.ns, tid * per), b = min(sl.ns, a + per);
+        const int ng = sl.groups(), per = (ng + THREADS - 1) / THREADS, a = min(ng, tid * per), b = min(ng, a + per);
         uint64_t own = 0;
         for (int s = a; s < b; ++s)
             own += sub[s];
@@ -1127,14 +1299,22 @@ struct Row {
         __syncthreads();
         if (warp > 0)
             return -1;
-        const int s = sh->found[0];
+        int s = sh->found[0] * Part::G;
         at = sh->warp[0][3];
         float z[E];
-        sl.get(s, lane, z);
-        const uint64_t sum = f.lane_sum(z, sl.index0(s, lane));
-        uint64_t to = at + warp_incl64(sum, lane);
-        const uint32_t hit = __ballot_sync(0xFFFFFFFFu, target < to);
-        const int who = __ffs(hit) - 1;  // (the sub-chunk's sum is the lanes': one is hit)
+        uint64_t sum, to;
+        uint32_t hit;
+        for (int end = s + Part::G;;) {  // (the group's sum is its lanes': one is hit)
+            sl.get(s, lane, z);
+            sum = f.lane_sum(z, sl.index0(s, lane));
+            to = at + warp_incl64(sum, lane);
+            hit = __ballot_sync(0xFFFFFFFFu, target < to);
+            if (Part::G == 1 || hit != 0 || s + 1 == end)
+                break;
+            at = __shfl_sync(0xFFFFFFFFu, to, 31);
+            ++s;
+        }
+        const int who = __ffs(hit) - 1;
         at = __shfl_sync(0xFFFFFFFFu, to - sum, who);
 #pragma unroll
         for (int e = 0; e < E; ++e)
@@ -1155,16 +1335,18 @@ struct Row {
     template <typename F>
     DDT_DEVINL uint64_t total(const F &f, uint64_t *sub, const uint64_t (**all)[4])
     {
-        uint64_t own = 0;
-        for (int s = warp; s < sl.ns; s += SR_WARPS) {
+        uint64_t own = 0, group = 0;
+        each([&](int s, const uint4 &v) {
             float z[E];
-            sl.get(s, lane, z);
-            const uint64_t q = warp_sum64(f.lane_sum(z, sl.index0(s, lane)));
-            if (lane == 0) {
-                sub[s] = q;
-                own += q;
-            }
-        }
+            sl.values(v, z);
+            group += f.lane_sum(z, sl.index0(s, lane));
+        }, [&](int g) {
+            own += group;
+            group = warp_sum64(group);
+            if (lane == 0)
+                sub[g] = group;
+            group = 0;
+        });
         const uint64_t(*a)[4] = exchange(block_sum(own), 0, 0, 0);
         uint64_t t = 0;
         for (uint32_t c = 0; c < cl; ++c)
@@ -1216,15 +1398,15 @@ struct Row {
         for (int it = 0; it < 64; ++it) {
             const float scale = bin_scale(vhi, vlo);
             clear_hist();
-            for (int s = warp; s < sl.ns; s += SR_WARPS) {
+            each([&](int, const uint4 &v) {
                 float z[E];
-                sl.get(s, lane, z);
+                sl.values(v, z);
 #pragma unroll
                 for (int e = 0; e < E; ++e)
                     if (z[e] >= vlo && z[e] <= vhi)
                         atomicAdd(&sh->hist[bin_of(vhi, scale, z[e])], 1u);
-            }
-            cl_sync();
+            });
+            sync_row();
             uint32_t n0, n1;
             row_bins(n0, n1);
             const uint64_t incl = before + block_incl(n0 + n1);
@@ -1241,7 +1423,7 @@ struct Row {
             const uint64_t n = sh->warp[0][2];
             auto in = [=](float z, int) { return z >= vlo && z <= vhi && bin_of(vhi, scale, z) == b; };
             if (n <= SR_CAP) {
-                collect(in);
+                collect(vlo, in);
                 fetched();
                 return cut_list(sc, (int)n, (int)(want - before), 0, 0).b;
             }
@@ -1268,16 +1450,16 @@ struct Row {
         for (int it = 0; it < 64; ++it) {
             const float scale = bin_scale(vhi, vlo);
             clear_hist();
-            for (int s = warp; s < sl.ns; s += SR_WARPS) {
+            each([&](int s, const uint4 &v) {
                 float z[E];
-                sl.get(s, lane, z);
+                sl.values(v, z);
                 const int i0 = sl.index0(s, lane);
 #pragma unroll
                 for (int e = 0; e < E; ++e)
                     if (z[e] >= vlo && z[e] <= vhi && kept(b, z[e], i0 + e))
                         atomicAdd(&sh->hist[bin_of(vhi, scale, z[e])], 1u);
-            }
-            cl_sync();
+            });
+            sync_row();
             uint32_t n[2];
             row_bins(n[0], n[1]);
             uint64_t up[2], low[2];
@@ -1314,7 +1496,7 @@ struct Row {
             if (m.n == 0)  // (not so: the bounds hold)
                 break;
             if (m.n <= SR_CAP) {
-                collect(in);
+                collect(vlo, in);
                 fetched();
                 return cut_list(sc, (int)m.n, (int)m.n, above, least);
             }
@@ -1341,6 +1523,7 @@ struct Row {
         Border b;
         uint64_t mass;
         int token;
+        bool quick;
     };
     template <bool COUNTS>
     DDT_DEVINL bool solve(const Top &t, const Scale &sc, const Settings &set, float min_z, float u, uint64_t *sub, Found &r)
@@ -1350,9 +1533,10 @@ struct Row {
         Border b = {lo, 0x7FFFFFFF};
         r.token = -1;
         r.mass = 0;
+        r.quick = false;
         if (k > 0 && k <= SR_PROBE) {
             const float tau = probe(t, lo, k);
-            const uint32_t n = collect([=](float z, int) { return z >= tau; });
+            const uint32_t n = collect(tau, [=](float z, int) { return z >= tau; });
             if (n <= SR_SMALL) {
                 if (rank == 0) {
                     const Cut c = small_list(sc, (int)n, k, p, 0, 0, u, r.token);
@@ -1378,16 +1562,18 @@ struct Row {
                 return false;
             b = count_border(t, sc, lo, k, sub);
         }
+        if (FAR && COUNTS && p < 1.f)
+            return false;
         if (p < 1.f) {
             const bool whole = b.last == 0x7FFFFFFF && b.z == lo;
-            const uint64_t about = whole ? quick_mass(sc, lo, nullptr, nullptr) : mass(sc, b, nullptr, nullptr);
+            const uint64_t about = whole ? quick_mass(sc, b, nullptr, nullptr) : mass(sc, b, nullptr, nullptr);
             // (a share of which more tokens are needed than the list takes, as no token weighs
             // more than 1, or very likely so, is not looked for there)
             uint32_t n = SR_CAP + 1;
             float tau = b.z;
             if (about < (uint64_t)SR_FLAT << SR_ONE) {
                 tau = probe(t, b.z, SR_PROBE / 2);
-                n = collect([=](float z, int i) { return z >= tau && kept(b, z, i); });
+                n = collect(tau, [=](float z, int i) { return z >= tau && kept(b, z, i); });
             }
             if (n <= SR_SMALL) {
                 // (all that is kept: its own sum is exact)
@@ -1411,17 +1597,27 @@ struct Row {
             r.mass = c.mass;
         }
         r.b = b;
+        finish(sc, u, k > 0 || p < 1.f, sub, r);
+        return true;
+    }
+    // The border and (or 0) the mass are known: the mass where no token is asked for (FAR: by
+    // quick weights, which r.quick tells), or the token. exact: the mass is to be exact
+    DDT_DEVINL void finish(const Scale &sc, float u, bool exact, uint64_t *sub, Found &r)
+    {
+        const Border b = r.b;
         if (u < 0.f) {
-            if (r.mass == 0)
-                r.mass = mass(sc, b, nullptr, nullptr);
-            return true;
+            if (r.mass == 0) {
+                r.quick = FAR;
+                r.mass = FAR ? quick_mass(sc, b, nullptr, nullptr) : mass(sc, b, nullptr, nullptr);
+            }
+            return;
         }
         const uint64_t(*all)[4];
-        if (b.last == 0x7FFFFFFF && !(p < 1.f)) {
+        if (r.mass > 0 || !exact) {
             // by quick weights; they stand unless the token's ends lie within their error
-            const QuickWeight f = {sc, b.z};
-            r.mass = quick_mass(sc, b.z, sub, &all);
-            const uint64_t target = draw_target(u, r.mass), slack = 2 * quick_slack(r.mass);
+            const QuickWeight f = {sc, b};
+            const uint64_t q = quick_mass(sc, b, sub, &all);
+            const uint64_t target = draw_target(u, q), slack = 2 * quick_slack(q);
             uint64_t from = 0, to = 0;
             r.token = locate(sub, all, target, f, &from, &to);
             __syncthreads();
@@ -1429,19 +1625,21 @@ struct Row {
                 sh->found[1] = 0;
             __syncthreads();
             if (r.token >= 0)
-                sh->found[1] = (from == 0 || target - from >= slack) && (to == r.mass || to - target > slack);
+                sh->found[1] = (from == 0 || target - from >= slack) && (to == q || to - target > slack);
             __syncthreads();
             const uint64_t(*sure)[4] = exchange(sh->found[1], 0, 0, 0);
             uint64_t any = 0;
             for (uint32_t c = 0; c < cl; ++c)
                 any |= sure[c][0];
-            if (any)
-                return true;
+            if (any) {
+                if (r.mass == 0)
+                    r.mass = q;
+                return;
+            }
         }
         r.mass = mass(sc, b, sub, &all);
         const Weight w = {sc, b, sh->tab};
         r.token = locate(sub, all, draw_target(u, r.mass), w);
-        return true;
     }
 
     struct Weight {  // adds up the kept tokens' weights
