@@ -443,8 +443,9 @@ ddt_status ddt_sample(ddt_ctx *ctx, const void *logits, int32_t dtype, int32_t N
  * setting, or whose drawn row has no weights, gets -1 as its drawn token (with a bad
  * setting no guess is kept either: acc_len 1). The call uses the context's workspace:
  * calls on one context, and graphs captured from them, must not overlap. Outputs may
- * not share memory with what the call reads, nor with each other. The calling thread's
- * current device stays as it was. */
+ * not share memory with what the call reads, nor with each other. A draft row and a
+ * target row together may have some 3.4 MB (two of bf16: 850000 tokens), else the call
+ * is DDT_EUNSUPPORTED. The calling thread's current device stays as it was. */
 ddt_status ddt_accept_sampled(ddt_ctx *ctx, const void *draft_logits, const void *target_logits,
                               const int32_t *draft_tokens, const float *u, const float *r, int32_t R,
                               const ddt_filter *draft_filter, const ddt_filter *target_filter,

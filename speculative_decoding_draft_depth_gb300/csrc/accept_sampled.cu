@@ -435,6 +435,14 @@ cudaError_t chains(const ddt_ctx *c, const void *draft, const void *target, cons
 
 size_t sample_row_bytes() { return sizeof(KeptRow); }
 
+// chain_kernel holds a row of both
+bool accept_sampled_fits(const ddt_config &c)
+{
+    const int q = c.draft_dtype == DDT_BF16 ? 2 : 4;
+    return (c.target_dtype == DDT_BF16 ? slice_bytes<uint16_t>(c.V, SR_MAX_CL, q) : slice_bytes<float>(c.V, SR_MAX_CL, q)) <=
+           SR_SMEM_MAX;
+}
+
 cudaError_t launch_accept_sampled(const ddt_ctx *c, const void *draft, const void *target, const ddt_filter &fd,
                                   const ddt_filter &ft, const int32_t *tokens, const float *u, const float *r, int R,
                                   const int32_t *n_guess, int32_t *acc_len, int32_t *acc_tokens, cudaStream_t s)

@@ -780,6 +780,8 @@ ddt_status ddt_accept_sampled(ddt_ctx *ctx, const void *draft_logits, const void
     const ddt_status st = check_R(ctx, R);
     if (st != DDT_OK)
         return st;
+    if (!accept_sampled_fits(ctx->cfg))
+        return DDT_EUNSUPPORTED;
     if (R == 0)
         return DDT_OK;
     DDT_CHECK(draft_logits && target_logits && draft_tokens && u && r && acc_len && acc_tokens);

@@ -160,6 +160,7 @@ cudaError_t launch_accept_stochastic(const ddt_ctx *c, const void *draft, const 
 
 // sampling under settings, and chain verification with them (sample.cu)
 size_t sample_row_bytes();
+bool accept_sampled_fits(const ddt_config &c);
 cudaError_t launch_sample(const ddt_ctx *c, const void *logits, int dtype, int N, const ddt_filter &f, const float *u,
                           int32_t *tokens, float *logprobs, cudaStream_t s);
 cudaError_t launch_accept_sampled(const ddt_ctx *c, const void *draft, const void *target, const ddt_filter &fd,

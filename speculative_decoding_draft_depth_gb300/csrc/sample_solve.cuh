@@ -202,13 +202,14 @@ int bins_cluster(int V)
     return 0;
 }
 
-// Rows enough for every SM's CTAs twice over: a CTA each (0: not so). Its groups of sub-chunks,
-// and its bytes of shared memory
+// Rows enough for every SM's CTAs twice over, or of which a cluster cannot hold one: a CTA each
+// (0: not so). Its groups of sub-chunks, and its bytes of shared memory
 template <typename T>
 int far_groups(int V, int64_t rows, int num_sms)
 {
     const int groups = (row_subs<T>(V) + SR_GROUP - 1) / SR_GROUP;
-    return rows >= 2 * FAR_CTAS * num_sms && groups * 8 <= SR_SMEM_MAX / FAR_CTAS - FB_BYTES ? groups : 0;
+    const bool far = rows >= 2 * FAR_CTAS * num_sms || slice_bytes<T>(V, SR_MAX_CL, 0) > SR_SMEM_MAX;
+    return far && groups * 8 <= SR_SMEM_MAX / FAR_CTAS - FB_BYTES ? groups : 0;
 }
 int far_bytes(int groups) { return (groups * 8 + 15) / 16 * 16 + FB_BYTES; }
 

@@ -1,6 +1,8 @@
 """Sampling of many rows, where each has a CTA of its own that reads it from global memory:
 tokens and log probabilities against the plain 64-bit form, as for few rows (the tolerance's
 terms are those of test_gpu_sample), and drafted chains of many requests."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -8,7 +10,7 @@ import torch
 import sample_ref
 import test_gpu_accept_sampled as accept
 from speculative_decoding_draft_depth_gb300 import ddt
-from test_gpu_sample import check, settings
+from test_gpu_sample import check, make_ctx, settings
 
 pytestmark = pytest.mark.gpu
 N = 640  # (rows enough to have a CTA each)
@@ -116,3 +118,63 @@ def test_draws_next_to_the_ratio(types):
                 end = np.float32(0 if j < i % (L + 1) else 2)
                 u[i, j] = np.nextafter(np.nextafter(ratio, end), end)
     accept.check(d, t, tok, u, r, s, s)
+
+
+def test_rows_larger_than_a_cluster_holds():
+    """4 MB a row."""
+    z = logits(2, 1048576, torch.float32, 61)
+    for s in (dict(), dict(k=40, p=0.9), dict(p=0.9, T=0.8)):
+        check(z, [0.3, 0.97], settings(2, **s), ctx=make_ctx(1048576))
+
+
+def test_refusals():
+    """Null and misaligned pointers, unknown types, outputs that overlap: an error, and nothing is written."""
+    n, V = 4, 64
+    ctx = make_ctx(V, n, 2)
+    lib, h = ddt.load(), ctx._h
+    buf = torch.zeros(4096, dtype=torch.int32, device="cuda")
+    z = torch.zeros(n * 3 * V + 8, dtype=torch.bfloat16, device="cuda")
+    p, zp = buf.data_ptr(), z.data_ptr()
+    null = ctypes.POINTER(ddt.FilterArgs)()
+
+    def sample(logits=zp, dtype=ddt.BF16, rows=n, filter=null, u=p, tokens=p + 64, logprobs=p + 128):
+        return lib.ddt_sample(h, logits, dtype, rows, filter, u, tokens, logprobs, None)
+
+    def odd(**kw):
+        return ctypes.byref(ddt.FilterArgs(**kw))
+
+    assert sample() == ddt.OK and sample(logprobs=None) == ddt.OK and sample(rows=0, logits=None) == ddt.OK
+    torch.cuda.synchronize()
+    buf.fill_(-9)
+    for bad in (dict(logits=None), dict(logits=zp + 2), dict(dtype=2), dict(rows=-1), dict(u=None), dict(u=p + 1),
+                dict(tokens=None), dict(tokens=p + 66), dict(logprobs=p + 130), dict(tokens=p), dict(logprobs=p + 76),
+                dict(tokens=zp), dict(filter=odd(temperature=p + 258)), dict(filter=odd(top_k=p + 64)),
+                dict(filter=odd(min_p=p + 124))):
+        assert sample(**bad) == ddt.EINVAL, bad
+    a = dict(d=zp, t=zp, tok=p, u=p + 512, r=p + 1024, R=n, fd=null, ft=null, al=p + 2048, at=p + 3072, ng=None)
+
+    def accept_(**kw):
+        x = {**a, **kw}
+        return lib.ddt_accept_sampled(h, x["d"], x["t"], x["tok"], x["u"], x["r"], x["R"], x["fd"], x["ft"], x["al"], x["at"],
+                                      x["ng"], None)
+
+    for bad in (dict(d=None), dict(t=zp + 2), dict(tok=None), dict(u=p + 513), dict(r=None), dict(R=n + 1), dict(R=-1),
+                dict(al=None), dict(at=p + 3073), dict(al=p + 512), dict(at=p + 1000), dict(al=p + 3072), dict(ng=p + 2049),
+                dict(ng=p + 2052), dict(fd=odd(top_p=p + 2)), dict(ft=odd(min_p=p + 2048))):
+        assert accept_(**bad) == ddt.EINVAL, bad
+    torch.cuda.synchronize()
+    assert buf.unique().tolist() == [-9]
+    assert accept_(R=0, d=None) == ddt.OK
+    big = make_ctx(1048576, 1, 1)
+    assert lib.ddt_accept_sampled(big._h, zp, zp, p, p, p, 0, null, null, p, p, None, None) == ddt.EUNSUPPORTED
+
+
+def test_strided_tensors_are_refused():
+    ctx = make_ctx(64, 4, 2)
+    z, f, i = torch.zeros(4, 65, device="cuda"), torch.zeros(8, device="cuda"), torch.zeros(8, dtype=torch.int32, device="cuda")
+    good = dict(logits=z[:, :64].contiguous(), u=f[:4], tokens=i[:4])
+    ctx.ddt_sample(**good)
+    for bad in (dict(logits=z[:, :64]), dict(u=f[::2]), dict(tokens=i[::2]), dict(filter=ddt.Filter(top_p=f[:1].expand(4))),
+                dict(filter=ddt.Filter(top_k=i[::2])), dict(u=f[:4].cpu())):
+        with pytest.raises(ValueError):
+            ctx.ddt_sample(**{**good, **bad})
