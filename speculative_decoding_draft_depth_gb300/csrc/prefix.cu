@@ -8,8 +8,13 @@
 // The prefix is one more item of the tensor-core kernel (prompt_tc.cuh): the group's
 // tokens, packed one behind the other, fill its tiles of 256 rows, against keys without a
 // mask. Own keys are a launch that begins beside that one, of the same kernel or, where
-// requests have few rows, of one for few rows (prefix_few.cu, prompt_few.cu). Items leave their parts in a store by rows, cut ones in the
-// CTAs' slots, and prefix_merge_kernel adds each row's up.
+// requests have few rows, of one for few rows (prefix_few.cu, prompt_few.cu). Items leave
+// their parts in a store by rows, cut ones in the CTAs' slots, and prefix_merge_kernel adds
+// each row's up.
+//
+// What bounds it: 64 requests of a token behind 8192 shared keys (32/8 heads of 128) take 63 us
+// where the bytes take 25: a tile of the prefix 2 us on its SM, own keys in waves beside and
+// behind them, the merge 5 to 10. The same requests one by one read 64 prefixes: 340 us.
 #include "prompt_tc.cuh"
 
 namespace {

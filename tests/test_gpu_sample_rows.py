@@ -151,7 +151,7 @@ def test_refusals():
                 dict(tokens=zp), dict(filter=odd(temperature=p + 258)), dict(filter=odd(top_k=p + 64)),
                 dict(filter=odd(min_p=p + 124))):
         assert sample(**bad) == ddt.EINVAL, bad
-    a = dict(d=zp, t=zp, tok=p, u=p + 512, r=p + 1024, R=n, fd=null, ft=null, al=p + 2048, at=p + 3072, ng=None)
+    a = dict(d=zp, t=zp, tok=p, u=p + 512, r=p + 1024, R=n, fd=null, ft=null, al=p + 2048, at=p + 3200, ng=None)
 
     def accept_(**kw):
         x = {**a, **kw}
@@ -159,7 +159,7 @@ def test_refusals():
                                       x["ng"], None)
 
     for bad in (dict(d=None), dict(t=zp + 2), dict(tok=None), dict(u=p + 513), dict(r=None), dict(R=n + 1), dict(R=-1),
-                dict(al=None), dict(at=p + 3073), dict(al=p + 512), dict(at=p + 1000), dict(al=p + 3072), dict(ng=p + 2049),
+                dict(al=None), dict(at=p + 3201), dict(al=p + 512), dict(at=p + 1000), dict(al=p + 3200), dict(ng=p + 2049),
                 dict(ng=p + 2052), dict(fd=odd(top_p=p + 2)), dict(ft=odd(min_p=p + 2048))):
         assert accept_(**bad) == ddt.EINVAL, bad
     torch.cuda.synchronize()
