@@ -12,7 +12,7 @@
 // their parts in a store by rows, cut ones in the CTAs' slots, and prefix_merge_kernel adds
 // each row's up.
 //
-// What bounds it: 64 requests of a token behind 8192 shared keys (32/8 heads of 128) take 63 us
+// What bounds it: 64 requests of a token behind 8192 shared keys (32/8 heads of 128) take 60 us
 // where the bytes take 25: a tile of the prefix 2 us on its SM, own keys in waves beside and
 // behind them, the merge 5 to 10. Prompt attention of the same requests, a prefix each (in
 // L2 mostly), takes 210 us.
@@ -66,8 +66,10 @@ DDT_DEVINL void add_parts(const float *so, const float2 *sml, int rows, int c0, 
 
 // A CTA: items (request, KV head) by turns. What counts is the parts' way from L2: where an
 // item has few rows, several warps share a row's parts.
+// (Four CTAs an SM against three: 64 requests of a token 60.4 and 62.9 us a call, over 4 bits
+// 59.9 and 62.2; 8 prefixes of chains 193 and 186, 8 tokens 21.8 and 20.9.)
 template <int D>
-__global__ void __launch_bounds__(PM_THREADS) prefix_merge_kernel(const PtArgs a)
+__global__ void __launch_bounds__(PM_THREADS, 4) prefix_merge_kernel(const PtArgs a)
 {
     __shared__ Acc s_acc[PM_WARPS][32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -85,6 +87,15 @@ __global__ void __launch_bounds__(PM_THREADS) prefix_merge_kernel(const PtArgs a
         for (int qt = 0; qt * tq < q.len; ++qt) {
             const int ntok = min(tq, q.len - qt * tq), nrows = ntok << a.g_shift, row0 = q.q0 + qt * tq;
             const int2 oc = __ldcg(a.item_ctas[1] + (int64_t)h * a.T + row0);
+            // (its tokens lie in two query tiles of the prefix at most: tq <= tp)
+            int first_in = 0;
+            int2 pcs[2] = {{0, 0}, {0, 0}};
+            if (q.off > 0) {
+                const int last_in = (row0 + ntok - 1 - pre.q0) % tp;
+                first_in = (row0 - pre.q0) % tp;
+                pcs[0] = __ldcg(a.item_ctas[0] + (int64_t)h * a.T + row0 - first_in);
+                pcs[1] = __ldcg(a.item_ctas[0] + (int64_t)h * a.T + row0 + ntok - 1 - last_in);
+            }
             if (q.off == 0 && oc.x == oc.y)
                 continue;  // (the kernel before wrote the result)
             // a warp: up to eight rows (side by side in the parts), the rest of its lanes
@@ -106,7 +117,7 @@ __global__ void __launch_bounds__(PM_THREADS) prefix_merge_kernel(const PtArgs a
                     };
                     if (q.off > 0) {
                         const int in = (int)(t - pre.q0) % tp;
-                        const int2 pc = __ldcg(a.item_ctas[0] + (int64_t)h * a.T + t - in);
+                        const int2 pc = pcs[first_in + tok >= tp];
                         if (pc.x != pc.y)
                             add_parts<D>(a.part_o, a.part_ml, PP_ROWS, pc.x, pc.y, (in << a.g_shift) + hl, c4, from, by, acc);
                         else if (from == 0)
